@@ -80,19 +80,27 @@ extern "C" {
 #define TS_ROW_BAD_P        3      /* p not in (0, 1] (NaN included) */
 #define TS_ROW_BAD_T        4      /* temperature negative, NaN or infinite */
 #define TS_ROW_BAD_MINP     5      /* min_p outside [0, 1] or NaN (the _minp entry points) */
+#define TS_ROW_BAD_TOKEN    6      /* given token outside [0, vocab) and not -1 (ts_token_logp) */
 
 /* Operation ids for ts_workspace_bytes. */
 #define TS_OP_TOPK_SELECT   0
 #define TS_OP_TOPP_MASK     1
 #define TS_OP_SAMPLE_ROWS   2
+#define TS_OP_TOKEN_LOGP    3      /* k_max: n_top */
+#define TS_OP_CACHE_EVICT   4      /* vocab: slots, k_max: keep_max */
+
+/* Element types of the entry points that take one. */
+#define TS_DTYPE_F32        0
+#define TS_DTYPE_BF16       1
+#define TS_DTYPE_F16        2
 
 /* Largest supported row length (ids are int32). */
 #define TS_MAX_VOCAB        ((int64_t)1 << 30)
 
 /*
  * Workspace size in bytes for one call of `op` on `rows` rows of `vocab` logits
- * (k_max is the ts_topk_select output width; ignored for the other ops). Returns 0 for
- * invalid sizes. Pure host function: needs no device.
+ * (k_max is the ts_topk_select output width, n_top for TS_OP_TOKEN_LOGP, keep_max for
+ * TS_OP_CACHE_EVICT; ignored for the other ops). Returns 0 for invalid sizes. Pure host function: needs no device.
  */
 size_t ts_workspace_bytes(int op, int64_t rows, int64_t vocab, int32_t k_max);
 
@@ -265,6 +273,100 @@ int ts_sample_rows_rejection(const float* logits, int64_t rows, int64_t vocab, i
                              const float* min_p, const uint64_t* seed, int32_t max_rounds,
                              int32_t* out_token, int32_t* out_rounds, int32_t* row_status,
                              void* stream);
+
+/*
+ * ts_token_logp -- log probabilities of given tokens, with rank, entropy, log-sum-exp and the
+ * row's best alternatives ([LOGP] "Design: the numeric contract", for tokens that the caller
+ * names: prompt scoring, a draft's tokens, the tokens of a training batch). For row x at
+ * temperature T over the WHOLE row, with m = max x, d_i = (x_i - m)/T, S = sum exp(d_i):
+ *   logp = d_t - log S,  lse = m/T + log S,  entropy = log S - sum exp(d_i) d_i / S,
+ *   rank = 1 + the number of tokens before t in the row ordering.
+ *   logits      [rows, row_stride] of `dtype` (TS_DTYPE_*), read once; any element-aligned
+ *               address and stride.
+ *   tokens      [rows] int32 or NULL: the given token, -1 for none (logp 0, rank 0; the other
+ *               outputs as usual); any other id outside [0, vocab) gives TS_ROW_BAD_TOKEN.
+ *   temperature [rows] or NULL. Temperatures below 2^-100 act as 2^-100. T == 0: lse +inf,
+ *               entropy 0, logp 0 for the first token of the ordering and -inf for others.
+ *   n_top       alternatives per row, in [0, TS_LOGP_TOP_MAX].
+ *   out_logp, out_entropy, out_lse   [rows] fp32 or NULL (out_logp needs tokens).
+ *   out_rank    [rows] int32 or NULL (needs tokens), 1-based.
+ *   out_top_idx, out_top_logp   [rows, n_top], required if n_top > 0: the first n_top tokens
+ *               of the row ordering and their log probabilities. Masked (-inf) tokens are not
+ *               listed: unused places hold -1 and -inf.
+ *   out_stats   [rows, 4] fp32 or NULL, 16-byte aligned: what ts_token_logp_backward takes.
+ * Rows with a non-OK status get NaN, rank -1 and ids -1. -inf logits are masked tokens (a
+ * given one has logp -inf, no error). The sums run over tiles of 8192 logits (fp32
+ * exponentials, fp32 sums of a thread's 32 terms, binary64 beyond) that are joined in tile
+ * order: the same bits for every call with the same vocabulary and type, whatever the batch,
+ * the row's place in it or its address.
+ * Workspace: TS_OP_TOKEN_LOGP; rows of at most 8192 logits need none (it may be NULL).
+ */
+#define TS_LOGP_TOP_MAX 64
+int ts_token_logp(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride,
+                  const int32_t* tokens, const float* temperature, int32_t n_top, float* out_logp,
+                  int32_t* out_rank, float* out_entropy, float* out_lse, int32_t* out_top_idx,
+                  float* out_top_logp, float* out_stats, int32_t* row_status, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/*
+ * ts_token_logp_backward -- the gradient of sum(grad_logp * logp + grad_entropy * entropy +
+ * grad_lse * lse) with respect to the logits. With p_i = exp(d_i)/S, D = sum p_i d_i and
+ * a, h, l the row's gradients:  g_i = (a [i == t] + p_i (l - a - h (d_i - D))) / T.
+ *   logits, tokens, temperature   those of the forward call.
+ *   stats       [rows, 4] fp32, 16-byte aligned: the forward call's out_stats.
+ *   grad_logp (needs tokens), grad_entropy, grad_lse   [rows] fp32 or NULL (0).
+ *   grad_logits [rows, grad_stride] of `dtype`, written (the first vocab of each row). It may be
+ *               the logits themselves (same address and stride) and may not overlap them otherwise.
+ * Computed in fp32 and rounded once to `dtype`. Rows without a token (-1) ignore grad_logp;
+ * T == 0 gives 0; rows that the forward call rejected, or whose token or temperature is
+ * invalid here, get NaN. Needs no workspace.
+ */
+int ts_token_logp_backward(const void* logits, int dtype, int64_t rows, int64_t vocab,
+                           int64_t row_stride, const int32_t* tokens, const float* temperature,
+                           const float* stats, const float* grad_logp, const float* grad_entropy,
+                           const float* grad_lse, void* grad_logits, int64_t grad_stride, void* stream);
+
+/*
+ * ts_cache_evict -- which positions of a key / value cache stay: the ordered top-k select of
+ * [DETK] over accumulated attention weights, carried through to the caches. A row is one head
+ * of one sequence; its slots [0, n) are in use, n = lengths[r] clamped to [0, slots]. With
+ *   s_j = fp32(score_j + sum over w of weights[r, w, j])        (binary64 sum, one rounding)
+ * the row keeps its first k = min(keep[r], n) slots in the order (protected first, s
+ * descending, slot ascending). A slot is protected when its position is below `sinks` or above
+ * the row's largest position less `recent`. The i-th slot below k that is not kept takes over
+ * the i-th kept slot at or past k: kept slots below k stay where they are, so the order of the
+ * positions in the cache is not kept and `position` says which is where.
+ *   score       [rows, score_stride] fp32: weight accumulated so far.
+ *   position    [rows, position_stride] int32: each slot's position in its sequence.
+ *   keep        [rows] int32, >= 1; min(keep, n) <= keep_max, else TS_ROW_BAD_K.
+ *   weights     this step's attention weights of `weights_dtype`, n_weights (>= 0) for each
+ *               slot: weight w of row r starts weights_row_stride * r + weights_stride * w
+ *               elements in (the heads that share the row, times the queries). NULL if 0.
+ *   out_score, out_position   [rows, out_*_stride], [rows, keep_max] written: slots past the
+ *               new length get 0 and -1. Either may be its input (same address and stride).
+ *   out_lengths [rows] int32: k. May be `lengths`.
+ *   out_source  [rows, keep_max] int32: the slot that each slot's contents came from, then -1.
+ *   k_cache, v_cache   NULL, or a cache whose rows are moved alike, in place: row r's slot j is
+ *               at data + (r / heads) * batch_stride + (r % heads) * head_stride + j *
+ *               slot_stride (bytes), slot_bytes long. Slots must not overlap each other.
+ * Slots at or past n are never read. A row with a NaN or infinite s_j (TS_ROW_NONFINITE) or a
+ * bad keep stays as it is: its caches are not touched, out_lengths is n, out_source -1, and outputs
+ * that are not their inputs get NaN and -1. Apart from the cases named, arrays must not overlap.
+ * Workspace: TS_OP_CACHE_EVICT.
+ */
+typedef struct ts_cache {
+  void* data;
+  int64_t batch_stride, head_stride, slot_stride, slot_bytes;
+} ts_cache;
+int ts_cache_evict(const float* score, int64_t rows, int64_t slots, int64_t score_stride,
+                   const int32_t* position, int64_t position_stride, const int32_t* lengths,
+                   const int32_t* keep, int32_t keep_max, const void* weights, int weights_dtype,
+                   int64_t n_weights, int64_t weights_row_stride, int64_t weights_stride,
+                   int32_t sinks, int32_t recent, float* out_score, int64_t out_score_stride,
+                   int32_t* out_position, int64_t out_position_stride, int32_t* out_lengths,
+                   int32_t* out_source, int32_t* row_status, const ts_cache* k_cache,
+                   const ts_cache* v_cache, int64_t heads, void* workspace, size_t workspace_bytes,
+                   void* stream);
 
 /*
  * Diagnostic: the noise the sampler uses. For each tokens[j] of row `row` under `seed`,

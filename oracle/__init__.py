@@ -9,8 +9,18 @@ V <= 16, closed forms (all-equal rows, two-token rows, dominant tokens, p = 1), 
 cross-checks (numpy stable argsort, scipy logsumexp), an independent Philox4x32
 implementation (Triton's CPU interpreter, when importable), the inverse Gumbel CDF, and
 chi-square / z tests of the sampling law; for the rejection sampler, hand-worked
-trajectories with injected random words and the law of the truncated distribution. No function here is "parity unpinned".
+trajectories with injected random words and the law of the truncated distribution; for token
+log probabilities, scipy's logsumexp and entropy, closed forms and central differences; for
+cache eviction, enumeration of every kept set. No function here is "parity unpinned".
 """
+from .logprobs import (
+    EvictResult,
+    LogpResult,
+    STATUS_BAD_TOKEN,
+    cache_evict_row,
+    token_logp_grad_row,
+    token_logp_row,
+)
 from .philox import philox4x32, philox4x32_np, seed_key, token_words
 from .rejection import RejectionResult, rejection_sample_row, rejection_sample_rows, round_word
 from .sampler import (

@@ -12,7 +12,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libtopselect.so")
@@ -28,11 +28,16 @@ TS_ROW_BAD_K = 2
 TS_ROW_BAD_P = 3
 TS_ROW_BAD_T = 4
 TS_ROW_BAD_MINP = 5
+TS_ROW_BAD_TOKEN = 6
 TS_ORDER_INDEX = 0
 TS_ORDER_VALUE = 1
 TS_OP_TOPK_SELECT = 0
 TS_OP_TOPP_MASK = 1
 TS_OP_SAMPLE_ROWS = 2
+TS_OP_TOKEN_LOGP = 3
+TS_OP_CACHE_EVICT = 4
+TS_LOGP_TOP_MAX = 64
+TS_LOGP_TILE = 8192            # rows of at most this many logits need no ts_token_logp workspace
 TS_KNOB_CHUNK_ELEMS = 1
 TS_KNOB_FORCE_EXACT = 2
 TS_KNOB_DIRECT = 3
@@ -40,7 +45,8 @@ TS_KNOB_NUCLEUS_PASSES = 4
 
 EXPORTED = (
     "ts_workspace_bytes", "ts_workspace_init", "ts_topk_select", "ts_topk_select_rows", "ts_topp_mask",
-    "ts_sample_rows", "ts_sample_rows_noalloc", "ts_sample_rows_logp", "ts_topp_mask_minp", "ts_sample_rows_minp", "ts_sample_rows_rejection", "ts_gumbel_noise", "ts_noise_transform", "ts_read_ceiling", "ts_debug_set", "ts_status_string", "ts_last_error",
+    "ts_sample_rows", "ts_sample_rows_noalloc", "ts_sample_rows_logp", "ts_topp_mask_minp", "ts_sample_rows_minp", "ts_sample_rows_rejection",
+    "ts_token_logp", "ts_token_logp_backward", "ts_cache_evict", "ts_gumbel_noise", "ts_noise_transform", "ts_read_ceiling", "ts_debug_set", "ts_status_string", "ts_last_error",
 )
 
 _lib = None
@@ -87,6 +93,13 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         lib.ts_sample_rows_minp.restype = c.c_int
         lib.ts_sample_rows_rejection.restype = c.c_int
         lib.ts_sample_rows_rejection.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp]
+        lib.ts_token_logp.argtypes = [vp, c.c_int, i64, i64, i64, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        lib.ts_token_logp.restype = c.c_int
+        lib.ts_token_logp_backward.argtypes = [vp, c.c_int, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, i64, vp]
+        lib.ts_token_logp_backward.restype = c.c_int
+        lib.ts_cache_evict.argtypes = [vp, i64, i64, i64, vp, i64, vp, vp, i32, vp, c.c_int, i64, i64, i64, i32, i32, vp, i64,
+                                       vp, i64, vp, vp, vp, vp, vp, i64, vp, sz, vp]
+        lib.ts_cache_evict.restype = c.c_int
         lib.ts_gumbel_noise.argtypes = [c.c_uint64, i32, vp, i64, vp, vp, vp, vp]
         lib.ts_noise_transform.restype = c.c_int
         lib.ts_noise_transform.argtypes = [vp, i64, vp, vp, vp]
@@ -339,6 +352,192 @@ def ts_sample_rows_rejection(logits, top_k, top_p, temperature, min_p, seed, max
                                         _ptr(temperature), _ptr(min_p), _ptr(seed), int(max_rounds),
                                         _ptr(tok), _ptr(rnd), _ptr(st), _stream()))
     return tok, rnd, st
+
+
+_DTYPES = {"torch.float32": 0, "torch.bfloat16": 1, "torch.float16": 2}
+
+
+def _typed_rows(x, name: str):
+    """(dtype code, rows, columns, row stride) of a 2-D fp32, bf16 or fp16 device tensor."""
+    code = _DTYPES.get(str(x.dtype))
+    if code is None or not x.is_cuda:
+        raise TopSelectError(f"{name} must be a float32, bfloat16 or float16 CUDA/HIP tensor")
+    if x.dim() != 2 or (x.shape[0] and x.shape[1] > 1 and x.stride(1) != 1):
+        raise TopSelectError(f"{name} must be a 2-D tensor with unit column stride")
+    if x.shape[0] <= 1:      # a single row's stride carries no layout
+        return code, x.shape[0], x.shape[1], max(x.shape[1], 1)
+    return code, x.shape[0], x.shape[1], x.stride(0)
+
+
+def _param(t, dtype_name: str, rows: int, device, name: str):
+    """Pointer of an optional contiguous per-row parameter on `device`."""
+    if t is None:
+        return None
+    if str(t.dtype) != dtype_name or t.device != device or t.numel() != rows or not t.is_contiguous():
+        raise TopSelectError(f"{name} must be a contiguous {dtype_name} tensor of {rows} on {device}")
+    return t.data_ptr()
+
+
+class _on:
+    """Makes a tensor's device current for a call (its current stream is the call's)."""
+
+    def __init__(self, device):
+        import torch
+        self._guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+class TokenLogp(NamedTuple):
+    """Outputs of ts_token_logp; None for what was not asked for."""
+    logp: object        # fp32 [rows]
+    rank: object        # int32 [rows], 1-based
+    entropy: object     # fp32 [rows]
+    lse: object         # fp32 [rows]
+    top_idx: object     # int32 [rows, n_top]
+    top_logp: object    # fp32 [rows, n_top]
+    stats: object       # fp32 [rows, 4]: for ts_token_logp_backward
+    status: object      # int32 [rows]
+
+
+def ts_token_logp(logits, tokens=None, temperature=None, n_top: int = 0, want_rank: bool = True,
+                  want_entropy: bool = True, want_lse: bool = True, want_stats: bool = False) -> TokenLogp:
+    """Log probabilities and ranks of given tokens (int32 [rows], -1: none) over whole rows of fp32, bf16
+    or fp16 logits, with entropy, log-sum-exp and the n_top best tokens."""
+    import torch
+    lib = load_library()
+    code, rows, v, stride = _typed_rows(logits, "logits")
+    device = logits.device
+    tok, temp = _param(tokens, "torch.int32", rows, device, "tokens"), _param(temperature, "torch.float32", rows, device, "temperature")
+    with _on(device):
+        def new(want, shape, dtype=torch.float32):
+            return torch.empty(shape, dtype=dtype, device=device) if want else None
+        out = TokenLogp(new(tokens is not None, rows), new(tokens is not None and want_rank, rows, torch.int32),
+                        new(want_entropy, rows), new(want_lse, rows), new(n_top > 0, (rows, n_top), torch.int32),
+                        new(n_top > 0, (rows, n_top)), new(want_stats, (rows, 4)), new(True, rows, torch.int32))
+        # A workspace of the call's own: two calls captured into graphs that replay at once share none.
+        nb = 0 if v <= TS_LOGP_TILE else lib.ts_workspace_bytes(TS_OP_TOKEN_LOGP, rows, v, n_top)
+        ws = torch.empty(nb, dtype=torch.uint8, device=device) if nb else None
+        _check(lib.ts_token_logp(_ptr(logits), code, rows, v, stride, tok, temp, n_top, _ptr(out.logp), _ptr(out.rank),
+                                 _ptr(out.entropy), _ptr(out.lse), _ptr(out.top_idx), _ptr(out.top_logp),
+                                 _ptr(out.stats), _ptr(out.status), _ptr(ws), nb, _stream()))
+    return out
+
+
+def ts_token_logp_backward(logits, tokens, temperature, stats, grad_logp=None, grad_entropy=None, grad_lse=None, out=None):
+    """Gradient of sum(grad_logp * logp + grad_entropy * entropy + grad_lse * lse) with respect to the logits, in
+    their type. stats: the forward call's (want_stats). out: a tensor for it; the logits themselves are allowed."""
+    import torch
+    lib = load_library()
+    code, rows, v, stride = _typed_rows(logits, "logits")
+    device = logits.device
+    tok, temp = _param(tokens, "torch.int32", rows, device, "tokens"), _param(temperature, "torch.float32", rows, device, "temperature")
+    st = _param(stats, "torch.float32", 4 * rows, device, "stats")
+    grads = [_param(g, "torch.float32", rows, device, n)
+             for g, n in ((grad_logp, "grad_logp"), (grad_entropy, "grad_entropy"), (grad_lse, "grad_lse"))]
+    with _on(device):
+        if out is None:
+            out = torch.empty((rows, v), dtype=logits.dtype, device=device)
+        ocode, orows, ov, ostride = _typed_rows(out, "out")
+        if (ocode, orows, ov) != (code, rows, v) or out.device != device:
+            raise TopSelectError("out must have the logits' shape, type and device")
+        _check(lib.ts_token_logp_backward(_ptr(logits), code, rows, v, stride, tok, temp, st, *grads, _ptr(out), ostride, _stream()))
+    return out
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p)] + [(n, ctypes.c_int64) for n in ("batch_stride", "head_stride", "slot_stride", "slot_bytes")]
+
+
+def _cache(t, rows: int, slots: int, device, name: str):
+    """The ts_cache of a [batch, heads, slots, dim] tensor whose last dimension is contiguous."""
+    if t is None:
+        return None, 1
+    if t.dim() != 4 or t.shape[0] * t.shape[1] != rows or t.shape[2] != slots or t.device != device:
+        raise TopSelectError(f"{name} must be a [batch, heads, {slots}, dim] tensor on {device} with batch * heads = {rows}")
+    size, dim = t.element_size(), t.shape[3]
+    if dim < 1 or (dim > 1 and t.stride(3) != 1):
+        raise TopSelectError(f"{name} must have a contiguous last dimension")
+    b, h, s = (t.stride(i) if t.shape[i] > 1 else 0 for i in range(3))
+    # no two slots may share memory: along the ascending strides each must clear what lies below it
+    reach = dim
+    for stride, n in sorted((x, n) for x, n in zip((b, h, s), t.shape[:3]) if n > 1):
+        if stride < reach:
+            raise TopSelectError(f"{name} has slots that share memory")
+        reach = stride * (n - 1) + reach
+    return _Cache(t.data_ptr(), b * size, h * size, max(s, dim) * size, dim * size), t.shape[1]
+
+
+class CacheEvict(NamedTuple):
+    """Outputs of ts_cache_evict."""
+    source: object      # int32 [rows, keep_max]: the slot that each slot's contents came from, then -1
+    lengths: object     # int32 [rows]: the new lengths
+    score: object       # fp32 [rows, keep_max] (in place: the given tensor)
+    position: object    # int32 [rows, keep_max] (in place: the given tensor)
+    status: object      # int32 [rows]
+
+
+def ts_cache_evict(score, position, lengths, keep, keep_max: int, weights=None, k_cache=None, v_cache=None, sinks: int = 0,
+                   recent: int = 0, in_place: bool = False) -> CacheEvict:
+    """Keep the min(keep, lengths) slots of the largest accumulated attention weight in each row of a cache.
+
+    score fp32 [rows, slots], position int32 [rows, slots], lengths and keep int32 [rows]; weights [rows, n, slots] (fp32,
+    bf16 or fp16) is this step's attention, added first. k_cache, v_cache [batch, heads, slots, dim] with batch * heads =
+    rows are changed in place. in_place: score, position and lengths are updated too; else new tensors are returned."""
+    import torch
+    lib = load_library()
+    device = score.device
+    if str(score.dtype) != "torch.float32":
+        raise TopSelectError("score must be a float32 CUDA/HIP tensor")
+    _, rows, slots, score_stride = _typed_rows(score, "score")
+    if (str(position.dtype) != "torch.int32" or position.shape != score.shape or position.device != device
+            or (rows and slots > 1 and position.stride(1) != 1)):
+        raise TopSelectError(f"position must be an int32 [{rows}, {slots}] tensor with unit column stride on {device}")
+    position_stride = max(position.stride(0) if rows > 1 else slots, 1)
+    plen, pkeep = _param(lengths, "torch.int32", rows, device, "lengths"), _param(keep, "torch.int32", rows, device, "keep")
+    if plen is None or pkeep is None:
+        raise TopSelectError("lengths and keep are required")
+    wcode, n_w, w_row, w_stride = 0, 0, 0, slots
+    if weights is not None:
+        wcode = _DTYPES.get(str(weights.dtype))
+        if wcode is None or weights.dim() != 3 or weights.shape[0] != rows or weights.shape[2] != slots or weights.device != device:
+            raise TopSelectError(f"weights must be a float32, bfloat16 or float16 [{rows}, n, {slots}] tensor on {device}")
+        if weights.numel() and slots > 1 and weights.stride(2) != 1:
+            raise TopSelectError("weights must have a contiguous last dimension")
+        n_w = weights.shape[1]
+        w_row, w_stride = (weights.stride(0) if rows > 1 else 0), (weights.stride(1) if n_w > 1 else slots)
+    kc, k_heads = _cache(k_cache, rows, slots, device, "k_cache")
+    vc, v_heads = _cache(v_cache, rows, slots, device, "v_cache")
+    if kc and vc and k_heads != v_heads:
+        raise TopSelectError("k_cache and v_cache have different heads")
+    heads = k_heads if kc else v_heads
+    with _on(device):
+        if in_place:
+            if keep_max > slots:
+                raise TopSelectError("in place, keep_max is at most the number of slots")
+            out_score, out_position, out_lengths = score, position, lengths
+            os, op = score_stride, position_stride
+        else:
+            out_score = torch.empty((rows, keep_max), dtype=torch.float32, device=device)
+            out_position = torch.empty((rows, keep_max), dtype=torch.int32, device=device)
+            out_lengths = torch.empty(rows, dtype=torch.int32, device=device)
+            os = op = max(keep_max, 1)
+        source = torch.empty((rows, keep_max), dtype=torch.int32, device=device)
+        status = torch.empty(rows, dtype=torch.int32, device=device)
+        nb = lib.ts_workspace_bytes(TS_OP_CACHE_EVICT, rows, slots, keep_max)
+        ws = torch.empty(nb, dtype=torch.uint8, device=device)
+        _check(lib.ts_cache_evict(_ptr(score), rows, slots, score_stride, _ptr(position), position_stride, plen, pkeep, keep_max,
+                                  _ptr(weights) if n_w else None, wcode, n_w, w_row, w_stride, sinks, recent, _ptr(out_score), os,
+                                  _ptr(out_position), op, _ptr(out_lengths), _ptr(source), _ptr(status),
+                                  ctypes.byref(kc) if kc else None, ctypes.byref(vc) if vc else None, heads, _ptr(ws), nb,
+                                  _stream()))
+    return CacheEvict(source, out_lengths, out_score, out_position, status)
 
 
 def ts_gumbel_noise(seed: int, row: int, tokens):

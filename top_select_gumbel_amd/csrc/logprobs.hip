@@ -1,0 +1,653 @@
+// logprobs.hip -- log probabilities of given tokens with rank, entropy and the best alternatives, and their gradient.
+//
+// For a row x of V logits at temperature T, with m = max x, d_i = (x_i - m) / T and S = sum exp(d_i):
+//   logp_t  = d_t - log S                      lse = m / T + log S
+//   entropy = log S - (1/S) sum exp(d_i) d_i   rank_t = 1 + #{x_i > x_t} + #{i < t : x_i = x_t}
+// and with a, h, l the gradients of logp, entropy and lse, p_i = exp(d_i) / S and D = (1/S) sum exp(d_i) d_i
+//   dL/dx_i = (a [i = t] + p_i (l - a - h (d_i - D))) / T
+// since log p_i + entropy = d_i - D.
+//
+// ts_logp_tile_kernel  reads a tile of a row (8192 logits, 32 a thread, in registers) once: its maximum, the two sums
+//                      relative to it, how many logits rank above the given token, and, where alternatives are asked
+//                      for, every logit that can be among the row's best n. The sums are fp32 over a thread's
+//                      32 terms and binary64 beyond. A row of one tile is finished by the same workgroup.
+// ts_logp_row_kernel   joins a row's tiles in tile order (binary64) and ranks the candidates.
+// ts_logp_grad_kernel  one pass: reads a tile, writes its gradient.
+#include <math.h>
+
+#include <algorithm>
+
+#include "topselect.h"
+#include "ts_device.hpp"
+#include "ts_host.hpp"
+#include "ts_logits.hpp"
+
+using namespace tsd;
+using namespace tsl;
+using tsh::check_device;
+using tsh::fail;
+
+namespace {
+
+constexpr int kLW = kLT / 64;        // waves a tile
+constexpr int kRowItems = 8;         // candidates a thread takes at a time when a row is finished
+constexpr double kLn2 = 0.6931471805599453;
+
+// What a tile leaves for its row: its maximum (NaN seen: +inf; nothing but -inf: -inf), the sums of 2^z and
+// 2^z z over it (z = (x - m) log2(e) / T) and how many of its logits rank above the given token.
+struct Part {
+  double s, d;
+  float m;
+  uint32_t above;
+  uint32_t pad[2];
+};
+static_assert(sizeof(Part) == 32, "Part layout");
+
+struct LParams {
+  const char* x;
+  int64_t stride;              // bytes
+  int32_t V, rows, tiles, n_top, cap;
+  const int32_t* tokens;
+  const float* t;
+  float* logp;
+  int32_t* rank;
+  float* entropy;
+  float* lse;
+  int32_t* top_idx;
+  float* top_logp;
+  float4* stats;
+  int32_t* status;
+  Part* part;
+  uint2* cand;                 // per (row, tile): cap (key, id) slots, unused ones 0
+};
+
+// Candidates kept a tile: at least n, and room for the threads that hold several.
+__host__ __device__ constexpr int cand_cap(int n) { return n ? (2 * n + 32 + 15) / 16 * 16 : 0; }
+constexpr int kCapMax = cand_cap(TS_LOGP_TOP_MAX);
+static_assert(kCapMax <= kLT, "a thread ranks one candidate");
+
+struct LSmem {
+  uint32_t tk[kLT];            // each thread's largest key
+  uint2 list[kCapMax];         // (key, id), in no order
+  uint32_t count;
+  uint32_t red[kLW];
+  double reds[kLW], redd[kLW];
+  uint32_t redn[kLW];
+  Part part;
+  float m;
+  double log_s, c2;
+  int32_t ok;
+};
+
+__device__ __forceinline__ double wave_sum_f64(double v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// ------------------------------------------------------------------ the best n of a workgroup's items
+// Count over the workgroup of items i < N of every thread with pred(i).
+template <int N, class P>
+__device__ __forceinline__ uint32_t count_items(LSmem& sm, P pred) {
+  uint32_t c = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) c += (uint32_t)__popcll(__ballot(pred(i)));
+  if (lane() == 0) sm.redn[wave()] = c;
+  bar();
+  uint32_t s = 0;
+#pragma unroll
+  for (int w = 0; w < kLW; ++w) s += sm.redn[w];
+  bar();
+  return s;
+}
+
+// Writes to sm.list a set of at most `cap` items that holds the best n in the order (key descending, id
+// ascending) and returns its size. key(i), id(i): the calling thread's N items; keys up to that of -inf are
+// absent ones. tk: the thread's largest key. Every thread calls it; the result's order in the list is open.
+//
+// The n-th largest of the threads' largest keys is a bound that n items at least reach and, where large items are
+// spread over the threads, few more. Where too many reach it (equal keys), the n-th item is found exactly, bit by
+// bit: first its key, then, among equals, its id.
+template <int N, class K, class I>
+__device__ __forceinline__ int best_items(LSmem& sm, uint32_t tk, int n, int cap, K key, I id) {
+  sm.tk[threadIdx.x] = tk;
+  if (threadIdx.x == 0) sm.count = 0;
+  bar();
+  uint32_t k4[kLW];
+#pragma unroll
+  for (int w = 0; w < kLW; ++w) k4[w] = sm.tk[64 * w + lane()];
+  uint32_t low = 0;
+  for (int b = 31; b >= 0; --b) {
+    const uint32_t t = low | (1u << b);
+    int c = 0;
+#pragma unroll
+    for (int w = 0; w < kLW; ++w) c += __popcll(__ballot(k4[w] >= t));
+    if (c >= n) {
+      low = t;
+      if (c <= n + 8) break;   // close enough: each further bit costs more than the candidates it saves
+    }
+  }
+  low = max(low, kKeyNegInf + 1);
+  if (tk >= low) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t k = key(i);
+      if (k >= low) {
+        const uint32_t at = atomicAdd(&sm.count, 1u);
+        if (at < (uint32_t)cap) sm.list[at] = make_uint2(k, id(i));
+      }
+    }
+  }
+  bar();
+  const uint32_t found = sm.count;
+  if (found <= (uint32_t)cap) return (int)found;
+  uint32_t t = 0;                                   // the n-th largest key
+  for (int b = 31; b >= 0; --b) {
+    const uint32_t u = t | (1u << b);
+    if (count_items<N>(sm, [&](int i) { return key(i) >= u; }) >= (uint32_t)n) t = u;
+  }
+  const uint32_t need = n - count_items<N>(sm, [&](int i) { return key(i) > t; });
+  uint32_t last = 0;                                // the id of the need-th item with that key
+  for (int b = 30; b >= 0; --b) {
+    const uint32_t u = last | (1u << b);
+    if (count_items<N>(sm, [&](int i) { return key(i) == t && id(i) < u; }) < need) last = u;
+  }
+  if (threadIdx.x == 0) sm.count = 0;
+  bar();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t k = key(i);
+    if (k > t || (k == t && id(i) <= last)) sm.list[atomicAdd(&sm.count, 1u)] = make_uint2(k, id(i));
+  }
+  bar();
+  return n;
+}
+
+// ------------------------------------------------------------------ a row's parameters
+struct RowIn {
+  float t;
+  int32_t token;    // -1: none
+  bool bad_t, bad_token;
+};
+__device__ __forceinline__ RowIn row_in(const LParams& P, int r) {
+  RowIn in;
+  in.t = P.t ? P.t[r] : 1.0f;
+  in.bad_t = !(in.t >= 0.0f && in.t <= 3.402823466e38f);
+  in.token = P.tokens ? P.tokens[r] : -1;
+  in.bad_token = in.token < -1 || in.token >= P.V;
+  if (in.bad_token) in.token = -1;
+  return in;
+}
+
+// ------------------------------------------------------------------ a tile
+// The sums over a workgroup's tile; thread 0 holds them in the returned part.
+template <int DT>
+__device__ __forceinline__ Part tile_sums(const LParams& P, const RowIn& in, const char* row, int tile, const float* xs,
+                                          float tm, LSmem& sm) {
+  const int w = wave();
+  const uint32_t km = wave_max(f2key(tm));
+  if (lane() == 0) sm.red[w] = km;
+  bar();
+  uint32_t k = sm.red[0];
+#pragma unroll
+  for (int i = 1; i < kLW; ++i) k = max(k, sm.red[i]);
+  Part pt;
+  pt.m = key2f(k);
+  pt.s = pt.d = 0.0;
+  pt.above = 0;
+  const float m = k == kKeyNegInf ? 0.0f : pt.m;
+  const float c = (float)exponent_scale(in.t);
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < kLE; ++i) {
+    const float z = exponent(xs[i], m, c);
+    const float e = __builtin_amdgcn_exp2f(z);
+    s[i & 3] += e;
+    d[i & 3] = fmaf(e, z, d[i & 3]);
+  }
+  uint32_t above = 0;
+  if (P.tokens && in.token >= 0) {
+    const float xt = load_logit<DT>(row, in.token);
+    const int at = in.token / kTile;
+    if (tile < at) {
+#pragma unroll
+      for (int i = 0; i < kLE; ++i) above += (uint32_t)__popcll(__ballot(xs[i] >= xt));
+    } else if (tile > at) {
+#pragma unroll
+      for (int i = 0; i < kLE; ++i) above += (uint32_t)__popcll(__ballot(xs[i] > xt));
+    } else {
+#pragma unroll
+      for (int v = 0; v < Logits<DT>::kNV; ++v) {
+        const Place<DT> pl(tile, threadIdx.x, v, P.V);
+#pragma unroll
+        for (int j = 0; j < Logits<DT>::kW; ++j) {
+          const float x = xs[v * Logits<DT>::kW + j];
+          above += (uint32_t)__popcll(__ballot(x > xt || (x == xt && pl.at + j < in.token && pl.counts(j, P.V))));
+        }
+      }
+    }
+  }
+  const double ws = wave_sum_f64((double)(s[0] + s[1]) + (double)(s[2] + s[3]));
+  const double wd = wave_sum_f64((double)(d[0] + d[1]) + (double)(d[2] + d[3]));
+  if (lane() == 0) {
+    sm.reds[w] = ws;
+    sm.redd[w] = wd;
+    sm.redn[w] = above;
+  }
+  bar();
+#pragma unroll
+  for (int i = 0; i < kLW; ++i) {
+    pt.s += sm.reds[i];
+    pt.d += sm.redd[i];
+    pt.above += sm.redn[i];
+  }
+  bar();
+  return pt;
+}
+
+// The thread's largest logit; +inf if one of its logits is NaN.
+__device__ __forceinline__ float thread_max(const float* xs) {
+  float m = xs[0];
+#pragma unroll
+  for (int i = 1; i + 1 < kLE; i += 2)
+    m = __builtin_elementwise_maximum(m, __builtin_elementwise_maximum(xs[i], xs[i + 1]));
+  m = __builtin_elementwise_maximum(m, xs[kLE - 1]);
+  return m != m ? INFINITY : m;
+}
+
+// ------------------------------------------------------------------ a row
+// Joins a row's tiles and writes its scalars; called by one whole wave. Leaves in sm (thread 0's copy) what the
+// alternatives need.
+template <int DT>
+__device__ __forceinline__ void finish_row(const LParams& P, const RowIn& in, int r, const Part* part, LSmem* sm) {
+  const int l = lane();
+  const float nan = __uint_as_float(0x7FC00000u);
+  const float xt = (P.tokens && in.token >= 0) ? load_logit<DT>(P.x + (int64_t)r * P.stride, in.token) : 0.0f;
+  uint32_t km = 0;
+  for (int i = l; i < P.tiles; i += 64) km = max(km, f2key(part[i].m));
+  km = wave_max(km);
+  const float m = key2f(km);
+  const double c2 = exponent_scale(in.t);
+  double s = 0.0, d = 0.0;
+  uint32_t above = 0;
+  const bool finite = km < kKeyPosInf && km > kKeyNegInf;
+  if (finite) {
+    for (int i = l; i < P.tiles; i += 64) {
+      const Part p = part[i];
+      above += p.above;
+      if (p.m == -INFINITY) continue;
+      const double dz = ((double)p.m - (double)m) * c2;
+      const double w = exp2(dz);
+      if (w > 0.0) {
+        s += w * p.s;
+        d += w * (p.d + dz * p.s);
+      }
+    }
+    s = wave_sum_f64(s);
+    d = wave_sum_f64(d);
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) above += (uint32_t)__shfl_xor((int)above, o);
+  }
+  if (l != 0) return;
+  int st = TS_ROW_OK;
+  if (!finite) st = TS_ROW_NONFINITE;
+  else if (in.bad_t) st = TS_ROW_BAD_T;
+  else if (in.bad_token) st = TS_ROW_BAD_TOKEN;
+  const bool ok = st == TS_ROW_OK, greedy = in.t == 0.0f, given = in.token >= 0;
+  const double log_s = ok && !greedy ? log(s) : 0.0, mean = ok && !greedy ? d / s * kLn2 : 0.0;
+  float logp = 0.0f;
+  if (given && greedy) logp = above == 0 ? 0.0f : -INFINITY;
+  else if (given) logp = fminf((float)(((double)xt - (double)m) * c2 * kLn2 - log_s), 0.0f);
+  if (P.logp) P.logp[r] = ok ? logp : nan;
+  if (P.rank) P.rank[r] = ok ? (given ? (int32_t)above + 1 : 0) : -1;
+  if (P.entropy) P.entropy[r] = ok ? fmaxf((float)(log_s - mean), 0.0f) : nan;
+  if (P.lse) P.lse[r] = ok ? (greedy ? INFINITY : (float)((double)m * c2 * kLn2 + log_s)) : nan;
+  if (P.stats) P.stats[r] = ok ? make_float4(m, greedy ? 1.0f : (float)s, (float)mean, 0.0f) : make_float4(nan, nan, nan, nan);
+  if (P.status) P.status[r] = st;
+  if (sm) {
+    sm->m = m;
+    sm->log_s = log_s;
+    sm->c2 = c2;
+    sm->ok = ok ? (greedy ? 2 : 1) : 0;
+  }
+}
+
+// Ranks the `count` candidates of sm.list and writes the row's n_top alternatives.
+__device__ __forceinline__ void write_top(const LParams& P, int r, int count, LSmem& sm) {
+  const int t = threadIdx.x;
+  int32_t* idx = P.top_idx + (int64_t)r * P.n_top;
+  float* lp = P.top_logp + (int64_t)r * P.n_top;
+  const int ok = sm.ok;
+  if (t < P.n_top && (!ok || t >= count)) {
+    idx[t] = -1;
+    lp[t] = ok ? -INFINITY : __uint_as_float(0x7FC00000u);
+  }
+  if (!ok || t >= count) return;
+  const uint2 me = sm.list[t];
+  int above = 0;
+  for (int i = 0; i < count; ++i) {
+    const uint2 o = sm.list[i];
+    above += (o.x > me.x || (o.x == me.x && o.y < me.y)) ? 1 : 0;
+  }
+  if (above >= P.n_top) return;
+  idx[above] = (int32_t)me.y;
+  const float v = (float)(((double)key2f(me.x) - (double)sm.m) * sm.c2 * kLn2 - sm.log_s);
+  lp[above] = ok == 2 ? (above == 0 ? 0.0f : -INFINITY) : fminf(v, 0.0f);
+}
+
+template <int DT, bool TOP, bool WHOLE>
+__global__ __launch_bounds__(kLT) void ts_logp_tile_kernel(LParams P) {
+  __shared__ LSmem sm;
+  const int r = WHOLE ? (int)blockIdx.x : (int)(blockIdx.x / (unsigned)P.tiles);
+  const int tile = WHOLE ? 0 : (int)(blockIdx.x - (unsigned)r * (unsigned)P.tiles);
+  const char* row = P.x + (int64_t)r * P.stride;
+  float xs[kLE];
+  load_tile<DT>(row, P.V, tile, threadIdx.x, xs);
+  const RowIn in = row_in(P, r);
+  const float tm = thread_max(xs);
+  const Part pt = tile_sums<DT>(P, in, row, tile, xs, tm, sm);
+  if (WHOLE) {
+    if (threadIdx.x == 0) sm.part = pt;
+    bar();
+    if (wave() == 0) finish_row<DT>(P, in, r, &sm.part, &sm);
+    if (!TOP) return;
+    bar();
+  } else if (threadIdx.x == 0) {
+    P.part[blockIdx.x] = pt;
+  }
+  if (TOP) {
+    const int count = best_items<kLE>(
+        sm, f2key(tm), P.n_top, P.cap, [&](int i) { return f2key(xs[i]); },
+        [&](int i) {
+          return (uint32_t)(Place<DT>(tile, threadIdx.x, i / Logits<DT>::kW, P.V).at + i % Logits<DT>::kW);
+        });
+    if (WHOLE) {
+      write_top(P, r, count, sm);
+    } else {
+      uint2* out = P.cand + (int64_t)blockIdx.x * P.cap;
+      if ((int)threadIdx.x < P.cap) out[threadIdx.x] = (int)threadIdx.x < count ? sm.list[threadIdx.x] : make_uint2(0u, 0u);
+    }
+  }
+}
+
+// One row a wave without alternatives, one row a workgroup with them.
+template <int DT, bool TOP>
+__global__ __launch_bounds__(kLT) void ts_logp_row_kernel(LParams P) {
+  __shared__ LSmem sm;
+  const int r = TOP ? (int)blockIdx.x : (int)(blockIdx.x * kLW + wave());
+  if (r >= P.rows) return;
+  if (!TOP || wave() == 0) finish_row<DT>(P, row_in(P, r), r, P.part + (int64_t)r * P.tiles, TOP ? &sm : nullptr);
+  if (!TOP) return;
+  const uint2* cand = P.cand + (int64_t)r * P.tiles * P.cap;
+  const int64_t n = (int64_t)P.tiles * P.cap;
+  int count = 0;
+  for (int64_t base = 0; base < n; base += kLT * kRowItems) {
+    uint2 c[kRowItems + 1];
+    uint32_t tk = 0;
+#pragma unroll
+    for (int i = 0; i < kRowItems; ++i) {
+      const int64_t at = base + i * kLT + threadIdx.x;
+      c[i] = at < n ? cand[at] : make_uint2(0u, 0u);
+      tk = max(tk, c[i].x);
+    }
+    // what is left of the slots before takes part again
+    c[kRowItems] = (int)threadIdx.x < count ? sm.list[threadIdx.x] : make_uint2(0u, 0u);
+    tk = max(tk, c[kRowItems].x);
+    bar();
+    count = best_items<kRowItems + 1>(sm, tk, P.n_top, P.cap, [&](int i) { return c[i].x; }, [&](int i) { return c[i].y; });
+  }
+  bar();
+  write_top(P, r, count, sm);
+}
+
+// ------------------------------------------------------------------ gradient
+struct GParams {
+  const char* x;
+  char* g;
+  int64_t x_stride, g_stride;   // bytes
+  int32_t V, rows, tiles;
+  const int32_t* tokens;
+  const float* t;
+  const float4* stats;
+  const float* g_logp;
+  const float* g_entropy;
+  const float* g_lse;
+};
+
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (DT == TS_DTYPE_BF16) {
+    typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){a, b}, bf2));   // round to nearest even
+  } else {
+    return (uint32_t)__half_as_ushort(__float2half_rn(a)) | ((uint32_t)__half_as_ushort(__float2half_rn(b)) << 16);
+  }
+}
+template <int DT>
+__device__ __forceinline__ void store_logit(char* row, int64_t i, float v) {
+  if constexpr (DT == TS_DTYPE_F32) reinterpret_cast<float*>(row)[i] = v;
+  else reinterpret_cast<unsigned short*>(row)[i] = (unsigned short)pack2<DT>(v, 0.0f);
+}
+
+// Each element is read and then written by one thread and read by no other, so the gradient may take the
+// logits' own place. (A row's last vector, where it is not whole, is taken element by element for that.)
+template <int DT>
+__global__ __launch_bounds__(kLT) void ts_logp_grad_kernel(GParams P) {
+  using L = Logits<DT>;
+  const int r = (int)(blockIdx.x / (unsigned)P.tiles), tile = (int)(blockIdx.x - (unsigned)r * (unsigned)P.tiles);
+  const char* row = P.x + (int64_t)r * P.x_stride;
+  char* out = P.g + (int64_t)r * P.g_stride;
+  const int t0 = tile * kTile + (int)threadIdx.x * L::kW;
+  u32x4 raw[L::kNV];
+#pragma unroll
+  for (int v = 0; v < L::kNV; ++v) {
+    const int at = t0 + v * kLT * L::kW;
+    if (at + L::kW <= P.V) raw[v] = load16(row + (int64_t)at * L::kSize);
+  }
+  const float4 st = P.stats[r];
+  const float temp = P.t ? P.t[r] : 1.0f;
+  const int32_t token = P.tokens ? P.tokens[r] : -1;
+  const bool ok = st.x == st.x && temp >= 0.0f && temp <= 3.402823466e38f && token >= -1 && token < P.V;
+  const float inv_t = temp > 0.0f ? 1.0f / fmaxf(temp, 0x1p-100f) : 0.0f;   // greedy rows do not depend on the logits
+  const float c = (float)exponent_scale(temp);
+  const float a = token >= 0 && P.g_logp ? P.g_logp[r] : 0.0f;
+  const float h = P.g_entropy ? P.g_entropy[r] : 0.0f;
+  const float l = P.g_lse ? P.g_lse[r] : 0.0f;
+  // p (l - a - h (d - D)) / T = 2^z (k0 + k1 z)
+  const float q = inv_t / st.y;
+  float k0 = q * (l - a + h * st.z), k1 = -q * h * (float)kLn2;
+  const float add = a * inv_t, m = st.x;
+  if (!ok) k0 = k1 = __uint_as_float(0x7FC00000u);
+  auto grad = [&](float x, int id) -> float {
+    const float z = exponent(x, m, c);
+    const float g = __builtin_amdgcn_exp2f(z) * fmaf(k1, z, k0);
+    return id == token ? g + add : g;
+  };
+#pragma unroll
+  for (int v = 0; v < L::kNV; ++v) {
+    const int at = t0 + v * kLT * L::kW;
+    if (at + L::kW <= P.V) {
+      u32x4 o;
+      if constexpr (DT == TS_DTYPE_F32) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = __float_as_uint(grad(unpack<DT>(raw[v], j), at + j));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          o[j] = pack2<DT>(grad(unpack<DT>(raw[v], 2 * j), at + 2 * j), grad(unpack<DT>(raw[v], 2 * j + 1), at + 2 * j + 1));
+      }
+      store16(out + (int64_t)at * L::kSize, o);
+    } else {
+      for (int j = at; j < P.V; ++j) store_logit<DT>(out, j, grad(load_logit<DT>(row, j), j));
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host side
+struct LPlan {
+  int64_t tiles = 0;
+  int cap = 0;
+  size_t off_cand = 0, total = 0;
+};
+bool logp_plan(int64_t rows, int64_t V, int n_top, LPlan& pl) {
+  if (rows < 0 || V < 1 || V > TS_MAX_VOCAB || n_top < 0 || n_top > TS_LOGP_TOP_MAX) return false;
+  pl.tiles = (V + kTile - 1) / kTile;
+  pl.cap = cand_cap(n_top);
+  if (rows * pl.tiles > (int64_t)0xFFFFFFFF / kLT) return false;   // a launch holds at most 2^32 - 1 threads
+  if (pl.tiles == 1) {
+    pl.total = 256;
+    return true;
+  }
+  const size_t parts = (size_t)(std::max<int64_t>(rows, 1) * pl.tiles);
+  pl.off_cand = (parts * sizeof(Part) + 255) & ~(size_t)255;
+  pl.total = pl.off_cand + ((parts * pl.cap * sizeof(uint2) + 255) & ~(size_t)255);
+  return true;
+}
+
+template <int DT>
+hipError_t launch_logp(const LParams& P, hipStream_t s) {
+  const dim3 tiles((unsigned)((int64_t)P.rows * P.tiles)), block(kLT);
+  const bool top = P.n_top > 0;
+  if (P.tiles == 1) {
+    if (top) hipLaunchKernelGGL((ts_logp_tile_kernel<DT, true, true>), tiles, block, 0, s, P);
+    else hipLaunchKernelGGL((ts_logp_tile_kernel<DT, false, true>), tiles, block, 0, s, P);
+    return hipGetLastError();
+  }
+  if (top) hipLaunchKernelGGL((ts_logp_tile_kernel<DT, true, false>), tiles, block, 0, s, P);
+  else hipLaunchKernelGGL((ts_logp_tile_kernel<DT, false, false>), tiles, block, 0, s, P);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (top) hipLaunchKernelGGL((ts_logp_row_kernel<DT, true>), dim3((unsigned)P.rows), block, 0, s, P);
+  else hipLaunchKernelGGL((ts_logp_row_kernel<DT, false>), dim3((unsigned)((P.rows + kLW - 1) / kLW)), block, 0, s, P);
+  return hipGetLastError();
+}
+
+int dtype_size(int dtype) {
+  return dtype == TS_DTYPE_F32 ? 4 : (dtype == TS_DTYPE_BF16 || dtype == TS_DTYPE_F16) ? 2 : 0;
+}
+
+// The checks that both entry points share; TS_OK also for an empty batch.
+int check_logits(const void* x, int dtype, int64_t rows, int64_t vocab, int64_t stride) {
+  if (rows < 0) return fail(TS_ERR_INVALID_ARG, "rows = %lld < 0", (long long)rows);
+  if (vocab < 1 || vocab > TS_MAX_VOCAB) return fail(TS_ERR_INVALID_ARG, "vocab = %lld outside [1, 2^30]", (long long)vocab);
+  if (stride < vocab) return fail(TS_ERR_INVALID_ARG, "row_stride %lld < vocab %lld", (long long)stride, (long long)vocab);
+  if (!dtype_size(dtype)) return fail(TS_ERR_INVALID_ARG, "dtype = %d is none of TS_DTYPE_*", dtype);
+  if (rows == 0) return TS_OK;
+  if (!x) return fail(TS_ERR_INVALID_ARG, "logits pointer is NULL");
+  if ((uintptr_t)x % dtype_size(dtype)) return fail(TS_ERR_INVALID_ARG, "logits are not aligned to their type");
+  return TS_OK;
+}
+
+}  // namespace
+
+namespace tsh {
+size_t token_logp_workspace(int64_t rows, int64_t vocab, int n_top) {
+  LPlan pl;
+  return logp_plan(rows, vocab, n_top, pl) ? pl.total : 0;
+}
+}  // namespace tsh
+
+extern "C" {
+
+int ts_token_logp(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride, const int32_t* tokens,
+                  const float* temperature, int32_t n_top, float* out_logp, int32_t* out_rank, float* out_entropy,
+                  float* out_lse, int32_t* out_top_idx, float* out_top_logp, float* out_stats, int32_t* row_status,
+                  void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_logits(logits, dtype, rows, vocab, row_stride);
+  if (rc != TS_OK) return rc;
+  if (n_top < 0 || n_top > TS_LOGP_TOP_MAX)
+    return fail(TS_ERR_INVALID_ARG, "n_top = %d outside [0, %d]", (int)n_top, TS_LOGP_TOP_MAX);
+  if (rows == 0) return TS_OK;
+  if (!tokens && (out_logp || out_rank)) return fail(TS_ERR_INVALID_ARG, "out_logp and out_rank need tokens");
+  if (n_top > 0 && (!out_top_idx || !out_top_logp))
+    return fail(TS_ERR_INVALID_ARG, "n_top > 0 needs out_top_idx and out_top_logp");
+  if (((uintptr_t)out_stats & 15u) != 0) return fail(TS_ERR_INVALID_ARG, "out_stats is not 16-byte aligned");
+  LPlan pl;
+  if (!logp_plan(rows, vocab, n_top, pl)) return fail(TS_ERR_INVALID_ARG, "rows x tiles too large");
+  if (pl.tiles > 1) {
+    if (!workspace) return fail(TS_ERR_WORKSPACE, "workspace is NULL");
+    if (((uintptr_t)workspace & 255u) != 0) return fail(TS_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+    if (workspace_bytes < pl.total)
+      return fail(TS_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, pl.total);
+  }
+  int dev;
+  rc = check_device(&dev);
+  if (rc != TS_OK) return rc;
+  LParams P;
+  P.x = static_cast<const char*>(logits);
+  P.stride = row_stride * dtype_size(dtype);
+  P.V = (int32_t)vocab;
+  P.rows = (int32_t)rows;
+  P.tiles = (int32_t)pl.tiles;
+  P.n_top = n_top;
+  P.cap = pl.cap;
+  P.tokens = tokens;
+  P.t = temperature;
+  P.logp = out_logp;
+  P.rank = out_rank;
+  P.entropy = out_entropy;
+  P.lse = out_lse;
+  P.top_idx = out_top_idx;
+  P.top_logp = out_top_logp;
+  P.stats = reinterpret_cast<float4*>(out_stats);
+  P.status = row_status;
+  P.part = static_cast<Part*>(workspace);
+  P.cand = reinterpret_cast<uint2*>(static_cast<char*>(workspace) + pl.off_cand);
+  const hipStream_t s = (hipStream_t)stream;
+  const hipError_t e = dtype == TS_DTYPE_F32    ? launch_logp<TS_DTYPE_F32>(P, s)
+                       : dtype == TS_DTYPE_BF16 ? launch_logp<TS_DTYPE_BF16>(P, s)
+                                                : launch_logp<TS_DTYPE_F16>(P, s);
+  if (e != hipSuccess) return fail(TS_ERR_LAUNCH, "token logprob launch failed: %s", hipGetErrorString(e));
+  return TS_OK;
+}
+
+int ts_token_logp_backward(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride,
+                           const int32_t* tokens, const float* temperature, const float* stats, const float* grad_logp,
+                           const float* grad_entropy, const float* grad_lse, void* grad_logits, int64_t grad_stride,
+                           void* stream) {
+  int rc = check_logits(logits, dtype, rows, vocab, row_stride);
+  if (rc != TS_OK) return rc;
+  if (grad_stride < vocab)
+    return fail(TS_ERR_INVALID_ARG, "grad_stride %lld < vocab %lld", (long long)grad_stride, (long long)vocab);
+  if (rows == 0) return TS_OK;
+  if (!stats || !grad_logits) return fail(TS_ERR_INVALID_ARG, "stats and grad_logits are required");
+  if (grad_logp && !tokens) return fail(TS_ERR_INVALID_ARG, "grad_logp needs tokens");
+  if (((uintptr_t)stats & 15u) != 0) return fail(TS_ERR_INVALID_ARG, "stats is not 16-byte aligned");
+  const int size = dtype_size(dtype);
+  if ((uintptr_t)grad_logits % size) return fail(TS_ERR_INVALID_ARG, "grad_logits are not aligned to their type");
+  // the gradient may take the logits' place exactly, and may not overlap them otherwise
+  const uintptr_t x0 = (uintptr_t)logits, x1 = x0 + (uintptr_t)((rows - 1) * row_stride + vocab) * size;
+  const uintptr_t g0 = (uintptr_t)grad_logits, g1 = g0 + (uintptr_t)((rows - 1) * grad_stride + vocab) * size;
+  if (g0 < x1 && x0 < g1 && !(g0 == x0 && grad_stride == row_stride))
+    return fail(TS_ERR_INVALID_ARG, "grad_logits overlap the logits without taking their place");
+  const int64_t tiles = (vocab + kTile - 1) / kTile;
+  if (rows * tiles > (int64_t)0xFFFFFFFF / kLT) return fail(TS_ERR_INVALID_ARG, "rows x tiles too large");
+  int dev;
+  rc = check_device(&dev);
+  if (rc != TS_OK) return rc;
+  GParams P;
+  P.x = static_cast<const char*>(logits);
+  P.g = static_cast<char*>(grad_logits);
+  P.x_stride = row_stride * size;
+  P.g_stride = grad_stride * size;
+  P.V = (int32_t)vocab;
+  P.rows = (int32_t)rows;
+  P.tiles = (int32_t)tiles;
+  P.tokens = tokens;
+  P.t = temperature;
+  P.stats = reinterpret_cast<const float4*>(stats);
+  P.g_logp = grad_logp;
+  P.g_entropy = grad_entropy;
+  P.g_lse = grad_lse;
+  const dim3 grid((unsigned)(rows * tiles)), block(kLT);
+  const hipStream_t s = (hipStream_t)stream;
+  if (dtype == TS_DTYPE_F32) hipLaunchKernelGGL(ts_logp_grad_kernel<TS_DTYPE_F32>, grid, block, 0, s, P);
+  else if (dtype == TS_DTYPE_BF16) hipLaunchKernelGGL(ts_logp_grad_kernel<TS_DTYPE_BF16>, grid, block, 0, s, P);
+  else hipLaunchKernelGGL(ts_logp_grad_kernel<TS_DTYPE_F16>, grid, block, 0, s, P);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return fail(TS_ERR_LAUNCH, "token logprob gradient launch failed: %s", hipGetErrorString(e));
+  return TS_OK;
+}
+
+}  // extern "C"

@@ -3609,7 +3609,8 @@ int scratch_address(int dev, void** out) {
 extern "C" {
 
 size_t ts_workspace_bytes(int op, int64_t rows, int64_t vocab, int32_t k_max) {
-  (void)k_max;
+  if (op == TS_OP_TOKEN_LOGP) return tsh::token_logp_workspace(rows, vocab, k_max);
+  if (op == TS_OP_CACHE_EVICT) return tsh::cache_evict_workspace(rows, vocab, k_max);
   if (op < TS_OP_TOPK_SELECT || op > TS_OP_SAMPLE_ROWS) return 0;
   Plan pl;
   if (!make_plan(rows, vocab, pl)) return 0;
@@ -3802,6 +3803,7 @@ const char* ts_status_string(int status) {
     case TS_ROW_BAD_P: return "row top_p outside (0, 1]";
     case TS_ROW_BAD_T: return "row temperature negative or non-finite";
     case TS_ROW_BAD_MINP: return "row min_p outside [0, 1]";
+    case TS_ROW_BAD_TOKEN: return "row token outside [0, vocab)";
     default: return "unknown status";
   }
 }

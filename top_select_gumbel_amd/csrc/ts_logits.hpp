@@ -1,0 +1,111 @@
+// ts_logits.hpp -- 16-byte loads of logits in fp32, bf16 or fp16 as fp32 values, by tiles of a row.
+//
+// A row is cut into tiles of kTile logits, whatever its type and wherever the batch puts it, so that
+// every sum over a tile has the same terms in the same order in every call. A tile belongs to kLT
+// threads; thread t holds the 16-byte vectors t, t + kLT, ... of it, kLE logits in all. Rows
+// start at any multiple of their element's size: gfx950 loads and stores 16 bytes from any address, so
+// the vectors are counted from the row's first logit and not from an aligned address.
+#pragma once
+#include <hip/hip_bf16.h>
+#include <hip/hip_fp16.h>
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "topselect.h"
+#include "ts_device.hpp"
+
+namespace tsl {
+
+constexpr int kLT = 256;          // threads a tile
+constexpr int kLE = 32;           // logits a thread
+constexpr int kTile = kLT * kLE;  // 8192
+
+template <int DT>
+struct Logits {
+  static constexpr int kSize = DT == TS_DTYPE_F32 ? 4 : 2;
+  static constexpr int kW = 16 / kSize;     // logits a vector
+  static constexpr int kNV = kLE / kW;      // vectors a thread
+};
+
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x4_any __attribute__((ext_vector_type(4), aligned(2)));   // 16 bytes at any logit's address
+
+__device__ __forceinline__ u32x4 load16(const char* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
+}
+__device__ __forceinline__ void store16(char* p, u32x4 v) { *reinterpret_cast<u32x4_any*>(p) = v; }
+
+// Element j of a vector as fp32 (exact for every type).
+template <int DT>
+__device__ __forceinline__ float unpack(const u32x4& v, int j) {
+  if constexpr (DT == TS_DTYPE_F32) {
+    return __uint_as_float(v[j]);
+  } else if constexpr (DT == TS_DTYPE_BF16) {
+    return __uint_as_float((j & 1) ? (v[j >> 1] & 0xFFFF0000u) : (v[j >> 1] << 16));
+  } else {
+    return __half2float(__ushort_as_half((unsigned short)((j & 1) ? (v[j >> 1] >> 16) : v[j >> 1])));
+  }
+}
+template <int DT>
+__device__ __forceinline__ float load_logit(const char* row, int64_t i) {
+  if constexpr (DT == TS_DTYPE_F32) return reinterpret_cast<const float*>(row)[i];
+  const unsigned short b = reinterpret_cast<const unsigned short*>(row)[i];
+  if constexpr (DT == TS_DTYPE_BF16) return __uint_as_float((uint32_t)b << 16);
+  return __half2float(__ushort_as_half(b));
+}
+
+// Where thread t's vector v of a tile starts: its first logit's id. `own` is where it starts by the
+// layout; a vector that would reach past the row's end is moved back to end with the row (or
+// starts at 0 where the row is shorter than a vector), and only its logits at or past `own` count.
+template <int DT>
+struct Place {
+  int own, at;
+  __device__ __forceinline__ Place(int tile, int t, int v, int V) {
+    own = tile * kTile + (v * kLT + t) * Logits<DT>::kW;
+    at = min(own, max(V - Logits<DT>::kW, 0));
+  }
+  __device__ __forceinline__ bool counts(int j, int V) const { return at + j >= own && at + j < V; }
+};
+
+// The thread's kLE logits of a tile; what does not count is -inf. Every address lies in the row.
+template <int DT>
+__device__ __forceinline__ void load_tile(const char* row, int V, int tile, int t, float* xs) {
+  using L = Logits<DT>;
+  u32x4 raw[L::kNV];
+  if ((tile + 1) * kTile <= V) {
+    const char* p = row + ((int64_t)tile * kTile + (int64_t)t * L::kW) * L::kSize;
+#pragma unroll
+    for (int v = 0; v < L::kNV; ++v) raw[v] = load16(p + v * (kLT * 16));
+#pragma unroll
+    for (int v = 0; v < L::kNV; ++v)
+#pragma unroll
+      for (int j = 0; j < L::kW; ++j) xs[v * L::kW + j] = unpack<DT>(raw[v], j);
+  } else if (V >= L::kW) {
+#pragma unroll
+    for (int v = 0; v < L::kNV; ++v) raw[v] = load16(row + (int64_t)Place<DT>(tile, t, v, V).at * L::kSize);
+#pragma unroll
+    for (int v = 0; v < L::kNV; ++v) {
+      const Place<DT> pl(tile, t, v, V);
+#pragma unroll
+      for (int j = 0; j < L::kW; ++j) xs[v * L::kW + j] = pl.at + j >= pl.own ? unpack<DT>(raw[v], j) : -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kLE; ++i) xs[i] = -INFINITY;
+    if (t == 0) {
+#pragma unroll
+      for (int j = 0; j < L::kW; ++j)
+        if (j < V) xs[j] = load_logit<DT>(row, j);
+    }
+  }
+}
+
+// 1/T in the base-2 exponent. A temperature below 2^-100 acts as 2^-100: beside the maximum every
+// logit more than 2^-93 below it has weight 0 there, as it would at the smaller one.
+__device__ __forceinline__ double exponent_scale(float t) { return tsd::kLog2e / (double)fmaxf(t, 0x1p-100f); }
+
+// (x - m) log2(e) / T, not below kZMin, where 2^z is 0 (so that -inf gives 0 in products with z too).
+constexpr float kZMin = -151.0f;
+__device__ __forceinline__ float exponent(float x, float m, float c) { return fmaxf((x - m) * c, kZMin); }
+
+}  // namespace tsl
