@@ -354,6 +354,7 @@ int ts_token_logp_backward(const void* logits, int dtype, int64_t rows, int64_t 
  * that are not their inputs get NaN and -1. Apart from the cases named, arrays must not overlap.
  * Workspace: TS_OP_CACHE_EVICT.
  */
+#define TS_EVICT_MAX_SLOTS (1 << 22)   /* most slots of a row, and largest keep_max */
 typedef struct ts_cache {
   void* data;
   int64_t batch_stride, head_stride, slot_stride, slot_bytes;

@@ -184,6 +184,37 @@ def test_long_rows(slots, keep, batch):
     check(batch, 1, slots, keep, n_w=1, wtype="bfloat16", dim=8, ties=2, seed=slots)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_long_ragged_and_rejected_rows(in_place):
+    slots = 9000
+    rng = np.random.default_rng(11)
+    score = rng.standard_normal((10, slots)).astype(np.float32)
+    score[4, 8000] = math.nan
+    score[5, 8500:] = math.nan                          # behind its row's end
+    n = [0, 1, 9000, 8999, 9000, 8500, 1024, 1025, -3, 12000]
+    check(5, 2, slots, 4000, score=score, lengths=n, keeps=[4000, 1, 3999, 4000, 4000, 1, 1024, 1024, 4000, 0], sinks=3, recent=700,
+          dim=4, in_place=in_place, seed=11)
+
+
+@pytest.mark.parametrize("slots", [8192, 8193, 9216, 20000])
+@pytest.mark.parametrize("sinks,recent", [(0, 0), (5000, 0), (10, 6000), (2 ** 31 - 1, 0)])
+def test_long_protected_positions(slots, sinks, recent):
+    check(1, 2, slots, 5000, sinks=sinks, recent=recent, dim=2, seed=slots)
+    check(1, 2, slots, slots, sinks=sinks, recent=recent, dim=2, seed=slots)
+    check(1, 1, slots, 5000, sinks=sinks, recent=recent, dim=2, ties=2, n_w=1, seed=slots)
+
+
+@pytest.mark.parametrize("slots", [3000, 20000])
+def test_outliers_crowd_the_other_weights_together(slots):
+    # one huge weight stretches the row's range, so that all others share a few of the first bins
+    rng = np.random.default_rng(slots)
+    score = (1 + rng.random((3, slots))).astype(np.float32)
+    score[0, 7], score[1, 7], score[1, 9] = 1e30, 1e30, -1e30
+    score[2] = np.round(score[2] * 64) / 64             # and many ties besides
+    score[2, 7] = 1e30
+    check(3, 1, slots, slots // 3, n_w=0, score=score, dim=2, seed=1)
+
+
 def test_steps_in_a_row_against_the_oracle():
     """A cache at its budget over many steps: append, add the step's weights, drop one; in place throughout."""
     torch = torch_cuda()

@@ -6,11 +6,22 @@
 // `recent` ones. The i-th slot below k that is not kept takes over the i-th kept slot at or past k, so
 // that a row of which few positions go moves few, and nothing that is read is written.
 //
-// ts_evict_sum_kernel     s of every slot (grid over rows and slots): reads the weights once.
-// ts_evict_select_kernel  one workgroup a row: the k-th slot of the order by radix select on ordered keys, then the
-//                         freed slots and their fillers in slot order, and the row's small outputs.
-// ts_evict_move_kernel    copies the fillers' keys and values (grid over rows and moves).
+// Short rows (ts_evict_row_kernel, one workgroup a row, its sums in registers) are summed, cut and listed, and their few
+// moves made, in one launch where one compute unit alone reads and copies that fast enough; else the sums come from
+// ts_evict_sum_kernel and the moves go to ts_evict_move_kernel, both spread over the chip.
+//
+// Long rows are spread in every step (a tile of 1024 slots a workgroup), a launch each:
+//   sum    s, and each tile's largest position and extreme keys
+//   bin    both classes (protected, others) counted by the first 11 bits of u = key - smallest key of the row
+//   list   the bin that holds the cut, its slots listed
+//   cut    one workgroup a row: the cut's (u, slot)
+//   emit   what stays in place; each tile's freed slots and fillers
+//   move   the i-th freed slot of a row receives the i-th filler (found by the tiles' counts), caches and small outputs
+//
+// The cut is found by radix select on u = key - smallest key of the row (ordered keys, so that the first 2048 bins
+// span the row's own range and not the whole of fp32), then, once few slots share its bin, by ranking those.
 #include <algorithm>
+#include <type_traits>
 
 #include "topselect.h"
 #include "ts_device.hpp"
@@ -25,11 +36,45 @@ namespace {
 
 constexpr int kST = 256;                 // threads of the sum kernel
 constexpr int kSumSlots = 4;             // slots a thread
-constexpr int kET = 1024;                // threads of the select kernel
+constexpr int kSumTile = kST * kSumSlots;
+constexpr int kET = 1024;                // threads of the row kernels
 constexpr int kEW = kET / 64;
 constexpr int kEBits = 11;
 constexpr int kEBins = 1 << kEBits;
+constexpr int kMaxTiles = TS_EVICT_MAX_SLOTS / kSumTile;
+static_assert(kEBins == 2 * kET, "a thread owns two bins");
+constexpr int kRowSlots = 2 * 4 * kET;   // longest row held in registers: two 16-byte vectors a thread
+constexpr int kListRow = 256;            // slots of the cut's bin that are ranked rather than binned again, ...
+constexpr int kListLong = 4096;          // ... and that are listed for a long row's cut
 constexpr int kMT = 256;                 // threads of the move kernel
+
+// What a tile of the sum kernel leaves for long rows: largest position, smallest and largest key.
+struct TileInfo {
+  int32_t newest;
+  uint32_t kmin, kmax, pad;
+};
+
+// What the steps of a long row leave for the next ones.
+struct RowInfo {
+  uint32_t protected_;         // bin: protected slots
+  uint32_t listed;             // list: slots listed
+  uint32_t among_first;        // list: whether the cut falls among the protected slots
+  uint32_t prefix, lo;         // the cut's bin: u >> lo == prefix
+  uint32_t need, in_bin;       // the cut is the need-th of the in_bin slots in it
+  uint32_t whole;              // 0: a cut is to be found; 1: the class stays as a whole
+  uint32_t cut_u, cut_slot;    // cut
+  int32_t st, k, tiles, pad;   // cut: the row's status, new length, tiles in use
+};
+// What a tile of a long row leaves: slots of the cut's bin and their extreme u; freed slots and fillers.
+struct TileBin {
+  uint32_t count, umin, umax, holes, fills, pad[3];
+};
+
+struct Cache {
+  char* p;
+  int64_t batch, head, slot;   // bytes
+  int32_t units;               // units of the copy a slot; 0: no cache
+};
 
 struct EParams {
   const float* score;
@@ -49,42 +94,147 @@ struct EParams {
   int32_t* out_lengths;
   int32_t* out_source;
   int32_t* status;
-  float* sum;                            // [rows, slots]
+  float* sum;                            // [rows, sum_stride]
+  int64_t sum_stride;                    // slots, rounded up to whole vectors
+  TileInfo* info;                        // [rows, tiles]
+  RowInfo* row;                          // [rows] long rows, like the next ones
+  TileBin* bin;                          // [rows, tiles]
+  uint32_t* hist;                        // [rows, 2, kEBins]
+  uint2* list;                           // [rows, kListLong]: (u, slot)
+  int32_t* fill_position;                // [rows, sum_stride]; hole and fill are [rows, sum_stride] there, by tiles
+  int32_t tiles;
   int32_t* moves;                        // [rows]
   int32_t* hole;                         // [rows, cap]: the freed slots, ascending
   int32_t* fill;                         // [rows, cap]: what each takes over, ascending
   int32_t cap;
+  Cache k, v;
+  int32_t heads;
 };
 
 __device__ __forceinline__ int row_length(const EParams& P, int r) { return max(0, min(P.lengths[r], P.slots)); }
 
-template <int DT>
-__device__ __forceinline__ double weight_at(const char* w, int j) {
-  return (double)tsl::load_logit<DT>(w, j);
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+typedef i32x4 i32x4_any __attribute__((aligned(4)));
+
+// Slots j .. j + 3 of an array of n; what lies past the end is `rest`.
+template <class V, class VA, class T>
+__device__ __forceinline__ V load4(const T* p, int j, int n, T rest) {
+  if (j + 4 <= n) return *reinterpret_cast<const VA*>(p + j);
+  V v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = j + i < n ? p[j + i] : rest;
+  return v;
 }
 
-template <int DT>
-__global__ __launch_bounds__(kST) void ts_evict_sum_kernel(EParams P, int blocks) {
-  const int r = (int)(blockIdx.x / (unsigned)blocks);
-  const int j0 = (int)(blockIdx.x - (unsigned)r * (unsigned)blocks) * kST * kSumSlots + (int)threadIdx.x;
-  const int n = row_length(P, r);
-  const float* score = P.score + (int64_t)r * P.score_stride;
-  const char* wr = P.weights + (int64_t)r * P.w_row;
+// Adds one weight row's slots j .. j + N - 1 to s (N * size: 16 bytes, or two loads of 16).
+template <int DT, int N>
+__device__ __forceinline__ void add_weights(const char* w, int j, int n, double* s) {
+  constexpr int size = tsl::Logits<DT>::kSize, per = 16 / size;
+  if constexpr (N < per) {                   // half a vector of 16-bit weights
+    typedef unsigned int u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+    tsl::u32x4 v = {0u, 0u, 0u, 0u};
+    if (j + N <= n) {
+      const u32x2_any h = *reinterpret_cast<const u32x2_any*>(w + (int64_t)j * size);
+      v[0] = h[0];
+      v[1] = h[1];
 #pragma unroll
-  for (int i = 0; i < kSumSlots; ++i) {
-    const int j = j0 + i * kST;
-    if (j >= n) continue;
-    double s = (double)score[j];
-    for (int w = 0; w < P.n_w; ++w) s += weight_at<DT>(wr + (int64_t)w * P.w_stride, j);
-    P.sum[(int64_t)r * P.slots + j] = (float)s;
+      for (int i = 0; i < N; ++i) s[i] += (double)tsl::unpack<DT>(v, i);
+    } else {
+      for (int i = 0; i < N; ++i)
+        if (j + i < n) s[i] += (double)tsl::load_logit<DT>(w, j + i);
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < N / per; ++h) {
+      if (j + (h + 1) * per <= n) {
+        const tsl::u32x4 v = tsl::load16(w + (int64_t)(j + h * per) * size);
+#pragma unroll
+        for (int i = 0; i < per; ++i) s[h * per + i] += (double)tsl::unpack<DT>(v, i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < per; ++i)
+          if (j + h * per + i < n) s[h * per + i] += (double)tsl::load_logit<DT>(w, j + h * per + i);
+      }
+    }
   }
 }
 
+// The sums of slots j .. j + N - 1 in binary64, in the order of the weight rows.
+template <int DT, int N>
+__device__ __forceinline__ void sum_slots(const EParams& P, int r, int j, int n, double* s) {
+  const float* score = P.score + (int64_t)r * P.score_stride;
+  const char* w = P.weights + (int64_t)r * P.w_row;
+#pragma unroll
+  for (int h = 0; h < N; h += 4) {
+    const f32x4 v = load4<f32x4, f32x4_any>(score, j + h, n, 0.0f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[h + i] = (double)v[i];
+  }
+#pragma unroll 8
+  for (int i = 0; i < P.n_w; ++i) add_weights<DT, N>(w + (int64_t)i * P.w_stride, j, n, s);
+}
+
+template <int DT>
+__global__ __launch_bounds__(kST) void ts_evict_sum_kernel(EParams P) {
+  __shared__ uint32_t red[3 * kST / 64];
+  const int r = (int)(blockIdx.x / (unsigned)P.tiles), tile = (int)(blockIdx.x - (unsigned)r * (unsigned)P.tiles);
+  const int n = row_length(P, r);
+  const int j = tile * kSumTile + (int)threadIdx.x * kSumSlots;
+  uint32_t newest = 0, kmin = 0xFFFFFFFFu, kmax = 0;
+  if (j < n) {
+    double s[kSumSlots];
+    sum_slots<DT, kSumSlots>(P, r, j, n, s);
+    f32x4* out = reinterpret_cast<f32x4*>(P.sum + (int64_t)r * P.sum_stride + j);
+#pragma unroll
+    for (int h = 0; h < kSumSlots / 4; ++h)
+      if (j + 4 * h < n) out[h] = f32x4{(float)s[4 * h], (float)s[4 * h + 1], (float)s[4 * h + 2], (float)s[4 * h + 3]};
+    if (P.slots > kRowSlots) {
+      const int32_t* pos = P.position + (int64_t)r * P.position_stride;
+#pragma unroll
+      for (int i = 0; i < kSumSlots; ++i) {
+        if (j + i >= n) continue;
+        newest = max(newest, (uint32_t)pos[j + i] ^ 0x80000000u);
+        const uint32_t k = f2key((float)s[i]);
+        kmin = min(kmin, k);
+        kmax = max(kmax, k);
+      }
+    }
+  }
+  if (P.slots <= kRowSlots) return;
+  if (tile == 0) {
+    uint32_t* h = P.hist + (int64_t)r * 2 * kEBins;
+    for (int i = threadIdx.x; i < 2 * kEBins; i += kST) h[i] = 0u;
+    if (threadIdx.x == 0) P.row[r] = RowInfo{};
+  }
+  newest = wave_max(newest);
+  kmin = wave_min(kmin);
+  kmax = wave_max(kmax);
+  if (lane() == 0) {
+    red[3 * wave()] = newest;
+    red[3 * wave() + 1] = kmin;
+    red[3 * wave() + 2] = kmax;
+  }
+  bar();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kST / 64; ++w) {
+      newest = max(newest, red[3 * w]);
+      kmin = min(kmin, red[3 * w + 1]);
+      kmax = max(kmax, red[3 * w + 2]);
+    }
+    P.info[(int64_t)r * P.tiles + tile] = TileInfo{(int32_t)(newest ^ 0x80000000u), kmin, kmax, 0u};
+  }
+}
+
+// ------------------------------------------------------------------ selection within a row
 struct ESmem {
   uint32_t hist[kEBins];
-  uint32_t red[kEW];
-  uint32_t red2[kEW];
-  uint32_t res[4];
+  uint2 list[kListRow];        // (u, slot) of the cut's bin
+  uint32_t red[kEW], red2[kEW], red3[kEW];
+  uint32_t res[3];
+  uint32_t count;
+  uint32_t cut_u, cut_slot;
 };
 
 // Exclusive prefix over the waves of two counts that every wave holds uniformly, and their totals.
@@ -106,212 +256,788 @@ __device__ __forceinline__ void wave_offsets(ESmem& sm, uint32_t a, uint32_t b, 
   }
   bar();
 }
+__device__ __forceinline__ uint32_t block_total(ESmem& sm, uint32_t per_wave) {
+  uint32_t a, b, t, u;
+  wave_offsets(sm, per_wave, 0u, a, b, t, u);
+  return t;
+}
 
-__global__ __launch_bounds__(kET) void ts_evict_select_kernel(EParams P) {
-  __shared__ ESmem sm;
-  const int r = (int)blockIdx.x, t = (int)threadIdx.x, l = lane();
-  const int n = row_length(P, r);
-  const int32_t kr = P.keep[r];
-  const int k = min(kr, n);
-  const float* sum = P.sum + (int64_t)r * P.slots;
-  const int32_t* pos = P.position + (int64_t)r * P.position_stride;
-  int32_t* source = P.out_source + (int64_t)r * P.keep_max;
-  float* score = P.out_score + (int64_t)r * P.out_score_stride;
-  int32_t* place = P.out_position + (int64_t)r * P.out_position_stride;
-  const bool same_score = P.out_score == P.score, same_place = P.out_position == P.position;
+// A row's parameters and status.
+struct Row {
+  int n, k, st;
+  int64_t from;       // positions above this are protected
+  int32_t sinks;
+  uint32_t kmin;
+  __device__ __forceinline__ bool first(int32_t p) const { return p < sinks || (int64_t)p > from; }
+  __device__ __forceinline__ uint32_t u(float s) const { return f2key(s) - kmin; }
+};
 
-  // newest position, finiteness
-  uint32_t newest = 0, bad = 0;
-  for (int j = t; j < n; j += kET) {
-    newest = max(newest, (uint32_t)pos[j] ^ 0x80000000u);
-    const uint32_t b = __float_as_uint(sum[j]);
-    bad |= (b & 0x7F800000u) == 0x7F800000u ? 1u : 0u;
+// Kept of the cut's class: u above `u`, or equal to it and the slot not past `slot`.
+struct Cut {
+  uint32_t u, slot;
+  __device__ __forceinline__ bool keeps(uint32_t x, int j) const { return x > u || (x == u && (uint32_t)j <= slot); }
+};
+
+// Finds the bin of the need-th largest of the binned values: sm.res = {bin, count above it, count in it}.
+__device__ __forceinline__ void find_bin(ESmem& sm, uint32_t need) {
+  const int t = threadIdx.x;
+  const uint32_t c0 = sm.hist[2 * t], c1 = sm.hist[2 * t + 1];
+  const uint32_t incl = wave_incl_scan(c0 + c1);
+  uint32_t before, eb, all, tb;
+  wave_offsets(sm, wave_total(incl), 0u, before, eb, all, tb);
+  const uint32_t above = all - (before + incl);
+  if (above < need && above + c1 >= need) {
+    sm.res[0] = 2 * t + 1;
+    sm.res[1] = above;
+    sm.res[2] = c1;
+  } else if (above + c1 < need && above + c1 + c0 >= need) {
+    sm.res[0] = 2 * t;
+    sm.res[1] = above + c1;
+    sm.res[2] = c0;
   }
-  newest = block_max_u32<kEW>(newest, sm.red);
-  bad = block_max_u32<kEW>(bad, sm.red);
-  const int st = bad ? TS_ROW_NONFINITE : (kr < 1 || k > P.keep_max) ? TS_ROW_BAD_K : TS_ROW_OK;
-  if (st != TS_ROW_OK) {   // the row stays as it is
-    for (int j = t; j < P.keep_max; j += kET) {
-      source[j] = -1;
-      if (!same_score) score[j] = __uint_as_float(0x7FC00000u);
-      if (!same_place) place[j] = -1;
-    }
-    if (t == 0) {
-      P.out_lengths[r] = n;
-      P.moves[r] = 0;
-      if (P.status) P.status[r] = st;
-    }
-    return;
-  }
-  const int64_t from = (int64_t)(int32_t)(newest ^ 0x80000000u) - P.recent;
-  auto first = [&](int32_t p) { return p < P.sinks || (int64_t)p > from; };
+  bar();
+}
 
-  // Which class the cut falls into: among the protected slots where they alone fill the row, else among the others.
-  uint32_t np = 0;
-  for (int j = t; j < n; j += kET) np += first(pos[j]) ? 1u : 0u;
-  np = wave_incl_scan(np);
-  uint32_t ea, eb, total, unused;
-  wave_offsets(sm, wave_total(np), 0u, ea, eb, total, unused);
-  const bool among_first = total >= (uint32_t)k;
-  uint32_t need = among_first ? (uint32_t)k : (uint32_t)k - total;
-  const uint32_t pool = among_first ? total : (uint32_t)n - total;
-
-  // Radix select of the need-th largest key of that class; the kept ones are those whose top (32 - lo) bits are above
-  // `prefix`, or equal it with a slot not past `last`.
-  uint32_t prefix = 0, last = 0xFFFFFFFFu;
-  int lo = 32;
-  if (need < pool) {
-    while (lo > 0) {
-      const int d = min(kEBits, lo), sh = lo - d;
-      for (int i = t; i < kEBins; i += kET) sm.hist[i] = 0u;
-      bar();
-      for (int j = t; j < n; j += kET) {
-        const uint32_t key = f2key(sum[j]);
-        if (first(pos[j]) == among_first && shr(key, lo) == prefix) atomicAdd(&sm.hist[(key >> sh) & ((1u << d) - 1u)], 1u);
-      }
-      bar();
-      // thread t owns bins 2t, 2t + 1
-      const uint32_t c0 = sm.hist[2 * t], c1 = sm.hist[2 * t + 1];
-      const uint32_t incl = wave_incl_scan(c0 + c1);
-      uint32_t before, all;
-      wave_offsets(sm, wave_total(incl), 0u, before, eb, all, unused);
-      const uint32_t above = all - (before + incl);         // in the bins above this thread's
-      if (above < need && above + c1 >= need) {
-        sm.res[0] = 2 * t + 1;
-        sm.res[1] = above;
-        sm.res[2] = c1;
-      } else if (above + c1 < need && above + c1 + c0 >= need) {
-        sm.res[0] = 2 * t;
-        sm.res[1] = above + c1;
-        sm.res[2] = c0;
-      }
-      bar();
-      prefix = shl(prefix, d) | sm.res[0];
-      need -= sm.res[1];
-      const uint32_t in_bin = sm.res[2];
-      lo = sh;
-      bar();
-      if (in_bin == need) {
-        need = 0;
-        break;
-      }
+// The cut among the `count` (u, slot) pairs of sm.list: its need-th in the order (u descending, slot ascending).
+__device__ __forceinline__ Cut rank_list(ESmem& sm, uint32_t count, uint32_t need) {
+  if (threadIdx.x < count) {
+    const uint2 me = sm.list[threadIdx.x];
+    uint32_t above = 0;
+    for (uint32_t i = 0; i < count; ++i) {
+      const uint2 o = sm.list[i];
+      above += (o.x > me.x || (o.x == me.x && o.y < me.y)) ? 1u : 0u;
     }
-  } else {
-    need = 0;   // the whole class
+    if (above + 1 == need) {
+      sm.cut_u = me.x;
+      sm.cut_slot = me.y;
+    }
   }
-  auto inside = [&](int j) {
-    const bool f = first(pos[j]);
-    if (f != among_first) return f;              // protected slots beside a cut among the others
-    const uint32_t h = shr(f2key(sum[j]), lo);
-    return h > prefix || (h == prefix && (uint32_t)j <= last);
-  };
-  // A wave looks at consecutive slots, 64 at a time.
-  const int span = ((n + kEW - 1) / kEW + 63) & ~63;
-  const int w0 = wave() * span, w1 = min(n, w0 + span);
-  if (need > 0) {   // equal keys on both sides of the cut: the lowest slots stay
-    uint32_t c = 0;
-    for (int j = w0 + l; j - l < w1; j += 64)
-      c += (uint32_t)__popcll(__ballot(j < w1 && first(pos[j]) == among_first && f2key(sum[j]) == prefix));
-    wave_offsets(sm, c, 0u, ea, eb, total, unused);
-    if (ea < need && ea + c >= need) {
-      uint32_t run = ea;
-      for (int j = w0 + l; j - l < w1; j += 64) {
-        const bool eq = j < w1 && first(pos[j]) == among_first && f2key(sum[j]) == prefix;
-        const uint64_t m = __ballot(eq);
-        if (eq && run + mbcnt(m) + 1 == need) sm.res[3] = (uint32_t)j;
-        run += (uint32_t)__popcll(m);
-      }
-    }
+  bar();
+  return Cut{sm.cut_u, sm.cut_slot};
+}
+
+// The cut of a class: the need-th of its slots (1 <= need < their number). each(f) calls f(u, slot) for the calling
+// thread's slots of the class; ordered(bin_lo, need) finds the need-th slot, in slot order, whose u is bin_lo.
+// It lies among those with u >> lo == prefix.
+template <class E, class O>
+__device__ __forceinline__ Cut find_cut(ESmem& sm, int lo, uint32_t prefix, uint32_t need, E each, O ordered) {
+  if (lo == 0) return Cut{prefix, ordered(prefix, need)};
+  while (true) {
+    const int d = min(kEBits, lo), sh = lo - d;
+    sm.hist[threadIdx.x] = 0u;
+    sm.hist[threadIdx.x + kET] = 0u;
     bar();
-    last = sm.res[3];
-  }
-
-  // Freed slots and fillers, in slot order.
-  uint32_t ch = 0, cf = 0;
-  for (int j = w0 + l; j - l < w1; j += 64) {
-    const bool in = j < w1 && inside(j);
-    ch += (uint32_t)__popcll(__ballot(j < w1 && j < k && !in));
-    cf += (uint32_t)__popcll(__ballot(j >= k && in));
-  }
-  uint32_t ih, jf, th, tf;
-  wave_offsets(sm, ch, cf, ih, jf, th, tf);
-  int32_t* hole = P.hole + (int64_t)r * P.cap;
-  int32_t* fill = P.fill + (int64_t)r * P.cap;
-  for (int j = w0 + l; j - l < w1; j += 64) {
-    const bool in = j < w1 && inside(j);
-    const bool h = j < w1 && j < k && !in, f = j >= k && in;
-    const uint64_t mh = __ballot(h), mf = __ballot(f);
-    if (h) hole[ih + mbcnt(mh)] = j;
-    if (f) fill[jf + mbcnt(mf)] = j;
-    if (in && j < k) {
-      source[j] = j;
-      score[j] = sum[j];
-      if (!same_place) place[j] = pos[j];
+    const uint32_t mask = (1u << d) - 1u;
+    each([&](uint32_t u, int) {
+      if (shr(u, lo) == prefix) atomicAdd(&sm.hist[(u >> sh) & mask], 1u);
+    });
+    bar();
+    find_bin(sm, need);
+    prefix = shl(prefix, d) | sm.res[0];
+    need -= sm.res[1];
+    const uint32_t in_bin = sm.res[2];
+    lo = sh;
+    bar();
+    if (in_bin == need) return Cut{shl(prefix, lo), 0xFFFFFFFFu};   // the whole bin stays
+    if (in_bin <= (uint32_t)kListRow) {
+      if (threadIdx.x == 0) sm.count = 0;
+      bar();
+      each([&](uint32_t u, int j) {
+        if (shr(u, lo) == prefix) sm.list[atomicAdd(&sm.count, 1u)] = make_uint2(u, (uint32_t)j);
+      });
+      bar();
+      return rank_list(sm, in_bin, need);
     }
-    ih += (uint32_t)__popcll(mh);
-    jf += (uint32_t)__popcll(mf);
-  }
-  bar_all();
-  for (uint32_t i = t; i < th; i += kET) {
-    const int h = hole[i], f = fill[i];
-    source[h] = f;
-    score[h] = sum[f];
-    place[h] = pos[f];
-  }
-  bar_all();
-  for (int j = k + t; j < P.keep_max; j += kET) {
-    source[j] = -1;
-    score[j] = 0.0f;
-    place[j] = -1;
-  }
-  if (t == 0) {
-    P.out_lengths[r] = k;
-    P.moves[r] = (int32_t)th;
-    if (P.status) P.status[r] = TS_ROW_OK;
+    if (lo == 0) return Cut{prefix, ordered(prefix, need)};   // many equal: the lowest slots stay
   }
 }
 
-struct Cache {
-  char* p;
-  int64_t batch, head, slot;   // bytes
-  int32_t units;               // units of U bytes a slot
-};
+// Status, k and the class of the cut, once the row's extremes are known.
+__device__ __forceinline__ Row row_of(const EParams& P, int r, uint32_t newest, uint32_t kmin, uint32_t kmax) {
+  Row R;
+  R.n = row_length(P, r);
+  const int32_t keep = P.keep[r];
+  R.k = min(keep, R.n);
+  R.from = (int64_t)(int32_t)(newest ^ 0x80000000u) - P.recent;
+  R.sinks = P.sinks;
+  R.kmin = kmin;
+  const bool bad = R.n > 0 && (kmax >= kKeyPosInf || kmin <= kKeyNegInf);
+  R.st = bad ? TS_ROW_NONFINITE : (keep < 1 || R.k > P.keep_max) ? TS_ROW_BAD_K : TS_ROW_OK;
+  return R;
+}
 
-// Copies units of U bytes: thread i of a row's moves takes unit i % units of move i / units.
+// A rejected row: nothing of it changes, and outputs that are not its inputs are poisoned.
+__device__ __forceinline__ void reject_row(const EParams& P, int r, const Row& R) {
+  int32_t* source = P.out_source + (int64_t)r * P.keep_max;
+  float* score = P.out_score + (int64_t)r * P.out_score_stride;
+  int32_t* place = P.out_position + (int64_t)r * P.out_position_stride;
+  for (int j = threadIdx.x; j < P.keep_max; j += kET) {
+    source[j] = -1;
+    if (P.out_score != P.score) score[j] = __uint_as_float(0x7FC00000u);
+    if (P.out_position != P.position) place[j] = -1;
+  }
+  if (threadIdx.x == 0) {
+    P.out_lengths[r] = R.n;
+    P.moves[r] = 0;
+    if (P.status) P.status[r] = R.st;
+  }
+}
+
+// The i-th unit of U bytes of a row's `moves`: unit i % units of move i / units.
 template <class U>
-__global__ __launch_bounds__(kMT) void ts_evict_move_kernel(EParams P, Cache C, int heads, int blocks) {
-  const int r = (int)(blockIdx.x / (unsigned)blocks);
-  const int64_t i0 = (int64_t)(blockIdx.x - (unsigned)r * (unsigned)blocks) * kMT + threadIdx.x;
-  const int64_t n = (int64_t)P.moves[r] * C.units;
+__device__ __forceinline__ void copy_units(const Cache& C, int r, int heads, const int32_t* hole, const int32_t* fill,
+                                           int64_t moves, int64_t i0, int64_t step) {
   char* base = C.p + (int64_t)(r / heads) * C.batch + (int64_t)(r % heads) * C.head;
-  const int32_t* hole = P.hole + (int64_t)r * P.cap;
-  const int32_t* fill = P.fill + (int64_t)r * P.cap;
-  for (int64_t i = i0; i < n; i += (int64_t)blocks * kMT) {
+  const int64_t n = moves * C.units;
+  for (int64_t i = i0; i < n; i += step) {
     const int64_t m = i / C.units, u = i - m * C.units;
     const U v = *reinterpret_cast<const U*>(base + (int64_t)fill[m] * C.slot + u * (int64_t)sizeof(U));
     *reinterpret_cast<U*>(base + (int64_t)hole[m] * C.slot + u * (int64_t)sizeof(U)) = v;
   }
 }
 
+// The row's lists are whole: the freed slots' small outputs, the unused places, the length.
+__device__ __forceinline__ void finish_row(const EParams& P, int r, const Row& R, uint32_t moves) {
+  const int32_t* pos = P.position + (int64_t)r * P.position_stride;
+  const float* sum = P.sum + (int64_t)r * P.sum_stride;
+  int32_t* source = P.out_source + (int64_t)r * P.keep_max;
+  float* score = P.out_score + (int64_t)r * P.out_score_stride;
+  int32_t* place = P.out_position + (int64_t)r * P.out_position_stride;
+  const int32_t* hole = P.hole + (int64_t)r * P.cap;
+  const int32_t* fill = P.fill + (int64_t)r * P.cap;
+  for (uint32_t i = threadIdx.x; i < moves; i += kET) {
+    const int h = hole[i], f = fill[i];
+    source[h] = f;
+    score[h] = sum[f];
+    place[h] = pos[f];
+  }
+  bar_all();   // in place, the unused places below may be fillers' own
+  for (int j = R.k + (int)threadIdx.x; j < P.keep_max; j += kET) {
+    source[j] = -1;
+    score[j] = 0.0f;
+    place[j] = -1;
+  }
+  if (threadIdx.x == 0) {
+    P.out_lengths[r] = R.k;
+    P.moves[r] = (int32_t)moves;
+    if (P.status) P.status[r] = TS_ROW_OK;
+  }
+}
+
+// Ranks of a vector's four flags among all flags of the wave's vector (lanes, then elements, in order).
+__device__ __forceinline__ uint32_t rank4(const uint64_t* m, int i) {
+  uint32_t before = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) before += mbcnt(m[e]);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) before += e < i ? (uint32_t)((m[e] >> lane()) & 1u) : 0u;
+  return before;
+}
+__device__ __forceinline__ uint32_t count4(const uint64_t* m) {
+  return (uint32_t)(__popcll(m[0]) + __popcll(m[1]) + __popcll(m[2]) + __popcll(m[3]));
+}
+
+// A vector of four slots from j on whose kept ones are the bits of `kept`: writes what stays in place and lists
+// freed slots and fillers from ih and jf on (both advanced).
+__device__ __forceinline__ void emit4(const EParams& P, int r, const Row& R, int j, uint32_t kept, const f32x4& s, const i32x4& p,
+                                      uint32_t& ih, uint32_t& jf, bool keep_sums) {
+  int32_t* source = P.out_source + (int64_t)r * P.keep_max;
+  float* score = P.out_score + (int64_t)r * P.out_score_stride;
+  int32_t* place = P.out_position + (int64_t)r * P.out_position_stride;
+  int32_t* hole = P.hole + (int64_t)r * P.cap;
+  int32_t* fill = P.fill + (int64_t)r * P.cap;
+  const bool same_place = P.out_position == P.position;
+  uint64_t mh[4], mf[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool in = (kept >> i) & 1u;
+    mh[i] = __ballot(j + i < R.k && !in);
+    mf[i] = __ballot(j + i >= R.k && in);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool in = (kept >> i) & 1u;
+    if (j + i < R.k) {
+      if (in) {
+        source[j + i] = j + i;
+        score[j + i] = s[i];
+        if (!same_place) place[j + i] = p[i];
+      } else {
+        hole[ih + rank4(mh, i)] = j + i;
+      }
+    } else if (in) {
+      fill[jf + rank4(mf, i)] = j + i;
+      if (keep_sums) P.sum[(int64_t)r * P.sum_stride + j + i] = s[i];
+    }
+  }
+  ih += count4(mh);
+  jf += count4(mf);
+}
+
+// SRC: the weights' type where the row is summed here, -1 where the sum kernel has run. NV: vectors a thread.
+template <int NV, int SRC, class U>
+__global__ __launch_bounds__(kET) void ts_evict_row_kernel(EParams P) {
+  __shared__ ESmem sm;
+  const int r = (int)blockIdx.x, l = lane();
+  const int n = row_length(P, r);
+  const int32_t* pos = P.position + (int64_t)r * P.position_stride;
+  const float* sum = P.sum + (int64_t)r * P.sum_stride;
+  const int base = wave() * NV * 256 + 4 * l;   // a wave's slots are consecutive
+  f32x4 s[NV];
+  i32x4 p[NV];
+  uint32_t newest = 0, kmin = 0xFFFFFFFFu, kmax = 0;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int j = base + 256 * v;
+    if constexpr (SRC < 0) {
+      s[v] = j < n ? *reinterpret_cast<const f32x4*>(sum + j) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    } else {
+      double d[4] = {0.0, 0.0, 0.0, 0.0};
+      if (j < n) sum_slots<SRC, 4>(P, r, j, n, d);
+      s[v] = f32x4{(float)d[0], (float)d[1], (float)d[2], (float)d[3]};
+    }
+    p[v] = load4<i32x4, i32x4_any>(pos, j, n, (int32_t)0x80000000);
+  }
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (base + 256 * v + i >= n) continue;
+      newest = max(newest, (uint32_t)p[v][i] ^ 0x80000000u);
+      const uint32_t k = f2key(s[v][i]);
+      kmin = min(kmin, k);
+      kmax = max(kmax, k);
+    }
+  newest = wave_max(newest);
+  kmin = wave_min(kmin);
+  kmax = wave_max(kmax);
+  if (l == 0) {
+    sm.red[wave()] = newest;
+    sm.red2[wave()] = kmin;
+    sm.red3[wave()] = kmax;
+  }
+  bar();
+#pragma unroll
+  for (int w = 0; w < kEW; ++w) {
+    newest = max(newest, sm.red[w]);
+    kmin = min(kmin, sm.red2[w]);
+    kmax = max(kmax, sm.red3[w]);
+  }
+  bar();
+  const Row R = row_of(P, r, newest, kmin, kmax);
+  if (R.st != TS_ROW_OK) {
+    reject_row(P, r, R);
+    return;
+  }
+  // bit 4v + i: slot i of vector v is in use, is protected
+  uint32_t live = 0, first = 0;
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool in = base + 256 * v + i < n;
+      live |= (in ? 1u : 0u) << (4 * v + i);
+      first |= (in && R.first(p[v][i]) ? 1u : 0u) << (4 * v + i);
+    }
+  const uint32_t total = block_total(sm, wave_total(wave_incl_scan((uint32_t)__popc(first))));
+  const bool among_first = total >= (uint32_t)R.k;
+  const uint32_t need = among_first ? (uint32_t)R.k : (uint32_t)R.k - total;
+  const uint32_t pool = among_first ? total : (uint32_t)n - total;
+  const uint32_t cls = among_first ? first : live & ~first;   // the cut's class
+  Cut cut{0u, 0xFFFFFFFFu};                                    // all of it
+  if (need < pool) {
+    cut = find_cut(
+        sm, bitlen(kmax - kmin), 0u, need,
+        [&](auto f) {
+#pragma unroll
+          for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if ((cls >> (4 * v + i)) & 1u) f(R.u(s[v][i]), base + 256 * v + i);
+        },
+        [&](uint32_t u, uint32_t nth) {
+          uint32_t c = 0;
+          uint64_t m[NV][4];
+#pragma unroll
+          for (int v = 0; v < NV; ++v) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m[v][i] = __ballot(((cls >> (4 * v + i)) & 1u) && R.u(s[v][i]) == u);
+            c += count4(m[v]);
+          }
+          uint32_t run, e, t0, t1;
+          wave_offsets(sm, c, 0u, run, e, t0, t1);
+#pragma unroll
+          for (int v = 0; v < NV; ++v) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (((m[v][i] >> l) & 1u) && run + rank4(m[v], i) + 1 == nth) sm.cut_slot = (uint32_t)(base + 256 * v + i);
+            run += count4(m[v]);
+          }
+          bar();
+          return sm.cut_slot;
+        });
+  }
+  uint32_t kept = among_first ? 0u : first;
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (((cls >> (4 * v + i)) & 1u) && cut.keeps(R.u(s[v][i]), base + 256 * v + i)) kept |= 1u << (4 * v + i);
+  uint32_t ch = 0, cf = 0;
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = base + 256 * v + i;
+      const bool in = (kept >> (4 * v + i)) & 1u;
+      ch += (uint32_t)__popcll(__ballot(j < R.k && !in));
+      cf += (uint32_t)__popcll(__ballot(j >= R.k && in));
+    }
+  uint32_t ih, jf, moves, tf;
+  wave_offsets(sm, ch, cf, ih, jf, moves, tf);
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+    emit4(P, r, R, base + 256 * v, (kept >> (4 * v)) & 15u, s[v], p[v], ih, jf, SRC >= 0);
+  bar_all();
+  finish_row(P, r, R, moves);
+  if constexpr (!std::is_void_v<U>) {
+    const int32_t* hole = P.hole + (int64_t)r * P.cap;
+    const int32_t* fill = P.fill + (int64_t)r * P.cap;
+    if (P.k.units) copy_units<U>(P.k, r, P.heads, hole, fill, moves, threadIdx.x, kET);
+    if (P.v.units) copy_units<U>(P.v, r, P.heads, hole, fill, moves, threadIdx.x, kET);
+  }
+}
+
+// ------------------------------------------------------------------ long rows
+constexpr int kSW = kST / 64;
+
+// The row's extremes from its tiles; every thread of the workgroup gets them. red: 3 words a wave.
+__device__ __forceinline__ Row long_row(const EParams& P, int r, uint32_t* red, uint32_t& range) {
+  const int n = row_length(P, r);
+  uint32_t newest = 0, kmin = 0xFFFFFFFFu, kmax = 0;
+  for (int i = threadIdx.x; (int64_t)i * kSumTile < n; i += blockDim.x) {
+    const TileInfo ti = P.info[(int64_t)r * P.tiles + i];
+    newest = max(newest, (uint32_t)ti.newest ^ 0x80000000u);
+    kmin = min(kmin, ti.kmin);
+    kmax = max(kmax, ti.kmax);
+  }
+  newest = wave_max(newest);
+  kmin = wave_min(kmin);
+  kmax = wave_max(kmax);
+  if (lane() == 0) {
+    red[3 * wave()] = newest;
+    red[3 * wave() + 1] = kmin;
+    red[3 * wave() + 2] = kmax;
+  }
+  bar();
+  for (int w = 0; w < (int)(blockDim.x >> 6); ++w) {
+    newest = max(newest, red[3 * w]);
+    kmin = min(kmin, red[3 * w + 1]);
+    kmax = max(kmax, red[3 * w + 2]);
+  }
+  bar();
+  range = kmax - kmin;
+  return row_of(P, r, newest, kmin, kmax);
+}
+
+// A thread's four slots of a tile of a long row.
+struct Quad {
+  int j;
+  f32x4 s;
+  i32x4 p;
+};
+__device__ __forceinline__ Quad load_quad(const EParams& P, int r, int tile, int n) {
+  Quad q;
+  q.j = tile * kSumTile + (int)threadIdx.x * 4;
+  q.s = q.j < n ? *reinterpret_cast<const f32x4*>(P.sum + (int64_t)r * P.sum_stride + q.j) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  q.p = load4<i32x4, i32x4_any>(P.position + (int64_t)r * P.position_stride, q.j, n, (int32_t)0x80000000);
+  return q;
+}
+
+__global__ __launch_bounds__(kST) void ts_evict_bin_kernel(EParams P) {
+  __shared__ uint32_t hist[2][kEBins];
+  __shared__ uint32_t red[3 * kSW];
+  __shared__ uint32_t np;
+  const int r = (int)(blockIdx.x / (unsigned)P.tiles), tile = (int)(blockIdx.x - (unsigned)r * (unsigned)P.tiles);
+  const int n = row_length(P, r);
+  if (tile * kSumTile >= n) return;
+  const Quad q = load_quad(P, r, tile, n);
+  for (int i = threadIdx.x; i < 2 * kEBins; i += kST) (&hist[0][0])[i] = 0u;
+  if (threadIdx.x == 0) np = 0;
+  uint32_t range;
+  const Row R = long_row(P, r, red, range);
+  if (R.st != TS_ROW_OK) return;
+  const int sh = max(bitlen(range) - kEBits, 0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (q.j + i >= n) continue;
+    const bool f = R.first(q.p[i]);
+    atomicAdd(&hist[f ? 1 : 0][R.u(q.s[i]) >> sh], 1u);
+    if (f) atomicAdd(&np, 1u);
+  }
+  bar();
+  uint32_t* h = P.hist + (int64_t)r * 2 * kEBins;
+  for (int i = threadIdx.x; i < 2 * kEBins; i += kST) {
+    const uint32_t c = (&hist[0][0])[i];
+    if (c) atomicAdd(&h[i], c);
+  }
+  if (threadIdx.x == 0 && np) atomicAdd(&P.row[r].protected_, np);
+}
+
+__global__ __launch_bounds__(kST) void ts_evict_list_kernel(EParams P) {
+  __shared__ uint32_t red[3 * kSW];
+  __shared__ uint32_t res[3];
+  const int r = (int)(blockIdx.x / (unsigned)P.tiles), tile = (int)(blockIdx.x - (unsigned)r * (unsigned)P.tiles);
+  const int n = row_length(P, r), t = threadIdx.x;
+  if (tile * kSumTile >= n) return;
+  const Quad q = load_quad(P, r, tile, n);
+  const uint32_t total = P.row[r].protected_;
+  uint32_t range;
+  const Row R = long_row(P, r, red, range);
+  if (R.st != TS_ROW_OK) return;
+  const bool among_first = total >= (uint32_t)R.k;
+  const uint32_t need = among_first ? (uint32_t)R.k : (uint32_t)R.k - total;
+  const uint32_t pool = among_first ? total : (uint32_t)n - total;
+  TileBin out = {};
+  if (need < pool) {
+    // thread t owns eight bins
+    constexpr int kOwn = kEBins / kST;
+    const uint32_t* h = P.hist + ((int64_t)r * 2 + (among_first ? 1 : 0)) * kEBins + t * kOwn;
+    uint32_t c[kOwn], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      c[i] = h[i];
+      sum += c[i];
+    }
+    uint32_t all;
+    const uint32_t before = block_excl_scan<kSW>(sum, red, all);
+    uint32_t above = all - before - sum;
+    if (above < need && above + sum >= need) {
+      int i = kOwn - 1;
+      for (; i > 0; --i) {
+        if (above + c[i] >= need) break;
+        above += c[i];
+      }
+      res[0] = t * kOwn + i;
+      res[1] = above;
+      res[2] = c[i];
+    }
+    bar();
+    const int lo = max(bitlen(range) - kEBits, 0);
+    const uint32_t bin = res[0], left = need - res[1], in_bin = res[2];
+    const bool listed = in_bin > left && in_bin <= (uint32_t)kListLong;
+    uint32_t umin = 0xFFFFFFFFu, umax = 0, count = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u = R.u(q.s[i]);
+      const bool in = q.j + i < n && R.first(q.p[i]) == among_first && (u >> lo) == bin;
+      if (in) {
+        umin = min(umin, u);
+        umax = max(umax, u);
+        if (listed) P.list[(int64_t)r * kListLong + atomicAdd(&P.row[r].listed, 1u)] = make_uint2(u, (uint32_t)(q.j + i));
+      }
+      count += (uint32_t)__popcll(__ballot(in));
+    }
+    umin = wave_min(umin);
+    umax = wave_max(umax);
+    if (lane() == 0) {
+      red[3 * wave()] = count;
+      red[3 * wave() + 1] = umin;
+      red[3 * wave() + 2] = umax;
+    }
+    bar();
+    for (int w = 0; w < kSW; ++w) {
+      out.count += red[3 * w];
+      out.umin = w ? min(out.umin, red[3 * w + 1]) : red[1];
+      out.umax = max(out.umax, red[3 * w + 2]);
+    }
+    if (tile == 0 && t == 0) {
+      RowInfo& I = P.row[r];
+      I.among_first = among_first ? 1u : 0u;
+      I.prefix = bin;
+      I.lo = (uint32_t)lo;
+      I.need = left;
+      I.in_bin = in_bin;
+      I.whole = 0u;
+    }
+  } else if (tile == 0 && t == 0) {
+    P.row[r].among_first = among_first ? 1u : 0u;
+    P.row[r].whole = 1u;
+  }
+  if (t == 0) P.bin[(int64_t)r * P.tiles + tile] = out;
+}
+
+// One workgroup a row: the cut's u and slot, and the row's status and length.
+__global__ __launch_bounds__(kET) void ts_evict_cut_kernel(EParams P) {
+  __shared__ ESmem sm;
+  __shared__ uint32_t red[3 * kEW];
+  __shared__ uint2 list[kListLong];
+  const int r = (int)blockIdx.x, t = threadIdx.x, l = lane();
+  uint32_t range;
+  const Row R = long_row(P, r, red, range);
+  if (t == 0) {
+    P.row[r].st = R.st;
+    P.row[r].k = R.k;
+    P.row[r].tiles = (R.n + kSumTile - 1) / kSumTile;
+  }
+  if (R.st != TS_ROW_OK) {
+    reject_row(P, r, R);
+    return;
+  }
+  const RowInfo I = P.row[r];
+  Cut cut{0u, 0xFFFFFFFFu};
+  if (!I.whole && I.in_bin == I.need) {
+    cut.u = I.prefix << I.lo;
+  } else if (!I.whole && I.in_bin <= (uint32_t)kListLong) {
+    for (uint32_t i = t; i < I.in_bin; i += kET) list[i] = P.list[(int64_t)r * kListLong + i];
+    bar();
+    cut = find_cut(
+        sm, (int)I.lo, I.prefix, I.need,
+        [&](auto f) {
+          for (uint32_t i = t; i < I.in_bin; i += kET) f(list[i].x, (int)list[i].y);
+        },
+        [&](uint32_t u, uint32_t nth) {   // equal u: the nth smallest slot of the list, by counting
+          for (uint32_t i = t; i < I.in_bin; i += kET) {
+            const uint2 me = list[i];
+            if (me.x != u) continue;
+            uint32_t below = 0;
+            for (uint32_t o = 0; o < I.in_bin; ++o) below += list[o].x == u && list[o].y < me.y ? 1u : 0u;
+            if (below + 1 == nth) sm.cut_slot = me.y;
+          }
+          bar();
+          return sm.cut_slot;
+        });
+  } else if (!I.whole) {
+    // Too many to list. The extreme u of the tiles' shares say whether all are equal.
+    const bool af = I.among_first != 0;
+    uint32_t umin = 0xFFFFFFFFu, umax = 0;
+    for (int i = t; (int64_t)i * kSumTile < R.n; i += kET) {
+      const TileBin b = P.bin[(int64_t)r * P.tiles + i];
+      if (!b.count) continue;
+      umin = min(umin, b.umin);
+      umax = max(umax, b.umax);
+    }
+    umin = block_min_u32<kEW>(umin, sm.red);
+    umax = block_max_u32<kEW>(umax, sm.red);
+    const int32_t* pos = P.position + (int64_t)r * P.position_stride;
+    const float* sum = P.sum + (int64_t)r * P.sum_stride;
+    const int span = (((R.n + kEW - 1) / kEW) + 63) & ~63;
+    const int w0 = min(R.n, wave() * span), w1 = min(R.n, w0 + span);
+    auto of_class = [&](int j) { return j < w1 && R.first(pos[j]) == af; };
+    auto ordered = [&](uint32_t u, uint32_t nth) {
+      uint32_t c = 0;
+      for (int b = w0; b < w1; b += 64) c += (uint32_t)__popcll(__ballot(of_class(b + l) && R.u(sum[b + l]) == u));
+      uint32_t run, e0, t0, t1;
+      wave_offsets(sm, c, 0u, run, e0, t0, t1);
+      if (run < nth && run + c >= nth) {
+        for (int b = w0; b < w1; b += 64) {
+          const uint64_t m = __ballot(of_class(b + l) && R.u(sum[b + l]) == u);
+          if (((m >> l) & 1u) && run + mbcnt(m) + 1 == nth) sm.cut_slot = (uint32_t)(b + l);
+          run += (uint32_t)__popcll(m);
+        }
+      }
+      bar();
+      return sm.cut_slot;
+    };
+    if (umin == umax) cut = Cut{umin, ordered(umin, I.need)};
+    else
+      cut = find_cut(
+          sm, (int)I.lo, I.prefix, I.need,
+          [&](auto f) {
+            for (int j = w0 + l; j < w1; j += 64)
+              if (of_class(j)) f(R.u(sum[j]), j);
+          },
+          ordered);
+  }
+  if (t == 0) {
+    P.row[r].cut_u = cut.u;
+    P.row[r].cut_slot = cut.slot;
+  }
+}
+
+__global__ __launch_bounds__(kST) void ts_evict_emit_kernel(EParams P) {
+  __shared__ uint32_t red[3 * kSW];
+  const int r = (int)(blockIdx.x / (unsigned)P.tiles), tile = (int)(blockIdx.x - (unsigned)r * (unsigned)P.tiles);
+  const int n = row_length(P, r);
+  if (tile * kSumTile >= n) return;
+  const Quad q = load_quad(P, r, tile, n);
+  const RowInfo I = P.row[r];
+  uint32_t range;
+  const Row R = long_row(P, r, red, range);
+  if (R.st != TS_ROW_OK) return;
+  const Cut cut{I.cut_u, I.cut_slot};
+  const bool af = I.among_first != 0;
+  uint32_t kept = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool f = R.first(q.p[i]);
+    const bool in = q.j + i < n && (f != af ? f : cut.keeps(R.u(q.s[i]), q.j + i));
+    kept |= (in ? 1u : 0u) << i;
+  }
+  uint64_t mh[4], mf[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    mh[i] = __ballot(q.j + i < R.k && !((kept >> i) & 1u));
+    mf[i] = __ballot(q.j + i >= R.k && ((kept >> i) & 1u));
+  }
+  if (lane() == 0) {
+    red[2 * wave()] = count4(mh);
+    red[2 * wave() + 1] = count4(mf);
+  }
+  bar();
+  uint32_t ih = 0, jf = 0, holes = 0, fills = 0;
+#pragma unroll
+  for (int w = 0; w < kSW; ++w) {
+    ih += w < wave() ? red[2 * w] : 0u;
+    jf += w < wave() ? red[2 * w + 1] : 0u;
+    holes += red[2 * w];
+    fills += red[2 * w + 1];
+  }
+  const int64_t at = (int64_t)r * P.sum_stride + (int64_t)tile * kSumTile;
+  int32_t* source = P.out_source + (int64_t)r * P.keep_max;
+  float* score = P.out_score + (int64_t)r * P.out_score_stride;
+  int32_t* place = P.out_position + (int64_t)r * P.out_position_stride;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int j = q.j + i;
+    const bool in = (kept >> i) & 1u;
+    if (j < R.k) {
+      if (in) {
+        source[j] = j;
+        score[j] = q.s[i];
+        if (P.out_position != P.position) place[j] = q.p[i];
+      } else {
+        P.hole[at + ih + rank4(mh, i)] = j;
+      }
+    } else if (in) {
+      const uint32_t o = jf + rank4(mf, i);
+      P.fill[at + o] = j;
+      P.fill_position[at + o] = q.p[i];
+    }
+  }
+  if (threadIdx.x == 0) {
+    P.bin[(int64_t)r * P.tiles + tile].holes = holes;
+    P.bin[(int64_t)r * P.tiles + tile].fills = fills;
+  }
+}
+
+template <class U>
+__global__ __launch_bounds__(kMT) void ts_evict_move_kernel(EParams P, int blocks) {
+  const int r = (int)(blockIdx.x / (unsigned)blocks);
+  const int64_t i0 = (int64_t)(blockIdx.x - (unsigned)r * (unsigned)blocks) * kMT + threadIdx.x;
+  const int64_t n = P.moves[r], step = (int64_t)blocks * kMT;
+  const int32_t* hole = P.hole + (int64_t)r * P.cap;
+  const int32_t* fill = P.fill + (int64_t)r * P.cap;
+  if (P.k.units) copy_units<U>(P.k, r, P.heads, hole, fill, n, i0, step);
+  if (P.v.units) copy_units<U>(P.v, r, P.heads, hole, fill, n, i0, step);
+}
+
+// Long rows: a workgroup takes a share (one of `parts`) of a tile's freed slots. Their ranks among the row's freed slots
+// are those of their fillers among the row's fillers, which are found by the running count of the tiles' fillers.
+template <class U>
+__global__ __launch_bounds__(kMT) void ts_evict_long_move_kernel(EParams P, int hole_tiles, int parts) {
+  __shared__ uint32_t red[kMT / 64];
+  __shared__ uint32_t start[kMaxTiles + 1];     // fillers before each tile
+  __shared__ uint32_t before;                   // freed slots before this workgroup's tile
+  __shared__ int32_t to[kSumTile], from[kSumTile];
+  const unsigned per = (unsigned)hole_tiles * (unsigned)parts;
+  const int r = (int)(blockIdx.x / per), t = (int)threadIdx.x;
+  const unsigned rest = blockIdx.x - (unsigned)r * per;
+  const int tile = (int)(rest / (unsigned)parts), part = (int)(rest - (unsigned)tile * (unsigned)parts);
+  const RowInfo I = P.row[r];
+  if (I.st != TS_ROW_OK) return;
+  int32_t* source = P.out_source + (int64_t)r * P.keep_max;
+  float* score = P.out_score + (int64_t)r * P.out_score_stride;
+  int32_t* place = P.out_position + (int64_t)r * P.out_position_stride;
+  for (int j = max(I.k, tile * kSumTile) + part * kMT + t; j < min(P.keep_max, (tile + 1) * kSumTile); j += parts * kMT) {
+    source[j] = -1;
+    score[j] = 0.0f;
+    place[j] = -1;
+  }
+  if (tile == 0 && part == 0 && t == 0) {
+    P.out_lengths[r] = I.k;
+    if (P.status) P.status[r] = TS_ROW_OK;
+  }
+  if (tile * kSumTile >= I.k) return;
+  const TileBin* bin = P.bin + (int64_t)r * P.tiles;
+  const uint32_t mine = bin[tile].holes;
+  const uint32_t lo = (uint32_t)((uint64_t)mine * part / parts), hi = (uint32_t)((uint64_t)mine * (part + 1) / parts);
+  if (lo == hi) return;
+  const int own = (I.tiles + kMT - 1) / kMT;     // consecutive tiles a thread
+  uint32_t fills = 0, holes = 0;
+  for (int i = t * own; i < min(I.tiles, (t + 1) * own); ++i) {
+    fills += bin[i].fills;
+    holes += i < tile ? bin[i].holes : 0u;
+  }
+  uint32_t total;
+  const uint32_t h = block_excl_scan<kMT / 64>(holes, red, total);
+  (void)h;
+  if (t == 0) before = total;
+  uint32_t f = block_excl_scan<kMT / 64>(fills, red, total);
+  for (int i = t * own; i < min(I.tiles, (t + 1) * own); ++i) {
+    start[i] = f;
+    f += bin[i].fills;
+  }
+  if (t == 0) start[I.tiles] = total;
+  bar();
+  const int64_t base = (int64_t)r * P.sum_stride;
+  for (uint32_t i = lo + t; i < hi; i += kMT) {
+    const uint32_t rank = before + i;
+    int x = 0, y = I.tiles;                     // the last tile whose start is at most rank
+    while (y - x > 1) {
+      const int m = (x + y) >> 1;
+      if (start[m] <= rank) x = m;
+      else y = m;
+    }
+    const int64_t at = base + (int64_t)x * kSumTile + (rank - start[x]);
+    const int32_t src = P.fill[at], dst = P.hole[base + (int64_t)tile * kSumTile + i];
+    to[i - lo] = dst;
+    from[i - lo] = src;
+    source[dst] = src;
+    score[dst] = P.sum[base + src];
+    place[dst] = P.fill_position[at];
+  }
+  bar();
+  if (P.k.units) copy_units<U>(P.k, r, P.heads, to, from, hi - lo, t, kMT);
+  if (P.v.units) copy_units<U>(P.v, r, P.heads, to, from, hi - lo, t, kMT);
+}
+
 // ------------------------------------------------------------------ host side
 struct EPlan {
-  int64_t cap = 0;
-  size_t off_moves = 0, off_hole = 0, off_fill = 0, total = 0;
+  int64_t cap = 0, sum_stride = 0, tiles = 0;
+  size_t off_info = 0, off_row = 0, off_bin = 0, off_hist = 0, off_list = 0, off_moves = 0, off_hole = 0, off_fill = 0,
+         off_fill_position = 0, total = 0;
 };
 bool evict_plan(int64_t rows, int64_t slots, int64_t keep_max, EPlan& pl) {
-  if (rows < 0 || slots < 1 || slots > TS_MAX_VOCAB || keep_max < 1 || keep_max > TS_MAX_VOCAB) return false;
-  if (rows > 0x7FFFFF) return false;
+  if (rows < 0 || slots < 1 || slots > TS_EVICT_MAX_SLOTS || keep_max < 1 || keep_max > TS_EVICT_MAX_SLOTS) return false;
+  pl.tiles = (slots + kSumTile - 1) / kSumTile;
+  // a launch holds at most 2^32 - 1 threads
+  if (rows > (int64_t)0xFFFFFFFF / kET || rows * pl.tiles > (int64_t)0xFFFFFFFF / kST ||
+      rows * ((keep_max + kSumTile - 1) / kSumTile) > (int64_t)0xFFFFFFFF / kMT)
+    return false;
   // a row moves at most min(k, n - k) positions
   pl.cap = std::min(keep_max, std::max<int64_t>(slots / 2, 1));
-  const size_t rr = (size_t)std::max<int64_t>(rows, 1);
-  auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
-  size_t b = up(rr * (size_t)slots * 4);
-  pl.off_moves = b;
-  b += up(rr * 4);
-  pl.off_hole = b;
-  b += up(rr * (size_t)pl.cap * 4);
-  pl.off_fill = b;
-  b += up(rr * (size_t)pl.cap * 4);
+  pl.sum_stride = pl.tiles * kSumTile;
+  const bool spread = slots > kRowSlots;
+  const size_t rr = (size_t)std::max<int64_t>(rows, 1), listed = rr * (size_t)(spread ? pl.sum_stride : pl.cap) * 4;
+  size_t b = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = b;
+    b += (bytes + 255) & ~(size_t)255;
+    return at;
+  };
+  take(rr * (size_t)pl.sum_stride * 4);
+  pl.off_moves = take(rr * 4);
+  pl.off_hole = take(listed);
+  pl.off_fill = take(listed);
+  if (spread) {
+    pl.off_fill_position = take(listed);
+    pl.off_info = take(rr * (size_t)pl.tiles * sizeof(TileInfo));
+    pl.off_bin = take(rr * (size_t)pl.tiles * sizeof(TileBin));
+    pl.off_row = take(rr * sizeof(RowInfo));
+    pl.off_hist = take(rr * 2 * kEBins * 4);
+    pl.off_list = take(rr * kListLong * sizeof(uint2));
+  }
   pl.total = b;
   return true;
 }
@@ -320,27 +1046,50 @@ int dtype_size(int dtype) {
   return dtype == TS_DTYPE_F32 ? 4 : (dtype == TS_DTYPE_BF16 || dtype == TS_DTYPE_F16) ? 2 : 0;
 }
 
-template <class U>
-void launch_move(const EParams& P, const Cache& C, int heads, int64_t blocks, hipStream_t s) {
-  hipLaunchKernelGGL(ts_evict_move_kernel<U>, dim3((unsigned)(P.rows * blocks)), dim3(kMT), 0, s, P, C, heads, (int)blocks);
+// The widest unit that divides every address of the caches.
+int copy_unit(const ts_cache* k, const ts_cache* v) {
+  uint64_t all = 16;
+  for (const ts_cache* c : {k, v})
+    if (c)
+      all |= (uint64_t)(uintptr_t)c->data | (uint64_t)c->batch_stride | (uint64_t)c->head_stride | (uint64_t)c->slot_stride |
+             (uint64_t)c->slot_bytes;
+  return (int)(all & (~all + 1));
+}
+Cache cache_of(const ts_cache* c, int unit) {
+  return c ? Cache{static_cast<char*>(c->data), c->batch_stride, c->head_stride, c->slot_stride, (int32_t)(c->slot_bytes / unit)}
+           : Cache{nullptr, 0, 0, 0, 0};
+}
+// f(U) with the unit's type
+template <class F>
+void with_unit(int unit, F f) {
+  switch (unit) {
+    case 1: f(uint8_t{}); break;
+    case 2: f(uint16_t{}); break;
+    case 4: f(uint32_t{}); break;
+    case 8: f(uint2{}); break;
+    default: f(uint4{}); break;
+  }
 }
 
-hipError_t move_cache(const EParams& P, const ts_cache& c, int heads, hipStream_t s) {
-  // the widest unit that divides every address
-  const uint64_t all = (uint64_t)(uintptr_t)c.data | (uint64_t)c.batch_stride | (uint64_t)c.head_stride |
-                       (uint64_t)c.slot_stride | (uint64_t)c.slot_bytes;
-  const int unit = (all & 1) ? 1 : (all & 2) ? 2 : (all & 4) ? 4 : (all & 8) ? 8 : 16;
-  Cache C{static_cast<char*>(c.data), c.batch_stride, c.head_stride, c.slot_stride, (int32_t)(c.slot_bytes / unit)};
-  const int64_t most = (int64_t)P.cap * C.units;
-  int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((most + kMT - 1) / kMT, std::max<int64_t>(1, 4096 / P.rows)));
-  switch (unit) {
-    case 1: launch_move<uint8_t>(P, C, heads, blocks, s); break;
-    case 2: launch_move<uint16_t>(P, C, heads, blocks, s); break;
-    case 4: launch_move<uint32_t>(P, C, heads, blocks, s); break;
-    case 8: launch_move<uint2>(P, C, heads, blocks, s); break;
-    default: launch_move<uint4>(P, C, heads, blocks, s); break;
-  }
-  return hipGetLastError();
+// Where a row is summed, selected and moved by one workgroup: what a launch costs against what one compute unit
+// reads and copies alone.
+constexpr int64_t kFusedBytes = 128 << 10;   // weights of a row
+constexpr int64_t kFusedMoves = 256 << 10;   // cache bytes that a row can move
+
+constexpr int64_t kMoveGroups = 2048;        // workgroups that the moves of long rows are spread over, about,
+constexpr int64_t kMoveParts = 32;           // and at most so many to a tile's
+
+template <int SRC>
+void launch_rows(const EParams& P, hipStream_t s) {
+  const dim3 grid((unsigned)P.rows), block(kET);
+  if (P.slots <= 4 * kET) hipLaunchKernelGGL((ts_evict_row_kernel<1, SRC, void>), grid, block, 0, s, P);
+  else hipLaunchKernelGGL((ts_evict_row_kernel<2, SRC, void>), grid, block, 0, s, P);
+}
+template <int SRC, class U>
+void launch_whole(const EParams& P, hipStream_t s) {
+  const dim3 grid((unsigned)P.rows), block(kET);
+  if (P.slots <= 4 * kET) hipLaunchKernelGGL((ts_evict_row_kernel<1, SRC, U>), grid, block, 0, s, P);
+  else hipLaunchKernelGGL((ts_evict_row_kernel<2, SRC, U>), grid, block, 0, s, P);
 }
 
 int check_cache(const ts_cache* c, const char* name) {
@@ -373,11 +1122,12 @@ extern "C" int ts_cache_evict(const float* score, int64_t rows, int64_t slots, i
                               const ts_cache* v_cache, int64_t heads, void* workspace, size_t workspace_bytes,
                               void* stream) {
   if (rows < 0) return fail(TS_ERR_INVALID_ARG, "rows = %lld < 0", (long long)rows);
-  if (slots < 1 || slots > TS_MAX_VOCAB) return fail(TS_ERR_INVALID_ARG, "slots = %lld outside [1, 2^30]", (long long)slots);
+  if (slots < 1 || slots > TS_EVICT_MAX_SLOTS) return fail(TS_ERR_INVALID_ARG, "slots = %lld outside [1, 2^22]", (long long)slots);
   if (score_stride < slots || position_stride < slots)
     return fail(TS_ERR_INVALID_ARG, "score_stride %lld or position_stride %lld < slots %lld", (long long)score_stride,
                 (long long)position_stride, (long long)slots);
-  if (keep_max < 1 || keep_max > TS_MAX_VOCAB) return fail(TS_ERR_INVALID_ARG, "keep_max = %d outside [1, 2^30]", (int)keep_max);
+  if (keep_max < 1 || keep_max > TS_EVICT_MAX_SLOTS)
+    return fail(TS_ERR_INVALID_ARG, "keep_max = %d outside [1, 2^22]", (int)keep_max);
   if (out_score_stride < keep_max || out_position_stride < keep_max)
     return fail(TS_ERR_INVALID_ARG, "out_score_stride %lld or out_position_stride %lld < keep_max %d",
                 (long long)out_score_stride, (long long)out_position_stride, (int)keep_max);
@@ -402,9 +1152,7 @@ extern "C" int ts_cache_evict(const float* score, int64_t rows, int64_t slots, i
   if (rc == TS_OK) rc = check_cache(v_cache, "v_cache");
   if (rc != TS_OK) return rc;
   EPlan pl;
-  if (!evict_plan(rows, slots, keep_max, pl)) return fail(TS_ERR_INVALID_ARG, "rows too large");
-  const int64_t per = (slots + kST * kSumSlots - 1) / (kST * kSumSlots);
-  if (rows * per > (int64_t)0xFFFFFFFF / kST) return fail(TS_ERR_INVALID_ARG, "rows x slots too large");
+  if (!evict_plan(rows, slots, keep_max, pl)) return fail(TS_ERR_INVALID_ARG, "rows x slots too large");
   if (!workspace) return fail(TS_ERR_WORKSPACE, "workspace is NULL");
   if (((uintptr_t)workspace & 255u) != 0) return fail(TS_ERR_WORKSPACE, "workspace is not 256-byte aligned");
   if (workspace_bytes < pl.total)
@@ -439,23 +1187,70 @@ extern "C" int ts_cache_evict(const float* score, int64_t rows, int64_t slots, i
   P.out_source = out_source;
   P.status = row_status;
   P.sum = reinterpret_cast<float*>(ws);
+  P.sum_stride = pl.sum_stride;
+  P.info = reinterpret_cast<TileInfo*>(ws + pl.off_info);
+  P.row = reinterpret_cast<RowInfo*>(ws + pl.off_row);
+  P.bin = reinterpret_cast<TileBin*>(ws + pl.off_bin);
+  P.hist = reinterpret_cast<uint32_t*>(ws + pl.off_hist);
+  P.list = reinterpret_cast<uint2*>(ws + pl.off_list);
+  P.fill_position = reinterpret_cast<int32_t*>(ws + pl.off_fill_position);
+  P.tiles = (int32_t)pl.tiles;
   P.moves = reinterpret_cast<int32_t*>(ws + pl.off_moves);
   P.hole = reinterpret_cast<int32_t*>(ws + pl.off_hole);
   P.fill = reinterpret_cast<int32_t*>(ws + pl.off_fill);
   P.cap = (int32_t)pl.cap;
+  const int unit = copy_unit(k_cache, v_cache);
+  P.k = cache_of(k_cache, unit);
+  P.v = cache_of(v_cache, unit);
+  P.heads = (int32_t)heads;
   const hipStream_t s = (hipStream_t)stream;
-  const dim3 grid((unsigned)(rows * per)), block(kST);
-  if (n_weights == 0 || weights_dtype == TS_DTYPE_F32) hipLaunchKernelGGL(ts_evict_sum_kernel<TS_DTYPE_F32>, grid, block, 0, s, P, (int)per);
-  else if (weights_dtype == TS_DTYPE_BF16) hipLaunchKernelGGL(ts_evict_sum_kernel<TS_DTYPE_BF16>, grid, block, 0, s, P, (int)per);
-  else hipLaunchKernelGGL(ts_evict_sum_kernel<TS_DTYPE_F16>, grid, block, 0, s, P, (int)per);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return fail(TS_ERR_LAUNCH, "eviction sum launch failed: %s", hipGetErrorString(e));
-  hipLaunchKernelGGL(ts_evict_select_kernel, dim3((unsigned)rows), dim3(kET), 0, s, P);
+  const int type = n_weights ? weights_dtype : TS_DTYPE_F32;
+  const bool sum_here = slots <= kRowSlots && slots * n_weights * size <= kFusedBytes;
+  const int64_t slot_bytes = (k_cache ? k_cache->slot_bytes : 0) + (v_cache ? v_cache->slot_bytes : 0);
+  const bool move_here = sum_here && pl.cap * slot_bytes <= kFusedMoves;
+  auto with_type = [&](auto f) {
+    if (type == TS_DTYPE_F32) f(std::integral_constant<int, TS_DTYPE_F32>{});
+    else if (type == TS_DTYPE_BF16) f(std::integral_constant<int, TS_DTYPE_BF16>{});
+    else f(std::integral_constant<int, TS_DTYPE_F16>{});
+  };
+  hipError_t e;
+  if (move_here) {
+    with_type([&](auto dt) { with_unit(unit, [&](auto u) { launch_whole<dt(), decltype(u)>(P, s); }); });
+    e = hipGetLastError();
+    return e == hipSuccess ? TS_OK : fail(TS_ERR_LAUNCH, "eviction launch failed: %s", hipGetErrorString(e));
+  }
+  if (sum_here) {
+    with_type([&](auto dt) { launch_rows<dt()>(P, s); });
+  } else {
+    const dim3 grid((unsigned)(rows * pl.tiles)), block(kST);
+    with_type([&](auto dt) { hipLaunchKernelGGL(ts_evict_sum_kernel<dt()>, grid, block, 0, s, P); });
+    e = hipGetLastError();
+    if (e != hipSuccess) return fail(TS_ERR_LAUNCH, "eviction sum launch failed: %s", hipGetErrorString(e));
+    if (slots > kRowSlots) {
+      hipLaunchKernelGGL(ts_evict_bin_kernel, grid, block, 0, s, P);
+      hipLaunchKernelGGL(ts_evict_list_kernel, grid, block, 0, s, P);
+      hipLaunchKernelGGL(ts_evict_cut_kernel, dim3((unsigned)rows), dim3(kET), 0, s, P);
+      hipLaunchKernelGGL(ts_evict_emit_kernel, grid, block, 0, s, P);
+      const int64_t hole_tiles = (keep_max + kSumTile - 1) / kSumTile;
+      const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(kMoveParts, kMoveGroups / (rows * hole_tiles)));
+      with_unit(unit, [&](auto u) {
+        hipLaunchKernelGGL(ts_evict_long_move_kernel<decltype(u)>, dim3((unsigned)(rows * hole_tiles * parts)), dim3(kMT), 0, s, P,
+                           (int)hole_tiles, (int)parts);
+      });
+      e = hipGetLastError();
+      return e == hipSuccess ? TS_OK : fail(TS_ERR_LAUNCH, "eviction launch failed: %s", hipGetErrorString(e));
+    }
+    launch_rows<-1>(P, s);
+  }
   e = hipGetLastError();
-  if (e != hipSuccess) return fail(TS_ERR_LAUNCH, "eviction select launch failed: %s", hipGetErrorString(e));
-  for (const ts_cache* c : {k_cache, v_cache}) {
-    if (!c) continue;
-    e = move_cache(P, *c, (int)heads, s);
+  if (e != hipSuccess) return fail(TS_ERR_LAUNCH, "eviction row launch failed: %s", hipGetErrorString(e));
+  if (slot_bytes) {
+    const int64_t most = pl.cap * std::max(P.k.units, P.v.units);
+    const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((most + kMT - 1) / kMT, 4096 / rows));
+    with_unit(unit, [&](auto u) {
+      hipLaunchKernelGGL(ts_evict_move_kernel<decltype(u)>, dim3((unsigned)(rows * blocks)), dim3(kMT), 0, s, P, (int)blocks);
+    });
+    e = hipGetLastError();
     if (e != hipSuccess) return fail(TS_ERR_LAUNCH, "eviction move launch failed: %s", hipGetErrorString(e));
   }
   return TS_OK;
