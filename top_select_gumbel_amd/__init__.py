@@ -354,44 +354,52 @@ def ts_sample_rows_rejection(logits, top_k, top_p, temperature, min_p, seed, max
     return tok, rnd, st
 
 
-_DTYPES = {"torch.float32": 0, "torch.bfloat16": 1, "torch.float16": 2}
+_torch = None
+_DTYPES = {}
+
+
+def _t():
+    """torch, with the element types' codes filled in (looked up once: these calls are made every step)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _DTYPES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+        _torch = torch
+    return _torch
 
 
 def _typed_rows(x, name: str):
     """(dtype code, rows, columns, row stride) of a 2-D fp32, bf16 or fp16 device tensor."""
-    code = _DTYPES.get(str(x.dtype))
+    code = _DTYPES.get(x.dtype)
     if code is None or not x.is_cuda:
         raise TopSelectError(f"{name} must be a float32, bfloat16 or float16 CUDA/HIP tensor")
-    if x.dim() != 2 or (x.shape[0] and x.shape[1] > 1 and x.stride(1) != 1):
+    if x.dim() != 2:
         raise TopSelectError(f"{name} must be a 2-D tensor with unit column stride")
-    if x.shape[0] <= 1:      # a single row's stride carries no layout
-        return code, x.shape[0], x.shape[1], max(x.shape[1], 1)
-    return code, x.shape[0], x.shape[1], x.stride(0)
+    rows, cols = x.shape
+    row_stride, col_stride = x.stride()
+    if rows and cols > 1 and col_stride != 1:
+        raise TopSelectError(f"{name} must be a 2-D tensor with unit column stride")
+    return code, rows, cols, row_stride if rows > 1 else max(cols, 1)   # a single row's stride carries no layout
 
 
-def _param(t, dtype_name: str, rows: int, device, name: str):
+def _param(t, dtype, rows: int, device, name: str):
     """Pointer of an optional contiguous per-row parameter on `device`."""
     if t is None:
         return None
-    if str(t.dtype) != dtype_name or t.device != device or t.numel() != rows or not t.is_contiguous():
-        raise TopSelectError(f"{name} must be a contiguous {dtype_name} tensor of {rows} on {device}")
+    if t.dtype is not dtype or t.device != device or t.numel() != rows or not t.is_contiguous():
+        raise TopSelectError(f"{name} must be a contiguous {dtype} tensor of {rows} on {device}")
     return t.data_ptr()
 
 
-class _on:
-    """Makes a tensor's device current for a call (its current stream is the call's)."""
-
-    def __init__(self, device):
-        import torch
-        self._guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+def _call(device, f, *args):
+    """f(*args, stream) on the device's current stream with the device current, checked."""
+    torch = _torch
+    index = device.index
+    if index == torch._C._cuda_getDevice():
+        _check(f(*args, torch._C._cuda_getCurrentRawStream(index)))
+    else:
+        with torch.cuda.device(device):
+            _check(f(*args, torch._C._cuda_getCurrentRawStream(index)))
 
 
 class TokenLogp(NamedTuple):
@@ -410,44 +418,51 @@ def ts_token_logp(logits, tokens=None, temperature=None, n_top: int = 0, want_ra
                   want_entropy: bool = True, want_lse: bool = True, want_stats: bool = False) -> TokenLogp:
     """Log probabilities and ranks of given tokens (int32 [rows], -1: none) over whole rows of fp32, bf16
     or fp16 logits, with entropy, log-sum-exp and the n_top best tokens."""
-    import torch
+    torch = _t()
     lib = load_library()
     code, rows, v, stride = _typed_rows(logits, "logits")
     device = logits.device
-    tok, temp = _param(tokens, "torch.int32", rows, device, "tokens"), _param(temperature, "torch.float32", rows, device, "temperature")
-    with _on(device):
-        def new(want, shape, dtype=torch.float32):
-            return torch.empty(shape, dtype=dtype, device=device) if want else None
-        out = TokenLogp(new(tokens is not None, rows), new(tokens is not None and want_rank, rows, torch.int32),
-                        new(want_entropy, rows), new(want_lse, rows), new(n_top > 0, (rows, n_top), torch.int32),
-                        new(n_top > 0, (rows, n_top)), new(want_stats, (rows, 4)), new(True, rows, torch.int32))
-        # A workspace of the call's own: two calls captured into graphs that replay at once share none.
-        nb = 0 if v <= TS_LOGP_TILE else lib.ts_workspace_bytes(TS_OP_TOKEN_LOGP, rows, v, n_top)
-        ws = torch.empty(nb, dtype=torch.uint8, device=device) if nb else None
-        _check(lib.ts_token_logp(_ptr(logits), code, rows, v, stride, tok, temp, n_top, _ptr(out.logp), _ptr(out.rank),
-                                 _ptr(out.entropy), _ptr(out.lse), _ptr(out.top_idx), _ptr(out.top_logp),
-                                 _ptr(out.stats), _ptr(out.status), _ptr(ws), nb, _stream()))
-    return out
+    tok = _param(tokens, torch.int32, rows, device, "tokens")
+    temp = _param(temperature, torch.float32, rows, device, "temperature")
+    f, i = torch.float32, torch.int32
+    empty = torch.empty
+    logp = empty(rows, dtype=f, device=device) if tokens is not None else None
+    rank = empty(rows, dtype=i, device=device) if tokens is not None and want_rank else None
+    entropy = empty(rows, dtype=f, device=device) if want_entropy else None
+    lse = empty(rows, dtype=f, device=device) if want_lse else None
+    top_idx = empty((rows, n_top), dtype=i, device=device) if n_top > 0 else None
+    top_logp = empty((rows, n_top), dtype=f, device=device) if n_top > 0 else None
+    stats = empty((rows, 4), dtype=f, device=device) if want_stats else None
+    status = empty(rows, dtype=i, device=device)
+    # A workspace of the call's own: two calls captured into graphs that replay at once share none.
+    nb = 0 if v <= TS_LOGP_TILE else lib.ts_workspace_bytes(TS_OP_TOKEN_LOGP, rows, v, n_top)
+    ws = empty(nb, dtype=torch.uint8, device=device) if nb else None
+    _call(device, lib.ts_token_logp, logits.data_ptr(), code, rows, v, stride, tok, temp, n_top, _ptr(logp), _ptr(rank),
+          _ptr(entropy), _ptr(lse), _ptr(top_idx), _ptr(top_logp), _ptr(stats), status.data_ptr(), _ptr(ws), nb)
+    return TokenLogp(logp, rank, entropy, lse, top_idx, top_logp, stats, status)
 
 
 def ts_token_logp_backward(logits, tokens, temperature, stats, grad_logp=None, grad_entropy=None, grad_lse=None, out=None):
     """Gradient of sum(grad_logp * logp + grad_entropy * entropy + grad_lse * lse) with respect to the logits, in
     their type. stats: the forward call's (want_stats). out: a tensor for it; the logits themselves are allowed."""
-    import torch
+    torch = _t()
     lib = load_library()
     code, rows, v, stride = _typed_rows(logits, "logits")
-    device = logits.device
-    tok, temp = _param(tokens, "torch.int32", rows, device, "tokens"), _param(temperature, "torch.float32", rows, device, "temperature")
-    st = _param(stats, "torch.float32", 4 * rows, device, "stats")
-    grads = [_param(g, "torch.float32", rows, device, n)
-             for g, n in ((grad_logp, "grad_logp"), (grad_entropy, "grad_entropy"), (grad_lse, "grad_lse"))]
-    with _on(device):
-        if out is None:
-            out = torch.empty((rows, v), dtype=logits.dtype, device=device)
+    device, f = logits.device, torch.float32
+    tok = _param(tokens, torch.int32, rows, device, "tokens")
+    temp = _param(temperature, f, rows, device, "temperature")
+    st = _param(stats, f, 4 * rows, device, "stats")
+    ga = _param(grad_logp, f, rows, device, "grad_logp")
+    gh = _param(grad_entropy, f, rows, device, "grad_entropy")
+    gl = _param(grad_lse, f, rows, device, "grad_lse")
+    if out is None:
+        out, ostride = torch.empty((rows, v), dtype=logits.dtype, device=device), max(v, 1)
+    else:
         ocode, orows, ov, ostride = _typed_rows(out, "out")
         if (ocode, orows, ov) != (code, rows, v) or out.device != device:
             raise TopSelectError("out must have the logits' shape, type and device")
-        _check(lib.ts_token_logp_backward(_ptr(logits), code, rows, v, stride, tok, temp, st, *grads, _ptr(out), ostride, _stream()))
+    _call(device, lib.ts_token_logp_backward, logits.data_ptr(), code, rows, v, stride, tok, temp, st, ga, gh, gl,
+          out.data_ptr(), ostride)
     return out
 
 
@@ -456,22 +471,27 @@ class _Cache(ctypes.Structure):
 
 
 def _cache(t, rows: int, slots: int, device, name: str):
-    """The ts_cache of a [batch, heads, slots, dim] tensor whose last dimension is contiguous."""
+    """The ts_cache of a [batch, heads, slots, dim] tensor whose last dimension is contiguous, and its heads."""
     if t is None:
         return None, 1
-    if t.dim() != 4 or t.shape[0] * t.shape[1] != rows or t.shape[2] != slots or t.device != device:
+    if t.dim() != 4 or t.device != device:
+        raise TopSelectError(f"{name} must be a [batch, heads, {slots}, dim] tensor on {device}")
+    (nb, nh, ns, dim), (b, h, s, d) = t.shape, t.stride()
+    if nb * nh != rows or ns != slots:
         raise TopSelectError(f"{name} must be a [batch, heads, {slots}, dim] tensor on {device} with batch * heads = {rows}")
-    size, dim = t.element_size(), t.shape[3]
-    if dim < 1 or (dim > 1 and t.stride(3) != 1):
+    size = t.element_size()
+    if dim < 1 or (dim > 1 and d != 1):
         raise TopSelectError(f"{name} must have a contiguous last dimension")
-    b, h, s = (t.stride(i) if t.shape[i] > 1 else 0 for i in range(3))
-    # no two slots may share memory: along the ascending strides each must clear what lies below it
-    reach = dim
-    for stride, n in sorted((x, n) for x, n in zip((b, h, s), t.shape[:3]) if n > 1):
-        if stride < reach:
-            raise TopSelectError(f"{name} has slots that share memory")
-        reach = stride * (n - 1) + reach
-    return _Cache(t.data_ptr(), b * size, h * size, max(s, dim) * size, dim * size), t.shape[1]
+    if not t.is_contiguous():
+        # no two slots may share memory: along the ascending strides each must clear what lies below it
+        reach = dim
+        for stride, n in sorted(((b, nb), (h, nh), (s, ns))):
+            if n > 1:
+                if stride < reach:
+                    raise TopSelectError(f"{name} has slots that share memory")
+                reach += stride * (n - 1)
+    return _Cache(t.data_ptr(), b * size if nb > 1 else 0, h * size if nh > 1 else 0, max(s if ns > 1 else 0, dim) * size,
+                  dim * size), nh
 
 
 class CacheEvict(NamedTuple):
@@ -490,53 +510,52 @@ def ts_cache_evict(score, position, lengths, keep, keep_max: int, weights=None, 
     score fp32 [rows, slots], position int32 [rows, slots], lengths and keep int32 [rows]; weights [rows, n, slots] (fp32,
     bf16 or fp16) is this step's attention, added first. k_cache, v_cache [batch, heads, slots, dim] with batch * heads =
     rows are changed in place. in_place: score, position and lengths are updated too; else new tensors are returned."""
-    import torch
+    torch = _t()
     lib = load_library()
-    device = score.device
-    if str(score.dtype) != "torch.float32":
+    device, f, i = score.device, torch.float32, torch.int32
+    if score.dtype is not f:
         raise TopSelectError("score must be a float32 CUDA/HIP tensor")
     _, rows, slots, score_stride = _typed_rows(score, "score")
-    if (str(position.dtype) != "torch.int32" or position.shape != score.shape or position.device != device
+    if (position.dtype is not i or position.shape != score.shape or position.device != device
             or (rows and slots > 1 and position.stride(1) != 1)):
         raise TopSelectError(f"position must be an int32 [{rows}, {slots}] tensor with unit column stride on {device}")
-    position_stride = max(position.stride(0) if rows > 1 else slots, 1)
-    plen, pkeep = _param(lengths, "torch.int32", rows, device, "lengths"), _param(keep, "torch.int32", rows, device, "keep")
+    position_stride = position.stride(0) if rows > 1 else max(slots, 1)
+    plen, pkeep = _param(lengths, i, rows, device, "lengths"), _param(keep, i, rows, device, "keep")
     if plen is None or pkeep is None:
         raise TopSelectError("lengths and keep are required")
-    wcode, n_w, w_row, w_stride = 0, 0, 0, slots
+    wcode, n_w, w_row, w_stride, pw = 0, 0, 0, slots, None
     if weights is not None:
-        wcode = _DTYPES.get(str(weights.dtype))
-        if wcode is None or weights.dim() != 3 or weights.shape[0] != rows or weights.shape[2] != slots or weights.device != device:
+        wcode = _DTYPES.get(weights.dtype)
+        if wcode is None or weights.dim() != 3 or weights.device != device:
             raise TopSelectError(f"weights must be a float32, bfloat16 or float16 [{rows}, n, {slots}] tensor on {device}")
-        if weights.numel() and slots > 1 and weights.stride(2) != 1:
-            raise TopSelectError("weights must have a contiguous last dimension")
-        n_w = weights.shape[1]
-        w_row, w_stride = (weights.stride(0) if rows > 1 else 0), (weights.stride(1) if n_w > 1 else slots)
+        (wr, n_w, wslots), (w_row, w_stride, w_unit) = weights.shape, weights.stride()
+        if wr != rows or wslots != slots or (rows and n_w and slots > 1 and w_unit != 1):
+            raise TopSelectError(f"weights must be [{rows}, n, {slots}] with a contiguous last dimension")
+        pw = weights.data_ptr() if n_w else None
     kc, k_heads = _cache(k_cache, rows, slots, device, "k_cache")
     vc, v_heads = _cache(v_cache, rows, slots, device, "v_cache")
     if kc and vc and k_heads != v_heads:
         raise TopSelectError("k_cache and v_cache have different heads")
-    heads = k_heads if kc else v_heads
-    with _on(device):
-        if in_place:
-            if keep_max > slots:
-                raise TopSelectError("in place, keep_max is at most the number of slots")
-            out_score, out_position, out_lengths = score, position, lengths
-            os, op = score_stride, position_stride
-        else:
-            out_score = torch.empty((rows, keep_max), dtype=torch.float32, device=device)
-            out_position = torch.empty((rows, keep_max), dtype=torch.int32, device=device)
-            out_lengths = torch.empty(rows, dtype=torch.int32, device=device)
-            os = op = max(keep_max, 1)
-        source = torch.empty((rows, keep_max), dtype=torch.int32, device=device)
-        status = torch.empty(rows, dtype=torch.int32, device=device)
-        nb = lib.ts_workspace_bytes(TS_OP_CACHE_EVICT, rows, slots, keep_max)
-        ws = torch.empty(nb, dtype=torch.uint8, device=device)
-        _check(lib.ts_cache_evict(_ptr(score), rows, slots, score_stride, _ptr(position), position_stride, plen, pkeep, keep_max,
-                                  _ptr(weights) if n_w else None, wcode, n_w, w_row, w_stride, sinks, recent, _ptr(out_score), os,
-                                  _ptr(out_position), op, _ptr(out_lengths), _ptr(source), _ptr(status),
-                                  ctypes.byref(kc) if kc else None, ctypes.byref(vc) if vc else None, heads, _ptr(ws), nb,
-                                  _stream()))
+    empty = torch.empty
+    if in_place:
+        if keep_max > slots:
+            raise TopSelectError("in place, keep_max is at most the number of slots")
+        out_score, out_position, out_lengths = score, position, lengths
+        os, op = score_stride, position_stride
+    else:
+        out_score = empty((rows, keep_max), dtype=f, device=device)
+        out_position = empty((rows, keep_max), dtype=i, device=device)
+        out_lengths = empty(rows, dtype=i, device=device)
+        os = op = max(keep_max, 1)
+    source = empty((rows, keep_max), dtype=i, device=device)
+    status = empty(rows, dtype=i, device=device)
+    # a workspace of the call's own, as in ts_token_logp
+    nb = lib.ts_workspace_bytes(TS_OP_CACHE_EVICT, rows, slots, keep_max)
+    ws = empty(nb, dtype=torch.uint8, device=device)
+    _call(device, lib.ts_cache_evict, score.data_ptr(), rows, slots, score_stride, position.data_ptr(), position_stride, plen, pkeep,
+          keep_max, pw, wcode, n_w, w_row, w_stride, sinks, recent, out_score.data_ptr(), os, out_position.data_ptr(), op,
+          out_lengths.data_ptr(), source.data_ptr(), status.data_ptr(), ctypes.byref(kc) if kc else None,
+          ctypes.byref(vc) if vc else None, k_heads if kc else v_heads, ws.data_ptr(), nb)
     return CacheEvict(source, out_lengths, out_score, out_position, status)
 
 

@@ -36,6 +36,9 @@ namespace {
 
 constexpr int kST = 256;                 // threads of the sum kernel
 constexpr int kSumSlots = 4;             // slots a thread
+template <int DT>
+constexpr int kSumBatch = DT == TS_DTYPE_F32 ? 8 : 16;   // weight rows a thread has in flight: 128 bytes
+constexpr int kRowBatch = 4;             // the same where a row kernel sums: few weight rows
 constexpr int kSumTile = kST * kSumSlots;
 constexpr int kET = 1024;                // threads of the row kernels
 constexpr int kEW = kET / 64;
@@ -57,13 +60,12 @@ struct TileInfo {
 // What the steps of a long row leave for the next ones.
 struct RowInfo {
   uint32_t protected_;         // bin: protected slots
-  uint32_t listed;             // list: slots listed
   uint32_t among_first;        // list: whether the cut falls among the protected slots
   uint32_t prefix, lo;         // the cut's bin: u >> lo == prefix
   uint32_t need, in_bin;       // the cut is the need-th of the in_bin slots in it
   uint32_t whole;              // 0: a cut is to be found; 1: the class stays as a whole
   uint32_t cut_u, cut_slot;    // cut
-  int32_t st, k, tiles, pad;   // cut: the row's status, new length, tiles in use
+  int32_t st, k, tiles;        // cut: the row's status, new length, tiles in use
 };
 // What a tile of a long row leaves: slots of the cut's bin and their extreme u; freed slots and fillers.
 struct TileBin {
@@ -100,7 +102,6 @@ struct EParams {
   RowInfo* row;                          // [rows] long rows, like the next ones
   TileBin* bin;                          // [rows, tiles]
   uint32_t* hist;                        // [rows, 2, kEBins]
-  uint2* list;                           // [rows, kListLong]: (u, slot)
   int32_t* fill_position;                // [rows, sum_stride]; hole and fill are [rows, sum_stride] there, by tiles
   int32_t tiles;
   int32_t* moves;                        // [rows]
@@ -109,10 +110,12 @@ struct EParams {
   int32_t cap;
   Cache k, v;
   int32_t heads;
+  int32_t lane_bits;                     // of the threads that copy one move
 };
 
 __device__ __forceinline__ int row_length(const EParams& P, int r) { return max(0, min(P.lengths[r], P.slots)); }
 
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
@@ -128,52 +131,55 @@ __device__ __forceinline__ V load4(const T* p, int j, int n, T rest) {
   return v;
 }
 
-// Adds one weight row's slots j .. j + N - 1 to s (N * size: 16 bytes, or two loads of 16).
-template <int DT, int N>
-__device__ __forceinline__ void add_weights(const char* w, int j, int n, double* s) {
-  constexpr int size = tsl::Logits<DT>::kSize, per = 16 / size;
-  if constexpr (N < per) {                   // half a vector of 16-bit weights
-    typedef unsigned int u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
-    tsl::u32x4 v = {0u, 0u, 0u, 0u};
-    if (j + N <= n) {
-      const u32x2_any h = *reinterpret_cast<const u32x2_any*>(w + (int64_t)j * size);
-      v[0] = h[0];
-      v[1] = h[1];
-#pragma unroll
-      for (int i = 0; i < N; ++i) s[i] += (double)tsl::unpack<DT>(v, i);
-    } else {
-      for (int i = 0; i < N; ++i)
-        if (j + i < n) s[i] += (double)tsl::load_logit<DT>(w, j + i);
-    }
+// Four weights at w: 16 bytes, or 8 in the first half of the vector.
+template <int DT>
+__device__ __forceinline__ tsl::u32x4 load_weights(const char* w) {
+  if constexpr (DT == TS_DTYPE_F32) {
+    return tsl::load16(w);
   } else {
-#pragma unroll
-    for (int h = 0; h < N / per; ++h) {
-      if (j + (h + 1) * per <= n) {
-        const tsl::u32x4 v = tsl::load16(w + (int64_t)(j + h * per) * size);
-#pragma unroll
-        for (int i = 0; i < per; ++i) s[h * per + i] += (double)tsl::unpack<DT>(v, i);
-      } else {
-#pragma unroll
-        for (int i = 0; i < per; ++i)
-          if (j + h * per + i < n) s[h * per + i] += (double)tsl::load_logit<DT>(w, j + h * per + i);
-      }
-    }
+    typedef unsigned int u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+    const u32x2 h = __builtin_nontemporal_load(reinterpret_cast<const u32x2_any*>(w));
+    return tsl::u32x4{h[0], h[1], 0u, 0u};
   }
 }
 
-// The sums of slots j .. j + N - 1 in binary64, in the order of the weight rows.
-template <int DT, int N>
+// The sums of slots j .. j + 3 in binary64, in the order of the weight rows. All loads of a batch of weight rows are
+// in flight before the first is added.
+template <int DT, int BATCH>
 __device__ __forceinline__ void sum_slots(const EParams& P, int r, int j, int n, double* s) {
+  const char* w = P.weights + (int64_t)r * P.w_row + (int64_t)j * tsl::Logits<DT>::kSize;
   const float* score = P.score + (int64_t)r * P.score_stride;
-  const char* w = P.weights + (int64_t)r * P.w_row;
+  if (j + 4 <= n) {
+    const f32x4 v = *reinterpret_cast<const f32x4_any*>(score + j);
+    // Weight rows q .. q + BATCH - 1; past the last one it is loaded again and -0, which changes no sum, added.
+    auto batch = [&](int q, bool start) {
+      tsl::u32x4 x[BATCH];
 #pragma unroll
-  for (int h = 0; h < N; h += 4) {
-    const f32x4 v = load4<f32x4, f32x4_any>(score, j + h, n, 0.0f);
+      for (int b = 0; b < BATCH; ++b) x[b] = load_weights<DT>(w + (int64_t)min(q + b, P.n_w - 1) * P.w_stride);
+      if (start) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[h + i] = (double)v[i];
+        for (int i = 0; i < 4; ++i) s[i] = (double)v[i];
+      }
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] += (double)(q + b < P.n_w ? tsl::unpack<DT>(x[b], i) : -0.0f);
+    };
+    if (P.n_w > 0) {
+      batch(0, true);
+      for (int q = BATCH; q < P.n_w; q += BATCH) batch(q, false);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] = (double)v[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = j + i < n ? (double)score[j + i] : 0.0;
+    for (int q = 0; q < P.n_w; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (j + i < n) s[i] += (double)tsl::load_logit<DT>(w + (int64_t)q * P.w_stride, i);
   }
-#pragma unroll 8
-  for (int i = 0; i < P.n_w; ++i) add_weights<DT, N>(w + (int64_t)i * P.w_stride, j, n, s);
 }
 
 template <int DT>
@@ -185,11 +191,9 @@ __global__ __launch_bounds__(kST) void ts_evict_sum_kernel(EParams P) {
   uint32_t newest = 0, kmin = 0xFFFFFFFFu, kmax = 0;
   if (j < n) {
     double s[kSumSlots];
-    sum_slots<DT, kSumSlots>(P, r, j, n, s);
+    sum_slots<DT, kSumBatch<DT>>(P, r, j, n, s);
     f32x4* out = reinterpret_cast<f32x4*>(P.sum + (int64_t)r * P.sum_stride + j);
-#pragma unroll
-    for (int h = 0; h < kSumSlots / 4; ++h)
-      if (j + 4 * h < n) out[h] = f32x4{(float)s[4 * h], (float)s[4 * h + 1], (float)s[4 * h + 2], (float)s[4 * h + 3]};
+    *out = f32x4{(float)s[0], (float)s[1], (float)s[2], (float)s[3]};
     if (P.slots > kRowSlots) {
       const int32_t* pos = P.position + (int64_t)r * P.position_stride;
 #pragma unroll
@@ -383,16 +387,50 @@ __device__ __forceinline__ void reject_row(const EParams& P, int r, const Row& R
   }
 }
 
-// The i-th unit of U bytes of a row's `moves`: unit i % units of move i / units.
-template <class U>
-__device__ __forceinline__ void copy_units(const Cache& C, int r, int heads, const int32_t* hole, const int32_t* fill,
-                                           int64_t moves, int64_t i0, int64_t step) {
-  char* base = C.p + (int64_t)(r / heads) * C.batch + (int64_t)(r % heads) * C.head;
-  const int64_t n = moves * C.units;
-  for (int64_t i = i0; i < n; i += step) {
-    const int64_t m = i / C.units, u = i - m * C.units;
-    const U v = *reinterpret_cast<const U*>(base + (int64_t)fill[m] * C.slot + u * (int64_t)sizeof(U));
-    *reinterpret_cast<U*>(base + (int64_t)hole[m] * C.slot + u * (int64_t)sizeof(U)) = v;
+// Copies moves lo .. hi - 1 of a row by a workgroup of T threads: 2^lane_bits threads (about the units of U bytes that a slot
+// has) take a move, kCopyBatch moves of a cache, or of both, in flight at a time. A share's last batch repeats its last
+// move's loads and stores them once.
+constexpr int kCopyBatch = 4;
+template <class U, int T, bool TWO>
+__device__ __forceinline__ void copy_slots(const Cache& A, const Cache& B, int b, int h, int lane_bits, const int32_t* hole,
+                                           const int32_t* fill, int lo, int hi) {
+  char* ap = A.p + (int64_t)b * A.batch + (int64_t)h * A.head;
+  char* bp = B.p + (int64_t)b * B.batch + (int64_t)h * B.head;
+  const int lanes = 1 << lane_bits, sub = (int)threadIdx.x & (lanes - 1), per = T >> lane_bits;
+  for (int m0 = lo + ((int)threadIdx.x >> lane_bits); m0 < hi; m0 += per * kCopyBatch) {
+    int f[kCopyBatch], t[kCopyBatch];
+#pragma unroll
+    for (int i = 0; i < kCopyBatch; ++i) {
+      const int m = min(m0 + i * per, hi - 1);
+      f[i] = fill[m];
+      t[i] = hole[m];
+    }
+    for (int u = sub; u < A.units; u += lanes) {
+      U a[kCopyBatch], c[kCopyBatch];
+      const int64_t at = (int64_t)u * (int64_t)sizeof(U);
+#pragma unroll
+      for (int i = 0; i < kCopyBatch; ++i) {
+        a[i] = *reinterpret_cast<const U*>(ap + (int64_t)f[i] * A.slot + at);
+        if (TWO) c[i] = *reinterpret_cast<const U*>(bp + (int64_t)f[i] * B.slot + at);
+      }
+#pragma unroll
+      for (int i = 0; i < kCopyBatch; ++i) {
+        if (m0 + i * per >= hi) continue;
+        *reinterpret_cast<U*>(ap + (int64_t)t[i] * A.slot + at) = a[i];
+        if (TWO) *reinterpret_cast<U*>(bp + (int64_t)t[i] * B.slot + at) = c[i];
+      }
+    }
+  }
+}
+template <class U, int T>
+__device__ __forceinline__ void copy_moves(const EParams& P, int r, const int32_t* hole, const int32_t* fill, int lo, int hi) {
+  if (lo >= hi) return;
+  const int b = r / P.heads, h = r - b * P.heads;
+  if (P.k.units == P.v.units) {
+    copy_slots<U, T, true>(P.k, P.v, b, h, P.lane_bits, hole, fill, lo, hi);
+  } else {
+    copy_slots<U, T, false>(P.k, P.k, b, h, P.lane_bits, hole, fill, lo, hi);
+    copy_slots<U, T, false>(P.v, P.v, b, h, P.lane_bits, hole, fill, lo, hi);
   }
 }
 
@@ -493,7 +531,7 @@ __global__ __launch_bounds__(kET) void ts_evict_row_kernel(EParams P) {
       s[v] = j < n ? *reinterpret_cast<const f32x4*>(sum + j) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     } else {
       double d[4] = {0.0, 0.0, 0.0, 0.0};
-      if (j < n) sum_slots<SRC, 4>(P, r, j, n, d);
+      if (j < n) sum_slots<SRC, kRowBatch>(P, r, j, n, d);
       s[v] = f32x4{(float)d[0], (float)d[1], (float)d[2], (float)d[3]};
     }
     p[v] = load4<i32x4, i32x4_any>(pos, j, n, (int32_t)0x80000000);
@@ -603,19 +641,20 @@ __global__ __launch_bounds__(kET) void ts_evict_row_kernel(EParams P) {
   if constexpr (!std::is_void_v<U>) {
     const int32_t* hole = P.hole + (int64_t)r * P.cap;
     const int32_t* fill = P.fill + (int64_t)r * P.cap;
-    if (P.k.units) copy_units<U>(P.k, r, P.heads, hole, fill, moves, threadIdx.x, kET);
-    if (P.v.units) copy_units<U>(P.v, r, P.heads, hole, fill, moves, threadIdx.x, kET);
+    if (P.k.units | P.v.units) copy_moves<U, kET>(P, r, hole, fill, 0, (int)moves);
   }
 }
 
 // ------------------------------------------------------------------ long rows
 constexpr int kSW = kST / 64;
+constexpr int kBinTiles = 4;
 
-// The row's extremes from its tiles; every thread of the workgroup gets them. red: 3 words a wave.
+// The row's extremes from its tiles; every thread of the workgroup of NW waves gets them. red: 3 words a wave.
+template <int NW>
 __device__ __forceinline__ Row long_row(const EParams& P, int r, uint32_t* red, uint32_t& range) {
   const int n = row_length(P, r);
   uint32_t newest = 0, kmin = 0xFFFFFFFFu, kmax = 0;
-  for (int i = threadIdx.x; (int64_t)i * kSumTile < n; i += blockDim.x) {
+  for (int i = threadIdx.x; (int64_t)i * kSumTile < n; i += 64 * NW) {
     const TileInfo ti = P.info[(int64_t)r * P.tiles + i];
     newest = max(newest, (uint32_t)ti.newest ^ 0x80000000u);
     kmin = min(kmin, ti.kmin);
@@ -630,7 +669,8 @@ __device__ __forceinline__ Row long_row(const EParams& P, int r, uint32_t* red, 
     red[3 * wave() + 2] = kmax;
   }
   bar();
-  for (int w = 0; w < (int)(blockDim.x >> 6); ++w) {
+  #pragma unroll
+  for (int w = 0; w < NW; ++w) {
     newest = max(newest, red[3 * w]);
     kmin = min(kmin, red[3 * w + 1]);
     kmax = max(kmax, red[3 * w + 2]);
@@ -646,38 +686,43 @@ struct Quad {
   f32x4 s;
   i32x4 p;
 };
-__device__ __forceinline__ Quad load_quad(const EParams& P, int r, int tile, int n) {
+__device__ __forceinline__ Quad load_quad(const EParams& P, int r, int j, int n) {
   Quad q;
-  q.j = tile * kSumTile + (int)threadIdx.x * 4;
+  q.j = j + (int)threadIdx.x * 4;
   q.s = q.j < n ? *reinterpret_cast<const f32x4*>(P.sum + (int64_t)r * P.sum_stride + q.j) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   q.p = load4<i32x4, i32x4_any>(P.position + (int64_t)r * P.position_stride, q.j, n, (int32_t)0x80000000);
   return q;
 }
 
-__global__ __launch_bounds__(kST) void ts_evict_bin_kernel(EParams P) {
+// A workgroup bins kBinTiles tiles: what it counts goes to the row's bins by an atomic for each bin that it met.
+__global__ __launch_bounds__(kET) void ts_evict_bin_kernel(EParams P, int groups) {
   __shared__ uint32_t hist[2][kEBins];
-  __shared__ uint32_t red[3 * kSW];
+  __shared__ uint32_t red[3 * kEW];
   __shared__ uint32_t np;
-  const int r = (int)(blockIdx.x / (unsigned)P.tiles), tile = (int)(blockIdx.x - (unsigned)r * (unsigned)P.tiles);
+  const int r = (int)(blockIdx.x / (unsigned)groups), tile = (int)(blockIdx.x - (unsigned)r * (unsigned)groups) * kBinTiles * (kET / kST);
   const int n = row_length(P, r);
   if (tile * kSumTile >= n) return;
-  const Quad q = load_quad(P, r, tile, n);
-  for (int i = threadIdx.x; i < 2 * kEBins; i += kST) (&hist[0][0])[i] = 0u;
+  Quad q[kBinTiles];
+#pragma unroll
+  for (int b = 0; b < kBinTiles; ++b) q[b] = load_quad(P, r, (tile + b * (kET / kST)) * kSumTile, n);
+  for (int i = threadIdx.x; i < 2 * kEBins; i += kET) (&hist[0][0])[i] = 0u;
   if (threadIdx.x == 0) np = 0;
   uint32_t range;
-  const Row R = long_row(P, r, red, range);
+  const Row R = long_row<kEW>(P, r, red, range);
   if (R.st != TS_ROW_OK) return;
   const int sh = max(bitlen(range) - kEBits, 0);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (q.j + i >= n) continue;
-    const bool f = R.first(q.p[i]);
-    atomicAdd(&hist[f ? 1 : 0][R.u(q.s[i]) >> sh], 1u);
-    if (f) atomicAdd(&np, 1u);
-  }
+  for (int b = 0; b < kBinTiles; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (q[b].j + i >= n) continue;
+      const bool f = R.first(q[b].p[i]);
+      atomicAdd(&hist[f ? 1 : 0][R.u(q[b].s[i]) >> sh], 1u);
+      if (f) atomicAdd(&np, 1u);
+    }
   bar();
   uint32_t* h = P.hist + (int64_t)r * 2 * kEBins;
-  for (int i = threadIdx.x; i < 2 * kEBins; i += kST) {
+  for (int i = threadIdx.x; i < 2 * kEBins; i += kET) {
     const uint32_t c = (&hist[0][0])[i];
     if (c) atomicAdd(&h[i], c);
   }
@@ -690,15 +735,15 @@ __global__ __launch_bounds__(kST) void ts_evict_list_kernel(EParams P) {
   const int r = (int)(blockIdx.x / (unsigned)P.tiles), tile = (int)(blockIdx.x - (unsigned)r * (unsigned)P.tiles);
   const int n = row_length(P, r), t = threadIdx.x;
   if (tile * kSumTile >= n) return;
-  const Quad q = load_quad(P, r, tile, n);
+  const Quad q = load_quad(P, r, tile * kSumTile, n);
   const uint32_t total = P.row[r].protected_;
   uint32_t range;
-  const Row R = long_row(P, r, red, range);
+  const Row R = long_row<kSW>(P, r, red, range);
   if (R.st != TS_ROW_OK) return;
   const bool among_first = total >= (uint32_t)R.k;
   const uint32_t need = among_first ? (uint32_t)R.k : (uint32_t)R.k - total;
   const uint32_t pool = among_first ? total : (uint32_t)n - total;
-  TileBin out = {};
+  uint32_t out_count = 0, out_umin = 0xFFFFFFFFu, out_umax = 0;
   if (need < pool) {
     // thread t owns eight bins
     constexpr int kOwn = kEBins / kST;
@@ -713,20 +758,26 @@ __global__ __launch_bounds__(kST) void ts_evict_list_kernel(EParams P) {
     const uint32_t before = block_excl_scan<kSW>(sum, red, all);
     uint32_t above = all - before - sum;
     if (above < need && above + sum >= need) {
-      int i = kOwn - 1;
-      for (; i > 0; --i) {
-        if (above + c[i] >= need) break;
-        above += c[i];
+      uint32_t bin = 0, in_bin = 0;
+      bool found = false;
+#pragma unroll
+      for (int i = kOwn - 1; i >= 0; --i) {
+        if (found) continue;
+        bin = t * kOwn + i;
+        in_bin = c[i];
+        found = above + c[i] >= need;
+        above += found ? 0u : c[i];
       }
-      res[0] = t * kOwn + i;
+      res[0] = bin;
       res[1] = above;
-      res[2] = c[i];
+      res[2] = in_bin;
     }
     bar();
     const int lo = max(bitlen(range) - kEBits, 0);
     const uint32_t bin = res[0], left = need - res[1], in_bin = res[2];
     const bool listed = in_bin > left && in_bin <= (uint32_t)kListLong;
-    uint32_t umin = 0xFFFFFFFFu, umax = 0, count = 0;
+    uint32_t umin = 0xFFFFFFFFu, umax = 0;
+    uint64_t m[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t u = R.u(q.s[i]);
@@ -734,10 +785,10 @@ __global__ __launch_bounds__(kST) void ts_evict_list_kernel(EParams P) {
       if (in) {
         umin = min(umin, u);
         umax = max(umax, u);
-        if (listed) P.list[(int64_t)r * kListLong + atomicAdd(&P.row[r].listed, 1u)] = make_uint2(u, (uint32_t)(q.j + i));
       }
-      count += (uint32_t)__popcll(__ballot(in));
+      m[i] = __ballot(in);
     }
+    const uint32_t count = count4(m);
     umin = wave_min(umin);
     umax = wave_max(umax);
     if (lane() == 0) {
@@ -746,10 +797,22 @@ __global__ __launch_bounds__(kST) void ts_evict_list_kernel(EParams P) {
       red[3 * wave() + 2] = umax;
     }
     bar();
+#pragma unroll
     for (int w = 0; w < kSW; ++w) {
-      out.count += red[3 * w];
-      out.umin = w ? min(out.umin, red[3 * w + 1]) : red[1];
-      out.umax = max(out.umax, red[3 * w + 2]);
+      out_count += red[3 * w];
+      out_umin = min(out_umin, red[3 * w + 1]);
+      out_umax = max(out_umax, red[3 * w + 2]);
+    }
+    if (listed) {   // in the tile's own place, which its freed slots and fillers take later
+      int64_t at = (int64_t)r * P.sum_stride + (int64_t)tile * kSumTile;
+      for (int w = 0; w < wave(); ++w) at += red[3 * w];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if ((m[i] >> lane()) & 1u) {
+          const uint32_t o = rank4(m, i);
+          P.hole[at + o] = (int32_t)R.u(q.s[i]);
+          P.fill[at + o] = q.j + i;
+        }
     }
     if (tile == 0 && t == 0) {
       RowInfo& I = P.row[r];
@@ -764,7 +827,24 @@ __global__ __launch_bounds__(kST) void ts_evict_list_kernel(EParams P) {
     P.row[r].among_first = among_first ? 1u : 0u;
     P.row[r].whole = 1u;
   }
-  if (t == 0) P.bin[(int64_t)r * P.tiles + tile] = out;
+  if (t == 0) {   // (member by member: a struct of its own would be put into LDS, whose place the compiler finds by the
+                  // dispatch packet, in host memory: 12 us)
+    TileBin& out = P.bin[(int64_t)r * P.tiles + tile];
+    out.count = out_count;
+    out.umin = out_umin;
+    out.umax = out_umax;
+  }
+}
+
+// The tile whose share holds item `rank`: the last whose start is at most rank and below the next one's.
+__device__ __forceinline__ int tile_of(const uint32_t* start, int tiles, uint32_t rank) {
+  int x = 0, y = tiles;
+  while (y - x > 1) {
+    const int m = (x + y) >> 1;
+    if (start[m] <= rank) x = m;
+    else y = m;
+  }
+  return x;
 }
 
 // One workgroup a row: the cut's u and slot, and the row's status and length.
@@ -772,9 +852,10 @@ __global__ __launch_bounds__(kET) void ts_evict_cut_kernel(EParams P) {
   __shared__ ESmem sm;
   __shared__ uint32_t red[3 * kEW];
   __shared__ uint2 list[kListLong];
+  __shared__ uint32_t start[kMaxTiles + 1];
   const int r = (int)blockIdx.x, t = threadIdx.x, l = lane();
   uint32_t range;
-  const Row R = long_row(P, r, red, range);
+  const Row R = long_row<kEW>(P, r, red, range);
   if (t == 0) {
     P.row[r].st = R.st;
     P.row[r].k = R.k;
@@ -789,7 +870,22 @@ __global__ __launch_bounds__(kET) void ts_evict_cut_kernel(EParams P) {
   if (!I.whole && I.in_bin == I.need) {
     cut.u = I.prefix << I.lo;
   } else if (!I.whole && I.in_bin <= (uint32_t)kListLong) {
-    for (uint32_t i = t; i < I.in_bin; i += kET) list[i] = P.list[(int64_t)r * kListLong + i];
+    // the tiles' shares, one after the other
+    const int tiles = (R.n + kSumTile - 1) / kSumTile, own = (tiles + kET - 1) / kET;
+    uint32_t c = 0, all;
+    for (int i = t * own; i < min(tiles, (t + 1) * own); ++i) c += P.bin[(int64_t)r * P.tiles + i].count;
+    uint32_t at = block_excl_scan<kEW>(c, sm.red, all);
+    for (int i = t * own; i < min(tiles, (t + 1) * own); ++i) {
+      start[i] = at;
+      at += P.bin[(int64_t)r * P.tiles + i].count;
+    }
+    if (t == 0) start[tiles] = all;
+    bar();
+    for (uint32_t i = t; i < I.in_bin; i += kET) {
+      const int x = tile_of(start, tiles, i);
+      const int64_t o = (int64_t)r * P.sum_stride + (int64_t)x * kSumTile + (i - start[x]);
+      list[i] = make_uint2((uint32_t)P.hole[o], (uint32_t)P.fill[o]);
+    }
     bar();
     cut = find_cut(
         sm, (int)I.lo, I.prefix, I.need,
@@ -860,10 +956,10 @@ __global__ __launch_bounds__(kST) void ts_evict_emit_kernel(EParams P) {
   const int r = (int)(blockIdx.x / (unsigned)P.tiles), tile = (int)(blockIdx.x - (unsigned)r * (unsigned)P.tiles);
   const int n = row_length(P, r);
   if (tile * kSumTile >= n) return;
-  const Quad q = load_quad(P, r, tile, n);
+  const Quad q = load_quad(P, r, tile * kSumTile, n);
   const RowInfo I = P.row[r];
   uint32_t range;
-  const Row R = long_row(P, r, red, range);
+  const Row R = long_row<kSW>(P, r, red, range);
   if (R.st != TS_ROW_OK) return;
   const Cut cut{I.cut_u, I.cut_slot};
   const bool af = I.among_first != 0;
@@ -921,15 +1017,13 @@ __global__ __launch_bounds__(kST) void ts_evict_emit_kernel(EParams P) {
   }
 }
 
+// A workgroup takes a share (one of `parts`) of a row's moves.
 template <class U>
-__global__ __launch_bounds__(kMT) void ts_evict_move_kernel(EParams P, int blocks) {
-  const int r = (int)(blockIdx.x / (unsigned)blocks);
-  const int64_t i0 = (int64_t)(blockIdx.x - (unsigned)r * (unsigned)blocks) * kMT + threadIdx.x;
-  const int64_t n = P.moves[r], step = (int64_t)blocks * kMT;
-  const int32_t* hole = P.hole + (int64_t)r * P.cap;
-  const int32_t* fill = P.fill + (int64_t)r * P.cap;
-  if (P.k.units) copy_units<U>(P.k, r, P.heads, hole, fill, n, i0, step);
-  if (P.v.units) copy_units<U>(P.v, r, P.heads, hole, fill, n, i0, step);
+__global__ __launch_bounds__(kMT) void ts_evict_move_kernel(EParams P, int parts) {
+  const int r = (int)(blockIdx.x / (unsigned)parts), part = (int)(blockIdx.x - (unsigned)r * (unsigned)parts);
+  const int64_t n = P.moves[r];
+  copy_moves<U, kMT>(P, r, P.hole + (int64_t)r * P.cap, P.fill + (int64_t)r * P.cap, (int)(n * part / parts),
+                     (int)(n * (part + 1) / parts));
 }
 
 // Long rows: a workgroup takes a share (one of `parts`) of a tile's freed slots. Their ranks among the row's freed slots
@@ -939,7 +1033,7 @@ __global__ __launch_bounds__(kMT) void ts_evict_long_move_kernel(EParams P, int 
   __shared__ uint32_t red[kMT / 64];
   __shared__ uint32_t start[kMaxTiles + 1];     // fillers before each tile
   __shared__ uint32_t before;                   // freed slots before this workgroup's tile
-  __shared__ int32_t to[kSumTile], from[kSumTile];
+  __shared__ int32_t to[kSumTile], from[kSumTile], place_of[kSumTile];
   const unsigned per = (unsigned)hole_tiles * (unsigned)parts;
   const int r = (int)(blockIdx.x / per), t = (int)threadIdx.x;
   const unsigned rest = blockIdx.x - (unsigned)r * per;
@@ -983,29 +1077,26 @@ __global__ __launch_bounds__(kMT) void ts_evict_long_move_kernel(EParams P, int 
   const int64_t base = (int64_t)r * P.sum_stride;
   for (uint32_t i = lo + t; i < hi; i += kMT) {
     const uint32_t rank = before + i;
-    int x = 0, y = I.tiles;                     // the last tile whose start is at most rank
-    while (y - x > 1) {
-      const int m = (x + y) >> 1;
-      if (start[m] <= rank) x = m;
-      else y = m;
-    }
+    const int x = tile_of(start, I.tiles, rank);
     const int64_t at = base + (int64_t)x * kSumTile + (rank - start[x]);
-    const int32_t src = P.fill[at], dst = P.hole[base + (int64_t)tile * kSumTile + i];
-    to[i - lo] = dst;
-    from[i - lo] = src;
-    source[dst] = src;
-    score[dst] = P.sum[base + src];
-    place[dst] = P.fill_position[at];
+    to[i - lo] = P.hole[base + (int64_t)tile * kSumTile + i];
+    from[i - lo] = P.fill[at];
+    place_of[i - lo] = P.fill_position[at];
   }
   bar();
-  if (P.k.units) copy_units<U>(P.k, r, P.heads, to, from, hi - lo, t, kMT);
-  if (P.v.units) copy_units<U>(P.v, r, P.heads, to, from, hi - lo, t, kMT);
+  if (P.k.units | P.v.units) copy_moves<U, kMT>(P, r, to, from, 0, (int)(hi - lo));
+  for (int i = t; i < (int)(hi - lo); i += kMT) {
+    const int dst = to[i], src = from[i];
+    source[dst] = src;
+    score[dst] = P.sum[base + src];
+    place[dst] = place_of[i];
+  }
 }
 
 // ------------------------------------------------------------------ host side
 struct EPlan {
   int64_t cap = 0, sum_stride = 0, tiles = 0;
-  size_t off_info = 0, off_row = 0, off_bin = 0, off_hist = 0, off_list = 0, off_moves = 0, off_hole = 0, off_fill = 0,
+  size_t off_info = 0, off_row = 0, off_bin = 0, off_hist = 0, off_moves = 0, off_hole = 0, off_fill = 0,
          off_fill_position = 0, total = 0;
 };
 bool evict_plan(int64_t rows, int64_t slots, int64_t keep_max, EPlan& pl) {
@@ -1036,7 +1127,6 @@ bool evict_plan(int64_t rows, int64_t slots, int64_t keep_max, EPlan& pl) {
     pl.off_bin = take(rr * (size_t)pl.tiles * sizeof(TileBin));
     pl.off_row = take(rr * sizeof(RowInfo));
     pl.off_hist = take(rr * 2 * kEBins * 4);
-    pl.off_list = take(rr * kListLong * sizeof(uint2));
   }
   pl.total = b;
   return true;
@@ -1066,8 +1156,8 @@ void with_unit(int unit, F f) {
     case 1: f(uint8_t{}); break;
     case 2: f(uint16_t{}); break;
     case 4: f(uint32_t{}); break;
-    case 8: f(uint2{}); break;
-    default: f(uint4{}); break;
+    case 8: f(u32x2{}); break;
+    default: f(tsl::u32x4{}); break;
   }
 }
 
@@ -1192,7 +1282,6 @@ extern "C" int ts_cache_evict(const float* score, int64_t rows, int64_t slots, i
   P.row = reinterpret_cast<RowInfo*>(ws + pl.off_row);
   P.bin = reinterpret_cast<TileBin*>(ws + pl.off_bin);
   P.hist = reinterpret_cast<uint32_t*>(ws + pl.off_hist);
-  P.list = reinterpret_cast<uint2*>(ws + pl.off_list);
   P.fill_position = reinterpret_cast<int32_t*>(ws + pl.off_fill_position);
   P.tiles = (int32_t)pl.tiles;
   P.moves = reinterpret_cast<int32_t*>(ws + pl.off_moves);
@@ -1203,6 +1292,8 @@ extern "C" int ts_cache_evict(const float* score, int64_t rows, int64_t slots, i
   P.k = cache_of(k_cache, unit);
   P.v = cache_of(v_cache, unit);
   P.heads = (int32_t)heads;
+  P.lane_bits = 0;
+  while ((1 << P.lane_bits) < std::max(P.k.units, P.v.units) && (1 << P.lane_bits) < kMT) ++P.lane_bits;
   const hipStream_t s = (hipStream_t)stream;
   const int type = n_weights ? weights_dtype : TS_DTYPE_F32;
   const bool sum_here = slots <= kRowSlots && slots * n_weights * size <= kFusedBytes;
@@ -1227,7 +1318,8 @@ extern "C" int ts_cache_evict(const float* score, int64_t rows, int64_t slots, i
     e = hipGetLastError();
     if (e != hipSuccess) return fail(TS_ERR_LAUNCH, "eviction sum launch failed: %s", hipGetErrorString(e));
     if (slots > kRowSlots) {
-      hipLaunchKernelGGL(ts_evict_bin_kernel, grid, block, 0, s, P);
+      const int64_t groups = (slots + kBinTiles * 4 * kET - 1) / (kBinTiles * 4 * kET);
+      hipLaunchKernelGGL(ts_evict_bin_kernel, dim3((unsigned)(rows * groups)), dim3(kET), 0, s, P, (int)groups);
       hipLaunchKernelGGL(ts_evict_list_kernel, grid, block, 0, s, P);
       hipLaunchKernelGGL(ts_evict_cut_kernel, dim3((unsigned)rows), dim3(kET), 0, s, P);
       hipLaunchKernelGGL(ts_evict_emit_kernel, grid, block, 0, s, P);
@@ -1245,8 +1337,7 @@ extern "C" int ts_cache_evict(const float* score, int64_t rows, int64_t slots, i
   e = hipGetLastError();
   if (e != hipSuccess) return fail(TS_ERR_LAUNCH, "eviction row launch failed: %s", hipGetErrorString(e));
   if (slot_bytes) {
-    const int64_t most = pl.cap * std::max(P.k.units, P.v.units);
-    const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((most + kMT - 1) / kMT, 4096 / rows));
+    const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((pl.cap << P.lane_bits) / (kMT * kCopyBatch), kMoveGroups / rows));
     with_unit(unit, [&](auto u) {
       hipLaunchKernelGGL(ts_evict_move_kernel<decltype(u)>, dim3((unsigned)(rows * blocks)), dim3(kMT), 0, s, P, (int)blocks);
     });
