@@ -138,7 +138,7 @@ __device__ __forceinline__ tsl::u32x4 load_weights(const char* w) {
     return tsl::load16(w);
   } else {
     typedef unsigned int u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
-    const u32x2 h = __builtin_nontemporal_load(reinterpret_cast<const u32x2_any*>(w));
+    const u32x2 h = *reinterpret_cast<const u32x2_any*>(w);
     return tsl::u32x4{h[0], h[1], 0u, 0u};
   }
 }

@@ -16,6 +16,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "topselect.h"
 #include "ts_device.hpp"
@@ -68,10 +69,9 @@ static_assert(kCapMax <= kLT, "a thread ranks one candidate");
 
 struct LSmem {
   uint32_t tk[kLT];            // each thread's largest key
+  float2 sums[kLT];            // each thread's sums of 2^z and 2^z z
   uint2 list[kCapMax];         // (key, id), in no order
-  uint32_t count;
-  uint32_t red[kLW];
-  double reds[kLW], redd[kLW];
+  uint32_t count, low;
   uint32_t redn[kLW];
   Part part;
   float m;
@@ -79,19 +79,24 @@ struct LSmem {
   int32_t ok;
 };
 
+// Sum over the wave, in a fixed order: the lane moves of wave_incl_scan on both halves. Every lane gets it.
+template <int CTRL, int RMASK>
+__device__ __forceinline__ double moved(double v) {
+  return __longlong_as_double((long long)dpp64<CTRL, RMASK>((uint64_t)__double_as_longlong(v)));
+}
 __device__ __forceinline__ double wave_sum_f64(double v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  v += moved<0x111, 0xf>(v);
+  v += moved<0x112, 0xf>(v);
+  v += moved<0x114, 0xf>(v);
+  v += moved<0x118, 0xf>(v);
+  v += moved<0x142, 0xa>(v);
+  v += moved<0x143, 0xc>(v);
+  return __longlong_as_double((long long)readlane64((uint64_t)__double_as_longlong(v), 63));
 }
 
 // ------------------------------------------------------------------ the best n of a workgroup's items
-// Count over the workgroup of items i < N of every thread with pred(i).
-template <int N, class P>
-__device__ __forceinline__ uint32_t count_items(LSmem& sm, P pred) {
-  uint32_t c = 0;
-#pragma unroll
-  for (int i = 0; i < N; ++i) c += (uint32_t)__popcll(__ballot(pred(i)));
+// Sum over the workgroup of a count that every lane of a wave holds.
+__device__ __forceinline__ uint32_t block_count(LSmem& sm, uint32_t c) {
   if (lane() == 0) sm.redn[wave()] = c;
   bar();
   uint32_t s = 0;
@@ -100,22 +105,15 @@ __device__ __forceinline__ uint32_t count_items(LSmem& sm, P pred) {
   bar();
   return s;
 }
+__device__ __forceinline__ void append(LSmem& sm, uint32_t key, uint32_t id) {
+  const uint32_t at = atomicAdd(&sm.count, 1u);
+  if (at < (uint32_t)kCapMax) sm.list[at] = make_uint2(key, id);
+}
 
-// Writes to sm.list a set of at most `cap` items that holds the best n in the order (key descending, id
-// ascending) and returns its size. key(i), id(i): the calling thread's N items; keys up to that of -inf are
-// absent ones. tk: the thread's largest key. Every thread calls it; the result's order in the list is open.
-//
-// The n-th largest of the threads' largest keys is a bound that n items at least reach and, where large items are
-// spread over the threads, few more. Where too many reach it (equal keys), the n-th item is found exactly, bit by
-// bit: first its key, then, among equals, its id.
-template <int N, class K, class I>
-__device__ __forceinline__ int best_items(LSmem& sm, uint32_t tk, int n, int cap, K key, I id) {
-  sm.tk[threadIdx.x] = tk;
-  if (threadIdx.x == 0) sm.count = 0;
-  bar();
-  uint32_t k4[kLW];
-#pragma unroll
-  for (int w = 0; w < kLW; ++w) k4[w] = sm.tk[64 * w + lane()];
+// A bound that at least n of the workgroup's items reach and, where large items are spread over the threads, few
+// more: about the n-th largest of the threads' largest keys in sm.tk (keys up to that of -inf are absent items). Called by
+// one wave, which has its four keys of each lane in k4.
+__device__ __forceinline__ uint32_t find_low(const uint32_t* k4, int n) {
   uint32_t low = 0;
   for (int b = 31; b >= 0; --b) {
     const uint32_t t = low | (1u << b);
@@ -127,40 +125,97 @@ __device__ __forceinline__ int best_items(LSmem& sm, uint32_t tk, int n, int cap
       if (c <= n + 8) break;   // close enough: each further bit costs more than the candidates it saves
     }
   }
-  low = max(low, kKeyNegInf + 1);
-  if (tk >= low) {
+  return max(low, kKeyNegInf + 1);
+}
+
+// A tile's exact best n, for tiles with many equal logits around the bound (a mask of the type's lowest value, a constant
+// row) or their large ones in few threads (a sorted row). The tile is read again, a vector at a time, so that this path
+// holds no registers of the usual one. low: a bound that more than n logits reach.
+template <int DT>
+__device__ void exact_tile(LSmem& sm, const char* row, int V, int tile, int n, uint32_t low) {
+  using L = Logits<DT>;
+  // f(v, keys): the keys of the thread's vector v, those that do not count 0
+  auto vectors = [&](auto f) {
+#pragma nounroll
+    for (int v = 0; v < L::kNV; ++v) {
+      const Place<DT> pl(tile, threadIdx.x, v, V);
+      uint32_t key[L::kW];
+      if (V >= L::kW) {
+        const u32x4 raw = load16(row + (int64_t)pl.at * L::kSize);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const uint32_t k = key(i);
-      if (k >= low) {
-        const uint32_t at = atomicAdd(&sm.count, 1u);
-        if (at < (uint32_t)cap) sm.list[at] = make_uint2(k, id(i));
+        for (int j = 0; j < L::kW; ++j) key[j] = pl.counts(j, V) ? f2key(unpack<DT>(raw, j)) : 0u;
+      } else {
+#pragma unroll
+        for (int j = 0; j < L::kW; ++j) key[j] = pl.counts(j, V) ? f2key(load_logit<DT>(row, pl.at + j)) : 0u;
       }
+      f(pl, key);
     }
+  };
+  auto count = [&](uint32_t least) {
+    uint32_t c = 0;
+    vectors([&](const Place<DT>&, const uint32_t* key) {
+#pragma unroll
+      for (int j = 0; j < L::kW; ++j) c += (uint32_t)__popcll(__ballot(key[j] >= least));
+    });
+    return block_count(sm, c);
+  };
+  uint32_t t = low;   // becomes the n-th largest key: the bound itself where fewer are above it, else bit by bit
+  uint32_t above = count(low + 1);
+  if (above >= (uint32_t)n) {
+    t = 0;
+#pragma nounroll
+    for (int b = 31; b >= 0; --b) {
+      const uint32_t u = t | (1u << b);
+      if (count(u) >= (uint32_t)n) t = u;
+    }
+    above = count(t + 1);
   }
+  const uint32_t need = n - above;   // of the logits equal to it, in id order
+  if (threadIdx.x == 0) sm.count = 0;
   bar();
-  const uint32_t found = sm.count;
-  if (found <= (uint32_t)cap) return (int)found;
-  uint32_t t = 0;                                   // the n-th largest key
+  uint32_t seen = 0;
+  vectors([&](const Place<DT>& pl, const uint32_t* key) {
+    uint32_t eq = 0;
+#pragma unroll
+    for (int j = 0; j < L::kW; ++j) eq += key[j] == t ? 1u : 0u;
+    uint32_t total;
+    uint32_t rank = seen + block_excl_scan<kLW>(eq, sm.redn, total);
+    seen += total;
+#pragma unroll
+    for (int j = 0; j < L::kW; ++j) {
+      if (key[j] > t || (key[j] == t && rank < need)) append(sm, key[j], (uint32_t)(pl.at + j));
+      rank += key[j] == t ? 1u : 0u;
+    }
+  });
+  bar();
+}
+
+// The exact best n of items that the threads hold N each, found bit by bit: the n-th largest key, then, among those
+// equal to it, the id of the last that stays (ids are below 2^30 and differ).
+template <int N>
+__device__ __forceinline__ void exact_items(LSmem& sm, const uint2* c, int n) {
+  auto count = [&](auto pred) {
+    uint32_t k = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) k += (uint32_t)__popcll(__ballot(pred(c[i])));
+    return block_count(sm, k);
+  };
+  uint32_t t = 0, last = 0;
   for (int b = 31; b >= 0; --b) {
     const uint32_t u = t | (1u << b);
-    if (count_items<N>(sm, [&](int i) { return key(i) >= u; }) >= (uint32_t)n) t = u;
+    if (count([&](const uint2& q) { return q.x >= u; }) >= (uint32_t)n) t = u;
   }
-  const uint32_t need = n - count_items<N>(sm, [&](int i) { return key(i) > t; });
-  uint32_t last = 0;                                // the id of the need-th item with that key
-  for (int b = 30; b >= 0; --b) {
+  const uint32_t need = n - count([&](const uint2& q) { return q.x > t; });
+  for (int b = 29; b >= 0; --b) {
     const uint32_t u = last | (1u << b);
-    if (count_items<N>(sm, [&](int i) { return key(i) == t && id(i) < u; }) < need) last = u;
+    if (count([&](const uint2& q) { return q.x == t && q.y < u; }) < need) last = u;
   }
   if (threadIdx.x == 0) sm.count = 0;
   bar();
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const uint32_t k = key(i);
-    if (k > t || (k == t && id(i) <= last)) sm.list[atomicAdd(&sm.count, 1u)] = make_uint2(k, id(i));
-  }
+  for (int i = 0; i < N; ++i)
+    if (c[i].x > t || (c[i].x == t && c[i].y <= last)) append(sm, c[i].x, c[i].y);
   bar();
-  return n;
 }
 
 // ------------------------------------------------------------------ a row's parameters
@@ -180,79 +235,50 @@ __device__ __forceinline__ RowIn row_in(const LParams& P, int r) {
 }
 
 // ------------------------------------------------------------------ a tile
-// The sums over a workgroup's tile; thread 0 holds them in the returned part.
+// log2(e) / T rounded once, or nearly (r + r e is 1/T to twice fp32's bits, and kHi + kLo log2(e)).
+__device__ __forceinline__ float scale32(const LParams& P, float t) {
+  constexpr float kHi = (float)kLog2e, kLo = (float)(kLog2e - (double)kHi);
+  if (!P.t) return kHi;
+  t = fmaxf(t, 0x1p-100f);
+  const float r = 1.0f / t, e = fmaf(-r, t, 1.0f);
+  return fmaf(kHi, r, fmaf(kLo, r, kHi * (e * r)));
+}
+
+// How many of the wave's logits of the tile rank above the given token.
 template <int DT>
-__device__ __forceinline__ Part tile_sums(const LParams& P, const RowIn& in, const char* row, int tile, const float* xs,
-                                          float tm, LSmem& sm) {
-  const int w = wave();
-  const uint32_t km = wave_max(f2key(tm));
-  if (lane() == 0) sm.red[w] = km;
-  bar();
-  uint32_t k = sm.red[0];
-#pragma unroll
-  for (int i = 1; i < kLW; ++i) k = max(k, sm.red[i]);
-  Part pt;
-  pt.m = key2f(k);
-  pt.s = pt.d = 0.0;
-  pt.above = 0;
-  const float m = k == kKeyNegInf ? 0.0f : pt.m;
-  const float c = (float)exponent_scale(in.t);
-  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int i = 0; i < kLE; ++i) {
-    const float z = exponent(xs[i], m, c);
-    const float e = __builtin_amdgcn_exp2f(z);
-    s[i & 3] += e;
-    d[i & 3] = fmaf(e, z, d[i & 3]);
-  }
+__device__ __forceinline__ uint32_t wave_above(const LParams& P, const RowIn& in, const char* row, int tile, const float* xs) {
+  const float xt = load_logit<DT>(row, in.token);
+  const int at = in.token / kTile;
   uint32_t above = 0;
-  if (P.tokens && in.token >= 0) {
-    const float xt = load_logit<DT>(row, in.token);
-    const int at = in.token / kTile;
-    if (tile < at) {
+  if (tile < at) {
 #pragma unroll
-      for (int i = 0; i < kLE; ++i) above += (uint32_t)__popcll(__ballot(xs[i] >= xt));
-    } else if (tile > at) {
+    for (int i = 0; i < kLE; ++i) above += (uint32_t)__popcll(__ballot(xs[i] >= xt));
+  } else if (tile > at) {
 #pragma unroll
-      for (int i = 0; i < kLE; ++i) above += (uint32_t)__popcll(__ballot(xs[i] > xt));
-    } else {
+    for (int i = 0; i < kLE; ++i) above += (uint32_t)__popcll(__ballot(xs[i] > xt));
+  } else {
 #pragma unroll
-      for (int v = 0; v < Logits<DT>::kNV; ++v) {
-        const Place<DT> pl(tile, threadIdx.x, v, P.V);
+    for (int v = 0; v < Logits<DT>::kNV; ++v) {
+      const Place<DT> pl(tile, threadIdx.x, v, P.V);
 #pragma unroll
-        for (int j = 0; j < Logits<DT>::kW; ++j) {
-          const float x = xs[v * Logits<DT>::kW + j];
-          above += (uint32_t)__popcll(__ballot(x > xt || (x == xt && pl.at + j < in.token && pl.counts(j, P.V))));
-        }
+      for (int j = 0; j < Logits<DT>::kW; ++j) {
+        const float x = xs[v * Logits<DT>::kW + j];
+        above += (uint32_t)__popcll(__ballot(x > xt || (x == xt && pl.at + j < in.token && pl.counts(j, P.V))));
       }
     }
   }
-  const double ws = wave_sum_f64((double)(s[0] + s[1]) + (double)(s[2] + s[3]));
-  const double wd = wave_sum_f64((double)(d[0] + d[1]) + (double)(d[2] + d[3]));
-  if (lane() == 0) {
-    sm.reds[w] = ws;
-    sm.redd[w] = wd;
-    sm.redn[w] = above;
-  }
-  bar();
-#pragma unroll
-  for (int i = 0; i < kLW; ++i) {
-    pt.s += sm.reds[i];
-    pt.d += sm.redd[i];
-    pt.above += sm.redn[i];
-  }
-  bar();
-  return pt;
+  return above;
 }
 
-// The thread's largest logit; +inf if one of its logits is NaN.
-__device__ __forceinline__ float thread_max(const float* xs) {
+// The largest of N logits, NaN if one is.
+template <int N>
+__device__ __forceinline__ float max_of(const float* xs) {
   float m = xs[0];
 #pragma unroll
-  for (int i = 1; i + 1 < kLE; i += 2)
+  for (int i = 1; i + 1 < N; i += 2)
     m = __builtin_elementwise_maximum(m, __builtin_elementwise_maximum(xs[i], xs[i + 1]));
-  m = __builtin_elementwise_maximum(m, xs[kLE - 1]);
-  return m != m ? INFINITY : m;
+  if (N % 2 == 0) m = __builtin_elementwise_maximum(m, xs[N - 1]);
+  return m;
 }
 
 // ------------------------------------------------------------------ a row
@@ -335,38 +361,140 @@ __device__ __forceinline__ void write_top(const LParams& P, int r, int count, LS
   lp[above] = ok == 2 ? (above == 0 ? 0.0f : -INFINITY) : fminf(v, 0.0f);
 }
 
+// The exponent of a term is z = fma(x, c, -fl(m c)), c = log2(e) / T: one operation and one rounding, and off by the
+// same eta = m c - fl(m c) in every term, which is known exactly (an fma) and taken out of the sums at the end. Where
+// |m c| is so large that 2^-eta needs more than the terms taken below, z is (x - m) c.
+//
+// What bounds it: the vector unit, for 16-bit logits (an unpacking, half a maximum, fma, exp2 at a quarter of the rate,
+// add and fma a logit, and what a wave spends beside its 32 logits a lane); HBM for fp32 ones. So what can be done
+// once a workgroup is done by one wave, a different one in neighbouring workgroups: the last steps of the sums and the
+// search of the candidates' bound.
 template <int DT, bool TOP, bool WHOLE>
-__global__ __launch_bounds__(kLT) void ts_logp_tile_kernel(LParams P) {
+__global__ __launch_bounds__(kLT) __attribute__((amdgpu_waves_per_eu(7))) void ts_logp_tile_kernel(LParams P) {
+  using L = Logits<DT>;
   __shared__ LSmem sm;
   const int r = WHOLE ? (int)blockIdx.x : (int)(blockIdx.x / (unsigned)P.tiles);
   const int tile = WHOLE ? 0 : (int)(blockIdx.x - (unsigned)r * (unsigned)P.tiles);
+  const int t = (int)threadIdx.x, w = __builtin_amdgcn_readfirstlane(wave());
+  const bool lead = w == (int)(blockIdx.x % kLW);
   const char* row = P.x + (int64_t)r * P.stride;
-  float xs[kLE];
-  load_tile<DT>(row, P.V, tile, threadIdx.x, xs);
+  float xs[kLE], vm[L::kNV];
+  load_tile<DT>(row, P.V, tile, t, xs);
   const RowIn in = row_in(P, r);
-  const float tm = thread_max(xs);
-  const Part pt = tile_sums<DT>(P, in, row, tile, xs, tm, sm);
-  if (WHOLE) {
-    if (threadIdx.x == 0) sm.part = pt;
-    bar();
-    if (wave() == 0) finish_row<DT>(P, in, r, &sm.part, &sm);
-    if (!TOP) return;
-    bar();
-  } else if (threadIdx.x == 0) {
-    P.part[blockIdx.x] = pt;
+#pragma unroll
+  for (int v = 0; v < L::kNV; ++v) vm[v] = max_of<L::kW>(xs + v * L::kW);
+  float tm = max_of<L::kNV>(vm);
+  if (tm != tm) tm = INFINITY;
+  sm.tk[t] = f2key(tm);
+  bar();
+
+  uint32_t k4[kLW], k = 0;
+#pragma unroll
+  for (int i = 0; i < kLW; ++i) {
+    k4[i] = sm.tk[64 * i + lane()];
+    k = max(k, k4[i]);
   }
-  if (TOP) {
-    const int count = best_items<kLE>(
-        sm, f2key(tm), P.n_top, P.cap, [&](int i) { return f2key(xs[i]); },
-        [&](int i) {
-          return (uint32_t)(Place<DT>(tile, threadIdx.x, i / Logits<DT>::kW, P.V).at + i % Logits<DT>::kW);
-        });
-    if (WHOLE) {
-      write_top(P, r, count, sm);
-    } else {
-      uint2* out = P.cand + (int64_t)blockIdx.x * P.cap;
-      if ((int)threadIdx.x < P.cap) out[threadIdx.x] = (int)threadIdx.x < count ? sm.list[threadIdx.x] : make_uint2(0u, 0u);
+  k = wave_max(k);
+  if (TOP && lead) {
+    const uint32_t low = find_low(k4, P.n_top);
+    if (lane() == 0) {
+      sm.low = low;
+      sm.count = 0;
     }
+  }
+  const float m = k == kKeyNegInf ? 0.0f : key2f(k);
+  const float c = scale32(P, in.t), mc = m * c;
+  const bool fused = fabsf(mc) <= 4096.0f;                       // eta below 2^-12
+  {
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto sums = [&](auto exponent) {
+#pragma unroll
+      for (int i = 0; i < kLE; ++i) {
+        const float z = exponent(xs[i]);
+        const float e = __builtin_amdgcn_exp2f(z);
+        s[i & 3] += e;
+        d[i & 3] = fmaf(e, z, d[i & 3]);
+      }
+    };
+    if (fused) sums([&](float x) { return fmaf(x, c, -mc); });
+    else sums([&](float x) { return (x - m) * c; });
+    float dd = (d[0] + d[1]) + (d[2] + d[3]);
+    if (__ballot(dd != dd)) {   // a masked logit's 0 * -inf (or a NaN, which S tells): the products again, without it
+      d[0] = d[1] = d[2] = d[3] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kLE; ++i) {
+        float x = xs[i];
+        asm volatile("" : "+v"(x));   // computed anew: the first loop's values are not kept for this one
+        const float z = fmaxf(fused ? fmaf(x, c, -mc) : (x - m) * c, kZMin);
+        d[i & 3] = fmaf(__builtin_amdgcn_exp2f(z), z, d[i & 3]);
+      }
+      dd = (d[0] + d[1]) + (d[2] + d[3]);
+    }
+    sm.sums[t] = make_float2((s[0] + s[1]) + (s[2] + s[3]), dd);
+  }
+  if (P.tokens && in.token >= 0 && (P.rank || in.t == 0.0f)) {
+    const uint32_t above = wave_above<DT>(P, in, row, tile, xs);
+    if (lane() == 0) sm.redn[w] = above;
+  } else if (lane() == 0) {
+    sm.redn[w] = 0;
+  }
+  bar();
+
+  if (TOP) {
+    const uint32_t low = sm.low;
+    const float low_f = key2f(low);
+#pragma unroll
+    for (int v = 0; v < L::kNV; ++v) {
+      if (!__ballot(vm[v] >= low_f)) continue;
+      const int at = Place<DT>(tile, t, v, P.V).at;
+#pragma unroll
+      for (int j = 0; j < L::kW; ++j)
+        if (xs[v * L::kW + j] >= low_f) append(sm, f2key(xs[v * L::kW + j]), (uint32_t)(at + j));
+    }
+  }
+  if (lead) {
+    double s = 0.0, d = 0.0;
+    uint32_t above = 0;
+#pragma unroll
+    for (int i = 0; i < kLW; ++i) {
+      const float2 q = sm.sums[64 * i + lane()];
+      s += (double)q.x;
+      d += (double)q.y;
+      above += sm.redn[i];
+    }
+    s = wave_sum_f64(s);
+    d = wave_sum_f64(d);
+    if (fused) {
+      const double eta = (double)fmaf(m, c, -mc), y = eta * kLn2;
+      const double scale = 1.0 + y * (-1.0 + y * (0.5 - y * (1.0 / 6.0)));   // 2^-eta, within 1e-15 of it
+      s *= scale;
+      d = d * scale - eta * s;
+    }
+    Part* out = WHOLE ? &sm.part : P.part + blockIdx.x;
+    if (lane() == 0) {
+      out->s = s;
+      out->d = d;
+      out->m = key2f(k);
+      out->above = above;
+    }
+    if (WHOLE) {
+      wave_lds_sync();
+      finish_row<DT>(P, in, r, &sm.part, &sm);
+    }
+  }
+  if (!TOP) return;
+  bar();
+  int count = (int)sm.count;
+  if (count > P.cap) {
+    bar();
+    exact_tile<DT>(sm, row, P.V, tile, P.n_top, sm.low);
+    count = P.n_top;
+  }
+  if (WHOLE) {
+    write_top(P, r, count, sm);
+  } else {
+    uint2* out = P.cand + (int64_t)blockIdx.x * P.cap;
+    if (t < P.cap) out[t] = t < count ? sm.list[t] : make_uint2(0u, 0u);
   }
 }
 
@@ -376,25 +504,48 @@ __global__ __launch_bounds__(kLT) void ts_logp_row_kernel(LParams P) {
   __shared__ LSmem sm;
   const int r = TOP ? (int)blockIdx.x : (int)(blockIdx.x * kLW + wave());
   if (r >= P.rows) return;
-  if (!TOP || wave() == 0) finish_row<DT>(P, row_in(P, r), r, P.part + (int64_t)r * P.tiles, TOP ? &sm : nullptr);
-  if (!TOP) return;
+  if (!TOP) {
+    finish_row<DT>(P, row_in(P, r), r, P.part + (int64_t)r * P.tiles, nullptr);
+    return;
+  }
   const uint2* cand = P.cand + (int64_t)r * P.tiles * P.cap;
   const int64_t n = (int64_t)P.tiles * P.cap;
-  int count = 0;
-  for (int64_t base = 0; base < n; base += kLT * kRowItems) {
-    uint2 c[kRowItems + 1];
-    uint32_t tk = 0;
+  uint2 c[kRowItems + 1];
+  auto load = [&](int64_t base) {
 #pragma unroll
     for (int i = 0; i < kRowItems; ++i) {
       const int64_t at = base + i * kLT + threadIdx.x;
       c[i] = at < n ? cand[at] : make_uint2(0u, 0u);
-      tk = max(tk, c[i].x);
     }
+  };
+  load(0);   // in flight while wave 0 joins the tiles
+  if (wave() == 0) finish_row<DT>(P, row_in(P, r), r, P.part + (int64_t)r * P.tiles, &sm);
+  int count = 0;
+  for (int64_t base = 0; base < n; base += kLT * kRowItems) {
+    if (base) load(base);
     // what is left of the slots before takes part again
     c[kRowItems] = (int)threadIdx.x < count ? sm.list[threadIdx.x] : make_uint2(0u, 0u);
-    tk = max(tk, c[kRowItems].x);
+    uint32_t tk = 0;
+#pragma unroll
+    for (int i = 0; i <= kRowItems; ++i) tk = max(tk, c[i].x);
+    sm.tk[threadIdx.x] = tk;
     bar();
-    count = best_items<kRowItems + 1>(sm, tk, P.n_top, P.cap, [&](int i) { return c[i].x; }, [&](int i) { return c[i].y; });
+    uint32_t k4[kLW];
+#pragma unroll
+    for (int w = 0; w < kLW; ++w) k4[w] = sm.tk[64 * w + lane()];
+    const uint32_t low = find_low(k4, P.n_top);   // every wave for itself: there is nothing else to do
+    if (threadIdx.x == 0) sm.count = 0;
+    bar();
+#pragma unroll
+    for (int i = 0; i <= kRowItems; ++i)
+      if (c[i].x >= low) append(sm, c[i].x, c[i].y);
+    bar();
+    count = (int)sm.count;
+    if (count > P.cap) {
+      bar();
+      exact_items<kRowItems + 1>(sm, c, P.n_top);
+      count = P.n_top;
+    }
   }
   bar();
   write_top(P, r, count, sm);
@@ -432,8 +583,8 @@ __device__ __forceinline__ void store_logit(char* row, int64_t i, float v) {
 
 // Each element is read and then written by one thread and read by no other, so the gradient may take the
 // logits' own place. (A row's last vector, where it is not whole, is taken element by element for that.)
-template <int DT>
-__global__ __launch_bounds__(kLT) void ts_logp_grad_kernel(GParams P) {
+template <int DT, bool ONCE>
+__global__ __launch_bounds__(kLT) __attribute__((amdgpu_waves_per_eu(8))) void ts_logp_grad_kernel(GParams P) {
   using L = Logits<DT>;
   const int r = (int)(blockIdx.x / (unsigned)P.tiles), tile = (int)(blockIdx.x - (unsigned)r * (unsigned)P.tiles);
   const char* row = P.x + (int64_t)r * P.x_stride;
@@ -443,7 +594,7 @@ __global__ __launch_bounds__(kLT) void ts_logp_grad_kernel(GParams P) {
 #pragma unroll
   for (int v = 0; v < L::kNV; ++v) {
     const int at = t0 + v * kLT * L::kW;
-    if (at + L::kW <= P.V) raw[v] = load16(row + (int64_t)at * L::kSize);
+    if (at + L::kW <= P.V) raw[v] = ONCE ? load16_once(row + (int64_t)at * L::kSize) : load16(row + (int64_t)at * L::kSize);
   }
   const float4 st = P.stats[r];
   const float temp = P.t ? P.t[r] : 1.0f;
@@ -459,10 +610,11 @@ __global__ __launch_bounds__(kLT) void ts_logp_grad_kernel(GParams P) {
   float k0 = q * (l - a + h * st.z), k1 = -q * h * (float)kLn2;
   const float add = a * inv_t, m = st.x;
   if (!ok) k0 = k1 = __uint_as_float(0x7FC00000u);
+  const bool here = token >= 0 && token / kTile == tile;   // the tile holds the token
   auto grad = [&](float x, int id) -> float {
-    const float z = exponent(x, m, c);
+    const float z = fmaxf((x - m) * c, kZMin);
     const float g = __builtin_amdgcn_exp2f(z) * fmaf(k1, z, k0);
-    return id == token ? g + add : g;
+    return here && id == token ? g + add : g;
   };
 #pragma unroll
   for (int v = 0; v < L::kNV; ++v) {
@@ -477,10 +629,15 @@ __global__ __launch_bounds__(kLT) void ts_logp_grad_kernel(GParams P) {
         for (int j = 0; j < 4; ++j)
           o[j] = pack2<DT>(grad(unpack<DT>(raw[v], 2 * j), at + 2 * j), grad(unpack<DT>(raw[v], 2 * j + 1), at + 2 * j + 1));
       }
-      store16(out + (int64_t)at * L::kSize, o);
-    } else {
-      for (int j = at; j < P.V; ++j) store_logit<DT>(out, j, grad(load_logit<DT>(row, j), j));
+      if (ONCE) store16_once(out + (int64_t)at * L::kSize, o);
+      else store16(out + (int64_t)at * L::kSize, o);
     }
+  }
+  // the row's last, partial vector
+  const int tail = P.V / L::kW * L::kW, off = tail - t0;
+  if (tail < P.V && off >= 0 && off < kTile && off % (kLT * L::kW) == 0) {
+#pragma nounroll
+    for (int j = tail; j < P.V; ++j) store_logit<DT>(out, j, grad(load_logit<DT>(row, j), j));
   }
 }
 
@@ -522,6 +679,8 @@ hipError_t launch_logp(const LParams& P, hipStream_t s) {
   else hipLaunchKernelGGL((ts_logp_row_kernel<DT, false>), dim3((unsigned)((P.rows + kLW - 1) / kLW)), block, 0, s, P);
   return hipGetLastError();
 }
+
+constexpr int64_t kCacheBytes = 256 << 20;   // the last-level cache
 
 int dtype_size(int dtype) {
   return dtype == TS_DTYPE_F32 ? 4 : (dtype == TS_DTYPE_BF16 || dtype == TS_DTYPE_F16) ? 2 : 0;
@@ -640,11 +799,16 @@ int ts_token_logp_backward(const void* logits, int dtype, int64_t rows, int64_t 
   P.g_logp = grad_logp;
   P.g_entropy = grad_entropy;
   P.g_lse = grad_lse;
+  const bool once = 2 * rows * vocab * size > kCacheBytes;
   const dim3 grid((unsigned)(rows * tiles)), block(kLT);
   const hipStream_t s = (hipStream_t)stream;
-  if (dtype == TS_DTYPE_F32) hipLaunchKernelGGL(ts_logp_grad_kernel<TS_DTYPE_F32>, grid, block, 0, s, P);
-  else if (dtype == TS_DTYPE_BF16) hipLaunchKernelGGL(ts_logp_grad_kernel<TS_DTYPE_BF16>, grid, block, 0, s, P);
-  else hipLaunchKernelGGL(ts_logp_grad_kernel<TS_DTYPE_F16>, grid, block, 0, s, P);
+  auto launch = [&](auto dt) {
+    if (once) hipLaunchKernelGGL((ts_logp_grad_kernel<dt(), true>), grid, block, 0, s, P);
+    else hipLaunchKernelGGL((ts_logp_grad_kernel<dt(), false>), grid, block, 0, s, P);
+  };
+  if (dtype == TS_DTYPE_F32) launch(std::integral_constant<int, TS_DTYPE_F32>{});
+  else if (dtype == TS_DTYPE_BF16) launch(std::integral_constant<int, TS_DTYPE_BF16>{});
+  else launch(std::integral_constant<int, TS_DTYPE_F16>{});
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return fail(TS_ERR_LAUNCH, "token logprob gradient launch failed: %s", hipGetErrorString(e));
   return TS_OK;

@@ -30,10 +30,15 @@ struct Logits {
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x4_any __attribute__((ext_vector_type(4), aligned(2)));   // 16 bytes at any logit's address
 
-__device__ __forceinline__ u32x4 load16(const char* p) {
+__device__ __forceinline__ u32x4 load16(const char* p) { return *reinterpret_cast<const u32x4_any*>(p); }
+__device__ __forceinline__ void store16(char* p, u32x4 v) { *reinterpret_cast<u32x4_any*>(p) = v; }
+// Past the caches, for more than they hold.
+__device__ __forceinline__ u32x4 load16_once(const char* p) {
   return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
 }
-__device__ __forceinline__ void store16(char* p, u32x4 v) { *reinterpret_cast<u32x4_any*>(p) = v; }
+__device__ __forceinline__ void store16_once(char* p, u32x4 v) {
+  __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any*>(p));
+}
 
 // Element j of a vector as fp32 (exact for every type).
 template <int DT>
@@ -104,8 +109,7 @@ __device__ __forceinline__ void load_tile(const char* row, int V, int tile, int 
 // logit more than 2^-93 below it has weight 0 there, as it would at the smaller one.
 __device__ __forceinline__ double exponent_scale(float t) { return tsd::kLog2e / (double)fmaxf(t, 0x1p-100f); }
 
-// (x - m) log2(e) / T, not below kZMin, where 2^z is 0 (so that -inf gives 0 in products with z too).
+// 2^z is 0 here, so that max(z, kZMin) in a product 2^z z gives 0 for -inf too.
 constexpr float kZMin = -151.0f;
-__device__ __forceinline__ float exponent(float x, float m, float c) { return fmaxf((x - m) * c, kZMin); }
 
 }  // namespace tsl
