@@ -71,8 +71,9 @@ struct LSmem {
   uint32_t tk[kLT];            // each thread's largest key
   float2 sums[kLT];            // each thread's sums of 2^z and 2^z z
   uint2 list[kCapMax];         // (key, id), in no order
-  uint32_t count, low;
-  uint32_t redn[kLW];
+  uint8_t who[kLT];            // threads with candidates
+  uint32_t count;
+  uint32_t redn[kLW], redt[kLW];
   Part part;
   float m;
   double log_s, c2;
@@ -111,11 +112,17 @@ __device__ __forceinline__ void append(LSmem& sm, uint32_t key, uint32_t id) {
 }
 
 // A bound that at least n of the workgroup's items reach and, where large items are spread over the threads, few
-// more: about the n-th largest of the threads' largest keys in sm.tk (keys up to that of -inf are absent items). Called by
-// one wave, which has its four keys of each lane in k4.
-__device__ __forceinline__ uint32_t find_low(const uint32_t* k4, int n) {
-  uint32_t low = 0;
-  for (int b = 31; b >= 0; --b) {
+// more: about the n-th largest of the threads' largest keys (keys up to that of -inf are absent items). Called by one
+// wave, which has four of those keys a lane in k4; kmax is the largest. The bits above the highest one in which they differ
+// are common to all; the others are found one by one.
+__device__ __forceinline__ uint32_t find_low(const uint32_t* k4, uint32_t kmax, int n) {
+  uint32_t kmin = k4[0];
+#pragma unroll
+  for (int w = 1; w < kLW; ++w) kmin = min(kmin, k4[w]);
+  const uint32_t differ = kmax ^ wave_min(kmin);
+  const int bits = bitlen(differ);
+  uint32_t low = bits == 32 ? 0u : kmax >> bits << bits;
+  for (int b = bits - 1; b >= 0; --b) {
     const uint32_t t = low | (1u << b);
     int c = 0;
 #pragma unroll
@@ -128,36 +135,42 @@ __device__ __forceinline__ uint32_t find_low(const uint32_t* k4, int n) {
   return max(low, kKeyNegInf + 1);
 }
 
-// A tile's exact best n, for tiles with many equal logits around the bound (a mask of the type's lowest value, a constant
-// row) or their large ones in few threads (a sorted row). The tile is read again, a vector at a time, so that this path
-// holds no registers of the usual one. low: a bound that more than n logits reach.
+// The logits of a tile for one wave, 16 bytes a lane at a time, in id order: f(at, key) gets the first id and the keys of a
+// vector, those that do not count 0.
+template <int DT, class F>
+__device__ __forceinline__ void wave_vectors(const char* row, int V, int tile, F f) {
+  using L = Logits<DT>;
+  constexpr int kBatch = 4;
+  const int end = min(V, (tile + 1) * kTile);
+#pragma nounroll
+  for (int q = tile * kTile + lane() * L::kW; q - lane() * L::kW < end; q += 64 * L::kW * kBatch) {
+    u32x4 raw[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) raw[i] = load16(row + (int64_t)min(q + i * 64 * L::kW, V - L::kW) * L::kSize);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int own = q + i * 64 * L::kW, at = min(own, V - L::kW);
+      uint32_t key[L::kW];
+#pragma unroll
+      for (int j = 0; j < L::kW; ++j) key[j] = at + j >= own && at + j < end ? f2key(unpack<DT>(raw[i], j)) : 0u;
+      f(at, key);
+    }
+  }
+}
+
+// A tile's exact best n, for tiles with many equal logits around the bound `low`, which more than n reach (a mask of the type's
+// lowest value, a constant row), or their large ones in few threads (a sorted row). One wave reads the tile again, so
+// that this path holds no registers of the usual one. The row has more than n logits, so at least a vector's.
 template <int DT>
 __device__ void exact_tile(LSmem& sm, const char* row, int V, int tile, int n, uint32_t low) {
   using L = Logits<DT>;
-  // f(v, keys): the keys of the thread's vector v, those that do not count 0
-  auto vectors = [&](auto f) {
-#pragma nounroll
-    for (int v = 0; v < L::kNV; ++v) {
-      const Place<DT> pl(tile, threadIdx.x, v, V);
-      uint32_t key[L::kW];
-      if (V >= L::kW) {
-        const u32x4 raw = load16(row + (int64_t)pl.at * L::kSize);
-#pragma unroll
-        for (int j = 0; j < L::kW; ++j) key[j] = pl.counts(j, V) ? f2key(unpack<DT>(raw, j)) : 0u;
-      } else {
-#pragma unroll
-        for (int j = 0; j < L::kW; ++j) key[j] = pl.counts(j, V) ? f2key(load_logit<DT>(row, pl.at + j)) : 0u;
-      }
-      f(pl, key);
-    }
-  };
   auto count = [&](uint32_t least) {
     uint32_t c = 0;
-    vectors([&](const Place<DT>&, const uint32_t* key) {
+    wave_vectors<DT>(row, V, tile, [&](int, const uint32_t* key) {
 #pragma unroll
       for (int j = 0; j < L::kW; ++j) c += (uint32_t)__popcll(__ballot(key[j] >= least));
     });
-    return block_count(sm, c);
+    return c;
   };
   uint32_t t = low;   // becomes the n-th largest key: the bound itself where fewer are above it, else bit by bit
   uint32_t above = count(low + 1);
@@ -171,23 +184,70 @@ __device__ void exact_tile(LSmem& sm, const char* row, int V, int tile, int n, u
     above = count(t + 1);
   }
   const uint32_t need = n - above;   // of the logits equal to it, in id order
-  if (threadIdx.x == 0) sm.count = 0;
-  bar();
-  uint32_t seen = 0;
-  vectors([&](const Place<DT>& pl, const uint32_t* key) {
+  uint32_t seen = 0, put = 0;
+  wave_vectors<DT>(row, V, tile, [&](int at, const uint32_t* key) {
     uint32_t eq = 0;
 #pragma unroll
     for (int j = 0; j < L::kW; ++j) eq += key[j] == t ? 1u : 0u;
-    uint32_t total;
-    uint32_t rank = seen + block_excl_scan<kLW>(eq, sm.redn, total);
-    seen += total;
+    const uint32_t incl = wave_incl_scan(eq);
+    uint32_t rank = seen + incl - eq;
+    seen += wave_total(incl);
 #pragma unroll
     for (int j = 0; j < L::kW; ++j) {
-      if (key[j] > t || (key[j] == t && rank < need)) append(sm, key[j], (uint32_t)(pl.at + j));
+      const bool in = key[j] > t || (key[j] == t && rank < need);
       rank += key[j] == t ? 1u : 0u;
+      const uint64_t m = __ballot(in);
+      const uint32_t o = put + mbcnt(m);
+      if (in && o < (uint32_t)kCapMax) sm.list[o] = make_uint2(key[j], (uint32_t)(at + j));
+      put += (uint32_t)__popcll(m);
     }
   });
-  bar();
+}
+
+// The tile's candidates, into sm.list, by one wave: those of the threads' logits that reach `low`, of the threads whose
+// largest does (their keys in k4). Returns their number. The few threads' logits are read again, from the caches, by
+// as many lanes as they have vectors: looking through all threads' registers takes every wave longer.
+template <int DT>
+__device__ __forceinline__ int tile_candidates(LSmem& sm, const char* row, int V, int tile, int n, int cap, uint32_t low,
+                                               const uint32_t* k4) {
+  using L = Logits<DT>;
+  uint32_t threads = 0;
+#pragma unroll
+  for (int w = 0; w < kLW; ++w) {
+    const uint64_t m = __ballot(k4[w] >= low);
+    if (k4[w] >= low) sm.who[threads + mbcnt(m)] = (uint8_t)(64 * w + lane());
+    threads += (uint32_t)__popcll(m);
+  }
+  wave_lds_sync();
+  const float low_f = key2f(low);
+  const bool whole = (tile + 1) * kTile <= V;
+  uint32_t put = 0;
+  for (uint32_t q0 = 0; q0 < threads * L::kNV; q0 += 64) {
+    const uint32_t q = q0 + lane();
+    const bool mine = q < threads * L::kNV;
+    const Place<DT> pl(tile, mine ? sm.who[q / L::kNV] : 0, (int)(q % L::kNV), V);
+    u32x4 raw = {L::kNegInf, L::kNegInf, L::kNegInf, L::kNegInf};
+    if (V >= L::kW && mine) raw = load16(row + (int64_t)pl.at * L::kSize);
+#pragma unroll
+    for (int j = 0; j < L::kW; ++j) {
+      float x = unpack<DT>(raw, j);
+      if (!whole) {
+        if (V < L::kW && mine && j < V) x = load_logit<DT>(row, j);
+        if (!pl.counts(j, V)) x = -INFINITY;
+      }
+      const uint64_t m = __ballot(x >= low_f);
+      if (!m) continue;
+      const uint32_t o = put + mbcnt(m);
+      if (x >= low_f && o < (uint32_t)kCapMax) sm.list[o] = make_uint2(f2key(x), (uint32_t)(pl.at + j));
+      put += (uint32_t)__popcll(m);
+    }
+  }
+  if (put > (uint32_t)cap) {
+    exact_tile<DT>(sm, row, V, tile, n, low);
+    put = n;
+  }
+  wave_lds_sync();
+  return (int)put;
 }
 
 // The exact best n of items that the threads hold N each, found bit by bit: the n-th largest key, then, among those
@@ -235,6 +295,16 @@ __device__ __forceinline__ RowIn row_in(const LParams& P, int r) {
 }
 
 // ------------------------------------------------------------------ a tile
+// A workgroup's row and tile. Workgroups go to the eight XCDs in turn; each row starts at another tile, so that the rows'
+// last tiles, which cost another time than whole ones, do not all fall to one XCD (1777 rows of 16 tiles, bf16: 112 us
+// without it and with the masked loop below run after the other one, 85 us for rows of 16 whole tiles).
+__device__ __forceinline__ void place_block(int32_t tiles, int& r, int& tile) {
+  const unsigned b = blockIdx.x, n = (unsigned)tiles;
+  r = (int)(b / n);
+  const unsigned i = b - (unsigned)r * n + (unsigned)r % n;
+  tile = (int)(i >= n ? i - n : i);
+}
+
 // log2(e) / T rounded once, or nearly (r + r e is 1/T to twice fp32's bits, and kHi + kLo log2(e)).
 __device__ __forceinline__ float scale32(const LParams& P, float t) {
   constexpr float kHi = (float)kLog2e, kLo = (float)(kLog2e - (double)kHi);
@@ -244,10 +314,11 @@ __device__ __forceinline__ float scale32(const LParams& P, float t) {
   return fmaf(kHi, r, fmaf(kLo, r, kHi * (e * r)));
 }
 
-// How many of the wave's logits of the tile rank above the given token.
+// How many of the wave's logits of the tile, whose largest key is k, rank above the given token.
 template <int DT>
-__device__ __forceinline__ uint32_t wave_above(const LParams& P, const RowIn& in, const char* row, int tile, const float* xs) {
-  const float xt = load_logit<DT>(row, in.token);
+__device__ __forceinline__ uint32_t wave_above(const LParams& P, const RowIn& in, int tile, const float* xs,
+                                               uint32_t k, float xt) {
+  if (f2key(xt) > k) return 0;   // most tiles of a likely token
   const int at = in.token / kTile;
   uint32_t above = 0;
   if (tile < at) {
@@ -371,21 +442,25 @@ __device__ __forceinline__ void write_top(const LParams& P, int r, int count, LS
 // search of the candidates' bound.
 template <int DT, bool TOP, bool WHOLE>
 __global__ __launch_bounds__(kLT) __attribute__((amdgpu_waves_per_eu(7))) void ts_logp_tile_kernel(LParams P) {
-  using L = Logits<DT>;
   __shared__ LSmem sm;
-  const int r = WHOLE ? (int)blockIdx.x : (int)(blockIdx.x / (unsigned)P.tiles);
-  const int tile = WHOLE ? 0 : (int)(blockIdx.x - (unsigned)r * (unsigned)P.tiles);
+  int r, tile;
+  if (WHOLE) r = (int)blockIdx.x, tile = 0;
+  else place_block(P.tiles, r, tile);
   const int t = (int)threadIdx.x, w = __builtin_amdgcn_readfirstlane(wave());
   const bool lead = w == (int)(blockIdx.x % kLW);
   const char* row = P.x + (int64_t)r * P.stride;
-  float xs[kLE], vm[L::kNV];
-  load_tile<DT>(row, P.V, tile, t, xs);
+  Tile<DT> raw;
+  raw.load(row, P.V, tile, t);
+  // the row's parameters and the given token's logit, while the tile is on its way
   const RowIn in = row_in(P, r);
-#pragma unroll
-  for (int v = 0; v < L::kNV; ++v) vm[v] = max_of<L::kW>(xs + v * L::kW);
-  float tm = max_of<L::kNV>(vm);
+  const bool ranks = P.tokens && in.token >= 0 && (P.rank || in.t == 0.0f);
+  const float xt = ranks ? load_logit<DT>(row, in.token) : 0.0f;
+  float xs[kLE];
+  raw.values(row, P.V, tile, t, xs);
+  float tm = max_of<kLE>(xs);
   if (tm != tm) tm = INFINITY;
-  sm.tk[t] = f2key(tm);
+  const uint32_t mine = f2key(tm);
+  sm.tk[t] = mine;
   bar();
 
   uint32_t k4[kLW], k = 0;
@@ -395,72 +470,67 @@ __global__ __launch_bounds__(kLT) __attribute__((amdgpu_waves_per_eu(7))) void t
     k = max(k, k4[i]);
   }
   k = wave_max(k);
-  if (TOP && lead) {
-    const uint32_t low = find_low(k4, P.n_top);
-    if (lane() == 0) {
-      sm.low = low;
-      sm.count = 0;
-    }
-  }
+  const uint32_t low = TOP && lead ? find_low(k4, k, P.n_top) : 0u;
   const float m = k == kKeyNegInf ? 0.0f : key2f(k);
   const float c = scale32(P, in.t), mc = m * c;
   const bool fused = fabsf(mc) <= 4096.0f;                       // eta below 2^-12
+  // The sums without the terms of the tile's maximum, which are counted: they are 1 and 0 exactly, and where they are
+  // nearly all of S, log S lives in what the others add. Only waves that hold one have to look for them. They also go
+  // the careful way where the exponent needs its lower bound (a masked logit's 0 * -inf shows in the products, as a
+  // NaN does, which S tells) and in the row's last tile, whose unused places are -inf.
+  uint32_t tops = 0;
   {
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    auto sums = [&](auto exponent) {
+    bool careful = (tile + 1) * kTile > P.V || !fused || __ballot(mine == k) != 0;
+    if (!careful) {
 #pragma unroll
       for (int i = 0; i < kLE; ++i) {
-        const float z = exponent(xs[i]);
+        const float z = fmaf(xs[i], c, -mc);
         const float e = __builtin_amdgcn_exp2f(z);
         s[i & 3] += e;
         d[i & 3] = fmaf(e, z, d[i & 3]);
       }
-    };
-    if (fused) sums([&](float x) { return fmaf(x, c, -mc); });
-    else sums([&](float x) { return (x - m) * c; });
-    float dd = (d[0] + d[1]) + (d[2] + d[3]);
-    if (__ballot(dd != dd)) {   // a masked logit's 0 * -inf (or a NaN, which S tells): the products again, without it
-      d[0] = d[1] = d[2] = d[3] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kLE; ++i) {
-        float x = xs[i];
-        asm volatile("" : "+v"(x));   // computed anew: the first loop's values are not kept for this one
-        const float z = fmaxf(fused ? fmaf(x, c, -mc) : (x - m) * c, kZMin);
-        d[i & 3] = fmaf(__builtin_amdgcn_exp2f(z), z, d[i & 3]);
-      }
-      dd = (d[0] + d[1]) + (d[2] + d[3]);
+      const float dd = (d[0] + d[1]) + (d[2] + d[3]);
+      careful = __ballot(dd != dd) != 0;
     }
-    sm.sums[t] = make_float2((s[0] + s[1]) + (s[2] + s[3]), dd);
+    if (careful) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] = d[i] = 0.0f;
+      auto sums = [&](auto exponent) {
+#pragma unroll
+        for (int i = 0; i < kLE; ++i) {
+          float x = xs[i];
+          asm volatile("" : "+v"(x));   // computed anew: the first sums' values are not kept for these
+          const float z = fmaxf(exponent(x), kZMin);
+          const bool top = x == m;
+          tops += (uint32_t)__popcll(__ballot(top));
+          const float e = top ? 0.0f : __builtin_amdgcn_exp2f(z);
+          s[i & 3] += e;
+          d[i & 3] = fmaf(e, z, d[i & 3]);
+        }
+      };
+      if (fused) sums([&](float x) { return fmaf(x, c, -mc); });
+      else sums([&](float x) { return (x - m) * c; });
+    }
+    sm.sums[t] = make_float2((s[0] + s[1]) + (s[2] + s[3]), (d[0] + d[1]) + (d[2] + d[3]));
   }
-  if (P.tokens && in.token >= 0 && (P.rank || in.t == 0.0f)) {
-    const uint32_t above = wave_above<DT>(P, in, row, tile, xs);
-    if (lane() == 0) sm.redn[w] = above;
-  } else if (lane() == 0) {
-    sm.redn[w] = 0;
+  const uint32_t ahead = ranks ? wave_above<DT>(P, in, tile, xs, k, xt) : 0u;
+  if (lane() == 0) {
+    sm.redn[w] = ahead;
+    sm.redt[w] = tops;
   }
   bar();
 
-  if (TOP) {
-    const uint32_t low = sm.low;
-    const float low_f = key2f(low);
-#pragma unroll
-    for (int v = 0; v < L::kNV; ++v) {
-      if (!__ballot(vm[v] >= low_f)) continue;
-      const int at = Place<DT>(tile, t, v, P.V).at;
-#pragma unroll
-      for (int j = 0; j < L::kW; ++j)
-        if (xs[v * L::kW + j] >= low_f) append(sm, f2key(xs[v * L::kW + j]), (uint32_t)(at + j));
-    }
-  }
-  if (lead) {
+  if (w == (int)((blockIdx.x + 1) % kLW)) {
     double s = 0.0, d = 0.0;
-    uint32_t above = 0;
+    uint32_t above = 0, top = 0;
 #pragma unroll
     for (int i = 0; i < kLW; ++i) {
       const float2 q = sm.sums[64 * i + lane()];
       s += (double)q.x;
       d += (double)q.y;
       above += sm.redn[i];
+      top += sm.redt[i];
     }
     s = wave_sum_f64(s);
     d = wave_sum_f64(d);
@@ -470,9 +540,9 @@ __global__ __launch_bounds__(kLT) __attribute__((amdgpu_waves_per_eu(7))) void t
       s *= scale;
       d = d * scale - eta * s;
     }
-    Part* out = WHOLE ? &sm.part : P.part + blockIdx.x;
+    Part* out = WHOLE ? &sm.part : P.part + ((int64_t)r * P.tiles + tile);
     if (lane() == 0) {
-      out->s = s;
+      out->s = s + (double)top;
       out->d = d;
       out->m = key2f(k);
       out->above = above;
@@ -483,18 +553,18 @@ __global__ __launch_bounds__(kLT) __attribute__((amdgpu_waves_per_eu(7))) void t
     }
   }
   if (!TOP) return;
-  bar();
-  int count = (int)sm.count;
-  if (count > P.cap) {
-    bar();
-    exact_tile<DT>(sm, row, P.V, tile, P.n_top, sm.low);
-    count = P.n_top;
+  if (lead) {
+    const int count = tile_candidates<DT>(sm, row, P.V, tile, P.n_top, P.cap, low, k4);
+    if (WHOLE) {
+      if (lane() == 0) sm.count = (uint32_t)count;
+    } else {
+      uint2* out = P.cand + ((int64_t)r * P.tiles + tile) * P.cap;
+      for (int i = lane(); i < P.cap; i += 64) out[i] = i < count ? sm.list[i] : make_uint2(0u, 0u);
+    }
   }
   if (WHOLE) {
-    write_top(P, r, count, sm);
-  } else {
-    uint2* out = P.cand + (int64_t)blockIdx.x * P.cap;
-    if (t < P.cap) out[t] = t < count ? sm.list[t] : make_uint2(0u, 0u);
+    bar();
+    write_top(P, r, (int)sm.count, sm);
   }
 }
 
@@ -530,10 +600,13 @@ __global__ __launch_bounds__(kLT) void ts_logp_row_kernel(LParams P) {
     for (int i = 0; i <= kRowItems; ++i) tk = max(tk, c[i].x);
     sm.tk[threadIdx.x] = tk;
     bar();
-    uint32_t k4[kLW];
+    uint32_t k4[kLW], k = 0;
 #pragma unroll
-    for (int w = 0; w < kLW; ++w) k4[w] = sm.tk[64 * w + lane()];
-    const uint32_t low = find_low(k4, P.n_top);   // every wave for itself: there is nothing else to do
+    for (int w = 0; w < kLW; ++w) {
+      k4[w] = sm.tk[64 * w + lane()];
+      k = max(k, k4[w]);
+    }
+    const uint32_t low = find_low(k4, wave_max(k), P.n_top);   // every wave for itself: there is nothing else to do
     if (threadIdx.x == 0) sm.count = 0;
     bar();
 #pragma unroll
@@ -586,7 +659,8 @@ __device__ __forceinline__ void store_logit(char* row, int64_t i, float v) {
 template <int DT, bool ONCE>
 __global__ __launch_bounds__(kLT) __attribute__((amdgpu_waves_per_eu(8))) void ts_logp_grad_kernel(GParams P) {
   using L = Logits<DT>;
-  const int r = (int)(blockIdx.x / (unsigned)P.tiles), tile = (int)(blockIdx.x - (unsigned)r * (unsigned)P.tiles);
+  int r, tile;
+  place_block(P.tiles, r, tile);
   const char* row = P.x + (int64_t)r * P.x_stride;
   char* out = P.g + (int64_t)r * P.g_stride;
   const int t0 = tile * kTile + (int)threadIdx.x * L::kW;

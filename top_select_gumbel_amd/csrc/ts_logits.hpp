@@ -22,6 +22,7 @@ constexpr int kTile = kLT * kLE;  // 8192
 
 template <int DT>
 struct Logits {
+  static constexpr uint32_t kNegInf = DT == TS_DTYPE_F32 ? 0xFF800000u : DT == TS_DTYPE_BF16 ? 0xFF80FF80u : 0xFC00FC00u;   // a word of -inf
   static constexpr int kSize = DT == TS_DTYPE_F32 ? 4 : 2;
   static constexpr int kW = 16 / kSize;     // logits a vector
   static constexpr int kNV = kLE / kW;      // vectors a thread
@@ -72,38 +73,46 @@ struct Place {
   __device__ __forceinline__ bool counts(int j, int V) const { return at + j >= own && at + j < V; }
 };
 
-// The thread's kLE logits of a tile; what does not count is -inf. Every address lies in the row.
+// The thread's kLE logits of a tile: the loads, every address in the row, and later the values; what does not count is
+// -inf. (A row shorter than a vector is loaded with the values.)
 template <int DT>
-__device__ __forceinline__ void load_tile(const char* row, int V, int tile, int t, float* xs) {
+struct Tile {
   using L = Logits<DT>;
   u32x4 raw[L::kNV];
-  if ((tile + 1) * kTile <= V) {
-    const char* p = row + ((int64_t)tile * kTile + (int64_t)t * L::kW) * L::kSize;
+  __device__ __forceinline__ void load(const char* row, int V, int tile, int t) {
+    if ((tile + 1) * kTile <= V) {
+      const char* p = row + ((int64_t)tile * kTile + (int64_t)t * L::kW) * L::kSize;
 #pragma unroll
-    for (int v = 0; v < L::kNV; ++v) raw[v] = load16(p + v * (kLT * 16));
+      for (int v = 0; v < L::kNV; ++v) raw[v] = load16(p + v * (kLT * 16));
+    } else if (V >= L::kW) {
 #pragma unroll
-    for (int v = 0; v < L::kNV; ++v)
-#pragma unroll
-      for (int j = 0; j < L::kW; ++j) xs[v * L::kW + j] = unpack<DT>(raw[v], j);
-  } else if (V >= L::kW) {
-#pragma unroll
-    for (int v = 0; v < L::kNV; ++v) raw[v] = load16(row + (int64_t)Place<DT>(tile, t, v, V).at * L::kSize);
-#pragma unroll
-    for (int v = 0; v < L::kNV; ++v) {
-      const Place<DT> pl(tile, t, v, V);
-#pragma unroll
-      for (int j = 0; j < L::kW; ++j) xs[v * L::kW + j] = pl.at + j >= pl.own ? unpack<DT>(raw[v], j) : -INFINITY;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kLE; ++i) xs[i] = -INFINITY;
-    if (t == 0) {
-#pragma unroll
-      for (int j = 0; j < L::kW; ++j)
-        if (j < V) xs[j] = load_logit<DT>(row, j);
+      for (int v = 0; v < L::kNV; ++v) raw[v] = load16(row + (int64_t)Place<DT>(tile, t, v, V).at * L::kSize);
     }
   }
-}
+  __device__ __forceinline__ void values(const char* row, int V, int tile, int t, float* xs) const {
+    if ((tile + 1) * kTile <= V) {
+#pragma unroll
+      for (int v = 0; v < L::kNV; ++v)
+#pragma unroll
+        for (int j = 0; j < L::kW; ++j) xs[v * L::kW + j] = unpack<DT>(raw[v], j);
+    } else if (V >= L::kW) {
+#pragma unroll
+      for (int v = 0; v < L::kNV; ++v) {
+        const Place<DT> pl(tile, t, v, V);
+#pragma unroll
+        for (int j = 0; j < L::kW; ++j) xs[v * L::kW + j] = pl.at + j >= pl.own ? unpack<DT>(raw[v], j) : -INFINITY;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLE; ++i) xs[i] = -INFINITY;
+      if (t == 0) {
+#pragma unroll
+        for (int j = 0; j < L::kW; ++j)
+          if (j < V) xs[j] = load_logit<DT>(row, j);
+      }
+    }
+  }
+};
 
 // 1/T in the base-2 exponent. A temperature below 2^-100 acts as 2^-100: beside the maximum every
 // logit more than 2^-93 below it has weight 0 there, as it would at the smaller one.
