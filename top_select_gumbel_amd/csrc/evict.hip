@@ -185,7 +185,8 @@ __device__ __forceinline__ void sum_slots(const EParams& P, int r, int j, int n,
 template <int DT>
 __global__ __launch_bounds__(kST) void ts_evict_sum_kernel(EParams P) {
   __shared__ uint32_t red[3 * kST / 64];
-  const int r = (int)(blockIdx.x / (unsigned)P.tiles), tile = (int)(blockIdx.x - (unsigned)r * (unsigned)P.tiles);
+  int r, tile;
+  tsl::place_block(P.tiles, r, tile);
   const int n = row_length(P, r);
   const int j = tile * kSumTile + (int)threadIdx.x * kSumSlots;
   uint32_t newest = 0, kmin = 0xFFFFFFFFu, kmax = 0;
@@ -732,7 +733,8 @@ __global__ __launch_bounds__(kET) void ts_evict_bin_kernel(EParams P, int groups
 __global__ __launch_bounds__(kST) void ts_evict_list_kernel(EParams P) {
   __shared__ uint32_t red[3 * kSW];
   __shared__ uint32_t res[3];
-  const int r = (int)(blockIdx.x / (unsigned)P.tiles), tile = (int)(blockIdx.x - (unsigned)r * (unsigned)P.tiles);
+  int r, tile;
+  tsl::place_block(P.tiles, r, tile);
   const int n = row_length(P, r), t = threadIdx.x;
   if (tile * kSumTile >= n) return;
   const Quad q = load_quad(P, r, tile * kSumTile, n);
@@ -953,7 +955,8 @@ __global__ __launch_bounds__(kET) void ts_evict_cut_kernel(EParams P) {
 
 __global__ __launch_bounds__(kST) void ts_evict_emit_kernel(EParams P) {
   __shared__ uint32_t red[3 * kSW];
-  const int r = (int)(blockIdx.x / (unsigned)P.tiles), tile = (int)(blockIdx.x - (unsigned)r * (unsigned)P.tiles);
+  int r, tile;
+  tsl::place_block(P.tiles, r, tile);
   const int n = row_length(P, r);
   if (tile * kSumTile >= n) return;
   const Quad q = load_quad(P, r, tile * kSumTile, n);
@@ -1166,7 +1169,7 @@ void with_unit(int unit, F f) {
 constexpr int64_t kFusedBytes = 128 << 10;   // weights of a row
 constexpr int64_t kFusedMoves = 256 << 10;   // cache bytes that a row can move
 
-constexpr int64_t kMoveGroups = 2048;        // workgroups that the moves of long rows are spread over, about,
+constexpr int64_t kMoveGroups = 1024;        // workgroups that the moves of long rows are spread over, about,
 constexpr int64_t kMoveParts = 32;           // and at most so many to a tile's
 
 template <int SRC>

@@ -295,16 +295,6 @@ __device__ __forceinline__ RowIn row_in(const LParams& P, int r) {
 }
 
 // ------------------------------------------------------------------ a tile
-// A workgroup's row and tile. Workgroups go to the eight XCDs in turn; each row starts at another tile, so that the rows'
-// last tiles, which cost another time than whole ones, do not all fall to one XCD (1777 rows of 16 tiles, bf16: 112 us
-// without it and with the masked loop below run after the other one, 85 us for rows of 16 whole tiles).
-__device__ __forceinline__ void place_block(int32_t tiles, int& r, int& tile) {
-  const unsigned b = blockIdx.x, n = (unsigned)tiles;
-  r = (int)(b / n);
-  const unsigned i = b - (unsigned)r * n + (unsigned)r % n;
-  tile = (int)(i >= n ? i - n : i);
-}
-
 // log2(e) / T rounded once, or nearly (r + r e is 1/T to twice fp32's bits, and kHi + kLo log2(e)).
 __device__ __forceinline__ float scale32(const LParams& P, float t) {
   constexpr float kHi = (float)kLog2e, kLo = (float)(kLog2e - (double)kHi);
@@ -422,9 +412,13 @@ __device__ __forceinline__ void write_top(const LParams& P, int r, int count, LS
   if (!ok || t >= count) return;
   const uint2 me = sm.list[t];
   int above = 0;
-  for (int i = 0; i < count; ++i) {
-    const uint2 o = sm.list[i];
-    above += (o.x > me.x || (o.x == me.x && o.y < me.y)) ? 1 : 0;
+  for (int i = 0; i < count; i += 8) {   // eight in flight: the last ones again past the end, which count once
+    uint2 o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = sm.list[min(i + e, count - 1)];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      above += i + e < count && (o[e].x > me.x || (o[e].x == me.x && o[e].y < me.y)) ? 1 : 0;
   }
   if (above >= P.n_top) return;
   idx[above] = (int32_t)me.y;
@@ -449,10 +443,11 @@ __global__ __launch_bounds__(kLT) __attribute__((amdgpu_waves_per_eu(7))) void t
   const int t = (int)threadIdx.x, w = __builtin_amdgcn_readfirstlane(wave());
   const bool lead = w == (int)(blockIdx.x % kLW);
   const char* row = P.x + (int64_t)r * P.stride;
+  // The given token's logit is asked for right behind the tile's, so that its wait is hidden behind theirs (1777 x 128256
+  // in bf16: about 95 us with ranks, 99 us where it was loaded after the tile had come, 83 us without ranks).
+  const RowIn in = row_in(P, r);
   Tile<DT> raw;
   raw.load(row, P.V, tile, t);
-  // the row's parameters and the given token's logit, while the tile is on its way
-  const RowIn in = row_in(P, r);
   const bool ranks = P.tokens && in.token >= 0 && (P.rank || in.t == 0.0f);
   const float xt = ranks ? load_logit<DT>(row, in.token) : 0.0f;
   float xs[kLE];
@@ -609,9 +604,20 @@ __global__ __launch_bounds__(kLT) void ts_logp_row_kernel(LParams P) {
     const uint32_t low = find_low(k4, wave_max(k), P.n_top);   // every wave for itself: there is nothing else to do
     if (threadIdx.x == 0) sm.count = 0;
     bar();
+    // a wave's share of the list, by one atomic
+    uint32_t hits = 0;
+#pragma unroll
+    for (int i = 0; i <= kRowItems; ++i) hits += c[i].x >= low ? 1u : 0u;
+    const uint32_t incl = wave_incl_scan(hits), all = wave_total(incl);
+    uint32_t at = 0;
+    if (all && lane() == 0) at = atomicAdd(&sm.count, all);
+    at = (uint32_t)__builtin_amdgcn_readfirstlane((int)at) + incl - hits;
 #pragma unroll
     for (int i = 0; i <= kRowItems; ++i)
-      if (c[i].x >= low) append(sm, c[i].x, c[i].y);
+      if (c[i].x >= low) {
+        if (at < (uint32_t)kCapMax) sm.list[at] = c[i];
+        ++at;
+      }
     bar();
     count = (int)sm.count;
     if (count > P.cap) {
