@@ -128,6 +128,35 @@ def test_cache_types_and_layouts(ctype, dim, v_dim, layout):
     check(2, 3, 130, 61, dim=dim, ctype=ctype, v_dim=v_dim, slots_first=layout == "slots", wide=3 if layout == "wide" else 0, seed=dim)
 
 
+@pytest.mark.parametrize("slots", [40, 2048, 2049, 9000])
+def test_keep_may_exceed_the_slots(slots):
+    check(2, 2, slots, slots + 300, lengths=[slots, 3, 0, slots - 1], dim=4, seed=slots)
+    check(2, 2, slots, slots + 300, lengths=[slots, 3, 0, slots - 1], keeps=[5, 2, 1, slots // 2], dim=4, seed=slots)
+
+
+def test_many_short_rows():
+    check(60, 10, 90, 41, n_w=1, dim=6, sinks=1, recent=4, seed=5)
+
+
+@pytest.mark.parametrize("slots", [300, 9000])
+def test_shared_weights_and_one_tensor_as_both_caches(slots):
+    """Weights broadcast over rows and over the weight rows, and keys that are their own values."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(3)
+    score = gpu(rng.random((4, slots)).astype(np.float32))
+    position = gpu(np.tile(np.arange(slots, dtype=np.int32), (4, 1)))
+    n, keep = gpu(np.full(4, slots, np.int32)), gpu(np.full(4, slots // 3, np.int32))
+    one = gpu(rng.random((1, 1, slots)).astype(np.float32))
+    k = caches(2, 2, slots, 8, "bfloat16", 3)
+    k2 = k.clone()
+    a = ts.ts_cache_evict(score, position, n, keep, slots // 3, weights=one.expand(4, 3, slots).contiguous(), k_cache=k)
+    b = ts.ts_cache_evict(score, position, n, keep, slots // 3, weights=one.expand(4, 3, slots), k_cache=k2, v_cache=k2)
+    assert all(torch.equal(x, y) for x, y in zip(a, b)) and torch.equal(k, k2)
+    c = ts.ts_cache_evict(score, position, n, keep, slots // 3, weights=one.expand(4, 3, slots)[:, :0])
+    d = ts.ts_cache_evict(score, position, n, keep, slots // 3)
+    assert all(torch.equal(x, y) for x, y in zip(c, d))
+
+
 def test_one_cache_or_none():
     torch = torch_cuda()
     rng = np.random.default_rng(2)

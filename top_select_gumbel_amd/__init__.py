@@ -491,7 +491,7 @@ def _cache(t, rows: int, slots: int, device, name: str):
                     raise TopSelectError(f"{name} has slots that share memory")
                 reach += stride * (n - 1)
     return _Cache(t.data_ptr(), b * size if nb > 1 else 0, h * size if nh > 1 else 0, max(s if ns > 1 else 0, dim) * size,
-                  dim * size), nh
+                  dim * size), max(nh, 1)
 
 
 class CacheEvict(NamedTuple):
@@ -537,6 +537,8 @@ def ts_cache_evict(score, position, lengths, keep, keep_max: int, weights=None, 
     if kc and vc and k_heads != v_heads:
         raise TopSelectError("k_cache and v_cache have different heads")
     empty = torch.empty
+    if keep_max < 1:
+        raise TopSelectError("keep_max must be at least 1")
     if in_place:
         if keep_max > slots:
             raise TopSelectError("in place, keep_max is at most the number of slots")

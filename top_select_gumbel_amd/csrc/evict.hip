@@ -40,12 +40,13 @@ template <int DT>
 constexpr int kSumBatch = DT == TS_DTYPE_F32 ? 8 : 16;   // weight rows a thread has in flight: 128 bytes
 constexpr int kRowBatch = 4;             // the same where a row kernel sums: few weight rows
 constexpr int kSumTile = kST * kSumSlots;
-constexpr int kET = 1024;                // threads of the row kernels
+constexpr int kET = 1024;                // threads of the row kernels, of rows of up to kSmallSlots slots 256
 constexpr int kEW = kET / 64;
+constexpr int kSmallT = 256;
+constexpr int kSmallSlots = 2 * 4 * kSmallT;
 constexpr int kEBits = 11;
 constexpr int kEBins = 1 << kEBits;
 constexpr int kMaxTiles = TS_EVICT_MAX_SLOTS / kSumTile;
-static_assert(kEBins == 2 * kET, "a thread owns two bins");
 constexpr int kRowSlots = 2 * 4 * kET;   // longest row held in registers: two 16-byte vectors a thread
 constexpr int kListRow = 256;            // slots of the cut's bin that are ranked rather than binned again, ...
 constexpr int kListLong = 4096;          // ... and that are listed for a long row's cut
@@ -243,6 +244,7 @@ struct ESmem {
 };
 
 // Exclusive prefix over the waves of two counts that every wave holds uniformly, and their totals.
+template <int NW>
 __device__ __forceinline__ void wave_offsets(ESmem& sm, uint32_t a, uint32_t b, uint32_t& ea, uint32_t& eb, uint32_t& ta,
                                              uint32_t& tb) {
   if (lane() == 0) {
@@ -252,7 +254,7 @@ __device__ __forceinline__ void wave_offsets(ESmem& sm, uint32_t a, uint32_t b, 
   bar();
   ea = eb = ta = tb = 0;
 #pragma unroll
-  for (int w = 0; w < kEW; ++w) {
+  for (int w = 0; w < NW; ++w) {
     const uint32_t x = sm.red[w], y = sm.red2[w];
     ea += w < wave() ? x : 0u;
     eb += w < wave() ? y : 0u;
@@ -261,9 +263,10 @@ __device__ __forceinline__ void wave_offsets(ESmem& sm, uint32_t a, uint32_t b, 
   }
   bar();
 }
+template <int NW>
 __device__ __forceinline__ uint32_t block_total(ESmem& sm, uint32_t per_wave) {
   uint32_t a, b, t, u;
-  wave_offsets(sm, per_wave, 0u, a, b, t, u);
+  wave_offsets<NW>(sm, per_wave, 0u, a, b, t, u);
   return t;
 }
 
@@ -284,21 +287,34 @@ struct Cut {
 };
 
 // Finds the bin of the need-th largest of the binned values: sm.res = {bin, count above it, count in it}.
+template <int NT>
 __device__ __forceinline__ void find_bin(ESmem& sm, uint32_t need) {
+  constexpr int kOwn = kEBins / NT;
   const int t = threadIdx.x;
-  const uint32_t c0 = sm.hist[2 * t], c1 = sm.hist[2 * t + 1];
-  const uint32_t incl = wave_incl_scan(c0 + c1);
+  uint32_t c[kOwn], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    c[i] = sm.hist[kOwn * t + i];
+    sum += c[i];
+  }
+  const uint32_t incl = wave_incl_scan(sum);
   uint32_t before, eb, all, tb;
-  wave_offsets(sm, wave_total(incl), 0u, before, eb, all, tb);
-  const uint32_t above = all - (before + incl);
-  if (above < need && above + c1 >= need) {
-    sm.res[0] = 2 * t + 1;
+  wave_offsets<NT / 64>(sm, wave_total(incl), 0u, before, eb, all, tb);
+  uint32_t above = all - (before + incl);
+  if (above < need && above + sum >= need) {
+    uint32_t bin = 0, in_bin = 0;
+    bool found = false;
+#pragma unroll
+    for (int i = kOwn - 1; i >= 0; --i) {
+      if (found) continue;
+      bin = kOwn * t + i;
+      in_bin = c[i];
+      found = above + c[i] >= need;
+      above += found ? 0u : c[i];
+    }
+    sm.res[0] = bin;
     sm.res[1] = above;
-    sm.res[2] = c1;
-  } else if (above + c1 < need && above + c1 + c0 >= need) {
-    sm.res[0] = 2 * t;
-    sm.res[1] = above + c1;
-    sm.res[2] = c0;
+    sm.res[2] = in_bin;
   }
   bar();
 }
@@ -324,20 +340,20 @@ __device__ __forceinline__ Cut rank_list(ESmem& sm, uint32_t count, uint32_t nee
 // The cut of a class: the need-th of its slots (1 <= need < their number). each(f) calls f(u, slot) for the calling
 // thread's slots of the class; ordered(bin_lo, need) finds the need-th slot, in slot order, whose u is bin_lo.
 // It lies among those with u >> lo == prefix.
-template <class E, class O>
+template <int NT, class E, class O>
 __device__ __forceinline__ Cut find_cut(ESmem& sm, int lo, uint32_t prefix, uint32_t need, E each, O ordered) {
   if (lo == 0) return Cut{prefix, ordered(prefix, need)};
   while (true) {
     const int d = min(kEBits, lo), sh = lo - d;
-    sm.hist[threadIdx.x] = 0u;
-    sm.hist[threadIdx.x + kET] = 0u;
+#pragma unroll
+    for (int i = 0; i < kEBins; i += NT) sm.hist[i + threadIdx.x] = 0u;
     bar();
     const uint32_t mask = (1u << d) - 1u;
     each([&](uint32_t u, int) {
       if (shr(u, lo) == prefix) atomicAdd(&sm.hist[(u >> sh) & mask], 1u);
     });
     bar();
-    find_bin(sm, need);
+    find_bin<NT>(sm, need);
     prefix = shl(prefix, d) | sm.res[0];
     need -= sm.res[1];
     const uint32_t in_bin = sm.res[2];
@@ -372,11 +388,12 @@ __device__ __forceinline__ Row row_of(const EParams& P, int r, uint32_t newest, 
 }
 
 // A rejected row: nothing of it changes, and outputs that are not its inputs are poisoned.
+template <int NT>
 __device__ __forceinline__ void reject_row(const EParams& P, int r, const Row& R) {
   int32_t* source = P.out_source + (int64_t)r * P.keep_max;
   float* score = P.out_score + (int64_t)r * P.out_score_stride;
   int32_t* place = P.out_position + (int64_t)r * P.out_position_stride;
-  for (int j = threadIdx.x; j < P.keep_max; j += kET) {
+  for (int j = threadIdx.x; j < P.keep_max; j += NT) {
     source[j] = -1;
     if (P.out_score != P.score) score[j] = __uint_as_float(0x7FC00000u);
     if (P.out_position != P.position) place[j] = -1;
@@ -436,6 +453,7 @@ __device__ __forceinline__ void copy_moves(const EParams& P, int r, const int32_
 }
 
 // The row's lists are whole: the freed slots' small outputs, the unused places, the length.
+template <int NT>
 __device__ __forceinline__ void finish_row(const EParams& P, int r, const Row& R, uint32_t moves) {
   const int32_t* pos = P.position + (int64_t)r * P.position_stride;
   const float* sum = P.sum + (int64_t)r * P.sum_stride;
@@ -444,14 +462,14 @@ __device__ __forceinline__ void finish_row(const EParams& P, int r, const Row& R
   int32_t* place = P.out_position + (int64_t)r * P.out_position_stride;
   const int32_t* hole = P.hole + (int64_t)r * P.cap;
   const int32_t* fill = P.fill + (int64_t)r * P.cap;
-  for (uint32_t i = threadIdx.x; i < moves; i += kET) {
+  for (uint32_t i = threadIdx.x; i < moves; i += NT) {
     const int h = hole[i], f = fill[i];
     source[h] = f;
     score[h] = sum[f];
     place[h] = pos[f];
   }
   bar_all();   // in place, the unused places below may be fillers' own
-  for (int j = R.k + (int)threadIdx.x; j < P.keep_max; j += kET) {
+  for (int j = R.k + (int)threadIdx.x; j < P.keep_max; j += NT) {
     source[j] = -1;
     score[j] = 0.0f;
     place[j] = -1;
@@ -513,9 +531,9 @@ __device__ __forceinline__ void emit4(const EParams& P, int r, const Row& R, int
   jf += count4(mf);
 }
 
-// SRC: the weights' type where the row is summed here, -1 where the sum kernel has run. NV: vectors a thread.
-template <int NV, int SRC, class U>
-__global__ __launch_bounds__(kET) void ts_evict_row_kernel(EParams P) {
+// NT threads. SRC: the weights' type where the row is summed here, -1 where the sum kernel has run. NV: vectors a thread.
+template <int NT, int NV, int SRC, class U>
+__global__ __launch_bounds__(NT) void ts_evict_row_kernel(EParams P) {
   __shared__ ESmem sm;
   const int r = (int)blockIdx.x, l = lane();
   const int n = row_length(P, r);
@@ -557,7 +575,7 @@ __global__ __launch_bounds__(kET) void ts_evict_row_kernel(EParams P) {
   }
   bar();
 #pragma unroll
-  for (int w = 0; w < kEW; ++w) {
+  for (int w = 0; w < NT / 64; ++w) {
     newest = max(newest, sm.red[w]);
     kmin = min(kmin, sm.red2[w]);
     kmax = max(kmax, sm.red3[w]);
@@ -565,7 +583,7 @@ __global__ __launch_bounds__(kET) void ts_evict_row_kernel(EParams P) {
   bar();
   const Row R = row_of(P, r, newest, kmin, kmax);
   if (R.st != TS_ROW_OK) {
-    reject_row(P, r, R);
+    reject_row<NT>(P, r, R);
     return;
   }
   // bit 4v + i: slot i of vector v is in use, is protected
@@ -578,14 +596,14 @@ __global__ __launch_bounds__(kET) void ts_evict_row_kernel(EParams P) {
       live |= (in ? 1u : 0u) << (4 * v + i);
       first |= (in && R.first(p[v][i]) ? 1u : 0u) << (4 * v + i);
     }
-  const uint32_t total = block_total(sm, wave_total(wave_incl_scan((uint32_t)__popc(first))));
+  const uint32_t total = block_total<NT / 64>(sm, wave_total(wave_incl_scan((uint32_t)__popc(first))));
   const bool among_first = total >= (uint32_t)R.k;
   const uint32_t need = among_first ? (uint32_t)R.k : (uint32_t)R.k - total;
   const uint32_t pool = among_first ? total : (uint32_t)n - total;
   const uint32_t cls = among_first ? first : live & ~first;   // the cut's class
   Cut cut{0u, 0xFFFFFFFFu};                                    // all of it
   if (need < pool) {
-    cut = find_cut(
+    cut = find_cut<NT>(
         sm, bitlen(kmax - kmin), 0u, need,
         [&](auto f) {
 #pragma unroll
@@ -604,7 +622,7 @@ __global__ __launch_bounds__(kET) void ts_evict_row_kernel(EParams P) {
             c += count4(m[v]);
           }
           uint32_t run, e, t0, t1;
-          wave_offsets(sm, c, 0u, run, e, t0, t1);
+          wave_offsets<NT / 64>(sm, c, 0u, run, e, t0, t1);
 #pragma unroll
           for (int v = 0; v < NV; ++v) {
 #pragma unroll
@@ -633,16 +651,16 @@ __global__ __launch_bounds__(kET) void ts_evict_row_kernel(EParams P) {
       cf += (uint32_t)__popcll(__ballot(j >= R.k && in));
     }
   uint32_t ih, jf, moves, tf;
-  wave_offsets(sm, ch, cf, ih, jf, moves, tf);
+  wave_offsets<NT / 64>(sm, ch, cf, ih, jf, moves, tf);
 #pragma unroll
   for (int v = 0; v < NV; ++v)
     emit4(P, r, R, base + 256 * v, (kept >> (4 * v)) & 15u, s[v], p[v], ih, jf, SRC >= 0);
   bar_all();
-  finish_row(P, r, R, moves);
+  finish_row<NT>(P, r, R, moves);
   if constexpr (!std::is_void_v<U>) {
     const int32_t* hole = P.hole + (int64_t)r * P.cap;
     const int32_t* fill = P.fill + (int64_t)r * P.cap;
-    if (P.k.units | P.v.units) copy_moves<U, kET>(P, r, hole, fill, 0, (int)moves);
+    if (P.k.units | P.v.units) copy_moves<U, NT>(P, r, hole, fill, 0, (int)moves);
   }
 }
 
@@ -864,7 +882,7 @@ __global__ __launch_bounds__(kET) void ts_evict_cut_kernel(EParams P) {
     P.row[r].tiles = (R.n + kSumTile - 1) / kSumTile;
   }
   if (R.st != TS_ROW_OK) {
-    reject_row(P, r, R);
+    reject_row<kET>(P, r, R);
     return;
   }
   const RowInfo I = P.row[r];
@@ -889,7 +907,7 @@ __global__ __launch_bounds__(kET) void ts_evict_cut_kernel(EParams P) {
       list[i] = make_uint2((uint32_t)P.hole[o], (uint32_t)P.fill[o]);
     }
     bar();
-    cut = find_cut(
+    cut = find_cut<kET>(
         sm, (int)I.lo, I.prefix, I.need,
         [&](auto f) {
           for (uint32_t i = t; i < I.in_bin; i += kET) f(list[i].x, (int)list[i].y);
@@ -926,7 +944,7 @@ __global__ __launch_bounds__(kET) void ts_evict_cut_kernel(EParams P) {
       uint32_t c = 0;
       for (int b = w0; b < w1; b += 64) c += (uint32_t)__popcll(__ballot(of_class(b + l) && R.u(sum[b + l]) == u));
       uint32_t run, e0, t0, t1;
-      wave_offsets(sm, c, 0u, run, e0, t0, t1);
+      wave_offsets<kEW>(sm, c, 0u, run, e0, t0, t1);
       if (run < nth && run + c >= nth) {
         for (int b = w0; b < w1; b += 64) {
           const uint64_t m = __ballot(of_class(b + l) && R.u(sum[b + l]) == u);
@@ -939,7 +957,7 @@ __global__ __launch_bounds__(kET) void ts_evict_cut_kernel(EParams P) {
     };
     if (umin == umax) cut = Cut{umin, ordered(umin, I.need)};
     else
-      cut = find_cut(
+      cut = find_cut<kET>(
           sm, (int)I.lo, I.prefix, I.need,
           [&](auto f) {
             for (int j = w0 + l; j < w1; j += 64)
@@ -1172,17 +1190,14 @@ constexpr int64_t kFusedMoves = 256 << 10;   // cache bytes that a row can move
 constexpr int64_t kMoveGroups = 1024;        // workgroups that the moves of long rows are spread over, about,
 constexpr int64_t kMoveParts = 32;           // and at most so many to a tile's
 
-template <int SRC>
-void launch_rows(const EParams& P, hipStream_t s) {
-  const dim3 grid((unsigned)P.rows), block(kET);
-  if (P.slots <= 4 * kET) hipLaunchKernelGGL((ts_evict_row_kernel<1, SRC, void>), grid, block, 0, s, P);
-  else hipLaunchKernelGGL((ts_evict_row_kernel<2, SRC, void>), grid, block, 0, s, P);
-}
+// The row kernel with the threads and vectors that hold the row: a fourth of the threads for short rows, of which then
+// several share a compute unit (U: the moves' unit, void: they are made elsewhere).
 template <int SRC, class U>
-void launch_whole(const EParams& P, hipStream_t s) {
-  const dim3 grid((unsigned)P.rows), block(kET);
-  if (P.slots <= 4 * kET) hipLaunchKernelGGL((ts_evict_row_kernel<1, SRC, U>), grid, block, 0, s, P);
-  else hipLaunchKernelGGL((ts_evict_row_kernel<2, SRC, U>), grid, block, 0, s, P);
+void launch_rows(const EParams& P, hipStream_t s) {
+  const dim3 grid((unsigned)P.rows);
+  if (P.slots <= kSmallSlots) hipLaunchKernelGGL((ts_evict_row_kernel<kSmallT, 2, SRC, U>), grid, dim3(kSmallT), 0, s, P);
+  else if (P.slots <= 4 * kET) hipLaunchKernelGGL((ts_evict_row_kernel<kET, 1, SRC, U>), grid, dim3(kET), 0, s, P);
+  else hipLaunchKernelGGL((ts_evict_row_kernel<kET, 2, SRC, U>), grid, dim3(kET), 0, s, P);
 }
 
 int check_cache(const ts_cache* c, const char* name) {
@@ -1309,12 +1324,12 @@ extern "C" int ts_cache_evict(const float* score, int64_t rows, int64_t slots, i
   };
   hipError_t e;
   if (move_here) {
-    with_type([&](auto dt) { with_unit(unit, [&](auto u) { launch_whole<dt(), decltype(u)>(P, s); }); });
+    with_type([&](auto dt) { with_unit(unit, [&](auto u) { launch_rows<dt(), decltype(u)>(P, s); }); });
     e = hipGetLastError();
     return e == hipSuccess ? TS_OK : fail(TS_ERR_LAUNCH, "eviction launch failed: %s", hipGetErrorString(e));
   }
   if (sum_here) {
-    with_type([&](auto dt) { launch_rows<dt()>(P, s); });
+    with_type([&](auto dt) { launch_rows<dt(), void>(P, s); });
   } else {
     const dim3 grid((unsigned)(rows * pl.tiles)), block(kST);
     with_type([&](auto dt) { hipLaunchKernelGGL(ts_evict_sum_kernel<dt()>, grid, block, 0, s, P); });
@@ -1335,7 +1350,7 @@ extern "C" int ts_cache_evict(const float* score, int64_t rows, int64_t slots, i
       e = hipGetLastError();
       return e == hipSuccess ? TS_OK : fail(TS_ERR_LAUNCH, "eviction launch failed: %s", hipGetErrorString(e));
     }
-    launch_rows<-1>(P, s);
+    launch_rows<-1, void>(P, s);
   }
   e = hipGetLastError();
   if (e != hipSuccess) return fail(TS_ERR_LAUNCH, "eviction row launch failed: %s", hipGetErrorString(e));
