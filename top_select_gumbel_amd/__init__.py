@@ -417,29 +417,32 @@ class TokenLogp(NamedTuple):
 def ts_token_logp(logits, tokens=None, temperature=None, n_top: int = 0, want_rank: bool = True,
                   want_entropy: bool = True, want_lse: bool = True, want_stats: bool = False) -> TokenLogp:
     """Log probabilities and ranks of given tokens (int32 [rows], -1: none) over whole rows of fp32, bf16
-    or fp16 logits, with entropy, log-sum-exp and the n_top best tokens."""
+    or fp16 logits, with entropy, log-sum-exp and the n_top best tokens. The outputs are views of one allocation."""
     torch = _t()
     lib = load_library()
     code, rows, v, stride = _typed_rows(logits, "logits")
     device = logits.device
     tok = _param(tokens, torch.int32, rows, device, "tokens")
     temp = _param(temperature, torch.float32, rows, device, "temperature")
-    f, i = torch.float32, torch.int32
-    empty = torch.empty
-    logp = empty(rows, dtype=f, device=device) if tokens is not None else None
-    rank = empty(rows, dtype=i, device=device) if tokens is not None and want_rank else None
-    entropy = empty(rows, dtype=f, device=device) if want_entropy else None
-    lse = empty(rows, dtype=f, device=device) if want_lse else None
-    top_idx = empty((rows, n_top), dtype=i, device=device) if n_top > 0 else None
-    top_logp = empty((rows, n_top), dtype=f, device=device) if n_top > 0 else None
-    stats = empty((rows, 4), dtype=f, device=device) if want_stats else None
-    status = empty(rows, dtype=i, device=device)
+    # One allocation for the outputs, then views of it: eight of their own cost twice the kernels' time of a small call.
+    i = torch.int32
+    given, top = tokens is not None, max(n_top, 0)
+    sizes = [4 * rows if want_stats else 0, rows if given else 0, rows if want_entropy else 0, rows if want_lse else 0,
+             rows * top, rows if given and want_rank else 0, rows, rows * top]
+    flat = torch.empty(sum(sizes), dtype=torch.float32, device=device)
+    parts, at, ptrs = flat.split_with_sizes(sizes), flat.data_ptr(), []
+    for n in sizes:
+        ptrs.append(at if n else None)
+        at += 4 * n
     # A workspace of the call's own: two calls captured into graphs that replay at once share none.
     nb = 0 if v <= TS_LOGP_TILE else lib.ts_workspace_bytes(TS_OP_TOKEN_LOGP, rows, v, n_top)
-    ws = empty(nb, dtype=torch.uint8, device=device) if nb else None
-    _call(device, lib.ts_token_logp, logits.data_ptr(), code, rows, v, stride, tok, temp, n_top, _ptr(logp), _ptr(rank),
-          _ptr(entropy), _ptr(lse), _ptr(top_idx), _ptr(top_logp), _ptr(stats), status.data_ptr(), _ptr(ws), nb)
-    return TokenLogp(logp, rank, entropy, lse, top_idx, top_logp, stats, status)
+    ws = torch.empty(nb, dtype=torch.uint8, device=device) if nb else None
+    _call(device, lib.ts_token_logp, logits.data_ptr(), code, rows, v, stride, tok, temp, n_top, ptrs[1], ptrs[5], ptrs[2], ptrs[3],
+          ptrs[7], ptrs[4], ptrs[0], ptrs[6], _ptr(ws), nb)
+    return TokenLogp(parts[1] if given else None, parts[5].view(i) if given and want_rank else None,
+                     parts[2] if want_entropy else None, parts[3] if want_lse else None,
+                     parts[7].view(i).view(rows, top) if top else None, parts[4].view(rows, top) if top else None,
+                     parts[0].view(rows, 4) if want_stats else None, parts[6].view(i))
 
 
 def ts_token_logp_backward(logits, tokens, temperature, stats, grad_logp=None, grad_entropy=None, grad_lse=None, out=None):
