@@ -178,6 +178,29 @@ def test_wide_range_of_magnitudes():
     check(torch.from_numpy(x).cuda(), [100, 200, 8999, 0], [1.0, 1e-6, 50.0, 1e-30], 3, "magnitudes")
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("v", [6, 8192, 20011, 60000])
+def test_confident_rows_keep_their_small_log_probabilities(v, dtype):
+    # one token far above equal others: logp = -log1p((v - 1) exp(-d)), whose terms carry (3 d + 2) u and whose fp32 sums 9 u
+    # more; with the output's rounding the relative error is at most (3 d + 12) u. S itself is a binary64 number from 1 to 2,
+    # rounded in the tile, in its join with the others (a product and a sum each) and in the logarithm: at most 5 times
+    # 2^-53, absolutely, which only logp below 1e-9 feels
+    torch = torch_cuda()
+    gaps, t = [4.0, 9.0, 12.0, 16.0, 20.0, 24.0], 0.75
+    x = torch.full((len(gaps), v), 1.25)
+    where = [0, v - 1, v // 2, min(8191, v - 1), min(8192, v - 1), 1]
+    for r, (g, at) in enumerate(zip(gaps, where)):
+        x[r, at] = 1.25 + g
+    x = x.to(getattr(torch, dtype)).cuda()
+    for tv in (1.0, t):
+        r = ts.ts_token_logp(x, i32(where), f32([tv] * len(gaps)), n_top=1)
+        for i, g in enumerate(gaps):
+            d = float(x[i, where[i]].double() - 1.25) / oracle.to_f32(tv)
+            want = -math.log1p((v - 1) * math.exp(-d))
+            for got in (float(r.logp[i]), float(r.top_logp[i, 0])):
+                assert abs(got - want) <= (3 * d + 12) * U * abs(want) + 5 * 2.0 ** -53, (i, got, want)
+
+
 @pytest.mark.parametrize("v,dtype", [(151936, "float32"), (128256, "bfloat16"), (300007, "float16")])
 def test_long_rows(v, dtype):
     rng = np.random.default_rng(9)

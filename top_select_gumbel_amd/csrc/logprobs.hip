@@ -73,7 +73,7 @@ struct LSmem {
   uint2 list[kCapMax];         // (key, id), in no order
   uint8_t who[kLT];            // threads with candidates
   uint32_t count;
-  uint32_t redn[kLW], redt[kLW];
+  uint32_t redn[kLW];
   Part part;
   float m;
   double log_s, c2;
@@ -426,6 +426,29 @@ __device__ __forceinline__ void write_top(const LParams& P, int r, int count, LS
   lp[above] = ok == 2 ? (above == 0 ? 0.0f : -INFINITY) : fminf(v, 0.0f);
 }
 
+// A tile's sum of 2^z without its one largest logit, by one wave: where that term, 1, is nearly all of S, log S lives in
+// what the others add, which the fp32 sum of the thread that holds it has rounded away. That thread's other logits are
+// read again. (Sums below 1.5 have one largest logit.)
+template <int DT, class E>
+__device__ __forceinline__ double sum_beside_top(const LSmem& sm, const char* row, int V, int tile, const uint32_t* k4, uint32_t k,
+                                                 float m, E exponent) {
+  using L = Logits<DT>;
+  int top = 0;
+#pragma unroll
+  for (int i = kLW - 1; i >= 0; --i) {
+    const uint64_t at = __ballot(k4[i] == k);
+    if (at) top = 64 * i + __ffsll((unsigned long long)at) - 1;
+  }
+  const int e = lane() & (kLE - 1), j = e % L::kW;
+  const Place<DT> pl(tile, top, e / L::kW, V);
+  const bool counts = lane() < kLE && pl.counts(j, V);
+  const float x = counts ? load_logit<DT>(row, pl.at + j) : m;
+  double s = x == m ? 0.0 : (double)__builtin_amdgcn_exp2f(exponent(x));
+#pragma unroll
+  for (int i = 0; i < kLW; ++i) s += 64 * i + lane() == top ? 0.0 : (double)sm.sums[64 * i + lane()].x;
+  return wave_sum_f64(s);
+}
+
 // The exponent of a term is z = fma(x, c, -fl(m c)), c = log2(e) / T: one operation and one rounding, and off by the
 // same eta = m c - fl(m c) in every term, which is known exactly (an fma) and taken out of the sums at the end. Where
 // |m c| is so large that 2^-eta needs more than the terms taken below, z is (x - m) c.
@@ -454,8 +477,7 @@ __global__ __launch_bounds__(kLT) __attribute__((amdgpu_waves_per_eu(7))) void t
   raw.values(row, P.V, tile, t, xs);
   float tm = max_of<kLE>(xs);
   if (tm != tm) tm = INFINITY;
-  const uint32_t mine = f2key(tm);
-  sm.tk[t] = mine;
+  sm.tk[t] = f2key(tm);
   bar();
 
   uint32_t k4[kLW], k = 0;
@@ -469,14 +491,11 @@ __global__ __launch_bounds__(kLT) __attribute__((amdgpu_waves_per_eu(7))) void t
   const float m = k == kKeyNegInf ? 0.0f : key2f(k);
   const float c = scale32(P, in.t), mc = m * c;
   const bool fused = fabsf(mc) <= 4096.0f;                       // eta below 2^-12
-  // The sums without the terms of the tile's maximum, which are counted: they are 1 and 0 exactly, and where they are
-  // nearly all of S, log S lives in what the others add. Only waves that hold one have to look for them. They also go
-  // the careful way where the exponent needs its lower bound (a masked logit's 0 * -inf shows in the products, as a
-  // NaN does, which S tells) and in the row's last tile, whose unused places are -inf.
-  uint32_t tops = 0;
   {
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    bool careful = (tile + 1) * kTile > P.V || !fused || __ballot(mine == k) != 0;
+    // The exponent's lower bound is left out at first, where nothing is known to need it: a masked logit's 0 * -inf shows
+    // in the products (as a NaN does, which S tells). The unused places of the row's last tile are -inf.
+    bool careful = (tile + 1) * kTile > P.V || !fused;
     if (!careful) {
 #pragma unroll
       for (int i = 0; i < kLE; ++i) {
@@ -497,9 +516,7 @@ __global__ __launch_bounds__(kLT) __attribute__((amdgpu_waves_per_eu(7))) void t
           float x = xs[i];
           asm volatile("" : "+v"(x));   // computed anew: the first sums' values are not kept for these
           const float z = fmaxf(exponent(x), kZMin);
-          const bool top = x == m;
-          tops += (uint32_t)__popcll(__ballot(top));
-          const float e = top ? 0.0f : __builtin_amdgcn_exp2f(z);
+          const float e = __builtin_amdgcn_exp2f(z);
           s[i & 3] += e;
           d[i & 3] = fmaf(e, z, d[i & 3]);
         }
@@ -510,34 +527,33 @@ __global__ __launch_bounds__(kLT) __attribute__((amdgpu_waves_per_eu(7))) void t
     sm.sums[t] = make_float2((s[0] + s[1]) + (s[2] + s[3]), (d[0] + d[1]) + (d[2] + d[3]));
   }
   const uint32_t ahead = ranks ? wave_above<DT>(P, in, tile, xs, k, xt) : 0u;
-  if (lane() == 0) {
-    sm.redn[w] = ahead;
-    sm.redt[w] = tops;
-  }
+  if (lane() == 0) sm.redn[w] = ahead;
   bar();
 
   if (w == (int)((blockIdx.x + 1) % kLW)) {
     double s = 0.0, d = 0.0;
-    uint32_t above = 0, top = 0;
+    uint32_t above = 0;
 #pragma unroll
     for (int i = 0; i < kLW; ++i) {
       const float2 q = sm.sums[64 * i + lane()];
       s += (double)q.x;
       d += (double)q.y;
       above += sm.redn[i];
-      top += sm.redt[i];
     }
     s = wave_sum_f64(s);
     d = wave_sum_f64(d);
+    double scale = 1.0;
     if (fused) {
       const double eta = (double)fmaf(m, c, -mc), y = eta * kLn2;
-      const double scale = 1.0 + y * (-1.0 + y * (0.5 - y * (1.0 / 6.0)));   // 2^-eta, within 1e-15 of it
+      scale = 1.0 + y * (-1.0 + y * (0.5 - y * (1.0 / 6.0)));   // 2^-eta, within 1e-15 of it
       s *= scale;
       d = d * scale - eta * s;
     }
+    if (s < 1.5 && k != kKeyNegInf)
+      s = 1.0 + scale * sum_beside_top<DT>(sm, row, P.V, tile, k4, k, m, [&](float x) { return fused ? fmaf(x, c, -mc) : (x - m) * c; });
     Part* out = WHOLE ? &sm.part : P.part + ((int64_t)r * P.tiles + tile);
     if (lane() == 0) {
-      out->s = s + (double)top;
+      out->s = s;
       out->d = d;
       out->m = key2f(k);
       out->above = above;
