@@ -31,7 +31,6 @@ using tsh::fail;
 namespace {
 
 constexpr int kLW = kLT / 64;        // waves a tile
-constexpr int kRowItems = 8;         // candidates a thread takes at a time when a row is finished
 constexpr double kLn2 = 0.6931471805599453;
 
 // What a tile leaves for its row: its maximum (NaN seen: +inf; nothing but -inf: -inf), the sums of 2^z and
@@ -65,7 +64,7 @@ struct LParams {
 // Candidates kept a tile: at least n, and room for the threads that hold several.
 __host__ __device__ constexpr int cand_cap(int n) { return n ? (2 * n + 32 + 15) / 16 * 16 : 0; }
 constexpr int kCapMax = cand_cap(TS_LOGP_TOP_MAX);
-static_assert(kCapMax <= kLT, "a thread ranks one candidate");
+static_assert((kCapMax + 63) / 64 <= 4, "what is left of the candidates joins the four groups of a lane");
 
 struct LSmem {
   uint32_t tk[kLT];            // each thread's largest key
@@ -95,24 +94,9 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
   return __longlong_as_double((long long)readlane64((uint64_t)__double_as_longlong(v), 63));
 }
 
-// ------------------------------------------------------------------ the best n of a workgroup's items
-// Sum over the workgroup of a count that every lane of a wave holds.
-__device__ __forceinline__ uint32_t block_count(LSmem& sm, uint32_t c) {
-  if (lane() == 0) sm.redn[wave()] = c;
-  bar();
-  uint32_t s = 0;
-#pragma unroll
-  for (int w = 0; w < kLW; ++w) s += sm.redn[w];
-  bar();
-  return s;
-}
-__device__ __forceinline__ void append(LSmem& sm, uint32_t key, uint32_t id) {
-  const uint32_t at = atomicAdd(&sm.count, 1u);
-  if (at < (uint32_t)kCapMax) sm.list[at] = make_uint2(key, id);
-}
-
-// A bound that at least n of the workgroup's items reach and, where large items are spread over the threads, few
-// more: about the n-th largest of the threads' largest keys (keys up to that of -inf are absent items). Called by one
+// ------------------------------------------------------------------ the best n
+// A bound that at least n of some items reach and, where large items are spread over their 256 groups, few more: about the
+// n-th largest of the groups' largest keys (keys up to that of -inf are absent items). Called by one
 // wave, which has four of those keys a lane in k4; kmax is the largest. The bits above the highest one in which they differ
 // are common to all; the others are found one by one.
 __device__ __forceinline__ uint32_t find_low(const uint32_t* k4, uint32_t kmax, int n) {
@@ -250,7 +234,7 @@ __device__ __forceinline__ int tile_candidates(LSmem& sm, const char* row, int V
   return (int)put;
 }
 
-// The exact best n of items that the threads hold N each, found bit by bit: the n-th largest key, then, among those
+// The exact best n of items that a wave's lanes hold N each, found bit by bit: the n-th largest key, then, among those
 // equal to it, the id of the last that stays (ids are below 2^30 and differ).
 template <int N>
 __device__ __forceinline__ void exact_items(LSmem& sm, const uint2* c, int n) {
@@ -258,24 +242,29 @@ __device__ __forceinline__ void exact_items(LSmem& sm, const uint2* c, int n) {
     uint32_t k = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) k += (uint32_t)__popcll(__ballot(pred(c[i])));
-    return block_count(sm, k);
+    return k;
   };
   uint32_t t = 0, last = 0;
+#pragma nounroll
   for (int b = 31; b >= 0; --b) {
     const uint32_t u = t | (1u << b);
     if (count([&](const uint2& q) { return q.x >= u; }) >= (uint32_t)n) t = u;
   }
   const uint32_t need = n - count([&](const uint2& q) { return q.x > t; });
+#pragma nounroll
   for (int b = 29; b >= 0; --b) {
     const uint32_t u = last | (1u << b);
     if (count([&](const uint2& q) { return q.x == t && q.y < u; }) < need) last = u;
   }
-  if (threadIdx.x == 0) sm.count = 0;
-  bar();
+  uint32_t put = 0;
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (c[i].x > t || (c[i].x == t && c[i].y <= last)) append(sm, c[i].x, c[i].y);
-  bar();
+  for (int i = 0; i < N; ++i) {
+    const bool in = c[i].x > t || (c[i].x == t && c[i].y <= last);
+    const uint64_t m = __ballot(in);
+    const uint32_t o = put + mbcnt(m);
+    if (in && o < (uint32_t)kCapMax) sm.list[o] = c[i];
+    put += (uint32_t)__popcll(m);
+  }
 }
 
 // ------------------------------------------------------------------ a row's parameters
@@ -399,31 +388,33 @@ __device__ __forceinline__ void finish_row(const LParams& P, const RowIn& in, in
   }
 }
 
-// Ranks the `count` candidates of sm.list and writes the row's n_top alternatives.
-__device__ __forceinline__ void write_top(const LParams& P, int r, int count, LSmem& sm) {
-  const int t = threadIdx.x;
+// Ranks the `count` candidates of sm.list and writes the row's n_top alternatives; called by one wave, after finish_row.
+__device__ __forceinline__ void write_top(const LParams& P, int r, int count, const LSmem& sm) {
   int32_t* idx = P.top_idx + (int64_t)r * P.n_top;
   float* lp = P.top_logp + (int64_t)r * P.n_top;
   const int ok = sm.ok;
-  if (t < P.n_top && (!ok || t >= count)) {
-    idx[t] = -1;
-    lp[t] = ok ? -INFINITY : __uint_as_float(0x7FC00000u);
+  const float unused = ok ? -INFINITY : __uint_as_float(0x7FC00000u);
+  if (!ok) count = 0;
+  for (int i = count + lane(); i < P.n_top; i += 64) {
+    idx[i] = -1;
+    lp[i] = unused;
   }
-  if (!ok || t >= count) return;
-  const uint2 me = sm.list[t];
-  int above = 0;
-  for (int i = 0; i < count; i += 8) {   // eight in flight: the last ones again past the end, which count once
-    uint2 o[8];
+  for (int i = lane(); i < count; i += 64) {
+    const uint2 me = sm.list[i];
+    int above = 0;
+    for (int j = 0; j < count; j += 8) {   // eight in flight; past the end the last one again, not counted
+      uint2 o[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = sm.list[min(i + e, count - 1)];
+      for (int e = 0; e < 8; ++e) o[e] = sm.list[min(j + e, count - 1)];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      above += i + e < count && (o[e].x > me.x || (o[e].x == me.x && o[e].y < me.y)) ? 1 : 0;
+      for (int e = 0; e < 8; ++e)
+        above += j + e < count && (o[e].x > me.x || (o[e].x == me.x && o[e].y < me.y)) ? 1 : 0;
+    }
+    if (above >= P.n_top) continue;
+    idx[above] = (int32_t)me.y;
+    const float v = (float)(((double)key2f(me.x) - (double)sm.m) * sm.c2 * kLn2 - sm.log_s);
+    lp[above] = ok == 2 ? (above == 0 ? 0.0f : -INFINITY) : fminf(v, 0.0f);
   }
-  if (above >= P.n_top) return;
-  idx[above] = (int32_t)me.y;
-  const float v = (float)(((double)key2f(me.x) - (double)sm.m) * sm.c2 * kLn2 - sm.log_s);
-  lp[above] = ok == 2 ? (above == 0 ? 0.0f : -INFINITY) : fminf(v, 0.0f);
 }
 
 // A tile's sum of 2^z without its one largest logit, by one wave: where that term, 1, is nearly all of S, log S lives in
@@ -567,7 +558,7 @@ __global__ __launch_bounds__(kLT) __attribute__((amdgpu_waves_per_eu(7))) void t
   if (lead) {
     const int count = tile_candidates<DT>(sm, row, P.V, tile, P.n_top, P.cap, low, k4);
     if (WHOLE) {
-      if (lane() == 0) sm.count = (uint32_t)count;
+      sm.count = (uint32_t)count;
     } else {
       uint2* out = P.cand + ((int64_t)r * P.tiles + tile) * P.cap;
       for (int i = lane(); i < P.cap; i += 64) out[i] = i < count ? sm.list[i] : make_uint2(0u, 0u);
@@ -575,75 +566,67 @@ __global__ __launch_bounds__(kLT) __attribute__((amdgpu_waves_per_eu(7))) void t
   }
   if (WHOLE) {
     bar();
-    write_top(P, r, (int)sm.count, sm);
+    if (lead) write_top(P, r, (int)sm.count, sm);
   }
 }
 
-// One row a wave without alternatives, one row a workgroup with them.
-template <int DT, bool TOP>
+// One row a wave.
+template <int DT>
 __global__ __launch_bounds__(kLT) void ts_logp_row_kernel(LParams P) {
+  const int r = (int)(blockIdx.x * kLW + wave());
+  if (r < P.rows) finish_row<DT>(P, row_in(P, r), r, P.part + (int64_t)r * P.tiles, nullptr);
+}
+
+// One row a workgroup of two waves: one joins the tiles, the other finds the best n of the candidates meanwhile, 24 a lane
+// at a time (four groups of six: find_low's 256 groups) and what is left of the ones before.
+template <int DT>
+__global__ __launch_bounds__(128) void ts_logp_top_kernel(LParams P) {
   __shared__ LSmem sm;
-  const int r = TOP ? (int)blockIdx.x : (int)(blockIdx.x * kLW + wave());
-  if (r >= P.rows) return;
-  if (!TOP) {
-    finish_row<DT>(P, row_in(P, r), r, P.part + (int64_t)r * P.tiles, nullptr);
-    return;
-  }
-  const uint2* cand = P.cand + (int64_t)r * P.tiles * P.cap;
-  const int64_t n = (int64_t)P.tiles * P.cap;
-  uint2 c[kRowItems + 1];
-  auto load = [&](int64_t base) {
-#pragma unroll
-    for (int i = 0; i < kRowItems; ++i) {
-      const int64_t at = base + i * kLT + threadIdx.x;
-      c[i] = at < n ? cand[at] : make_uint2(0u, 0u);
-    }
-  };
-  load(0);   // in flight while wave 0 joins the tiles
-  if (wave() == 0) finish_row<DT>(P, row_in(P, r), r, P.part + (int64_t)r * P.tiles, &sm);
+  constexpr int kGroup = 6, kItems = 4 * kGroup, kLeft = (kCapMax + 63) / 64;
+  const int r = (int)blockIdx.x, l = lane();
   int count = 0;
-  for (int64_t base = 0; base < n; base += kLT * kRowItems) {
-    if (base) load(base);
-    // what is left of the slots before takes part again
-    c[kRowItems] = (int)threadIdx.x < count ? sm.list[threadIdx.x] : make_uint2(0u, 0u);
-    uint32_t tk = 0;
+  if (wave() == 0) {
+    finish_row<DT>(P, row_in(P, r), r, P.part + (int64_t)r * P.tiles, &sm);
+  } else {
+    const uint2* cand = P.cand + (int64_t)r * P.tiles * P.cap;
+    const int64_t n = (int64_t)P.tiles * P.cap;
+    for (int64_t base = 0; base < n; base += 64 * kItems) {
+      uint2 c[kItems + kLeft];
 #pragma unroll
-    for (int i = 0; i <= kRowItems; ++i) tk = max(tk, c[i].x);
-    sm.tk[threadIdx.x] = tk;
-    bar();
-    uint32_t k4[kLW], k = 0;
-#pragma unroll
-    for (int w = 0; w < kLW; ++w) {
-      k4[w] = sm.tk[64 * w + lane()];
-      k = max(k, k4[w]);
-    }
-    const uint32_t low = find_low(k4, wave_max(k), P.n_top);   // every wave for itself: there is nothing else to do
-    if (threadIdx.x == 0) sm.count = 0;
-    bar();
-    // a wave's share of the list, by one atomic
-    uint32_t hits = 0;
-#pragma unroll
-    for (int i = 0; i <= kRowItems; ++i) hits += c[i].x >= low ? 1u : 0u;
-    const uint32_t incl = wave_incl_scan(hits), all = wave_total(incl);
-    uint32_t at = 0;
-    if (all && lane() == 0) at = atomicAdd(&sm.count, all);
-    at = (uint32_t)__builtin_amdgcn_readfirstlane((int)at) + incl - hits;
-#pragma unroll
-    for (int i = 0; i <= kRowItems; ++i)
-      if (c[i].x >= low) {
-        if (at < (uint32_t)kCapMax) sm.list[at] = c[i];
-        ++at;
+      for (int i = 0; i < kItems; ++i) {
+        const int64_t at = base + 64 * i + l;
+        c[i] = at < n ? cand[at] : make_uint2(0u, 0u);
       }
-    bar();
-    count = (int)sm.count;
-    if (count > P.cap) {
-      bar();
-      exact_items<kRowItems + 1>(sm, c, P.n_top);
-      count = P.n_top;
+#pragma unroll
+      for (int i = 0; i < kLeft; ++i) c[kItems + i] = 64 * i + l < count ? sm.list[64 * i + l] : make_uint2(0u, 0u);
+      wave_lds_sync();
+      uint32_t k4[4], k = 0;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        k4[g] = g < kLeft ? c[kItems + g].x : 0u;
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) k4[g] = max(k4[g], c[g * kGroup + i].x);
+        k = max(k, k4[g]);
+      }
+      const uint32_t low = find_low(k4, wave_max(k), P.n_top);
+      count = 0;
+#pragma unroll
+      for (int i = 0; i < kItems + kLeft; ++i) {
+        const uint64_t m = __ballot(c[i].x >= low);
+        if (!m) continue;
+        const int o = count + (int)mbcnt(m);
+        if (c[i].x >= low && o < kCapMax) sm.list[o] = c[i];
+        count += __popcll(m);
+      }
+      if (count > P.cap) {
+        exact_items<kItems + kLeft>(sm, c, P.n_top);
+        count = P.n_top;
+      }
+      wave_lds_sync();
     }
   }
   bar();
-  write_top(P, r, count, sm);
+  if (wave() == 1) write_top(P, r, count, sm);
 }
 
 // ------------------------------------------------------------------ gradient
@@ -771,8 +754,8 @@ hipError_t launch_logp(const LParams& P, hipStream_t s) {
   else hipLaunchKernelGGL((ts_logp_tile_kernel<DT, false, false>), tiles, block, 0, s, P);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (top) hipLaunchKernelGGL((ts_logp_row_kernel<DT, true>), dim3((unsigned)P.rows), block, 0, s, P);
-  else hipLaunchKernelGGL((ts_logp_row_kernel<DT, false>), dim3((unsigned)((P.rows + kLW - 1) / kLW)), block, 0, s, P);
+  if (top) hipLaunchKernelGGL((ts_logp_top_kernel<DT>), dim3((unsigned)P.rows), dim3(128), 0, s, P);
+  else hipLaunchKernelGGL((ts_logp_row_kernel<DT>), dim3((unsigned)((P.rows + kLW - 1) / kLW)), block, 0, s, P);
   return hipGetLastError();
 }
 
