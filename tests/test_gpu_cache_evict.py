@@ -233,6 +233,14 @@ def test_long_protected_positions(slots, sinks, recent):
     check(1, 1, slots, 5000, sinks=sinks, recent=recent, dim=2, ties=2, n_w=1, seed=slots)
 
 
+@pytest.mark.parametrize("slots,keep", [(8193, 8000), (16384, 900), (16385, 16000), (12000, 12000)])
+def test_many_rows_of_middle_length(slots, keep):
+    # 64 rows and more are held in registers up to 16384 slots
+    check(16, 4, slots, keep, n_w=1, wtype="bfloat16", dim=2, ctype="uint8", sinks=4, recent=50, seed=slots,
+          lengths=[slots - (i * 977) % slots for i in range(64)])
+    check(16, 4, slots, keep, n_w=1, dim=2, ctype="uint8", ties=2, seed=slots)
+
+
 @pytest.mark.parametrize("slots", [3000, 20000])
 def test_outliers_crowd_the_other_weights_together(slots):
     # one huge weight stretches the row's range, so that all others share a few of the first bins

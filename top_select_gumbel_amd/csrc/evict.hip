@@ -7,16 +7,20 @@
 // that a row of which few positions go moves few, and nothing that is read is written.
 //
 // Short rows (ts_evict_row_kernel, one workgroup a row, its sums in registers) are summed, cut and listed, and their few
-// moves made, in one launch where one compute unit alone reads and copies that fast enough; else the sums come from
-// ts_evict_sum_kernel and the moves go to ts_evict_move_kernel, both spread over the chip.
+// moves made, in one launch where one compute unit alone reads and copies that fast enough (64 rows of 1025 slots, 4
+// weights each: 8.8 us, all of it the latency of a dozen dependent steps); else the sums come from ts_evict_sum_kernel
+// and the moves go to ts_evict_move_kernel, both spread over the chip.
 //
-// Long rows are spread in every step (a tile of 1024 slots a workgroup), a launch each:
-//   sum    s, and each tile's largest position and extreme keys
-//   bin    both classes (protected, others) counted by the first 11 bits of u = key - smallest key of the row
-//   list   the bin that holds the cut, its slots listed
-//   cut    one workgroup a row: the cut's (u, slot)
-//   emit   what stays in place; each tile's freed slots and fillers
+// Long rows are spread in every step (a tile of 1024 slots a workgroup), a launch each (in brackets: us for 8 rows of 131072
+// slots, 4 fp32 weights each, cut to 8192 positions of 2 x 256 bytes):
+//   sum    s, and each tile's largest position and extreme keys [9.2, 25 MB]
+//   bin    both classes (protected, others) counted by the first 11 bits of u = key - smallest key of the row [7.6]
+//   list   the bin that holds the cut, its slots listed [5.5]
+//   cut    one workgroup a row: the cut's (u, slot) [6.4]
+//   emit   what stays in place; each tile's freed slots and fillers [5.6]
 //   move   the i-th freed slot of a row receives the i-th filler (found by the tiles' counts), caches and small outputs
+//          [16.5, 63 MB]
+// The four in the middle read 4 MB from the caches each and are bound by the latency of their few dependent loads.
 //
 // The cut is found by radix select on u = key - smallest key of the row (ordered keys, so that the first 2048 bins
 // span the row's own range and not the whole of fp32), then, once few slots share its bin, by ranking those.
@@ -47,7 +51,12 @@ constexpr int kSmallSlots = 2 * 4 * kSmallT;
 constexpr int kEBits = 11;
 constexpr int kEBins = 1 << kEBits;
 constexpr int kMaxTiles = TS_EVICT_MAX_SLOTS / kSumTile;
-constexpr int kRowSlots = 2 * 4 * kET;   // longest row held in registers: two 16-byte vectors a thread
+// Rows held in registers by one workgroup: two 16-byte vectors a thread, or four where there are rows enough to fill the
+// chip that way. Longer ones are spread. (Rows x slots, one position dropped, one workgroup a row against spread: 8 x 8192
+// 19 us against 25, 512 x 8192 50 against 94; 8 x 16384 31 against 26, 64 x 16384 38 against 42, 512 x 16384 106
+// against 151.)
+constexpr int kRowSlots = 2 * 4 * kET;
+constexpr int kWideSlots = 4 * 4 * kET, kWideRows = 64;
 constexpr int kListRow = 256;            // slots of the cut's bin that are ranked rather than binned again, ...
 constexpr int kListLong = 4096;          // ... and that are listed for a long row's cut
 constexpr int kMT = 256;                 // threads of the move kernel
@@ -105,6 +114,7 @@ struct EParams {
   uint32_t* hist;                        // [rows, 2, kEBins]
   int32_t* fill_position;                // [rows, sum_stride]; hole and fill are [rows, sum_stride] there, by tiles
   int32_t tiles;
+  int32_t spread;                        // long rows
   int32_t* moves;                        // [rows]
   int32_t* hole;                         // [rows, cap]: the freed slots, ascending
   int32_t* fill;                         // [rows, cap]: what each takes over, ascending
@@ -196,7 +206,7 @@ __global__ __launch_bounds__(kST) void ts_evict_sum_kernel(EParams P) {
     sum_slots<DT, kSumBatch<DT>>(P, r, j, n, s);
     f32x4* out = reinterpret_cast<f32x4*>(P.sum + (int64_t)r * P.sum_stride + j);
     *out = f32x4{(float)s[0], (float)s[1], (float)s[2], (float)s[3]};
-    if (P.slots > kRowSlots) {
+    if (P.spread) {
       const int32_t* pos = P.position + (int64_t)r * P.position_stride;
 #pragma unroll
       for (int i = 0; i < kSumSlots; ++i) {
@@ -208,7 +218,7 @@ __global__ __launch_bounds__(kST) void ts_evict_sum_kernel(EParams P) {
       }
     }
   }
-  if (P.slots <= kRowSlots) return;
+  if (!P.spread) return;
   if (tile == 0) {
     uint32_t* h = P.hist + (int64_t)r * 2 * kEBins;
     for (int i = threadIdx.x; i < 2 * kEBins; i += kST) h[i] = 0u;
@@ -1117,6 +1127,7 @@ __global__ __launch_bounds__(kMT) void ts_evict_long_move_kernel(EParams P, int 
 // ------------------------------------------------------------------ host side
 struct EPlan {
   int64_t cap = 0, sum_stride = 0, tiles = 0;
+  bool spread = false;
   size_t off_info = 0, off_row = 0, off_bin = 0, off_hist = 0, off_moves = 0, off_hole = 0, off_fill = 0,
          off_fill_position = 0, total = 0;
 };
@@ -1130,8 +1141,8 @@ bool evict_plan(int64_t rows, int64_t slots, int64_t keep_max, EPlan& pl) {
   // a row moves at most min(k, n - k) positions
   pl.cap = std::min(keep_max, std::max<int64_t>(slots / 2, 1));
   pl.sum_stride = pl.tiles * kSumTile;
-  const bool spread = slots > kRowSlots;
-  const size_t rr = (size_t)std::max<int64_t>(rows, 1), listed = rr * (size_t)(spread ? pl.sum_stride : pl.cap) * 4;
+  pl.spread = slots > kWideSlots || (slots > kRowSlots && rows < kWideRows);
+  const size_t rr = (size_t)std::max<int64_t>(rows, 1), listed = rr * (size_t)(pl.spread ? pl.sum_stride : pl.cap) * 4;
   size_t b = 0;
   auto take = [&](size_t bytes) {
     const size_t at = b;
@@ -1142,7 +1153,7 @@ bool evict_plan(int64_t rows, int64_t slots, int64_t keep_max, EPlan& pl) {
   pl.off_moves = take(rr * 4);
   pl.off_hole = take(listed);
   pl.off_fill = take(listed);
-  if (spread) {
+  if (pl.spread) {
     pl.off_fill_position = take(listed);
     pl.off_info = take(rr * (size_t)pl.tiles * sizeof(TileInfo));
     pl.off_bin = take(rr * (size_t)pl.tiles * sizeof(TileBin));
@@ -1182,22 +1193,26 @@ void with_unit(int unit, F f) {
   }
 }
 
-// Where a row is summed, selected and moved by one workgroup: what a launch costs against what one compute unit
-// reads and copies alone.
+// Where a row is also summed, and its moves also made, by its one workgroup: what a launch costs against what one
+// compute unit reads and copies alone. (64 rows, one position dropped, summed here against a launch of its own: 1025
+// slots, 4 weights of 2 bytes 9 us against 14; 4096 slots, 16 weights 16.6 against 16.9, 64 weights 26.9 against 25.8.
+// Moves of 512 bytes made here: 2048 slots, one 9.8 us against 11.6, 1024 moves 24 against 18; the row's bound counts, as the
+// number is known on the device only.)
 constexpr int64_t kFusedBytes = 128 << 10;   // weights of a row
 constexpr int64_t kFusedMoves = 256 << 10;   // cache bytes that a row can move
-
-constexpr int64_t kMoveGroups = 1024;        // workgroups that the moves of long rows are spread over, about,
+constexpr int64_t kMoveGroups = 1024;        // workgroups that moves are spread over, about (evict-long's 61,000: 16.5 us, 2048: 19.5),
 constexpr int64_t kMoveParts = 32;           // and at most so many to a tile's
 
 // The row kernel with the threads and vectors that hold the row: a fourth of the threads for short rows, of which then
-// several share a compute unit (U: the moves' unit, void: they are made elsewhere).
+// several share a compute unit (1025 slots: 64 rows 8.8 us against 8.6 with 1024 threads, 512 rows 11 against 17, 2048
+// rows 26 against 65). U: the moves' unit, void: they are made elsewhere.
 template <int SRC, class U>
 void launch_rows(const EParams& P, hipStream_t s) {
   const dim3 grid((unsigned)P.rows);
   if (P.slots <= kSmallSlots) hipLaunchKernelGGL((ts_evict_row_kernel<kSmallT, 2, SRC, U>), grid, dim3(kSmallT), 0, s, P);
   else if (P.slots <= 4 * kET) hipLaunchKernelGGL((ts_evict_row_kernel<kET, 1, SRC, U>), grid, dim3(kET), 0, s, P);
-  else hipLaunchKernelGGL((ts_evict_row_kernel<kET, 2, SRC, U>), grid, dim3(kET), 0, s, P);
+  else if (P.slots <= kRowSlots) hipLaunchKernelGGL((ts_evict_row_kernel<kET, 2, SRC, U>), grid, dim3(kET), 0, s, P);
+  else if constexpr (SRC < 0) hipLaunchKernelGGL((ts_evict_row_kernel<kET, 4, SRC, U>), grid, dim3(kET), 0, s, P);
 }
 
 int check_cache(const ts_cache* c, const char* name) {
@@ -1302,6 +1317,7 @@ extern "C" int ts_cache_evict(const float* score, int64_t rows, int64_t slots, i
   P.hist = reinterpret_cast<uint32_t*>(ws + pl.off_hist);
   P.fill_position = reinterpret_cast<int32_t*>(ws + pl.off_fill_position);
   P.tiles = (int32_t)pl.tiles;
+  P.spread = pl.spread ? 1 : 0;
   P.moves = reinterpret_cast<int32_t*>(ws + pl.off_moves);
   P.hole = reinterpret_cast<int32_t*>(ws + pl.off_hole);
   P.fill = reinterpret_cast<int32_t*>(ws + pl.off_fill);
@@ -1335,7 +1351,7 @@ extern "C" int ts_cache_evict(const float* score, int64_t rows, int64_t slots, i
     with_type([&](auto dt) { hipLaunchKernelGGL(ts_evict_sum_kernel<dt()>, grid, block, 0, s, P); });
     e = hipGetLastError();
     if (e != hipSuccess) return fail(TS_ERR_LAUNCH, "eviction sum launch failed: %s", hipGetErrorString(e));
-    if (slots > kRowSlots) {
+    if (pl.spread) {
       const int64_t groups = (slots + kBinTiles * 4 * kET - 1) / (kBinTiles * 4 * kET);
       hipLaunchKernelGGL(ts_evict_bin_kernel, dim3((unsigned)(rows * groups)), dim3(kET), 0, s, P, (int)groups);
       hipLaunchKernelGGL(ts_evict_list_kernel, grid, block, 0, s, P);
