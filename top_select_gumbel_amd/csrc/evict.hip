@@ -13,13 +13,13 @@
 //
 // Long rows are spread in every step (a tile of 1024 slots a workgroup), a launch each (in brackets: us for 8 rows of 131072
 // slots, 4 fp32 weights each, cut to 8192 positions of 2 x 256 bytes):
-//   sum    s, and each tile's largest position and extreme keys [9.2, 25 MB]
-//   bin    both classes (protected, others) counted by the first 11 bits of u = key - smallest key of the row [7.6]
+//   sum    s, and each tile's largest position and extreme keys [9.0, 25 MB]
+//   bin    both classes (protected, others) counted by the first 11 bits of u = key - smallest key of the row [7.0]
 //   list   the bin that holds the cut, its slots listed [5.5]
-//   cut    one workgroup a row: the cut's (u, slot) [6.4]
-//   emit   what stays in place; each tile's freed slots and fillers [5.6]
+//   cut    one workgroup a row: the cut's (u, slot) [6.3]
+//   emit   what stays in place; each tile's freed slots and fillers [5.8]
 //   move   the i-th freed slot of a row receives the i-th filler (found by the tiles' counts), caches and small outputs
-//          [16.5, 63 MB]
+//          [17, 63 MB]
 // The four in the middle read 4 MB from the caches each and are bound by the latency of their few dependent loads.
 //
 // The cut is found by radix select on u = key - smallest key of the row (ordered keys, so that the first 2048 bins
@@ -1200,7 +1200,7 @@ void with_unit(int unit, F f) {
 // number is known on the device only.)
 constexpr int64_t kFusedBytes = 128 << 10;   // weights of a row
 constexpr int64_t kFusedMoves = 256 << 10;   // cache bytes that a row can move
-constexpr int64_t kMoveGroups = 1024;        // workgroups that moves are spread over, about (evict-long's 61,000: 16.5 us, 2048: 19.5),
+constexpr int64_t kMoveGroups = 1024;        // workgroups that moves are spread over, about (61,000 moves of 512 bytes: 17 us, with 2048 19.5),
 constexpr int64_t kMoveParts = 32;           // and at most so many to a tile's
 
 // The row kernel with the threads and vectors that hold the row: a fourth of the threads for short rows, of which then

@@ -16,9 +16,9 @@
 // ts_logp_grad_kernel  one pass: reads a tile, writes its gradient.
 //
 // Measured (MI355X; a plain read of the same bytes takes 92 us for 2048 x 151936 in bf16, 68 us for 1777 x 128256):
-//   2048 x 151936 bf16  tile 117 us (5.3 TB/s), row 6 us, gradient 193 us (6.4 TB/s read and written)
-//   1777 x 128256 bf16  tile 80 us without ranks and alternatives (5.7 TB/s), 96 us with both (n = 5), top 8 us
-//   64 x 151936 fp32    tile 14.5 us with ranks and 20 alternatives, top 6.3 us
+//   2048 x 151936 bf16  tile 95-116 us (6.5-5.4 TB/s), row 6 us, gradient 194 us (6.4 TB/s read and written)
+//   1777 x 128256 bf16  tile 80 us without ranks and alternatives (5.7 TB/s), 95-98 us with both (n = 5), top 8 us
+//   64 x 151936 fp32    tile 15 us with ranks and 20 alternatives, top 6.2 us (a plain read: 8 us)
 #include <math.h>
 
 #include <algorithm>
