@@ -8,6 +8,7 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,7 +22,6 @@ HIPCC_FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     # packed fp32 VALU forms stay off (see the design notes)
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-fno-gpu-flush-denormals-to-zero",
@@ -37,14 +37,23 @@ def hipcc() -> str:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile libtopselect.so (always recompiles). Returns the library path."""
+    """Compile libtopselect.so (always recompiles, a process a source). Returns the library path."""
     tmp = LIB + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, "-I", INC, "-I", os.path.join(PKG, "csrc"), *SRCS, "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + res.stdout[-4000:] + res.stderr[-8000:])
+    with tempfile.TemporaryDirectory() as work:
+        objs = [os.path.join(work, os.path.basename(src) + ".o") for src in SRCS]
+        jobs = []
+        for src, obj in zip(SRCS, objs):
+            cmd = [hipcc(), *HIPCC_FLAGS, "-I", INC, "-I", os.path.join(PKG, "csrc"), "-c", src, "-o", obj]
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            jobs.append(subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))
+        outs = [job.communicate()[0] for job in jobs]
+        for job, out in zip(jobs, outs):
+            if job.returncode != 0:
+                raise RuntimeError("hipcc failed:\n" + out[-12000:])
+        res = subprocess.run([hipcc(), "--offload-arch=gfx950", "-fPIC", "-shared", *objs, "-o", tmp], capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError("linking failed:\n" + res.stdout[-4000:] + res.stderr[-8000:])
     os.replace(tmp, LIB)
     return LIB
 
