@@ -93,7 +93,7 @@ struct EParams {
   int64_t score_stride;
   const char* weights;
   int64_t w_row, w_stride;               // bytes
-  int32_t w_type, n_w;
+  int32_t n_w;
   const int32_t* position;
   int64_t position_stride;
   const int32_t* lengths;
@@ -698,7 +698,7 @@ __device__ __forceinline__ Row long_row(const EParams& P, int r, uint32_t* red, 
     red[3 * wave() + 2] = kmax;
   }
   bar();
-  #pragma unroll
+#pragma unroll
   for (int w = 0; w < NW; ++w) {
     newest = max(newest, red[3 * w]);
     kmin = min(kmin, red[3 * w + 1]);
@@ -1291,7 +1291,6 @@ extern "C" int ts_cache_evict(const float* score, int64_t rows, int64_t slots, i
   P.weights = static_cast<const char*>(weights);
   P.w_row = weights_row_stride * size;
   P.w_stride = weights_stride * size;
-  P.w_type = weights_dtype;
   P.n_w = (int32_t)n_weights;
   P.position = position;
   P.position_stride = position_stride;
