@@ -402,6 +402,23 @@ def _call(device, f, *args):
             _check(f(*args, torch._C._cuda_getCurrentRawStream(index)))
 
 
+def _outputs(device, *sizes):
+    """Parts of one fp32 allocation with `sizes` elements each (None: no such part), and their addresses: a tensor of
+    its own for every output would cost the host twice the kernels' time of a small call."""
+    wanted = [n for n in sizes if n is not None]
+    flat = _torch.empty(sum(wanted), dtype=_torch.float32, device=device)
+    views, at, parts, ptrs = iter(flat.unsafe_split_with_sizes(wanted)), flat.data_ptr(), [], []
+    for n in sizes:
+        if n is None:
+            parts.append(None)
+            ptrs.append(None)
+        else:
+            parts.append(next(views))
+            ptrs.append(at)
+            at += 4 * n
+    return parts, ptrs
+
+
 class TokenLogp(NamedTuple):
     """Outputs of ts_token_logp; None for what was not asked for."""
     logp: object        # fp32 [rows]
@@ -424,25 +441,20 @@ def ts_token_logp(logits, tokens=None, temperature=None, n_top: int = 0, want_ra
     device = logits.device
     tok = _param(tokens, torch.int32, rows, device, "tokens")
     temp = _param(temperature, torch.float32, rows, device, "temperature")
-    # One allocation for the outputs, then views of it: eight of their own cost twice the kernels' time of a small call.
-    i = torch.int32
-    given, top = tokens is not None, max(n_top, 0)
-    sizes = [4 * rows if want_stats else 0, rows if given else 0, rows if want_entropy else 0, rows if want_lse else 0,
-             rows * top, rows if given and want_rank else 0, rows, rows * top]
-    flat = torch.empty(sum(sizes), dtype=torch.float32, device=device)
-    parts, at, ptrs = flat.split_with_sizes(sizes), flat.data_ptr(), []
-    for n in sizes:
-        ptrs.append(at if n else None)
-        at += 4 * n
+    given, top = tokens is not None, rows * n_top if n_top > 0 else None
+    (stats, logp, entropy, lse, rank, status, top_idx, top_logp), ptrs = _outputs(
+        device, 4 * rows if want_stats else None, rows if given else None, rows if want_entropy else None,
+        rows if want_lse else None, rows if given and want_rank else None, rows, top, top)
     # A workspace of the call's own: two calls captured into graphs that replay at once share none.
     nb = 0 if v <= TS_LOGP_TILE else lib.ts_workspace_bytes(TS_OP_TOKEN_LOGP, rows, v, n_top)
     ws = torch.empty(nb, dtype=torch.uint8, device=device) if nb else None
-    _call(device, lib.ts_token_logp, logits.data_ptr(), code, rows, v, stride, tok, temp, n_top, ptrs[1], ptrs[5], ptrs[2], ptrs[3],
-          ptrs[7], ptrs[4], ptrs[0], ptrs[6], _ptr(ws), nb)
-    return TokenLogp(parts[1] if given else None, parts[5].view(i) if given and want_rank else None,
-                     parts[2] if want_entropy else None, parts[3] if want_lse else None,
-                     parts[7].view(i).view(rows, top) if top else None, parts[4].view(rows, top) if top else None,
-                     parts[0].view(rows, 4) if want_stats else None, parts[6].view(i))
+    _call(device, lib.ts_token_logp, logits.data_ptr(), code, rows, v, stride, tok, temp, n_top, ptrs[1], ptrs[4], ptrs[2], ptrs[3],
+          ptrs[6], ptrs[7], ptrs[0], ptrs[5], _ptr(ws), nb)
+    i = torch.int32
+    if top is not None:
+        top_idx, top_logp = top_idx.view(i).view(rows, n_top), top_logp.view(rows, n_top)
+    return TokenLogp(logp, rank if rank is None else rank.view(i), entropy, lse, top_idx, top_logp,
+                     stats if stats is None else stats.view(rows, 4), status.view(i))
 
 
 def ts_token_logp_backward(logits, tokens, temperature, stats, grad_logp=None, grad_entropy=None, grad_lse=None, out=None):
