@@ -114,6 +114,22 @@ def test_ties(v, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("v", [70, 100, 200, 700, 8192, 8300, 20011])
+def test_alternatives_among_neighbours(v, dtype):
+    """Short rows, and masks that leave a run of neighbours: the candidates sit in few threads, several in each."""
+    rng = np.random.default_rng(v + 7)
+    live = [65, 100, 130, 300, 600, 1500]
+    x = make(len(live) + 2, v, dtype, v + 8)
+    for r, m in enumerate(live):
+        at = int(rng.integers(0, max(v - m, 1)))
+        x[r, :at] = -math.inf
+        x[r, at + m:] = -math.inf
+    x[len(live)] = x[len(live)].sort().values          # the large ones in the last threads
+    for n in (1, 5, 20, 64):
+        check(x, rng.integers(0, v, x.shape[0]), None, n, "neighbours")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("v", [33, 9000])
 def test_masked_and_rejected_rows(v, dtype):
     rng = np.random.default_rng(v + 2)

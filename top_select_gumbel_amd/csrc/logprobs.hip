@@ -101,10 +101,19 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
 }
 
 // ------------------------------------------------------------------ the best n
+// The key whose leading bits are u's: the fraction bits that the type lacks are 0 in its logits, 1 in the keys of negative ones.
+template <int DT>
+__device__ __forceinline__ uint32_t whole_key(uint32_t u) {
+  return u >> 31 ? u : u | ((1u << tsl::Logits<DT>::kLowBits) - 1u);
+}
+
 // A bound that at least n of some items reach and, where large items are spread over their 256 groups, few more: about the
 // n-th largest of the groups' largest keys (keys up to that of -inf are absent items). Called by one
 // wave, which has four of those keys a lane in k4; kmax is the largest. The bits above the highest one in which they differ
-// are common to all; the others are found one by one.
+// are common to all; the others are found one by one, until at most n + 8 groups reach the bound: each further bit would
+// cost more than the items it saves. Not so where that is more than half of the groups that have items (a short row, a mask
+// that leaves a few neighbours): each then has several above it (1325 x 100 in fp16, n = 5: 80 us for that reason).
+template <int DT>
 __device__ __forceinline__ uint32_t find_low(const uint32_t* k4, uint32_t kmax, int n) {
   uint32_t kmin = k4[0];
 #pragma unroll
@@ -112,70 +121,92 @@ __device__ __forceinline__ uint32_t find_low(const uint32_t* k4, uint32_t kmax, 
   const uint32_t differ = kmax ^ wave_min(kmin);
   const int bits = bitlen(differ);
   uint32_t low = bits == 32 ? 0u : kmax >> bits << bits;
-  for (int b = bits - 1; b >= 0; --b) {
+  int live = 0;
+#pragma unroll
+  for (int w = 0; w < kLW; ++w) live += __popcll(__ballot(k4[w] > kKeyNegInf));
+  const int enough = min(n + 8, live / 2);
+  for (int b = bits - 1; b >= tsl::Logits<DT>::kLowBits; --b) {
     const uint32_t t = low | (1u << b);
     int c = 0;
 #pragma unroll
     for (int w = 0; w < kLW; ++w) c += __popcll(__ballot(k4[w] >= t));
     if (c >= n) {
       low = t;
-      if (c <= n + 8) break;   // close enough: each further bit costs more than the candidates it saves
+      if (c <= enough) break;
     }
   }
-  return max(low, kKeyNegInf + 1);
+  return whole_key<DT>(max(low, kKeyNegInf + 1));
 }
 
-// The logits of a tile for one wave, 16 bytes a lane at a time, in id order: f(at, key) gets the first id and the keys of a
-// vector, those that do not count 0.
-template <int DT, class F>
-__device__ __forceinline__ void wave_vectors(const char* row, int V, int tile, F f) {
+// A tile's exact best n, where more candidates reach the bound `low` than the list holds: many equal logits around it (a mask
+// of the type's lowest value, a constant row), or the large ones in few threads (a sorted row, a mask that leaves a
+// few neighbours). One wave reads the vectors of the `threads` threads with candidates again, in id order, once for each
+// count where they are more than it holds in registers; so this path holds no registers of the usual one. The row has more than
+// n logits, so at least a vector's.
+template <int DT>
+__device__ void exact_tile(LSmem& sm, const char* row, int V, int tile, int n, uint32_t low, uint32_t kmax, int threads) {
   using L = Logits<DT>;
   constexpr int kBatch = 4;
-  const int end = min(V, (tile + 1) * kTile);
+  const int total = threads * L::kNV;
+  const uint32_t inverse = ((1u << 20) + (uint32_t)threads - 1) / (uint32_t)threads;   // exact for quotients of numbers up to 2^11
+  u32x4 raw[kBatch];
+  int at[kBatch];
+  bool held = false;
+  // f(first id, keys) for a vector a lane, until it returns true; what does not count is -inf, below every candidate.
+  auto each = [&](auto f) {
 #pragma nounroll
-  for (int q = tile * kTile + lane() * L::kW; q - lane() * L::kW < end; q += 64 * L::kW * kBatch) {
-    u32x4 raw[kBatch];
+    for (int q0 = 0; q0 < total; q0 += 64 * kBatch) {
+      if (!held || total > 64 * kBatch) {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) raw[i] = load16(row + (int64_t)min(q + i * 64 * L::kW, V - L::kW) * L::kSize);
+        for (int i = 0; i < kBatch; ++i) {
+          const int q = q0 + 64 * i + lane(), in = min(q, total - 1), v = (int)((uint32_t)in * inverse >> 20);
+          const Place<DT> pl(tile, sm.who[in - v * threads], v, V);
+          at[i] = pl.at;
+          raw[i] = load16(row + (int64_t)pl.at * L::kSize);
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int own = q + i * 64 * L::kW, at = min(own, V - L::kW);
-      uint32_t key[L::kW];
+          for (int j = 0; j < L::kW; ++j) {
+            const uint32_t half = L::kSize == 4 ? 0xFFFFFFFFu : (j & 1) ? 0xFFFF0000u : 0x0000FFFFu;
+            const int w = j * L::kSize / 4;
+            if (q >= total || !pl.counts(j, V)) raw[i][w] = (raw[i][w] & ~half) | (L::kNegInf & half);
+          }
+        }
+        held = true;
+      }
 #pragma unroll
-      for (int j = 0; j < L::kW; ++j) key[j] = at + j >= own && at + j < end ? f2key(unpack<DT>(raw[i], j)) : 0u;
-      f(at, key);
+      for (int i = 0; i < kBatch; ++i) {
+        if (q0 + 64 * i >= total) continue;
+        uint32_t key[L::kW];
+#pragma unroll
+        for (int j = 0; j < L::kW; ++j) key[j] = f2key(unpack<DT>(raw[i], j));
+        if (f(at[i], key)) return;
+      }
     }
-  }
-}
-
-// A tile's exact best n, for tiles with many equal logits around the bound `low`, which more than n reach (a mask of the type's
-// lowest value, a constant row), or their large ones in few threads (a sorted row). One wave reads the tile again, so
-// that this path holds no registers of the usual one. The row has more than n logits, so at least a vector's.
-template <int DT>
-__device__ void exact_tile(LSmem& sm, const char* row, int V, int tile, int n, uint32_t low) {
-  using L = Logits<DT>;
-  auto count = [&](uint32_t least) {
+  };
+  auto count = [&](uint32_t least) {   // of keys from `least` on, up to n
     uint32_t c = 0;
-    wave_vectors<DT>(row, V, tile, [&](int, const uint32_t* key) {
+    each([&](int, const uint32_t* key) {
 #pragma unroll
       for (int j = 0; j < L::kW; ++j) c += (uint32_t)__popcll(__ballot(key[j] >= least));
+      return c >= (uint32_t)n;
     });
     return c;
   };
-  uint32_t t = low;   // becomes the n-th largest key: the bound itself where fewer are above it, else bit by bit
-  uint32_t above = count(low + 1);
+  // t becomes the n-th largest key: the bound itself where fewer are above it, else, between it and the tile's largest, bit by bit.
+  uint32_t t = low, above = count(low + 1);
   if (above >= (uint32_t)n) {
-    t = 0;
+    const int bits = bitlen(low ^ kmax);
+    t = bits == 32 ? 0u : low >> bits << bits;
 #pragma nounroll
-    for (int b = 31; b >= 0; --b) {
+    for (int b = bits - 1; b >= L::kLowBits; --b) {
       const uint32_t u = t | (1u << b);
       if (count(u) >= (uint32_t)n) t = u;
     }
+    t = whole_key<DT>(t);
     above = count(t + 1);
   }
   const uint32_t need = n - above;   // of the logits equal to it, in id order
   uint32_t seen = 0, put = 0;
-  wave_vectors<DT>(row, V, tile, [&](int at, const uint32_t* key) {
+  each([&](int at, const uint32_t* key) {
     uint32_t eq = 0;
 #pragma unroll
     for (int j = 0; j < L::kW; ++j) eq += key[j] == t ? 1u : 0u;
@@ -191,6 +222,7 @@ __device__ void exact_tile(LSmem& sm, const char* row, int V, int tile, int n, u
       if (in && o < (uint32_t)kCapMax) sm.list[o] = make_uint2(key[j], (uint32_t)(at + j));
       put += (uint32_t)__popcll(m);
     }
+    return put == (uint32_t)n;
   });
 }
 
@@ -199,7 +231,7 @@ __device__ void exact_tile(LSmem& sm, const char* row, int V, int tile, int n, u
 // as many lanes as they have vectors: looking through all threads' registers takes every wave longer.
 template <int DT>
 __device__ __forceinline__ int tile_candidates(LSmem& sm, const char* row, int V, int tile, int n, int cap, uint32_t low,
-                                               const uint32_t* k4) {
+                                               uint32_t kmax, const uint32_t* k4) {
   using L = Logits<DT>;
   uint32_t threads = 0;
 #pragma unroll
@@ -233,7 +265,7 @@ __device__ __forceinline__ int tile_candidates(LSmem& sm, const char* row, int V
     }
   }
   if (put > (uint32_t)cap) {
-    exact_tile<DT>(sm, row, V, tile, n, low);
+    exact_tile<DT>(sm, row, V, tile, n, low, kmax, (int)threads);
     put = n;
   }
   wave_lds_sync();
@@ -485,7 +517,7 @@ __global__ __launch_bounds__(kLT) __attribute__((amdgpu_waves_per_eu(7))) void t
     k = max(k, k4[i]);
   }
   k = wave_max(k);
-  const uint32_t low = TOP && lead ? find_low(k4, k, P.n_top) : 0u;
+  const uint32_t low = TOP && lead ? find_low<DT>(k4, k, P.n_top) : 0u;
   const float m = k == kKeyNegInf ? 0.0f : key2f(k);
   const float c = scale32(P, in.t), mc = m * c;
   const bool fused = fabsf(mc) <= 4096.0f;                       // eta below 2^-12
@@ -563,7 +595,7 @@ __global__ __launch_bounds__(kLT) __attribute__((amdgpu_waves_per_eu(7))) void t
   }
   if (!TOP) return;
   if (lead) {
-    const int count = tile_candidates<DT>(sm, row, P.V, tile, P.n_top, P.cap, low, k4);
+    const int count = tile_candidates<DT>(sm, row, P.V, tile, P.n_top, P.cap, low, k, k4);
     if (WHOLE) {
       sm.count = (uint32_t)count;
     } else {
@@ -615,7 +647,7 @@ __global__ __launch_bounds__(128) void ts_logp_top_kernel(LParams P) {
         for (int i = 0; i < kGroup; ++i) k4[g] = max(k4[g], c[g * kGroup + i].x);
         k = max(k, k4[g]);
       }
-      const uint32_t low = find_low(k4, wave_max(k), P.n_top);
+      const uint32_t low = find_low<DT>(k4, wave_max(k), P.n_top);
       count = 0;
 #pragma unroll
       for (int i = 0; i < kItems + kLeft; ++i) {

@@ -36,6 +36,7 @@ struct Logits {
   static constexpr uint32_t kNegInf = DT == TS_DTYPE_F32 ? 0xFF800000u : DT == TS_DTYPE_BF16 ? 0xFF80FF80u : 0xFC00FC00u;   // a word of -inf
   static constexpr int kSize = DT == TS_DTYPE_F32 ? 4 : 2;
   static constexpr int kW = 16 / kSize;     // logits a vector
+  static constexpr int kLowBits = DT == TS_DTYPE_F32 ? 0 : DT == TS_DTYPE_BF16 ? 16 : 13;   // fraction bits that fp32 has more
   static constexpr int kNV = kLE / kW;      // vectors a thread
 };
 
