@@ -192,7 +192,7 @@ __device__ void exact_tile(LSmem& sm, const char* row, int V, int tile, int n, u
     return c;
   };
   // t becomes the n-th largest key: the bound itself where fewer are above it, else, between it and the tile's largest, bit by bit.
-  uint32_t t = low, above = count(low + 1);
+  uint32_t t = low, above = low < kmax ? count(low + 1) : 0u;
   if (above >= (uint32_t)n) {
     const int bits = bitlen(low ^ kmax);
     t = bits == 32 ? 0u : low >> bits << bits;
@@ -244,7 +244,7 @@ __device__ __forceinline__ int tile_candidates(LSmem& sm, const char* row, int V
   const float low_f = key2f(low);
   const bool whole = (tile + 1) * kTile <= V;
   uint32_t put = 0;
-  for (uint32_t q0 = 0; q0 < threads * L::kNV; q0 += 64) {
+  for (uint32_t q0 = 0; q0 < threads * L::kNV && put <= (uint32_t)cap; q0 += 64) {
     const uint32_t q = q0 + lane();
     const bool mine = q < threads * L::kNV;
     const Place<DT> pl(tile, mine ? sm.who[q / L::kNV] : 0, (int)(q % L::kNV), V);
@@ -272,25 +272,26 @@ __device__ __forceinline__ int tile_candidates(LSmem& sm, const char* row, int V
   return (int)put;
 }
 
-// The exact best n of items that a wave's lanes hold N each, found bit by bit: the n-th largest key, then, among those
-// equal to it, the id of the last that stays (ids are below 2^30 and differ).
+// The exact best n of items that a wave's lanes hold N each, more than n of which reach `low` and none is above kmax, found bit
+// by bit: the n-th largest key, then, among those equal to it, the id of the last that stays (ids are below V and differ).
 template <int N>
-__device__ __forceinline__ void exact_items(LSmem& sm, const uint2* c, int n) {
+__device__ __forceinline__ void exact_items(LSmem& sm, const uint2* c, int n, uint32_t low, uint32_t kmax, int V) {
   auto count = [&](auto pred) {
     uint32_t k = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) k += (uint32_t)__popcll(__ballot(pred(c[i])));
     return k;
   };
-  uint32_t t = 0, last = 0;
+  const int bits = bitlen(low ^ kmax);
+  uint32_t t = bits == 32 ? 0u : low >> bits << bits, last = 0;
 #pragma nounroll
-  for (int b = 31; b >= 0; --b) {
+  for (int b = bits - 1; b >= 0; --b) {
     const uint32_t u = t | (1u << b);
     if (count([&](const uint2& q) { return q.x >= u; }) >= (uint32_t)n) t = u;
   }
   const uint32_t need = n - count([&](const uint2& q) { return q.x > t; });
 #pragma nounroll
-  for (int b = 29; b >= 0; --b) {
+  for (int b = bitlen((uint32_t)V - 1u) - 1; b >= 0; --b) {
     const uint32_t u = last | (1u << b);
     if (count([&](const uint2& q) { return q.x == t && q.y < u; }) < need) last = u;
   }
@@ -426,32 +427,48 @@ __device__ __forceinline__ void finish_row(const LParams& P, const RowIn& in, in
   }
 }
 
-// Ranks the `count` candidates of sm.list and writes the row's n_top alternatives; called by one wave, after finish_row.
+// Ranks the `count` candidates of sm.list and writes the row's n_top alternatives; called by a workgroup of T threads, after
+// finish_row.
+template <int T>
 __device__ __forceinline__ void write_top(const LParams& P, int r, int count, const LSmem& sm) {
+  const int t = (int)threadIdx.x, ok = sm.ok;
   int32_t* idx = P.top_idx + (int64_t)r * P.n_top;
   float* lp = P.top_logp + (int64_t)r * P.n_top;
-  const int ok = sm.ok;
   const float unused = ok ? -INFINITY : __uint_as_float(0x7FC00000u);
   if (!ok) count = 0;
-  for (int i = count + lane(); i < P.n_top; i += 64) {
+  for (int i = count + t; i < P.n_top; i += T) {
     idx[i] = -1;
     lp[i] = unused;
   }
-  for (int i = lane(); i < count; i += 64) {
-    const uint2 me = sm.list[i];
-    int above = 0;
-    for (int j = 0; j < count; j += 8) {   // eight in flight; past the end the last one again, not counted
-      uint2 o[8];
+  // Key and id as one number, larger for an earlier one; each is held by a lane and compared with all (key and id by themselves, two
+  // conditions and a branch each, for one of a lane's at a time: 64 x 151936, n = 64, row step 17.2 us against 9.7).
+  constexpr int kOwn = (kCapMax + T - 1) / T, kStep = 8;
+  auto order = [](uint2 c) { return (uint64_t)c.x << 32 | (uint32_t)~c.y; };
+  uint64_t mine[kOwn];
+  int above[kOwn];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = sm.list[min(j + e, count - 1)];
+  for (int i = 0; i < kOwn; ++i) {
+    const int at = T * i + t;
+    mine[i] = at < count ? order(sm.list[at]) : 0u;
+    above[i] = 0;
+  }
+  for (int j = 0; j < count; j += kStep) {
+    uint64_t o[kStep];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        above += j + e < count && (o[e].x > me.x || (o[e].x == me.x && o[e].y < me.y)) ? 1 : 0;
+    for (int e = 0; e < kStep; ++e) o[e] = order(sm.list[min(j + e, count - 1)]);
+#pragma unroll
+    for (int e = 0; e < kStep; ++e) {
+      if (j + e >= count) o[e] = 0u;
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) above[i] += o[e] > mine[i] ? 1 : 0;
     }
-    if (above >= P.n_top) continue;
-    idx[above] = (int32_t)me.y;
-    const float v = (float)(((double)key2f(me.x) - (double)sm.m) * sm.c2 * kLn2 - sm.log_s);
-    lp[above] = ok == 2 ? (above == 0 ? 0.0f : -INFINITY) : fminf(v, 0.0f);
+  }
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    if (T * i + t >= count || above[i] >= P.n_top) continue;
+    idx[above[i]] = (int32_t)~(uint32_t)mine[i];
+    const float v = (float)(((double)key2f((uint32_t)(mine[i] >> 32)) - (double)sm.m) * sm.c2 * kLn2 - sm.log_s);
+    lp[above[i]] = ok == 2 ? (above[i] == 0 ? 0.0f : -INFINITY) : fminf(v, 0.0f);
   }
 }
 
@@ -605,7 +622,7 @@ __global__ __launch_bounds__(kLT) __attribute__((amdgpu_waves_per_eu(7))) void t
   }
   if (WHOLE) {
     bar();
-    if (lead) write_top(P, r, (int)sm.count, sm);
+    write_top<kLT>(P, r, (int)sm.count, sm);
   }
 }
 
@@ -623,10 +640,10 @@ __global__ __launch_bounds__(128) void ts_logp_top_kernel(LParams P) {
   __shared__ LSmem sm;
   constexpr int kGroup = 6, kItems = 4 * kGroup, kLeft = (kCapMax + 63) / 64;
   const int r = (int)blockIdx.x, l = lane();
-  int count = 0;
   if (wave() == 0) {
     finish_row<DT>(P, row_in(P, r), r, P.part + (int64_t)r * P.tiles, &sm);
   } else {
+    int count = 0;
     const uint2* cand = P.cand + (int64_t)r * P.tiles * P.cap;
     const int64_t n = (int64_t)P.tiles * P.cap;
     for (int64_t base = 0; base < n; base += 64 * kItems) {
@@ -647,7 +664,8 @@ __global__ __launch_bounds__(128) void ts_logp_top_kernel(LParams P) {
         for (int i = 0; i < kGroup; ++i) k4[g] = max(k4[g], c[g * kGroup + i].x);
         k = max(k, k4[g]);
       }
-      const uint32_t low = find_low<DT>(k4, wave_max(k), P.n_top);
+      k = wave_max(k);
+      const uint32_t low = find_low<DT>(k4, k, P.n_top);
       count = 0;
 #pragma unroll
       for (int i = 0; i < kItems + kLeft; ++i) {
@@ -658,14 +676,15 @@ __global__ __launch_bounds__(128) void ts_logp_top_kernel(LParams P) {
         count += __popcll(m);
       }
       if (count > P.cap) {
-        exact_items<kItems + kLeft>(sm, c, P.n_top);
+        exact_items<kItems + kLeft>(sm, c, P.n_top, low, k, P.V);
         count = P.n_top;
       }
       wave_lds_sync();
     }
+    if (l == 0) sm.count = (uint32_t)count;
   }
   bar();
-  if (wave() == 1) write_top(P, r, count, sm);
+  write_top<128>(P, r, (int)sm.count, sm);
 }
 
 // ------------------------------------------------------------------ gradient
