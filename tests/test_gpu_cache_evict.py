@@ -128,6 +128,16 @@ def test_cache_types_and_layouts(ctype, dim, v_dim, layout):
     check(2, 3, 130, 61, dim=dim, ctype=ctype, v_dim=v_dim, slots_first=layout == "slots", wide=3 if layout == "wide" else 0, seed=dim)
 
 
+@pytest.mark.parametrize("dim,v_dim", [(15, 16), (16, 17), (17, 15), (31, 33), (257, 31), (4099, 16)])
+@pytest.mark.parametrize("layout", ["heads", "slots", "wide"])
+def test_slots_of_any_size_and_address(dim, v_dim, layout):
+    """Bytes, so that slots start anywhere and end inside a copy's unit."""
+    for slots, keep in ((130, 61), (2500, 1200), (8300, 90)):
+        if dim * slots < 1 << 21:
+            check(1, 3, slots, keep, dim=dim, ctype="uint8", v_dim=v_dim, slots_first=layout == "slots",
+                  wide=3 if layout == "wide" else 0, seed=dim)
+
+
 @pytest.mark.parametrize("slots", [40, 2048, 2049, 9000])
 def test_keep_may_exceed_the_slots(slots):
     check(2, 2, slots, slots + 300, lengths=[slots, 3, 0, slots - 1], dim=4, seed=slots)

@@ -85,7 +85,7 @@ struct TileBin {
 struct Cache {
   char* p;
   int64_t batch, head, slot;   // bytes
-  int32_t units;               // units of the copy a slot; 0: no cache
+  int32_t units, last;         // units of the copy a slot (0: no cache) and where its last one starts
 };
 
 struct EParams {
@@ -417,8 +417,20 @@ __device__ __forceinline__ void reject_row(const EParams& P, int r, const Row& R
 
 // Copies moves lo .. hi - 1 of a row by a workgroup of T threads: 2^lane_bits threads (about the units of U bytes that a slot
 // has) take a move, kCopyBatch moves of a cache, or of both, in flight at a time. A share's last batch repeats its last
-// move's loads and stores them once.
+// move's loads and stores them once. (The last unit of a slot that is no whole number of them overlaps the one before; both
+// write the same bytes there.)
 constexpr int kCopyBatch = 4;
+typedef unsigned int u32x4_byte __attribute__((ext_vector_type(4), aligned(1)));   // 16 bytes at any address
+template <class U>
+__device__ __forceinline__ U load_unit(const char* p) {
+  if constexpr (sizeof(U) == 16) return *reinterpret_cast<const u32x4_byte*>(p);
+  else return *reinterpret_cast<const U*>(p);
+}
+template <class U>
+__device__ __forceinline__ void store_unit(char* p, U v) {
+  if constexpr (sizeof(U) == 16) *reinterpret_cast<u32x4_byte*>(p) = v;
+  else *reinterpret_cast<U*>(p) = v;
+}
 template <class U, int T, bool TWO>
 __device__ __forceinline__ void copy_slots(const Cache& A, const Cache& B, int b, int h, int lane_bits, const int32_t* hole,
                                            const int32_t* fill, int lo, int hi) {
@@ -435,17 +447,17 @@ __device__ __forceinline__ void copy_slots(const Cache& A, const Cache& B, int b
     }
     for (int u = sub; u < A.units; u += lanes) {
       U a[kCopyBatch], c[kCopyBatch];
-      const int64_t at = (int64_t)u * (int64_t)sizeof(U);
+      const int at = u * (int)sizeof(U), aa = min(at, A.last), ba = min(at, B.last);
 #pragma unroll
       for (int i = 0; i < kCopyBatch; ++i) {
-        a[i] = *reinterpret_cast<const U*>(ap + (int64_t)f[i] * A.slot + at);
-        if (TWO) c[i] = *reinterpret_cast<const U*>(bp + (int64_t)f[i] * B.slot + at);
+        a[i] = load_unit<U>(ap + (int64_t)f[i] * A.slot + aa);
+        if (TWO) c[i] = load_unit<U>(bp + (int64_t)f[i] * B.slot + ba);
       }
 #pragma unroll
       for (int i = 0; i < kCopyBatch; ++i) {
         if (m0 + i * per >= hi) continue;
-        *reinterpret_cast<U*>(ap + (int64_t)t[i] * A.slot + at) = a[i];
-        if (TWO) *reinterpret_cast<U*>(bp + (int64_t)t[i] * B.slot + at) = c[i];
+        store_unit<U>(ap + (int64_t)t[i] * A.slot + aa, a[i]);
+        if (TWO) store_unit<U>(bp + (int64_t)t[i] * B.slot + ba, c[i]);
       }
     }
   }
@@ -1168,27 +1180,29 @@ int dtype_size(int dtype) {
   return dtype == TS_DTYPE_F32 ? 4 : (dtype == TS_DTYPE_BF16 || dtype == TS_DTYPE_F16) ? 2 : 0;
 }
 
-// The widest unit that divides every address of the caches.
+// The copies' unit: 16 bytes at any address, where every slot has so many, else 4 where every address is a multiple, else 1.
 int copy_unit(const ts_cache* k, const ts_cache* v) {
-  uint64_t all = 16;
+  uint64_t all = 0;
+  bool wide = true;
   for (const ts_cache* c : {k, v})
-    if (c)
+    if (c) {
+      wide = wide && c->slot_bytes >= 16;
       all |= (uint64_t)(uintptr_t)c->data | (uint64_t)c->batch_stride | (uint64_t)c->head_stride | (uint64_t)c->slot_stride |
              (uint64_t)c->slot_bytes;
-  return (int)(all & (~all + 1));
+    }
+  return wide ? 16 : all % 4 == 0 ? 4 : 1;
 }
 Cache cache_of(const ts_cache* c, int unit) {
-  return c ? Cache{static_cast<char*>(c->data), c->batch_stride, c->head_stride, c->slot_stride, (int32_t)(c->slot_bytes / unit)}
-           : Cache{nullptr, 0, 0, 0, 0};
+  if (!c) return Cache{nullptr, 0, 0, 0, 0, 0};
+  return Cache{static_cast<char*>(c->data), c->batch_stride, c->head_stride, c->slot_stride,
+               (int32_t)((c->slot_bytes + unit - 1) / unit), (int32_t)(c->slot_bytes - unit)};
 }
 // f(U) with the unit's type
 template <class F>
 void with_unit(int unit, F f) {
   switch (unit) {
     case 1: f(uint8_t{}); break;
-    case 2: f(uint16_t{}); break;
     case 4: f(uint32_t{}); break;
-    case 8: f(u32x2{}); break;
     default: f(tsl::u32x4{}); break;
   }
 }
@@ -1199,7 +1213,7 @@ void with_unit(int unit, F f) {
 // Moves of 512 bytes made here: 2048 slots, one 9.8 us against 11.6, 1024 moves 24 against 18; the row's bound counts, as the
 // number is known on the device only.)
 constexpr int64_t kFusedBytes = 128 << 10;   // weights of a row
-constexpr int64_t kFusedMoves = 256 << 10;   // cache bytes that a row can move
+constexpr int64_t kFusedCopies = 8192;       // the threads' copies that a row's moves can take: 512 moves of 2 x 256 bytes
 constexpr int64_t kMoveGroups = 1024;        // workgroups that moves are spread over, about (61,000 moves of 512 bytes: 17 us, with 2048 19.5),
 constexpr int64_t kMoveParts = 32;           // and at most so many to a tile's
 
@@ -1325,13 +1339,13 @@ extern "C" int ts_cache_evict(const float* score, int64_t rows, int64_t slots, i
   P.k = cache_of(k_cache, unit);
   P.v = cache_of(v_cache, unit);
   P.heads = (int32_t)heads;
+  const int64_t units = std::max(P.k.units, P.v.units);
   P.lane_bits = 0;
-  while ((1 << P.lane_bits) < std::max(P.k.units, P.v.units) && (1 << P.lane_bits) < kMT) ++P.lane_bits;
+  while ((1 << P.lane_bits) < units && (1 << P.lane_bits) < kMT) ++P.lane_bits;
   const hipStream_t s = (hipStream_t)stream;
   const int type = n_weights ? weights_dtype : TS_DTYPE_F32;
   const bool sum_here = slots <= kRowSlots && slots * n_weights * size <= kFusedBytes;
-  const int64_t slot_bytes = (k_cache ? k_cache->slot_bytes : 0) + (v_cache ? v_cache->slot_bytes : 0);
-  const bool move_here = sum_here && pl.cap * slot_bytes <= kFusedMoves;
+  const bool move_here = sum_here && pl.cap * std::max<int64_t>(units, 1 << P.lane_bits) <= kFusedCopies;
   auto with_type = [&](auto f) {
     if (type == TS_DTYPE_F32) f(std::integral_constant<int, TS_DTYPE_F32>{});
     else if (type == TS_DTYPE_BF16) f(std::integral_constant<int, TS_DTYPE_BF16>{});
@@ -1369,7 +1383,7 @@ extern "C" int ts_cache_evict(const float* score, int64_t rows, int64_t slots, i
   }
   e = hipGetLastError();
   if (e != hipSuccess) return fail(TS_ERR_LAUNCH, "eviction row launch failed: %s", hipGetErrorString(e));
-  if (slot_bytes) {
+  if (units) {
     const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((pl.cap << P.lane_bits) / (kMT * kCopyBatch), kMoveGroups / rows));
     with_unit(unit, [&](auto u) {
       hipLaunchKernelGGL(ts_evict_move_kernel<decltype(u)>, dim3((unsigned)(rows * blocks)), dim3(kMT), 0, s, P, (int)blocks);
