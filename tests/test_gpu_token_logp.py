@@ -228,6 +228,17 @@ def test_long_rows(v, dtype):
     check(x, rng.integers(0, v, 4), None, 20, "long")
 
 
+@pytest.mark.parametrize("v,dtype", [(262144, "float32"), (1200007, "bfloat16"), (2500001, "float16")])
+def test_alternatives_of_the_longest_rows(v, dtype):
+    """More candidates than one wave takes at a time, in several shares; ties in all of them."""
+    torch = torch_cuda()
+    x = make(3, v, dtype, v + 3)
+    x[1] = torch.from_numpy(np.random.default_rng(v).integers(0, 3, v).astype(np.float32)).to(x.dtype).cuda()
+    x[2, 20000:] = torch.sort(x[2, 20000:]).values      # the large ones in the last tiles
+    for n in (5, 20, 64):
+        check(x, [7, v - 1, -1], None, n, "longest rows")
+
+
 def test_outputs_are_optional_and_nothing_else_is_written():
     torch = torch_cuda()
     x = make(3, 9001, "float32", 4)

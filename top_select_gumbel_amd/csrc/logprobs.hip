@@ -12,13 +12,13 @@
 //                      for, every logit that can be among the row's best n. The sums are fp32 over a thread's
 //                      32 terms and binary64 beyond. A row of one tile is finished by the same workgroup.
 // ts_logp_row_kernel   joins a row's tiles in tile order (binary64), a row a wave.
-// ts_logp_top_kernel   the same, while another wave finds the row's best n among the tiles' candidates.
+// ts_logp_top_kernel   the same, while other waves find the row's best n among the tiles' candidates.
 // ts_logp_grad_kernel  one pass: reads a tile, writes its gradient.
 //
 // Measured (MI355X; a plain read of the same bytes takes 92 us for 2048 x 151936 in bf16, 68 us for 1777 x 128256):
 //   2048 x 151936 bf16  tile 95-116 us (6.5-5.4 TB/s), row 6 us, gradient 194 us (6.4 TB/s read and written)
 //   1777 x 128256 bf16  tile 80 us without ranks and alternatives (5.7 TB/s), 95-98 us with both (n = 5), top 8 us
-//   64 x 151936 fp32    tile 15 us with ranks and 20 alternatives, top 6.2 us (a plain read: 8 us)
+//   64 x 151936 fp32    tile 12-15 us with ranks and 20 alternatives, top 5.6 us (a plain read: 8 us)
 #include <math.h>
 
 #include <algorithm>
@@ -275,7 +275,7 @@ __device__ __forceinline__ int tile_candidates(LSmem& sm, const char* row, int V
 // The exact best n of items that a wave's lanes hold N each, more than n of which reach `low` and none is above kmax, found bit
 // by bit: the n-th largest key, then, among those equal to it, the id of the last that stays (ids are below V and differ).
 template <int N>
-__device__ __forceinline__ void exact_items(LSmem& sm, const uint2* c, int n, uint32_t low, uint32_t kmax, int V) {
+__device__ __forceinline__ void exact_items(uint2* list, const uint2* c, int n, uint32_t low, uint32_t kmax, int V) {
   auto count = [&](auto pred) {
     uint32_t k = 0;
 #pragma unroll
@@ -301,7 +301,7 @@ __device__ __forceinline__ void exact_items(LSmem& sm, const uint2* c, int n, ui
     const bool in = c[i].x > t || (c[i].x == t && c[i].y <= last);
     const uint64_t m = __ballot(in);
     const uint32_t o = put + mbcnt(m);
-    if (in && o < (uint32_t)kCapMax) sm.list[o] = c[i];
+    if (in && o < (uint32_t)kCapMax) list[o] = c[i];
     put += (uint32_t)__popcll(m);
   }
 }
@@ -633,58 +633,89 @@ __global__ __launch_bounds__(kLT) void ts_logp_row_kernel(LParams P) {
   if (r < P.rows) finish_row<DT>(P, row_in(P, r), r, P.part + (int64_t)r * P.tiles, nullptr);
 }
 
-// One row a workgroup of two waves: one joins the tiles, the other finds the best n of the candidates meanwhile, 24 a lane
-// at a time (four groups of six: find_low's 256 groups) and what is left of the ones before.
-template <int DT>
-__global__ __launch_bounds__(128) void ts_logp_top_kernel(LParams P) {
+// The best n of slots begin, begin + 1, ... of n_slots (key and id; 0: none) by one wave, into `list`, in no order: kBatch slots at
+// a time, every `step`, 24 a lane (four groups of six: find_low's 256 groups), and what is left of the ones before.
+constexpr int kGroup = 6, kItems = 4 * kGroup, kBatch = 64 * kItems;
+template <int DT, class I>
+__device__ __forceinline__ int best_of(const LParams& P, uint2* list, I item, int64_t begin, int64_t n_slots, int64_t step) {
+  constexpr int kLeft = (kCapMax + 63) / 64;
+  const int l = lane();
+  int count = 0;
+  for (int64_t base = begin; base < n_slots; base += step) {
+    uint2 c[kItems + kLeft];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int64_t at = base + 64 * i + l;
+      c[i] = at < n_slots ? item(at) : make_uint2(0u, 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < kLeft; ++i) c[kItems + i] = 64 * i + l < count ? list[64 * i + l] : make_uint2(0u, 0u);
+    wave_lds_sync();
+    uint32_t k4[4], k = 0;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      k4[g] = g < kLeft ? c[kItems + g].x : 0u;
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) k4[g] = max(k4[g], c[4 * i + g].x);   // a few slots fall into as many groups
+      k = max(k, k4[g]);
+    }
+    k = wave_max(k);
+    const uint32_t low = find_low<DT>(k4, k, P.n_top);
+    count = 0;
+#pragma unroll
+    for (int i = 0; i < kItems + kLeft; ++i) {
+      const uint64_t m = __ballot(c[i].x >= low);
+      if (!m) continue;
+      const int o = count + (int)mbcnt(m);
+      if (c[i].x >= low && o < kCapMax) list[o] = c[i];
+      count += __popcll(m);
+    }
+    if (count > P.cap) {
+      exact_items<kItems + kLeft>(list, c, P.n_top, low, k, P.V);
+      count = P.n_top;
+    }
+    wave_lds_sync();
+  }
+  return count;
+}
+
+// One row a workgroup of F + 1 waves: one joins the tiles, the others find the best n of the candidates meanwhile, F shares of
+// their batches, whose best one of them joins.
+constexpr int kFinders = 7;   // kFinders x kCapMax slots are one batch
+static_assert(kFinders * kCapMax <= kBatch, "the shares' best are one batch");
+template <int DT, int F>
+__global__ __launch_bounds__(64 * (F + 1)) void ts_logp_top_kernel(LParams P) {
   __shared__ LSmem sm;
-  constexpr int kGroup = 6, kItems = 4 * kGroup, kLeft = (kCapMax + 63) / 64;
-  const int r = (int)blockIdx.x, l = lane();
-  if (wave() == 0) {
+  __shared__ uint2 shares[F > 1 ? F : 1][kCapMax];
+  __shared__ int counts[F];
+  const int r = (int)blockIdx.x, w = __builtin_amdgcn_readfirstlane(wave());
+  const uint2* cand = P.cand + (int64_t)r * P.tiles * P.cap;
+  const int64_t n = (int64_t)P.tiles * P.cap;
+  if (w == 0) {
     finish_row<DT>(P, row_in(P, r), r, P.part + (int64_t)r * P.tiles, &sm);
   } else {
-    int count = 0;
-    const uint2* cand = P.cand + (int64_t)r * P.tiles * P.cap;
-    const int64_t n = (int64_t)P.tiles * P.cap;
-    for (int64_t base = 0; base < n; base += 64 * kItems) {
-      uint2 c[kItems + kLeft];
-#pragma unroll
-      for (int i = 0; i < kItems; ++i) {
-        const int64_t at = base + 64 * i + l;
-        c[i] = at < n ? cand[at] : make_uint2(0u, 0u);
-      }
-#pragma unroll
-      for (int i = 0; i < kLeft; ++i) c[kItems + i] = 64 * i + l < count ? sm.list[64 * i + l] : make_uint2(0u, 0u);
-      wave_lds_sync();
-      uint32_t k4[4], k = 0;
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        k4[g] = g < kLeft ? c[kItems + g].x : 0u;
-#pragma unroll
-        for (int i = 0; i < kGroup; ++i) k4[g] = max(k4[g], c[g * kGroup + i].x);
-        k = max(k, k4[g]);
-      }
-      k = wave_max(k);
-      const uint32_t low = find_low<DT>(k4, k, P.n_top);
-      count = 0;
-#pragma unroll
-      for (int i = 0; i < kItems + kLeft; ++i) {
-        const uint64_t m = __ballot(c[i].x >= low);
-        if (!m) continue;
-        const int o = count + (int)mbcnt(m);
-        if (c[i].x >= low && o < kCapMax) sm.list[o] = c[i];
-        count += __popcll(m);
-      }
-      if (count > P.cap) {
-        exact_items<kItems + kLeft>(sm, c, P.n_top, low, k, P.V);
-        count = P.n_top;
-      }
-      wave_lds_sync();
+    const int count = best_of<DT>(P, F > 1 ? shares[w - 1] : sm.list, [&](int64_t at) { return cand[at]; }, (int64_t)(w - 1) * kBatch, n,
+                                  (int64_t)F * kBatch);
+    if (lane() == 0) {
+      if (F > 1) counts[w - 1] = count;
+      else sm.count = (uint32_t)count;
     }
-    if (l == 0) sm.count = (uint32_t)count;
   }
   bar();
-  write_top<128>(P, r, (int)sm.count, sm);
+  if (F > 1) {
+    if (w == 1) {
+      const int count = best_of<DT>(
+          P, sm.list,
+          [&](int64_t at) {
+            const int f = (int)at / kCapMax, i = (int)at - f * kCapMax;
+            return i < counts[f] ? shares[f][i] : make_uint2(0u, 0u);
+          },
+          0, F * kCapMax, kBatch);
+      if (lane() == 0) sm.count = (uint32_t)count;
+    }
+    bar();
+  }
+  write_top<64 * (F + 1)>(P, r, (int)sm.count, sm);
 }
 
 // ------------------------------------------------------------------ gradient
@@ -814,7 +845,12 @@ hipError_t launch_logp(const LParams& P, hipStream_t s) {
   else hipLaunchKernelGGL((ts_logp_tile_kernel<DT, false, false>), tiles, block, 0, s, P);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (top) hipLaunchKernelGGL((ts_logp_top_kernel<DT>), dim3((unsigned)P.rows), dim3(128), 0, s, P);
+  // Several finders from the third batch of candidates on (64 x 151936, n = 64, two batches: row step 11.0 us against 9.8; 64 x
+  // 262144, n = 64, four: the call 30 us against 34; 1 x 4000000, n = 20: 26 against 63).
+  if (top && (int64_t)P.tiles * P.cap > 2 * kBatch)
+    hipLaunchKernelGGL((ts_logp_top_kernel<DT, kFinders>), dim3((unsigned)P.rows), dim3(64 * (kFinders + 1)), 0, s, P);
+  else if (top)
+    hipLaunchKernelGGL((ts_logp_top_kernel<DT, 1>), dim3((unsigned)P.rows), dim3(128), 0, s, P);
   else hipLaunchKernelGGL((ts_logp_row_kernel<DT>), dim3((unsigned)((P.rows + kLW - 1) / kLW)), block, 0, s, P);
   return hipGetLastError();
 }
