@@ -318,3 +318,14 @@ def test_binding_refusals():
                 lambda: ts.ts_token_logp(x[:1].expand(3, 64), i32([0] * 3))):
         with pytest.raises(ts.TopSelectError):
             bad()
+
+
+@pytest.mark.parametrize("v", [100, 20000])
+def test_empty_batch(v):
+    torch = torch_cuda()
+    x, tokens = torch.empty((0, v), device="cuda"), torch.empty(0, dtype=torch.int32, device="cuda")
+    r = ts.ts_token_logp(x, tokens, n_top=5, want_stats=True)
+    assert [tuple(t.shape) for t in r] == [(0,), (0,), (0,), (0,), (0, 5), (0, 5), (0, 4), (0,)]
+    assert ts.ts_token_logp_backward(x, tokens, None, r.stats).shape == (0, v)
+    r = ts.ts_token_logp(x, want_entropy=False, want_lse=False)
+    assert all(t is None for t in r[:-1]) and r.status.shape == (0,)
