@@ -123,3 +123,18 @@ def test_binding_refuses_host_tensors():
         ts.ts_token_logp_backward(x, i, None, torch.zeros(2, 4))
     with pytest.raises(ts.TopSelectError):
         ts.ts_cache_evict(x, torch.zeros(2, 8, dtype=torch.int32), i, i, 4)
+
+
+@pytest.mark.parametrize("rows,vocab", [((1 << 47) + 1, 1 << 30), (1 << 62, 2), ((1 << 63) - 1, 1), ((1 << 61) + 1, 3 * 8192)])
+def test_row_counts_whose_products_wrap(lib, rows, vocab):
+    # rows x tiles (and rows x stride) of these are small or negative numbers in 64 bits
+    assert ts.ts_workspace_bytes(ts.TS_OP_TOKEN_LOGP, rows, vocab, 0) == 0
+    assert logp(lib, rows=rows, vocab=vocab, stride=vocab) == ts.TS_ERR_INVALID_ARG and "too large" in ts.ts_last_error()
+    assert backward(lib, rows=rows, vocab=vocab, stride=vocab, out_stride=vocab) == ts.TS_ERR_INVALID_ARG
+    assert "too large" in ts.ts_last_error()
+
+
+def test_strides_whose_products_wrap(lib):
+    assert logp(lib, rows=1 << 10, stride=1 << 60) == ts.TS_ERR_INVALID_ARG and "too large" in ts.ts_last_error()
+    for kw in (dict(stride=1 << 60), dict(out_stride=1 << 60)):
+        assert backward(lib, rows=1 << 10, **kw) == ts.TS_ERR_INVALID_ARG and "too large" in ts.ts_last_error()

@@ -817,11 +817,13 @@ struct LPlan {
   int cap = 0;
   size_t off_cand = 0, total = 0;
 };
+// Whether one launch, of at most 2^32 - 1 threads, holds the rows' tiles. (Divided: any number of rows is asked for, and a
+// product could wrap to a small one.)
+bool rows_fit(int64_t rows, int64_t V) { return rows <= (int64_t)0xFFFFFFFF / kLT / ((V + kTile - 1) / kTile); }
 bool logp_plan(int64_t rows, int64_t V, int n_top, LPlan& pl) {
-  if (rows < 0 || V < 1 || V > TS_MAX_VOCAB || n_top < 0 || n_top > TS_LOGP_TOP_MAX) return false;
+  if (rows < 0 || V < 1 || V > TS_MAX_VOCAB || n_top < 0 || n_top > TS_LOGP_TOP_MAX || !rows_fit(rows, V)) return false;
   pl.tiles = (V + kTile - 1) / kTile;
   pl.cap = cand_cap(n_top);
-  if (rows * pl.tiles > (int64_t)0xFFFFFFFF / kLT) return false;   // a launch holds at most 2^32 - 1 threads
   if (pl.tiles == 1) {
     pl.total = 256;
     return true;
@@ -861,6 +863,9 @@ int dtype_size(int dtype) {
   return dtype == TS_DTYPE_F32 ? 4 : (dtype == TS_DTYPE_BF16 || dtype == TS_DTYPE_F16) ? 2 : 0;
 }
 
+// Rows a stride apart end within 2^60 elements, so that their addresses' arithmetic does not wrap.
+bool stride_fits(int64_t rows, int64_t stride) { return stride <= ((int64_t)1 << 60) / std::max<int64_t>(rows, 1); }
+
 // The checks that both entry points share; TS_OK also for an empty batch.
 int check_logits(const void* x, int dtype, int64_t rows, int64_t vocab, int64_t stride) {
   if (rows < 0) return fail(TS_ERR_INVALID_ARG, "rows = %lld < 0", (long long)rows);
@@ -870,6 +875,8 @@ int check_logits(const void* x, int dtype, int64_t rows, int64_t vocab, int64_t 
   if (rows == 0) return TS_OK;
   if (!x) return fail(TS_ERR_INVALID_ARG, "logits pointer is NULL");
   if ((uintptr_t)x % dtype_size(dtype)) return fail(TS_ERR_INVALID_ARG, "logits are not aligned to their type");
+  if (!rows_fit(rows, vocab)) return fail(TS_ERR_INVALID_ARG, "rows x tiles too large");
+  if (!stride_fits(rows, stride)) return fail(TS_ERR_INVALID_ARG, "rows x row_stride too large");
   return TS_OK;
 }
 
@@ -898,7 +905,7 @@ int ts_token_logp(const void* logits, int dtype, int64_t rows, int64_t vocab, in
     return fail(TS_ERR_INVALID_ARG, "n_top > 0 needs out_top_idx and out_top_logp");
   if (((uintptr_t)out_stats & 15u) != 0) return fail(TS_ERR_INVALID_ARG, "out_stats is not 16-byte aligned");
   LPlan pl;
-  if (!logp_plan(rows, vocab, n_top, pl)) return fail(TS_ERR_INVALID_ARG, "rows x tiles too large");
+  logp_plan(rows, vocab, n_top, pl);   // (of sizes that the checks above have let through)
   if (pl.tiles > 1) {
     if (!workspace) return fail(TS_ERR_WORKSPACE, "workspace is NULL");
     if (((uintptr_t)workspace & 255u) != 0) return fail(TS_ERR_WORKSPACE, "workspace is not 256-byte aligned");
@@ -950,13 +957,13 @@ int ts_token_logp_backward(const void* logits, int dtype, int64_t rows, int64_t 
   if (((uintptr_t)stats & 15u) != 0) return fail(TS_ERR_INVALID_ARG, "stats is not 16-byte aligned");
   const int size = dtype_size(dtype);
   if ((uintptr_t)grad_logits % size) return fail(TS_ERR_INVALID_ARG, "grad_logits are not aligned to their type");
+  if (!stride_fits(rows, grad_stride)) return fail(TS_ERR_INVALID_ARG, "rows x grad_stride too large");
   // the gradient may take the logits' place exactly, and may not overlap them otherwise
   const uintptr_t x0 = (uintptr_t)logits, x1 = x0 + (uintptr_t)((rows - 1) * row_stride + vocab) * size;
   const uintptr_t g0 = (uintptr_t)grad_logits, g1 = g0 + (uintptr_t)((rows - 1) * grad_stride + vocab) * size;
   if (g0 < x1 && x0 < g1 && !(g0 == x0 && grad_stride == row_stride))
     return fail(TS_ERR_INVALID_ARG, "grad_logits overlap the logits without taking their place");
   const int64_t tiles = (vocab + kTile - 1) / kTile;
-  if (rows * tiles > (int64_t)0xFFFFFFFF / kLT) return fail(TS_ERR_INVALID_ARG, "rows x tiles too large");
   int dev;
   rc = check_device(&dev);
   if (rc != TS_OK) return rc;
