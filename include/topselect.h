@@ -316,7 +316,8 @@ int ts_token_logp(const void* logits, int dtype, int64_t rows, int64_t vocab, in
  *   stats       [rows, 4] fp32, 16-byte aligned: the forward call's out_stats.
  *   grad_logp (needs tokens), grad_entropy, grad_lse   [rows] fp32 or NULL (0).
  *   grad_logits [rows, grad_stride] of `dtype`, written (the first vocab of each row). It may be
- *               the logits themselves (same address and stride) and may not overlap them otherwise.
+ *               the logits themselves (same address and stride); with the same stride its rows may
+ *               lie between the logits' rows; else it has to lie apart from them as a whole.
  * Computed in fp32 and rounded once to `dtype`. Rows without a token (-1) ignore grad_logp;
  * T == 0 gives 0; rows that the forward call rejected, or whose token or temperature is
  * invalid here, get NaN. Needs no workspace.

@@ -138,3 +138,12 @@ def test_strides_whose_products_wrap(lib):
     assert logp(lib, rows=1 << 10, stride=1 << 60) == ts.TS_ERR_INVALID_ARG and "too large" in ts.ts_last_error()
     for kw in (dict(stride=1 << 60), dict(out_stride=1 << 60)):
         assert backward(lib, rows=1 << 10, **kw) == ts.TS_ERR_INVALID_ARG and "too large" in ts.ts_last_error()
+
+
+@pytest.mark.parametrize("offset", [0, 4, -4, 396, -396, 800 - 396, -800, 800 + 4, 3 * 800])
+def test_interleaved_gradient_rows_that_share_elements(lib, offset):
+    # rows of 400 bytes, 800 apart: from 400 to 400 bytes beside each other they are apart (offsets 400, -400, 1200 ...)
+    kw = dict(rows=5, vocab=100, stride=200, out=(1 << 20) + offset, out_stride=200)
+    if offset == 0:      # taking the logits' place is allowed, but not one row short
+        kw["out_stride"] = 199
+    assert backward(lib, **kw) == ts.TS_ERR_INVALID_ARG and "overlap" in ts.ts_last_error()

@@ -188,3 +188,27 @@ def test_refusals():
                 lambda: ts.ts_token_logp_backward(x, i32([0, 1]), None, st, f32([1, 1]), out=torch.empty(2, 64))):
         with pytest.raises(ts.TopSelectError):
             bad()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("v,gap", [(5, 0), (100, 0), (9001, 3)])
+def test_gradient_rows_between_the_logits_rows(v, gap, dtype):
+    """Logits and gradient in one buffer, row by row: their address spans intersect, their rows do not."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(v)
+    rows, width = 6, 2 * (v + gap)
+    x = make(rows, v, dtype, v + 17)
+    a, h, l = rng.standard_normal((3, rows))
+    tokens = rng.integers(0, v, rows)
+    _, want = run(x, tokens, None, a, h, l)
+    for first in (True, False):                     # the gradient behind and before each row's logits
+        buf = torch.full((rows, width), 7.0, dtype=x.dtype, device="cuda")
+        xs, gs = (buf[:, :v], buf[:, v + gap:2 * v + gap]) if first else (buf[:, v + gap:2 * v + gap], buf[:, :v])
+        xs.copy_(x)
+        _, got = run(xs, tokens, None, a, h, l, out=gs)
+        assert torch.equal(got, want) and torch.equal(xs, x)
+        assert (buf[:, v:v + gap] == 7).all() and (buf[:, 2 * v + gap:] == 7).all()
+    lower = torch.zeros(2 * rows, v, dtype=x.dtype, device="cuda")      # one row down, every second row
+    lower[::2].copy_(x)
+    _, got = run(lower[::2], tokens, None, a, h, l, out=lower[1::2])
+    assert torch.equal(got, want) and torch.equal(lower[::2], x)

@@ -958,11 +958,16 @@ int ts_token_logp_backward(const void* logits, int dtype, int64_t rows, int64_t 
   const int size = dtype_size(dtype);
   if ((uintptr_t)grad_logits % size) return fail(TS_ERR_INVALID_ARG, "grad_logits are not aligned to their type");
   if (!stride_fits(rows, grad_stride)) return fail(TS_ERR_INVALID_ARG, "rows x grad_stride too large");
-  // the gradient may take the logits' place exactly, and may not overlap them otherwise
-  const uintptr_t x0 = (uintptr_t)logits, x1 = x0 + (uintptr_t)((rows - 1) * row_stride + vocab) * size;
-  const uintptr_t g0 = (uintptr_t)grad_logits, g1 = g0 + (uintptr_t)((rows - 1) * grad_stride + vocab) * size;
-  if (g0 < x1 && x0 < g1 && !(g0 == x0 && grad_stride == row_stride))
-    return fail(TS_ERR_INVALID_ARG, "grad_logits overlap the logits without taking their place");
+  // The gradient may take the logits' place exactly; otherwise no element may be shared. Rows equally far apart may lie between
+  // each other: `by` bytes behind the start of one's row, the other's has to fit between its end and the next one's start.
+  const uint64_t width = (uint64_t)vocab * size, step = (uint64_t)row_stride * size;
+  const uintptr_t x0 = (uintptr_t)logits, x1 = x0 + (uint64_t)(rows - 1) * step + width;
+  const uintptr_t g0 = (uintptr_t)grad_logits, g1 = g0 + (uint64_t)(rows - 1) * grad_stride * size + width;
+  if (g0 < x1 && x0 < g1 && !(g0 == x0 && grad_stride == row_stride)) {
+    const uint64_t by = g0 >= x0 ? (g0 - x0) % step : step - 1 - (x0 - g0 - 1) % step;
+    if (grad_stride != row_stride || by < width || by > step - width)
+      return fail(TS_ERR_INVALID_ARG, "grad_logits overlap the logits without taking their place");
+  }
   const int64_t tiles = (vocab + kTile - 1) / kTile;
   int dev;
   rc = check_device(&dev);
