@@ -212,3 +212,16 @@ def test_gradient_rows_between_the_logits_rows(v, gap, dtype):
     lower[::2].copy_(x)
     _, got = run(lower[::2], tokens, None, a, h, l, out=lower[1::2])
     assert torch.equal(got, want) and torch.equal(lower[::2], x)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("v", [100, 9001, 60000])
+def test_gradients_at_large_temperatures(v, dtype):
+    # 1 / (T S) is below the smallest normal number, the gradient, of incoming ones about as large as T, is not
+    torch = torch_cuda()
+    rng = np.random.default_rng(v)
+    t = [2.0 ** 64, 2.0 ** 65, 1e30, 1e36, 1e38, 3e38]
+    x = torch.from_numpy((rng.standard_normal((len(t), v)) * np.array(t)[:, None] * 0.1).astype(np.float32)).to(getattr(torch, dtype)).cuda()
+    a, h, l = rng.standard_normal((3, len(t))) * np.array(t) * [[0.3], [0.01], [0.1]]
+    check(x, rng.integers(0, v, len(t)), t, a, None, l, "large T")
+    check(x, rng.integers(0, v, len(t)), t, a, h, l, "large T, entropy")

@@ -770,11 +770,13 @@ __global__ __launch_bounds__(kLT) __attribute__((amdgpu_waves_per_eu(8))) void t
   const float temp = P.t ? P.t[r] : 1.0f;
   const int32_t token = P.tokens ? P.tokens[r] : -1;
   const bool ok = st.x == st.x && temp >= 0.0f && temp <= 3.402823466e38f && token >= -1 && token < P.V;
-  const float inv_t = temp > 0.0f ? 1.0f / fmaxf(temp, 0x1p-100f) : 0.0f;   // greedy rows do not depend on the logits
+  // A large T and the gradients are both taken by 2^-64, where 1 / (T S) could lie below the normal numbers and lose its bits.
+  const float by = temp > 0x1p64f ? 0x1p-64f : 1.0f;
+  const float inv_t = temp > 0.0f ? 1.0f / fmaxf(temp * by, 0x1p-100f) : 0.0f;   // greedy rows do not depend on the logits
   const float c = (float)exponent_scale(temp);
-  const float a = token >= 0 && P.g_logp ? P.g_logp[r] : 0.0f;
-  const float h = P.g_entropy ? P.g_entropy[r] : 0.0f;
-  const float l = P.g_lse ? P.g_lse[r] : 0.0f;
+  const float a = token >= 0 && P.g_logp ? P.g_logp[r] * by : 0.0f;
+  const float h = P.g_entropy ? P.g_entropy[r] * by : 0.0f;
+  const float l = P.g_lse ? P.g_lse[r] * by : 0.0f;
   // p (l - a - h (d - D)) / T = 2^z (k0 + k1 z)
   const float q = inv_t / st.y;
   float k0 = q * (l - a + h * st.z), k1 = -q * h * (float)kLn2;
