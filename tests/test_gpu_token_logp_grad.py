@@ -225,3 +225,20 @@ def test_gradients_at_large_temperatures(v, dtype):
     a, h, l = rng.standard_normal((3, len(t))) * np.array(t) * [[0.3], [0.01], [0.1]]
     check(x, rng.integers(0, v, len(t)), t, a, None, l, "large T")
     check(x, rng.integers(0, v, len(t)), t, a, h, l, "large T, entropy")
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("v", [6, 9001])
+def test_distances_beyond_the_largest_number(v, dtype):
+    # x - m is below the lowest fp32, (x - m) / T a few units: such logits have weight
+    torch = torch_cuda()
+    rng = np.random.default_rng(v)
+    x = torch.from_numpy((rng.uniform(-3e38, 3e38, (3, v))).astype(np.float32))
+    x[:, 1], x[:, 3] = 3.2e38, -3.2e38
+    x[2] = -3.2e38
+    x[2, 1] = 3.2e38
+    x = x.to(getattr(torch, dtype)).cuda()
+    t = [1e38, 6e37, 1.5e38]
+    # gradients of about 1e38, so that p g / T is a few hundredths
+    check(x, [3, 1, 2], t, [1e38, -2e37, 3e37], None, [1e37, 0.0, 2e37], "far apart")
+    check(x, [3, 1, 2], t, [1e38, 1e37, 1e37], [1e36, -2e36, 1e36], None, "far apart, entropy")

@@ -773,18 +773,19 @@ __global__ __launch_bounds__(kLT) __attribute__((amdgpu_waves_per_eu(8))) void t
   // A large T and the gradients are both taken by 2^-64, where 1 / (T S) could lie below the normal numbers and lose its bits.
   const float by = temp > 0x1p64f ? 0x1p-64f : 1.0f;
   const float inv_t = temp > 0.0f ? 1.0f / fmaxf(temp * by, 0x1p-100f) : 0.0f;   // greedy rows do not depend on the logits
-  const float c = (float)exponent_scale(temp);
+  const float c2 = (float)(2.0 * exponent_scale(temp));
   const float a = token >= 0 && P.g_logp ? P.g_logp[r] * by : 0.0f;
   const float h = P.g_entropy ? P.g_entropy[r] * by : 0.0f;
   const float l = P.g_lse ? P.g_lse[r] * by : 0.0f;
   // p (l - a - h (d - D)) / T = 2^z (k0 + k1 z)
   const float q = inv_t / st.y;
   float k0 = q * (l - a + h * st.z), k1 = -q * h * (float)kLn2;
-  const float add = a * inv_t, m = st.x;
+  const float add = a * inv_t, half_m = 0.5f * st.x;
   if (!ok) k0 = k1 = __uint_as_float(0x7FC00000u);
   const bool here = token >= 0 && token / kTile == tile;   // the tile holds the token
   auto grad = [&](float x, int id) -> float {
-    const float z = fmaxf((x - m) * c, kZMin);
+    // half the distance: at a large T one beyond the largest number counts. Rounded once, as x - m elsewhere
+    const float z = fmaxf(fmaf(x, 0.5f, -half_m) * c2, kZMin);
     const float g = __builtin_amdgcn_exp2f(z) * fmaf(k1, z, k0);
     return here && id == token ? g + add : g;
   };
