@@ -242,3 +242,79 @@ def test_distances_beyond_the_largest_number(v, dtype):
     # gradients of about 1e38, so that p g / T is a few hundredths
     check(x, [3, 1, 2], t, [1e38, -2e37, 3e37], None, [1e37, 0.0, 2e37], "far apart")
     check(x, [3, 1, 2], t, [1e38, 1e37, 1e37], [1e36, -2e36, 1e36], None, "far apart, entropy")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("v", [6, 8192, 20011, 60000])
+def test_confident_rows_keep_the_given_tokens_gradient(v, dtype):
+    # one token far above equal others, and given: its gradient is a (1 - p) / T = a (S - 1) / (S T). S - 1 has terms off by
+    # (3 d + 2) u and fp32 sums that add 9 u, as the forward call's test says. (S - 1) / S is formed in binary64, where S is off by
+    # at most 4 times 2^-53, and rounded to fp32 (u); 1 / T and two products add 3 u: (3 d + 15) u. That holds where S < 4/3;
+    # above, nothing much cancels and the general tolerance is the bound
+    torch = torch_cuda()
+    gaps = [4.0, 9.0, 12.0, 16.0, 20.0, 24.0]
+    x = torch.full((len(gaps), v), 1.25)
+    where = [0, v - 1, v // 2, min(8191, v - 1), min(8192, v - 1), 1]
+    for r, (g, at) in enumerate(zip(gaps, where)):
+        x[r, at] = 1.25 + g
+    x = x.to(getattr(torch, dtype)).cuda()
+    a = [1.0, -0.7, 1.3, -1.0, 0.9, 2.5]
+    half = torch.finfo(x.dtype).eps / 2
+    floor = 2.0 ** -25 if dtype == "float16" else 0.0
+    for tv in (1.0, 0.75):
+        t = None if tv == 1.0 else [tv] * len(gaps)
+        check(x, where, t, a, None, None, "confident")
+        check(x, where, t, a, [0.3, -0.2, 1.0, 0.1, -1.0, 0.5], [1.0, 0.1, 1.3, 0.0, -0.9, 0.2], "confident, all")
+        g = run(x, where, t, a, None, None)[1].double().cpu().numpy()
+        sharp = 0
+        for i in range(len(gaps)):
+            d, av = float(x[i, where[i]].double() - 1.25) / tv, oracle.to_f32(a[i])
+            rest = (v - 1) * math.exp(-d)
+            if rest >= 0.333:
+                continue
+            sharp += 1
+            want = av * rest / (1 + rest) / tv
+            tol = (3 * d + 15) * U * abs(want) + 4 * 2.0 ** -53 * abs(av) / tv
+            assert abs(g[i, where[i]] - want) <= tol * (1 + half) + half * abs(want) + floor, (tv, i, g[i, where[i]], want)
+        assert sharp >= 3
+
+
+def test_confident_rows_at_the_largest_and_smallest_temperatures():
+    # the same at a temperature that is scaled and one that acts as 2^-100, for greedy and for rejected rows
+    x = np.full((5, 50), -3e38, np.float32)
+    x[:, 7] = 3e38
+    x[1] = -1e-30
+    x[1, 7] = 1e-30
+    t = [2e37, 1e-35, 2e37, np.nan, 0.0]
+    a = [1e37, 1.0, 1e37, 1.0, 1.0]
+    xt = torch_cuda().from_numpy(x).cuda()
+    tokens = [7, 7, 50, 7, 7]
+    g = host(run(xt, tokens, t, a, None, None)[1])
+    assert np.isnan(g[2]).all() and np.isnan(g[3]).all() and not g[4].any()
+    d = 2 * oracle.to_f32(3e38) / oracle.to_f32(2e37)
+    rest = 49 * math.exp(-d)
+    want = oracle.to_f32(1e37) / oracle.to_f32(2e37) * rest / (1 + rest)
+    assert rest < 1e-11 and abs(g[0, 7] - want) <= (3 * d + 15) * U * want + 4 * 2.0 ** -53
+    p = 1 / (1 + 49 * math.exp(-2 * oracle.to_f32(1e-30) * 2.0 ** 100))     # 2.5 away
+    want = (1 - p) * 2.0 ** 100
+    assert 0.15 < p < 0.3 and abs(g[1, 7] - want) <= want * 90 * U
+    g = host(run(xt, tokens, t, a, None, a)[1])       # l = a: what is left is a / T
+    assert abs(g[0, 7] - oracle.to_f32(1e37) / oracle.to_f32(2e37)) <= 3 * U
+    assert abs(g[1, 7] - 2.0 ** 100) <= 2.0 ** 100 * 90 * U
+
+
+def test_confident_row_whose_backward_call_is_invalid():
+    # the forward call's statistics are in order, the backward call's token or temperature is not
+    x = np.zeros((4, 30), np.float32)
+    x[:, 3] = 20.0
+    torch = torch_cuda()
+    xt, one = torch.from_numpy(x).cuda(), f32([1.0] * 4)
+    st = ts.ts_token_logp(xt, i32([3] * 4), one, want_stats=True).stats
+    g = ts.ts_token_logp_backward(xt, i32([3, 3, 30, -2]), f32([-1.0, math.inf, 1.0, 1.0]), st, one, one, one)
+    assert np.isnan(host(g)).all()
+    # statistics of a call without tokens serve any of them
+    other = ts.ts_token_logp(xt, None, one, want_stats=True).stats
+    assert torch.equal(other, st)
+    for token in (3, 4):
+        check(xt, [token] * 4, [1.0] * 4, [1.0] * 4, None, None, "stats without tokens",
+              g=ts.ts_token_logp_backward(xt, i32([token] * 4), one, other, one))

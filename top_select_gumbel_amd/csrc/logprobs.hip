@@ -417,7 +417,10 @@ __device__ __forceinline__ void finish_row(const LParams& P, const RowIn& in, in
   if (P.rank) P.rank[r] = ok ? (given ? (int32_t)above + 1 : 0) : -1;
   if (P.entropy) P.entropy[r] = ok ? fmaxf((float)(log_s - mean), 0.0f) : nan;
   if (P.lse) P.lse[r] = ok ? (greedy ? INFINITY : (float)((double)m * c2 * kLn2 + log_s)) : nan;
-  if (P.stats) P.stats[r] = ok ? make_float4(m, greedy ? 1.0f : (float)s, (float)mean, 0.0f) : make_float4(nan, nan, nan, nan);
+  if (P.stats) {   // maximum, S, D, 1 - 1/S
+    const double ss = greedy ? 1.0 : s;
+    P.stats[r] = ok ? make_float4(m, (float)ss, (float)mean, (float)((ss - 1.0) / ss)) : make_float4(nan, nan, nan, nan);
+  }
   if (P.status) P.status[r] = st;
   if (sm) {
     sm->m = m;
@@ -780,14 +783,18 @@ __global__ __launch_bounds__(kLT) __attribute__((amdgpu_waves_per_eu(8))) void t
   // p (l - a - h (d - D)) / T = 2^z (k0 + k1 z)
   const float q = inv_t / st.y;
   float k0 = q * (l - a + h * st.z), k1 = -q * h * (float)kLn2;
-  const float add = a * inv_t, half_m = 0.5f * st.x;
+  const float add = a * inv_t, m = st.x, half_m = 0.5f * m;
   if (!ok) k0 = k1 = __uint_as_float(0x7FC00000u);
   const bool here = token >= 0 && token / kTile == tile;   // the tile holds the token
+  // Where the given token is the maximum and nearly all of S, fp32 loses a / T - p a / T: its part of a is a (1 - p) / T then, by
+  // the forward call's 1 - 1/S. (Not where l makes up for a: then the sum is not small, and the usual one the closer.)
+  const bool sharp = here && ok && st.w < 0.25f && fabsf(l - a + h * st.z) >= 0.5f * fabsf(a);
+  const float top = fmaf(q, fmaf(h, st.z, l), a * (st.w * inv_t));
   auto grad = [&](float x, int id) -> float {
     // half the distance: at a large T one beyond the largest number counts. Rounded once, as x - m elsewhere
     const float z = fmaxf(fmaf(x, 0.5f, -half_m) * c2, kZMin);
     const float g = __builtin_amdgcn_exp2f(z) * fmaf(k1, z, k0);
-    return here && id == token ? g + add : g;
+    return here && id == token ? (sharp && x == m ? top : g + add) : g;
   };
 #pragma unroll
   for (int v = 0; v < L::kNV; ++v) {
