@@ -18,6 +18,7 @@ from .logprobs import (
     LogpResult,
     STATUS_BAD_TOKEN,
     cache_evict_row,
+    cache_evict_row_sorted,
     token_logp_grad_row,
     token_logp_row,
 )

@@ -96,3 +96,20 @@ def test_evict_edges():
     assert oracle.cache_evict_row([1.0, math.nan], [], [0, 1], 1, 1, 1, 0, 0).status == 0     # behind the length
     assert oracle.cache_evict_row([1.0, 2.0], [], [0, 1], 2, 0, 1, 0, 0).status == oracle.STATUS_BAD_K
     assert oracle.cache_evict_row([1.0, 2.0], [], [0, 1], 2, 2, 1, 0, 0).status == oracle.STATUS_BAD_K
+
+
+def test_evict_by_one_sort_equals_the_plain_oracle():
+    rng = np.random.default_rng(6)
+    for trial in range(120):
+        slots, keep = int(rng.integers(1, 40)), int(rng.integers(0, 42))
+        n, keep_max = int(rng.integers(0, slots + 1)), int(rng.integers(1, 42))
+        score = rng.integers(-1, 3, slots).astype(np.float32) if trial % 2 else rng.standard_normal(slots).astype(np.float32)
+        if trial % 7 == 0:
+            score[rng.integers(0, slots)] = [math.nan, math.inf, -math.inf, 3e38][trial % 4]
+        w = rng.random((trial % 3, slots)).astype(np.float32) * (3e38 if trial % 11 == 0 else 1)
+        position = rng.permutation(slots).astype(np.int32) - (20 if trial % 5 == 0 else 0)
+        args = (score, w, position, n, keep, keep_max, int(rng.integers(0, 9)), int(rng.choice([0, 3, 30, 2 ** 31 - 1])))
+        a, b = oracle.cache_evict_row(*args), oracle.cache_evict_row_sorted(*args)
+        assert (a.status, a.source, a.length) == (b.status, b.source, b.length), trial
+        if not a.status:
+            assert np.array_equal(a.score, b.score) and np.array_equal(a.position, b.position), trial
