@@ -772,14 +772,18 @@ __global__ __launch_bounds__(kLT) __attribute__((amdgpu_waves_per_eu(8))) void t
   const float4 st = P.stats[r];
   const float temp = P.t ? P.t[r] : 1.0f;
   const int32_t token = P.tokens ? P.tokens[r] : -1;
+  float a = P.g_logp ? P.g_logp[r] : 0.0f;
+  float h = P.g_entropy ? P.g_entropy[r] : 0.0f;
+  float l = P.g_lse ? P.g_lse[r] : 0.0f;
   const bool ok = st.x == st.x && temp >= 0.0f && temp <= 3.402823466e38f && token >= -1 && token < P.V;
+  if (token < 0) a = 0.0f;
   // A large T and the gradients are both taken by 2^-64, where 1 / (T S) could lie below the normal numbers and lose its bits.
   const float by = temp > 0x1p64f ? 0x1p-64f : 1.0f;
+  a *= by;
+  h *= by;
+  l *= by;
   const float inv_t = temp > 0.0f ? 1.0f / fmaxf(temp * by, 0x1p-100f) : 0.0f;   // greedy rows do not depend on the logits
   const float c2 = (float)(2.0 * exponent_scale(temp));
-  const float a = token >= 0 && P.g_logp ? P.g_logp[r] * by : 0.0f;
-  const float h = P.g_entropy ? P.g_entropy[r] * by : 0.0f;
-  const float l = P.g_lse ? P.g_lse[r] * by : 0.0f;
   // p (l - a - h (d - D)) / T = 2^z (k0 + k1 z)
   const float q = inv_t / st.y;
   float k0 = q * (l - a + h * st.z), k1 = -q * h * (float)kLn2;
@@ -790,34 +794,48 @@ __global__ __launch_bounds__(kLT) __attribute__((amdgpu_waves_per_eu(8))) void t
   // the forward call's 1 - 1/S. (Not where l makes up for a: then the sum is not small, and the usual one the closer.)
   const bool sharp = here && ok && st.w < 0.25f && fabsf(l - a + h * st.z) >= 0.5f * fabsf(a);
   const float top = fmaf(q, fmaf(h, st.z, l), a * (st.w * inv_t));
-  auto grad = [&](float x, int id) -> float {
+  auto grad = [&](float x) -> float {
     // half the distance: at a large T one beyond the largest number counts. Rounded once, as x - m elsewhere
     const float z = fmaxf(fmaf(x, 0.5f, -half_m) * c2, kZMin);
-    const float g = __builtin_amdgcn_exp2f(z) * fmaf(k1, z, k0);
-    return here && id == token ? (sharp && x == m ? top : g + add) : g;
+    return __builtin_amdgcn_exp2f(z) * fmaf(k1, z, k0);
   };
+  auto token_grad = [&](float x, float g) -> float { return sharp && x == m ? top : g + add; };
+  // A tile without the token, as most are, has no choice to make at its logits (64 of 525 instructions a wave). Past the caches,
+  // where it is whole, its vectors have none either: each one's wait would be for the stores of those before it too (2048 x 151936
+  // bf16, the call: 294 us against 299; in the caches the stores then come too close: 300 x 65536 fp32 51.7 us against 49.8).
+  auto vectors = [&](auto plain) {
 #pragma unroll
-  for (int v = 0; v < L::kNV; ++v) {
-    const int at = t0 + v * kLT * L::kW;
-    if (at + L::kW <= P.V) {
-      u32x4 o;
-      if constexpr (DT == TS_DTYPE_F32) {
+    for (int v = 0; v < L::kNV; ++v) {
+      const int at = t0 + v * kLT * L::kW;
+      if ((ONCE && plain()) || at + L::kW <= P.V) {
+        float g[L::kW];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = __float_as_uint(grad(unpack<DT>(raw[v], j), at + j));
-      } else {
+        for (int j = 0; j < L::kW; ++j) {
+          const float x = unpack<DT>(raw[v], j);
+          g[j] = grad(x);
+          if (!plain() && here && at + j == token) g[j] = token_grad(x, g[j]);
+        }
+        u32x4 o;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          o[j] = pack2<DT>(grad(unpack<DT>(raw[v], 2 * j), at + 2 * j), grad(unpack<DT>(raw[v], 2 * j + 1), at + 2 * j + 1));
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (DT == TS_DTYPE_F32) o[j] = __float_as_uint(g[j]);
+          else o[j] = pack2<DT>(g[2 * j], g[2 * j + 1]);
+        }
+        if (ONCE) store16_once(out + (int64_t)at * L::kSize, o);
+        else store16(out + (int64_t)at * L::kSize, o);
       }
-      if (ONCE) store16_once(out + (int64_t)at * L::kSize, o);
-      else store16(out + (int64_t)at * L::kSize, o);
     }
-  }
+  };
+  if (!here && (!ONCE || (tile + 1) * kTile <= P.V)) vectors(std::true_type{});
+  else vectors(std::false_type{});
   // the row's last, partial vector
   const int tail = P.V / L::kW * L::kW, off = tail - t0;
   if (tail < P.V && off >= 0 && off < kTile && off % (kLT * L::kW) == 0) {
 #pragma nounroll
-    for (int j = tail; j < P.V; ++j) store_logit<DT>(out, j, grad(load_logit<DT>(row, j), j));
+    for (int j = tail; j < P.V; ++j) {
+      const float x = load_logit<DT>(row, j), g = grad(x);
+      store_logit<DT>(out, j, j == token ? token_grad(x, g) : g);
+    }
   }
 }
 
