@@ -318,3 +318,26 @@ def test_confident_row_whose_backward_call_is_invalid():
     for token in (3, 4):
         check(xt, [token] * 4, [1.0] * 4, [1.0] * 4, None, None, "stats without tokens",
               g=ts.ts_token_logp_backward(xt, i32([token] * 4), one, other, one))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_same_gradient_bits_whatever_the_batch_and_the_token(dtype):
+    # alone, among others, in a batch that passes the caches by, at another address, and with a token that has no gradient
+    torch = torch_cuda()
+    v, rows = 100003, 720 if dtype != "float32" else 360
+    x = make(rows, v, dtype, 50)
+    rng = np.random.default_rng(50)
+    h, l = rng.standard_normal((2, rows)) * 30
+    tokens = rng.integers(0, v, rows)
+    tokens[:3] = 5, 50000, v - 1
+    none, zero = np.full(rows, -1), np.zeros(rows)
+    _, whole = run(x, none, None, zero, h, l)
+    _, given = run(x, tokens, None, zero, h, l)
+    assert torch.equal(whole, given)
+    few = [0, 1, 2, 77, rows - 1]
+    for shift in (0, 1):
+        y = torch.zeros(len(few) * (v + 5) + shift, dtype=x.dtype, device="cuda")[shift:].view(len(few), v + 5)[:, :v]
+        y.copy_(x[few])
+        for t in (tokens, none):
+            _, g = run(y, t[few], None, zero[few], h[few], l[few])
+            assert torch.equal(g, whole[few]), shift

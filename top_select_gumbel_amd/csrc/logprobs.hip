@@ -742,6 +742,8 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     typedef float f2 __attribute__((ext_vector_type(2)));
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){a, b}, bf2));   // round to nearest even
   } else {
+    // whole fp32 numbers first: some of the products would else be rounded to fp16 with their last operation, others after it
+    asm("" : "+v"(a), "+v"(b));
     return (uint32_t)__half_as_ushort(__float2half_rn(a)) | ((uint32_t)__half_as_ushort(__float2half_rn(b)) << 16);
   }
 }
