@@ -11,8 +11,8 @@
 // weights each: 8.8 us, all of it the latency of a dozen dependent steps); else the sums come from ts_evict_sum_kernel
 // and the moves go to ts_evict_move_kernel, both spread over the chip.
 //
-// Long rows are spread in every step (a tile of 1024 slots a workgroup), a launch each (in brackets: us for 8 rows of 131072
-// slots, 4 fp32 weights each, cut to 8192 positions of 2 x 256 bytes):
+// Long rows are spread in every step but the cut (a tile of 1024 slots a workgroup), a launch each (in brackets: us for 8 rows
+// of 131072 slots, 4 fp32 weights each, cut to 8192 positions of 2 x 256 bytes):
 //   sum    s, and each tile's largest position and extreme keys [9.0, 25 MB]
 //   bin    both classes (protected, others) counted by the first 11 bits of u = key - smallest key of the row [7.0]
 //   list   the bin that holds the cut, its slots listed [5.5]
@@ -24,6 +24,13 @@
 //
 // The cut is found by radix select on u = key - smallest key of the row (ordered keys, so that the first 2048 bins
 // span the row's own range and not the whole of fp32), then, once few slots share its bin, by ranking those.
+//
+// The limit of this: a long row's cut whose first bin holds more than 4096 slots. They are not listed then, and the row's one
+// workgroup goes through all of the row in memory, two to five times; the time is that of its dependent loads, 1.3 us for 1000
+// slots of the row. Such are rows that keep some of thousands of equal weights, and long ones: evenly spread weights from 524288
+// slots on, heavy-tailed ones from 2^20 on, both sooner where one sum is 0 and stretches the range. (One row, us a call, listed
+// against not: 131072 slots, 8 rows, 46 against 110-166; 524288 slots 42 against 490-530; 2^20 slots 52 against 1200-1360; 2^22
+// slots 5200-5400. A sort of the row in elementary operations takes 470-760, 600-1200 and 1300-2900 for the last three.)
 #include <algorithm>
 #include <type_traits>
 
