@@ -318,7 +318,9 @@ int ts_token_logp(const void* logits, int dtype, int64_t rows, int64_t vocab, in
  *   grad_logits [rows, grad_stride] of `dtype`, written (the first vocab of each row). It may be
  *               the logits themselves (same address and stride); with the same stride its rows may
  *               lie between the logits' rows; else it has to lie apart from them as a whole.
- * Computed in fp32 and rounded once to `dtype`. Rows without a token (-1) ignore grad_logp;
+ * Computed in fp32 and rounded once to `dtype`; exp(d) below 2^-126 counts as 0. The statistics
+ * keep a confident row's 1 - p, so a given token that is the maximum keeps its gradient's relative
+ * accuracy. Rows without a token (-1) ignore grad_logp;
  * T == 0 gives 0; rows that the forward call rejected, or whose token or temperature is
  * invalid here, get NaN. Needs no workspace.
  */

@@ -16,7 +16,7 @@
 // ts_logp_grad_kernel  one pass: reads a tile, writes its gradient.
 //
 // Measured (MI355X; a plain read of the same bytes takes 92 us for 2048 x 151936 in bf16, 68 us for 1777 x 128256):
-//   2048 x 151936 bf16  tile 95-116 us (6.5-5.4 TB/s), row 6 us, gradient 194 us (6.4 TB/s read and written)
+//   2048 x 151936 bf16  tile 93-116 us (6.7-5.4 TB/s), row 6 us, gradient 187 us (6.7 TB/s read and written)
 //   1777 x 128256 bf16  tile 80 us without ranks and alternatives (5.7 TB/s), 95-98 us with both (n = 5), top 8 us
 //   64 x 151936 fp32    tile 12-15 us with ranks and 20 alternatives, top 5.6 us (a plain read: 8 us)
 #include <math.h>
@@ -754,7 +754,7 @@ __device__ __forceinline__ void store_logit(char* row, int64_t i, float v) {
 }
 
 // Bound by HBM: bytes read and written. ONCE, for logits and gradient that do not fit the last-level cache together: loads
-// and stores past the caches (2048 x 151936 bf16: 193 us against 217; 301 x 65537 fp32, which fits: 33 us against 25).
+// and stores past the caches (2048 x 151936 bf16: 187 us against 209; 301 x 65537 fp32, which fits: 26 us against 25).
 // Each element is read and then written by one thread and read by no other, so the gradient may take the
 // logits' own place. (A row's last vector, where it is not whole, is taken element by element for that.)
 template <int DT, bool ONCE>
