@@ -165,7 +165,13 @@ def _prepare_append(c, gen, dev):
 
 
 def _pools(c, gen, dev):
-    return [_normal((c["pages"], c["heads"], c["page"], c["dim"]), c["type"], gen, dev) for _ in range(c["pools"])]
+    """The pools, and what a program that makes the library's calls keeps beside them: their addresses, taken once."""
+    pools = [_normal((c["pages"], c["heads"], c["page"], c["dim"]), c["type"], gen, dev) for _ in range(c["pools"])]
+    plan = None
+    if own:
+        import top_select_gumbel_amd as ts
+        plan = ts.PagePools(pools)
+    return dict(pools=pools, plan=plan)
 
 
 def _sequences(c, seqs, shared, gen, dev):
@@ -204,18 +210,18 @@ def _prepare_fork(c, gen, dev):
     gone = torch.rand(n, generator=gen, device=dev) < c["ended"]
     parent = torch.where(gone, torch.full_like(parent, -1), parent).to(torch.int32)
     new = torch.full((n,), c["new"], dtype=torch.int32, device=dev)
-    return dict(case=c, table=table, lengths=lengths, refs=refs, parent=parent, n_new=new, pools=_pools(c, gen, dev))
+    return dict(case=c, table=table, lengths=lengths, refs=refs, parent=parent, n_new=new, **_pools(c, gen, dev))
 
 
 def _prepare_compact(c, gen, dev):
     table, lengths, refs = _sequences(c, c["seqs"], 0, gen, dev)
-    return dict(case=c, table=table, lengths=lengths, refs=refs, pools=_pools(c, gen, dev))
+    return dict(case=c, table=table, lengths=lengths, refs=refs, **_pools(c, gen, dev))
 
 
 def _prepare_copy(c, gen, dev):
     order = torch.randperm(c["pages"], generator=gen, device=dev).to(torch.int32)
     return dict(case=c, source=order[: c["pairs"]].contiguous(), target=order[c["pairs"]: 2 * c["pairs"]].contiguous(),
-                pools=_pools(c, gen, dev))
+                **_pools(c, gen, dev))
 
 
 # ---------------------------------------------------------------- one pass
@@ -241,19 +247,19 @@ def _append_own(s):
 
 def _fork_own(s):
     import top_select_gumbel_amd as ts
-    r = ts.ts_pages_fork(s["table"], s["lengths"], s["refs"], s["parent"], s["case"]["page"], n_new=s["n_new"], pools=s["pools"])
+    r = ts.ts_pages_fork(s["table"], s["lengths"], s["refs"], s["parent"], s["case"]["page"], n_new=s["n_new"], pools=s["plan"])
     return dict(table=r.table, lengths=r.lengths, refs=r.refs, status=r.status, pools=s["pools"])
 
 
 def _compact_own(s):
     import top_select_gumbel_amd as ts
-    r = ts.ts_pages_compact(s["table"], s["lengths"], s["refs"], s["case"]["page"], pools=s["pools"])
+    r = ts.ts_pages_compact(s["table"], s["lengths"], s["refs"], s["case"]["page"], pools=s["plan"])
     return dict(table=r.table, refs=r.refs, map=r.map, count=r.count, status=r.status, pools=s["pools"])
 
 
 def _copy_own(s):
     import top_select_gumbel_amd as ts
-    return dict(status=ts.ts_pages_copy(s["source"], s["target"], s["pools"]), pools=s["pools"])
+    return dict(status=ts.ts_pages_copy(s["source"], s["target"], s["plan"]), pools=s["pools"])
 
 
 def _attend_plain(s):
