@@ -81,6 +81,10 @@ extern "C" {
 #define TS_ROW_BAD_T        4      /* temperature negative, NaN or infinite */
 #define TS_ROW_BAD_MINP     5      /* min_p outside [0, 1] or NaN (the _minp entry points) */
 #define TS_ROW_BAD_TOKEN    6      /* given token outside [0, vocab) and not -1 (ts_token_logp) */
+#define TS_ROW_BAD_PAGE     7      /* page number outside [0, pages) (the paged entry points) */
+#define TS_ROW_BAD_LENGTH   8      /* length negative or past what the table holds (the paged entry points) */
+#define TS_ROW_BAD_PARENT   9      /* parent outside [-1, seqs) (ts_pages_fork) */
+#define TS_ROW_NO_PAGE      10     /* too few free pages (ts_pages_fork) */
 
 /* Operation ids for ts_workspace_bytes. */
 #define TS_OP_TOPK_SELECT   0
@@ -371,6 +375,113 @@ int ts_cache_evict(const float* score, int64_t rows, int64_t slots, int64_t scor
                    int32_t* out_source, int32_t* row_status, const ts_cache* k_cache,
                    const ts_cache* v_cache, int64_t heads, void* workspace, size_t workspace_bytes,
                    void* stream);
+
+/*
+ * Paged caches. Keys and values lie in pages of page_slots slots; position j of sequence b lies in page table[b, j / page_slots],
+ * slot j % page_slots, for j < lengths[b]. `table` is [batch, table_stride] int32, of which the first table_width entries
+ * of a row are used; what lies past a sequence's last position is not read. A dense cache [batch, heads, slots, dim] is the
+ * case page_slots = slots, table[b] = b (so ts_cache_evict's caches are read as they are).
+ * Lengths outside [0, table_width * page_slots] give TS_ROW_BAD_LENGTH, page numbers outside [0, pages) TS_ROW_BAD_PAGE.
+ */
+typedef struct ts_paged {   /* one layer's keys or values: slot s of page p under head h is at data + p * page_stride + ... (bytes) */
+  void* data;
+  int64_t page_stride, head_stride, slot_stride;
+} ts_paged;
+
+/*
+ * ts_cache_attend -- attention of one new token of each sequence over its cached positions (the token's own among them).
+ * For query head h over j in [lo, n), n = lengths[b], lo = max(0, n - window) (window 0: 0), with keys and values of head
+ * h / (q_heads / kv_heads):  s_j = q . k_j,  m = max s,  p_j = exp(scale (s_j - m)),  S = sum p_j,
+ *   out = sum p_j v_j / S,  lse = scale m + log S,  weight_j = p_j / S.
+ *   q           [batch, q_heads, dim] of `dtype` (TS_DTYPE_*) at the given strides (elements), like out; dim in [1, 256].
+ *   k_pages, v_pages   of the same type, any strides.
+ *   scale       in [2^-64, 2^64].
+ *   out         may not overlap q.   out_lse  [batch, q_heads] fp32 or NULL.
+ *   out_weights [batch, q_heads, weights_slots] of `weights_dtype` at the given strides (elements) or NULL (weights_slots 0):
+ *               0 outside [lo, n). With batch * kv_heads rows of q_heads / kv_heads weights it is what ts_cache_evict takes.
+ *               A length above weights_slots gives TS_ROW_BAD_LENGTH.
+ *   row_status  [batch] int32 or NULL.
+ * A sequence of no positions, or whose scores are all -inf, gives out 0, lse -inf, weights 0. Slots outside [lo, n) may hold
+ * anything. NaN and infinities in attended keys and values act as in the formula (a non-finite value may give NaN where
+ * the formula has an infinity). Sequences with a non-OK status get NaN. Scores, sums and outputs are fp32, rounded once; p_j below 2^-126 counts as 0; results
+ * depend on the batch in their last bits only (the sums' order), and are the same bits for the same call.
+ * Workspace: ts_cache_attend_workspace(..., max_len = table_width * page_slots, ...); it may be 0.
+ */
+size_t ts_cache_attend_workspace(int64_t batch, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t max_len, int64_t weights_slots);
+int ts_cache_attend(const void* q, int dtype, int64_t batch, int32_t q_heads, int32_t kv_heads, int32_t dim,
+                    int64_t q_batch_stride, int64_t q_head_stride, const ts_paged* k_pages, const ts_paged* v_pages, int64_t pages,
+                    int32_t page_slots, const int32_t* table, int64_t table_width, int64_t table_stride, const int32_t* lengths,
+                    float scale, int32_t window, void* out, int64_t out_batch_stride, int64_t out_head_stride, float* out_lse,
+                    void* out_weights, int weights_dtype, int64_t weights_slots, int64_t weights_batch_stride,
+                    int64_t weights_head_stride, int32_t* row_status, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ts_cache_append -- the keys and values of each sequence's newest tokens into their pages. Tokens [offsets[b], offsets[b + 1])
+ * are the last positions of sequence b: token t goes to position lengths[b] - (offsets[b + 1] - t).
+ *   k_new, v_new   [tokens, kv_heads, slot_bytes] at the given strides (bytes): any element type; slot_bytes at most 4096.
+ *   offsets     [batch + 1] int32, ascending, from 0 to at most `tokens`. Tokens outside them are not written.
+ *   row_status  [batch] int32 or NULL: TS_ROW_BAD_LENGTH (fewer positions than new tokens too) leaves the sequence's slots as
+ *               they are, TS_ROW_BAD_PAGE those of the bad pages.
+ * Needs no workspace. Sequences whose new positions share a slot race.
+ */
+int ts_cache_append(const void* k_new, const void* v_new, int64_t tokens, int64_t batch, int32_t kv_heads, int64_t slot_bytes,
+                    int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                    const int32_t* offsets, const ts_paged* k_pages, const ts_paged* v_pages, int64_t pages, int32_t page_slots,
+                    const int32_t* table, int64_t table_width, int64_t table_stride, const int32_t* lengths, int32_t* row_status,
+                    void* stream);
+
+typedef struct ts_pool {   /* an array of pages: page p is the page_bytes bytes at data + p * page_stride */
+  void* data;
+  int64_t page_stride, page_bytes;
+} ts_pool;
+
+/*
+ * ts_pages_fork -- the next step's sequences: child i continues sequence parent[i] (-1: none), grown by n_new[i] positions.
+ * A sequence that no child continues is freed; one that several continue is forked: its whole pages are shared, its part-filled last
+ * page stays with its first child and is copied for each other. refs[p] counts the table entries that name page p (and
+ * whatever else holds it); pages whose count is not above 0 are free. Fresh pages are the lowest that are free once all
+ * children have taken over what they share, child after child, a child's copy first. Pages that the growth reaches are not cleared.
+ *   parent, n_new   [children] int32; n_new may be NULL (0).
+ *   out_table   [children, out_width] at out_stride, -1 past a child's pages; apart from `table`.
+ *   out_lengths [children];  out_refs [pages], may be refs.
+ *   pools       the n_pools arrays (host memory: keys and values of every layer) in which pages are copied.
+ *   row_status  [children] or NULL. TS_ROW_NO_PAGE: not enough free pages for the child (each takes its turn whether or not those
+ *               before it fit): it keeps its parent's positions and does not grow, and is left empty if it needed a copy.
+ *               TS_ROW_BAD_LENGTH: n_new negative or past out_width: the same, or the parent's length bad or past out_width: empty.
+ *               TS_ROW_BAD_PAGE, TS_ROW_BAD_PARENT: the parent's row, or parent[i], is bad: empty.
+ * The pages of a sequence whose own row is bad keep their counts. Workspace: ts_pages_fork_workspace.
+ */
+size_t ts_pages_fork_workspace(int64_t seqs, int64_t children, int64_t pages);
+int ts_pages_fork(const int32_t* table, int64_t seqs, int64_t table_width, int64_t table_stride, const int32_t* lengths,
+                  const int32_t* refs, int64_t pages, int32_t page_slots, const int32_t* parent, const int32_t* n_new,
+                  int64_t children, int32_t* out_table, int64_t out_width, int64_t out_stride, int32_t* out_lengths,
+                  int32_t* out_refs, const ts_pool* pools, int32_t n_pools, int32_t* row_status, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/*
+ * ts_pages_compact -- moves the pages in use to the lowest numbers: of n pages whose count is above 0, those below n stay, and the
+ * i-th free page below n receives the i-th page in use at or past n (as ts_cache_evict fills its slots).
+ *   out_table   [seqs, table_width] at out_stride, renumbered, -1 past a sequence's pages. May be `table` (same stride).
+ *   out_refs    [pages], may be refs.   out_map [pages]: each page's new number, -1 for free ones.   out_count [1] or NULL: n.
+ *   pools       as for ts_pages_fork.
+ *   row_status  [seqs] or NULL. TS_ROW_BAD_LENGTH: the row's table stays as it is; TS_ROW_BAD_PAGE: it names pages that do not exist
+ *               or are free; those entries stay.
+ * Workspace: ts_pages_compact_workspace.
+ */
+size_t ts_pages_compact_workspace(int64_t pages);
+int ts_pages_compact(const int32_t* table, int64_t seqs, int64_t table_width, int64_t table_stride, const int32_t* lengths,
+                     const int32_t* refs, int64_t pages, int32_t page_slots, int32_t* out_table, int64_t out_stride,
+                     int32_t* out_refs, int32_t* out_map, int32_t* out_count, const ts_pool* pools, int32_t n_pools,
+                     int32_t* row_status, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ts_pages_copy -- page source[i] of every pool to page target[i], for n pairs (device arrays).
+ *   pair_status [n] int32 or NULL: TS_ROW_BAD_PAGE for a pair that is not copied because a page of it does not exist or its source is
+ *               another pair's target. Of several pairs with one target the last is copied.
+ * Needs no workspace.
+ */
+int ts_pages_copy(const int32_t* source, const int32_t* target, int64_t n, int64_t pages, const ts_pool* pools, int32_t n_pools,
+                  int32_t* pair_status, void* stream);
 
 /*
  * Diagnostic: the noise the sampler uses. For each tokens[j] of row `row` under `seed`,

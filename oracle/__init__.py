@@ -11,7 +11,8 @@ implementation (Triton's CPU interpreter, when importable), the inverse Gumbel C
 chi-square / z tests of the sampling law; for the rejection sampler, hand-worked
 trajectories with injected random words and the law of the truncated distribution; for token
 log probabilities, scipy's logsumexp and entropy, closed forms and central differences; for
-cache eviction, enumeration of every kept set. No function here is "parity unpinned".
+cache eviction, enumeration of every kept set; for paged caches (`oracle.paged`), torch's softmax attention over the dense
+cache, closed forms and the invariants of the counts. No function here is "parity unpinned".
 """
 from .logprobs import (
     EvictResult,
@@ -22,6 +23,7 @@ from .logprobs import (
     token_logp_grad_row,
     token_logp_row,
 )
+from . import paged
 from .philox import philox4x32, philox4x32_np, seed_key, token_words
 from .rejection import RejectionResult, rejection_sample_row, rejection_sample_rows, round_word
 from .sampler import (

@@ -1,0 +1,186 @@
+"""Refusals of the paged cache's entry points before any device work, and their workspace sizes (no GPU: the calls here end in
+the argument checks)."""
+import ctypes
+
+import pytest
+
+import top_select_gumbel_amd as ts
+
+FAKE = 0x1000      # never dereferenced on these paths
+BIG = 1 << 40
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return ts.load_library()
+
+
+def call(f, a, **kw):
+    a.update(kw)
+    return f(*[ctypes.byref(x) if isinstance(x, ctypes.Structure) else x for x in a.values()], None)
+
+
+def attend(lib, **kw):
+    pages = ts._Paged(1 << 20, 4096, 1024, 64)
+    return call(lib.ts_cache_attend, dict(
+        q=FAKE, dtype=1, batch=3, q_heads=8, kv_heads=4, dim=32, q_b=256, q_h=32, k=pages, v=pages, pages=10, slots=16, table=FAKE,
+        width=20, stride=20, lengths=FAKE, scale=0.1, window=0, out=1 << 22, o_b=256, o_h=32, lse=None, weights=None, w_dtype=0,
+        w_slots=0, w_b=0, w_h=0, status=None, ws=FAKE, ws_bytes=BIG), **kw)
+
+
+@pytest.mark.parametrize("kw,word", [
+    (dict(dtype=3), "dtype"), (dict(dtype=-1), "dtype"), (dict(batch=-1), "batch"), (dict(kv_heads=0), "heads"), (dict(kv_heads=3), "heads"),
+    (dict(q_heads=0), "heads"), (dict(q_heads=-4), "heads"), (dict(q_heads=1 << 17), "q_heads"), (dict(dim=0), "dim"), (dict(dim=257), "dim"),
+    (dict(scale=0.0), "scale"), (dict(scale=-1.0), "scale"), (dict(scale=float("nan")), "scale"), (dict(scale=float("inf")), "scale"),
+    (dict(window=-1), "window"), (dict(pages=-1), "pages"), (dict(pages=1 << 31), "pages"), (dict(slots=0), "page_slots"),
+    (dict(width=-1), "table_width"), (dict(stride=19), "table_stride"), (dict(q=None), "NULL"), (dict(table=None), "NULL"),
+    (dict(lengths=None), "NULL"), (dict(out=None), "NULL"), (dict(pages=0), "pages"), (dict(q=FAKE + 1), "aligned"),
+    (dict(out=FAKE + 1), "aligned"), (dict(q_b=-1), "q:"), (dict(q_b=1 << 61), "q:"), (dict(o_h=31), "overlap"), (dict(o_b=255), "overlap"),
+    (dict(o_b=-256), "overlap"), (dict(k=ts._Paged(None, 64, 64, 64)), "NULL"), (dict(k=None), "NULL"), (dict(v=None), "NULL"),
+    (dict(k=ts._Paged(FAKE + 1, 64, 64, 64)), "aligned"), (dict(v=ts._Paged(FAKE, 64, 64, 63)), "aligned"),
+    (dict(v=ts._Paged(FAKE, -64, 64, 64)), "strides"), (dict(v=ts._Paged(FAKE, 1 << 60, 64, 64)), "strides"),
+    (dict(weights=FAKE, w_dtype=3, w_slots=8, w_b=64, w_h=8), "weights_dtype"), (dict(weights=FAKE), "weights_slots"),
+    (dict(w_slots=8), "out_weights"), (dict(weights=FAKE + 2, w_slots=8, w_b=64, w_h=8), "aligned"),
+    (dict(weights=FAKE, w_slots=8, w_b=64, w_h=7), "overlap"), (dict(weights=FAKE, w_slots=8, w_b=63, w_h=8), "overlap"),
+    (dict(batch=1 << 24), "too large"), (dict(batch=1 << 62), "strides"),
+])
+def test_attend_refusals(lib, kw, word):
+    assert attend(lib, **kw) == ts.TS_ERR_INVALID_ARG
+    assert word in ts.ts_last_error()
+
+
+def test_attend_workspace(lib):
+    assert attend(lib, batch=0, q=None, table=None, lengths=None, out=None, ws=None, ws_bytes=0) == ts.TS_OK
+    need = lib.ts_cache_attend_workspace(3, 8, 4, 32, 20 * 16, 0)
+    assert need > 0 and need % 256 == 0
+    assert attend(lib, ws=None) == ts.TS_ERR_WORKSPACE
+    assert attend(lib, ws=FAKE + 16) == ts.TS_ERR_WORKSPACE
+    assert attend(lib, ws_bytes=need - 1) == ts.TS_ERR_WORKSPACE and "needs" in ts.ts_last_error()
+    assert lib.ts_cache_attend_workspace(3, 8, 4, 32, 320, 100) > need
+    for bad in [(-1, 8, 4, 32, 9, 0), (1, 8, 3, 32, 9, 0), (1, 8, 0, 32, 9, 0), (1, 8, 4, 0, 9, 0), (1, 8, 4, 300, 9, 0), (1, 8, 4, 32, -1, 0),
+                (1, 8, 4, 32, 9, -1), (1 << 62, 8, 4, 32, 9, 0)]:
+        assert lib.ts_cache_attend_workspace(*bad) == 0
+
+
+def append(lib, **kw):
+    pages = ts._Paged(1 << 20, 4096, 1024, 64)
+    return call(lib.ts_cache_append, dict(
+        k_new=FAKE, v_new=FAKE, tokens=9, batch=3, heads=4, slot_bytes=64, k_t=256, k_h=64, v_t=256, v_h=64, offsets=FAKE, k=pages,
+        v=pages, pages=10, slots=16, table=FAKE, width=20, stride=20, lengths=FAKE, status=None), **kw)
+
+
+@pytest.mark.parametrize("kw,word", [
+    (dict(tokens=-1), "tokens"), (dict(tokens=1 << 31), "tokens"), (dict(batch=-1), "batch"), (dict(batch=(1 << 22) + 1), "batch"),
+    (dict(heads=0), "kv_heads"), (dict(slot_bytes=0), "slot_bytes"), (dict(slot_bytes=4097), "slot_bytes"), (dict(slots=0), "page_slots"),
+    (dict(stride=19), "table_stride"), (dict(offsets=None), "NULL"), (dict(table=None), "NULL"), (dict(lengths=None), "NULL"),
+    (dict(k_new=None), "NULL"), (dict(v_new=None), "NULL"), (dict(k_t=-1), "strides"), (dict(v_h=1 << 61), "strides"),
+    (dict(k=None), "NULL"), (dict(v=ts._Paged(None, 0, 0, 0)), "NULL"), (dict(k=ts._Paged(FAKE, 4096, 1024, 63)), "share"),
+    (dict(k=ts._Paged(FAKE, 4095, 1024, 64)), "share"), (dict(v=ts._Paged(FAKE, 4096, 0, 64)), "share"), (dict(v=ts._Paged(FAKE, -1, 0, 64)), "share"),
+])
+def test_append_refusals(lib, kw, word):
+    assert append(lib, **kw) == ts.TS_ERR_INVALID_ARG
+    assert word in ts.ts_last_error()
+
+
+def pools(*p):
+    return (ts._Pool * max(1, len(p)))(*p)
+
+
+def fork(lib, **kw):
+    return call(lib.ts_pages_fork, dict(
+        table=FAKE, seqs=4, width=8, stride=8, lengths=FAKE, refs=FAKE, pages=50, slots=16, parent=FAKE, n_new=None, children=5,
+        out_table=1 << 20, out_width=9, out_stride=9, out_lengths=FAKE, out_refs=FAKE, pools=pools(ts._Pool(FAKE, 64, 64)), n=1,
+        status=None, ws=FAKE, ws_bytes=BIG), **kw)
+
+
+@pytest.mark.parametrize("kw,word", [
+    (dict(seqs=-1), "seqs"), (dict(seqs=(1 << 22) + 1), "seqs"), (dict(children=-1), "children"), (dict(pages=-1), "pages"),
+    (dict(slots=0), "page_slots"), (dict(stride=7), "table_stride"), (dict(out_stride=8), "table_stride"), (dict(out_width=-1), "table_width"),
+    (dict(children=1 << 20, out_width=1 << 20, out_stride=1 << 20), "too large"), (dict(table=None), "NULL"), (dict(lengths=None), "NULL"),
+    (dict(parent=None), "NULL"), (dict(out_table=None), "NULL"), (dict(out_lengths=None), "NULL"), (dict(refs=None), "NULL"),
+    (dict(out_refs=None), "NULL"), (dict(out_table=FAKE), "may not be"), (dict(n=-1), "n_pools"), (dict(pools=None), "NULL"),
+    (dict(pools=pools(ts._Pool(None, 64, 64))), "NULL"), (dict(pools=pools(ts._Pool(FAKE, 63, 64))), "page_stride"),
+    (dict(pools=pools(ts._Pool(FAKE, 64, 0))), "page_bytes"), (dict(pools=pools(ts._Pool(FAKE, 1 << 60, 64))), "page_stride"),
+])
+def test_fork_refusals(lib, kw, word):
+    assert fork(lib, **kw) == ts.TS_ERR_INVALID_ARG
+    assert word in ts.ts_last_error()
+
+
+def test_fork_workspace(lib):
+    need = lib.ts_pages_fork_workspace(4, 5, 50)
+    assert need > 0 and fork(lib, ws_bytes=need - 1) == ts.TS_ERR_WORKSPACE and "needs" in ts.ts_last_error()
+    assert fork(lib, ws=None) == ts.TS_ERR_WORKSPACE and fork(lib, ws=FAKE + 1) == ts.TS_ERR_WORKSPACE
+    assert lib.ts_pages_fork_workspace(-1, 5, 50) == 0 and lib.ts_pages_fork_workspace(4, 5, 1 << 31) == 0
+    assert fork(lib, seqs=0, children=0, pages=0, n=0, table=None, ws=None) == ts.TS_OK
+
+
+def compact(lib, **kw):
+    return call(lib.ts_pages_compact, dict(
+        table=FAKE, seqs=4, width=8, stride=8, lengths=FAKE, refs=FAKE, pages=50, slots=16, out_table=FAKE, out_stride=8, out_refs=FAKE,
+        out_map=FAKE, count=None, pools=pools(ts._Pool(FAKE, 64, 64)), n=1, status=None, ws=FAKE, ws_bytes=BIG), **kw)
+
+
+@pytest.mark.parametrize("kw,word", [
+    (dict(seqs=-1), "seqs"), (dict(pages=-1), "pages"), (dict(pages=0), "pages"), (dict(slots=0), "page_slots"), (dict(stride=7), "table_stride"),
+    (dict(out_stride=7), "out_stride"), (dict(out_stride=9), "input's place"), (dict(table=None), "NULL"), (dict(out_table=None), "NULL"),
+    (dict(lengths=None), "NULL"), (dict(refs=None), "NULL"), (dict(out_refs=None), "NULL"), (dict(out_map=None), "NULL"),
+    (dict(pools=None), "NULL"), (dict(n=-1), "n_pools"), (dict(pools=pools(ts._Pool(FAKE, 63, 64))), "page_stride"),
+])
+def test_compact_refusals(lib, kw, word):
+    assert compact(lib, **kw) == ts.TS_ERR_INVALID_ARG
+    assert word in ts.ts_last_error()
+
+
+def test_compact_workspace(lib):
+    need = lib.ts_pages_compact_workspace(50)
+    assert need > 0 and compact(lib, ws_bytes=need - 1) == ts.TS_ERR_WORKSPACE and compact(lib, ws=None) == ts.TS_ERR_WORKSPACE
+    assert lib.ts_pages_compact_workspace(-1) == 0
+
+
+@pytest.mark.parametrize("kw,word", [
+    (dict(n=-1), "n ="), (dict(n=(1 << 22) + 1), "n ="), (dict(pages=-1), "pages"), (dict(source=None), "NULL"), (dict(target=None), "NULL"),
+    (dict(np=-1), "n_pools"), (dict(pools=None), "NULL"), (dict(pools=pools(ts._Pool(FAKE, 63, 64))), "page_stride"),
+])
+def test_copy_refusals(lib, kw, word):
+    a = dict(source=FAKE, target=FAKE, n=3, pages=50, pools=pools(ts._Pool(FAKE, 64, 64)), np=1, status=None)
+    assert call(lib.ts_pages_copy, a, **kw) == ts.TS_ERR_INVALID_ARG
+    assert word in ts.ts_last_error()
+
+
+def test_empty_calls(lib):
+    assert append(lib, batch=0, offsets=None, table=None, lengths=None) == ts.TS_OK
+    assert lib.ts_pages_copy(None, None, 0, 50, pools(ts._Pool(FAKE, 64, 64)), 1, None, None) == ts.TS_OK
+    for st, word in ((ts.TS_ROW_BAD_PAGE, "page"), (ts.TS_ROW_BAD_LENGTH, "length"), (ts.TS_ROW_BAD_PARENT, "parent"), (ts.TS_ROW_NO_PAGE, "free")):
+        assert word in ts.ts_status_string(st)
+
+
+def test_binding_refuses_host_tensors_and_bad_shapes():
+    torch = pytest.importorskip("torch")
+    i = torch.zeros(2, dtype=torch.int32)
+    q, pages, table = torch.zeros(2, 4, 8), torch.zeros(5, 2, 4, 8), torch.zeros(2, 3, dtype=torch.int32)
+    with pytest.raises(ts.TopSelectError):
+        ts.ts_cache_attend(q, pages, pages, table, i)
+    with pytest.raises(ts.TopSelectError):
+        ts.ts_cache_append(q, q, i, pages, pages, table, i)
+    with pytest.raises(ts.TopSelectError):
+        ts.ts_pages_fork(table, i, i, i, 4)
+    with pytest.raises(ts.TopSelectError):
+        ts.ts_pages_compact(table, i, i, 4)
+    with pytest.raises(ts.TopSelectError):
+        ts.ts_pages_copy(i, i, [pages])
+    with pytest.raises(ts.TopSelectError):
+        ts.PagePools([pages])
+
+
+def test_divisor_of_the_kernels():
+    """j / d by one product, as the kernels take it (for the divisors' extremes, in whole numbers)."""
+    import random
+    rng = random.Random(0)
+    for d in list(range(1, 70)) + [1025, (1 << 20) - 1, 1 << 20, (1 << 29) + 1, (1 << 30) - 1, 1 << 30] + [rng.randrange(1, 1 << 30) for _ in range(300)]:
+        bits = (d - 1).bit_length()
+        mul = ((1 << (31 + bits)) + d - 1) // d
+        assert mul < 1 << 32
+        for j in [0, 1, d - 1, d, d + 1, 2 * d - 1, (1 << 31) - 1, (1 << 31) // d * d - 1, (1 << 31) // d * d] + [rng.randrange(1 << 31) for _ in range(20)]:
+            if 0 <= j < 1 << 31:
+                assert (j * mul) >> (31 + bits) == j // d

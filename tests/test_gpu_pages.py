@@ -1,0 +1,449 @@
+"""GPU tests of ts_cache_append, ts_pages_fork, ts_pages_compact and ts_pages_copy against the oracle: whole numbers and bytes,
+equal in every bit."""
+import numpy as np
+import pytest
+
+from oracle import paged
+import top_select_gumbel_amd as ts
+from gpu_helpers import banner, host, torch_cuda
+
+pytestmark = pytest.mark.gpu
+
+
+def gpu(a):
+    return torch_cuda().from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()
+
+
+def pool_of(pages, shape, dtype, seed, gap=0):
+    """Random bit patterns; `gap`: unused elements between pages."""
+    torch = torch_cuda()
+    t = getattr(torch, dtype)
+    size = torch.empty(0, dtype=t).element_size()
+    n = int(np.prod(shape)) + gap
+    raw = np.random.default_rng(seed).integers(0, 256, (pages, n * size), dtype=np.uint8)
+    flat = torch.from_numpy(raw).cuda().view(t)
+    return flat[:, : n - gap].view(pages, *shape) if not gap else flat.as_strided((pages, n - gap), (n, 1))
+
+
+def same(a, b, what):
+    """Equality without the two arrays' print."""
+    equal = a.shape == b.shape and np.array_equal(a, b)
+    assert equal, f"{what} differs at {np.argwhere(a != b)[:5].tolist() if a.shape == b.shape else (a.shape, b.shape)}"
+
+
+def raw(t):
+    torch = torch_cuda()
+    return host((t._base if t._base is not None else t).contiguous().view(torch.uint8)).copy()
+
+
+def moved(before, pool, moves):
+    """The bytes that the pool's storage should hold."""
+    torch = torch_cuda()
+    want = torch.from_numpy(before.copy())
+    whole = want.view(pool.shape[0], -1)
+    page = pool[0].numel() * pool.element_size()
+    src = whole.clone()
+    for a, b in moves:
+        whole[b, :page] = src[a, :page]
+    return want.numpy()
+
+
+# ---------------------------------------------------------------- append
+def check_append(lengths, new, slots=16, heads=2, dim=16, dtype="bfloat16", spare=0, extra_pages=3, edit=None, seed=0, slots_first=False,
+                 strided=False, pages_too=True):
+    torch = torch_cuda()
+    lengths, new = np.asarray(lengths, np.int32), np.asarray(new, np.int32)
+    banner(f"append n={lengths[:5].tolist()} new={new[:5].tolist()} slots={slots} heads={heads} dim={dim} {dtype}")
+    b, width = len(lengths), max(1, -(-int(max(lengths, default=1)) // slots))
+    pages = b * width + extra_pages
+    rng = np.random.default_rng(seed)
+    table = rng.permutation(pages)[: b * width].reshape(b, width).astype(np.int32)
+    offsets = np.r_[0, np.cumsum(new)].astype(np.int32)
+    tokens = int(offsets[-1]) + spare
+    if edit is not None:
+        edit(table, lengths, offsets)
+    shape = (slots, heads, dim) if slots_first else (heads, slots, dim)
+    k, v = (pool_of(pages, shape, dtype, seed + i) for i in (1, 2))
+    kv = [x.transpose(1, 2) if slots_first else x for x in (k, v)]
+    fresh = [pool_of(max(tokens, 1), (heads, 2 * dim if strided else dim), dtype, seed + i)[:tokens, :, :dim] for i in (3, 4)]
+    want = [host(x.contiguous().view(torch.uint8)).reshape(pages, heads, slots, -1).copy() for x in kv]
+    new_bytes = [host(x.contiguous().view(torch.uint8)).reshape(tokens, heads, dim * x.element_size()) for x in fresh]
+    st = ts.ts_cache_append(fresh[0], fresh[1], gpu(offsets), kv[0], kv[1], gpu(table), gpu(lengths))
+    torch.cuda.synchronize()
+    moves, status = paged.append(lengths.tolist(), offsets.tolist(), table.tolist(), slots, pages, tokens)
+    for t, p, s in moves:
+        for w, x in zip(want, new_bytes):
+            w[p, :, s] = x[t]
+    assert host(st).tolist() == status
+    for got, w in zip(kv, want):
+        if pages_too:
+            same(host(got.contiguous().view(torch.uint8)).reshape(w.shape), w, "cache")
+
+
+@pytest.mark.parametrize("dtype,dim", [("bfloat16", 128), ("float32", 33), ("float16", 1), ("uint8", 7), ("float32", 1024), ("bfloat16", 33)])
+def test_append_types_and_sizes(dtype, dim):
+    check_append([5, 17, 16, 1, 40], [1, 1, 1, 1, 1], dtype=dtype, dim=dim)
+    check_append([5, 17, 16, 1, 40], [5, 3, 0, 1, 40], dtype=dtype, dim=dim, slots=7)
+
+
+@pytest.mark.parametrize("slots", [1, 5, 16, 64])
+@pytest.mark.parametrize("slots_first,strided", [(False, False), (True, True)])
+def test_append_layouts(slots, slots_first, strided):
+    check_append([100, 3, 64, 0, 77], [100, 2, 0, 0, 1], slots=slots, slots_first=slots_first, strided=strided, heads=3)
+
+
+def test_append_many_and_none():
+    rng = np.random.default_rng(1)
+    n = rng.integers(0, 60, 500)
+    check_append(n, np.minimum(n, rng.integers(0, 9, 500)), dim=8)
+    check_append([3, 4], [0, 0])
+    check_append([3, 4], [2, 4], spare=6)          # tokens behind the last sequence's go nowhere
+
+
+def test_append_statuses():
+    def edit(table, lengths, offsets):
+        table[1, 0], table[2, 1] = -1, 1 << 30
+        lengths[3], lengths[4] = 2, 1000
+    check_append([20, 20, 20, 20, 20, 20], [4, 20, 8, 3, 1, 2], edit=edit)
+
+    def torn(table, lengths, offsets):             # offsets that go down, or past the tokens
+        offsets[2], offsets[5] = 1, 99
+    check_append([20, 20, 20, 20, 20, 20], [4, 2, 8, 3, 1, 2], edit=torn, pages_too=False)   # which of two takes a token is left open
+
+    def negative(table, lengths, offsets):
+        offsets[0], lengths[1] = -3, -5
+    check_append([20, 20, 20], [4, 2, 8], edit=negative)
+
+
+# ---------------------------------------------------------------- fork
+def check_fork(table, lengths, refs, parent, new, slots, width=None, pools=2, page=(2, 16, 8), dtype="bfloat16", in_place=False, seed=0,
+               gap=0, spread=0):
+    torch = torch_cuda()
+    table = np.asarray(table, np.int32)
+    width = table.shape[1] if width is None else width
+    banner(f"fork seqs={len(lengths)} children={len(parent)} pages={len(refs)} slots={slots} width={table.shape[1]}->{width} pools={pools}")
+    p = [pool_of(len(refs), page if i % 3 else (3,) + tuple(page[1:]), dtype, seed + i, gap) for i in range(pools)]
+    before = [raw(x) for x in p]
+    t = gpu(table)
+    if spread:      # rows further apart than they are long
+        t = torch.nn.functional.pad(t, (0, spread), value=1 << 29)[:, : table.shape[1]]
+    r0 = gpu(refs)
+    r = ts.ts_pages_fork(t, gpu(lengths), r0, gpu(parent), slots, n_new=None if new is None else gpu(new), pools=p, width=width,
+                         in_place=in_place)
+    torch.cuda.synchronize()
+    o = paged.fork(table.tolist(), list(lengths), refs, list(parent), [0] * len(parent) if new is None else list(new), slots, width)
+    assert host(r.status).tolist() == o.status
+    assert host(r.lengths).tolist() == o.lengths
+    assert host(r.table).tolist() == o.table
+    assert host(r.refs).tolist() == o.refs
+    if in_place:
+        assert r.refs.data_ptr() == r0.data_ptr()
+    else:
+        assert host(r0).tolist() == list(refs)
+    for x, b in zip(p, before):
+        same(raw(x).ravel(), moved(b, x, o.copies).ravel(), "pool")
+    return r
+
+
+def sequences(rng, seqs, pages, slots, width, share=0.3, fill=0.6):
+    """Tables after some life: pages in no order, some of them shared, counts to match."""
+    order = rng.permutation(pages).tolist()
+    table, lengths = [], []
+    for s in range(seqs):
+        room = min(width * slots, int(fill * pages / seqs * slots * 2))
+        n = int(rng.integers(0, max(room, 1) + 1))
+        row = []
+        if table and rng.random() < share:
+            donor = int(rng.integers(0, len(table)))
+            row = table[donor][: min(lengths[donor] // slots, n // slots)]
+        need = -(-n // slots) - len(row)
+        if need > len(order):
+            n, row, need = 0, [], 0
+        row = list(row) + [order.pop() for _ in range(need)]
+        table.append(row + [int(rng.integers(-5, pages + 5)) for _ in range(width - len(row))])
+        lengths.append(n)
+    refs = [0] * pages
+    for row, n in zip(table, lengths):
+        for p in row[: -(-n // slots)]:
+            refs[p] += 1
+    return table, lengths, refs
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_fork_random(seed):
+    rng = np.random.default_rng(seed)
+    pages, slots, seqs = int(rng.integers(3, 300)), int(rng.choice([1, 3, 16, 50])), int(rng.integers(1, 30))
+    width = int(rng.integers(1, 40))
+    table, lengths, refs = sequences(rng, seqs, pages, slots, width)
+    n = int(rng.integers(1, 40))
+    parent = rng.integers(-1, seqs, n) if seed % 3 else np.where(np.arange(n) < seqs, np.arange(n), -1)
+    new = rng.integers(0, [2, 2 * slots, 10 * slots][seed % 3], n)
+    if seed % 4 == 3:
+        new[rng.integers(0, n)] = [-1, 1 << 30, (1 << 31) - 1][seed % 3]
+        parent[rng.integers(0, n)] = [-2, seqs, 1 << 30][seed % 3]
+    check_fork(table, lengths, refs, parent, new, slots, width=width + int(rng.integers(-1, 3)) if seed % 2 else None,
+               in_place=bool(seed % 2), seed=seed, page=(1, slots, 3), pools=int(rng.integers(0, 4)), spread=seed % 5)
+
+
+@pytest.mark.parametrize("pages", [4095, 4096, 4097, 20000])
+def test_fork_over_tiles_of_pages(pages):
+    rng = np.random.default_rng(pages)
+    table, lengths, refs = sequences(rng, 40, pages, 4, pages // 20, fill=0.9)
+    check_fork(table, lengths, refs, rng.integers(-1, 40, 60), rng.integers(0, pages // 20, 60), 4, pools=1, page=(4, 2), width=pages // 20)
+
+
+def test_fork_many_sequences():
+    rng = np.random.default_rng(8)
+    table, lengths, refs = sequences(rng, 700, 3000, 2, 6, fill=0.7)
+    check_fork(table, lengths, refs, rng.integers(0, 700, 900), rng.integers(0, 3, 900), 2, pools=1, page=(2, 2))
+
+
+def test_fork_all_from_one_and_none():
+    table, lengths, refs = [[4, 2, 0, 1]], [13], [1, 1, 1, 0, 1] + [0] * 30
+    check_fork(table, lengths, refs, [0] * 20, [3] * 20, 4, width=5)
+    check_fork(table, lengths, refs, [-1] * 3, [0, 9, 0], 4)                # all freed, one starts
+    check_fork(table, lengths, refs, [], [], 4)
+    check_fork(np.zeros((0, 3)), [], refs, [-1, -1], [5, 0], 4, width=3)
+    check_fork(table, lengths, refs, [0, 0], None, 4)
+    check_fork([[0, 1]], [8], [1, 1], [0, 0], [0, 0], 4)                    # no part-filled page: nothing to copy
+
+
+def test_fork_with_too_few_pages():
+    table, refs = [[0, 1, -1], [2, 3, -1]], [1, 1, 1, 1, 0, 0]
+    r = check_fork(table, [6, 8], refs, [0, 0, 1, 0], [0, 0, 9, 0], 4, width=5)
+    assert host(r.status).tolist() == [0, 0, ts.TS_ROW_NO_PAGE, ts.TS_ROW_NO_PAGE] and host(r.lengths).tolist() == [6, 6, 8, 0]
+    check_fork(table, [8, 8], refs, [0, 0, 1], [1, 2, 3], 4, width=5)       # the third finds none
+
+
+def test_fork_bad_rows():
+    table = [[0, 1], [9, 2], [3, -1], [4, 5], [1 << 30, 6]]
+    check_fork(table, [7, 5, -1, 9, 4], [1, 1, 1, 1, 1, 1, 0, 0], [0, 1, 2, 3, 4, 5, -2], [1] * 7, 4, width=2)
+    check_fork([[0, 1, 2]], [12], [1, 1, 1, 0], [0, 0], [0, 0], 4, width=2)  # the new tables are too narrow
+    # counts that say less than the tables: pages are free all the same, and nothing breaks
+    check_fork([[0, 1], [0, 1]], [8, 8], [1, 1, 0, 0], [0, -1], [1, 5], 4, width=3)
+
+
+@pytest.mark.parametrize("n,page,dtype,gap", [(70, (5,), "uint8", 0), (65, (2, 16, 8), "bfloat16", 8), (3, (40, 16, 33), "float16", 5),
+                                             (2, (200, 128), "float32", 0), (1, (15,), "uint8", 1), (1, (16,), "uint8", 3), (1, (17,), "uint8", 0)])
+def test_fork_pools(n, page, dtype, gap):
+    rng = np.random.default_rng(n)
+    table, lengths, refs = sequences(rng, 6, 40, 4, 8)
+    check_fork(table, lengths, refs, rng.integers(0, 6, 12), [1] * 12, 4, pools=n, page=page, dtype=dtype, gap=gap)
+
+
+# ---------------------------------------------------------------- compact
+def check_compact(table, lengths, refs, slots, pools=2, page=(2, 16, 8), dtype="bfloat16", in_place=False, seed=0, gap=0):
+    torch = torch_cuda()
+    table = np.asarray(table, np.int32)
+    banner(f"compact seqs={len(lengths)} pages={len(refs)} slots={slots} width={table.shape[1]} pools={pools}")
+    p = [pool_of(len(refs), page, dtype, seed + i, gap) for i in range(pools)]
+    before = [raw(x) for x in p]
+    t0, r0 = gpu(table), gpu(refs)
+    r = ts.ts_pages_compact(t0, gpu(lengths), r0, slots, pools=ts.PagePools(p), in_place=in_place)
+    torch.cuda.synchronize()
+    o = paged.compact(table.tolist(), list(lengths), refs, slots)
+    assert host(r.map).tolist() == o.map
+    assert host(r.count).tolist() == [o.count]
+    assert host(r.refs).tolist() == o.refs
+    assert host(r.table).tolist() == o.table
+    assert host(r.status).tolist() == o.status
+    if not in_place:
+        assert host(r0).tolist() == list(refs) and np.array_equal(host(t0), table)
+    for x, b in zip(p, before):
+        same(raw(x).ravel(), moved(b, x, o.moves).ravel(), "pool")
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_compact_random(seed):
+    rng = np.random.default_rng(100 + seed)
+    pages, slots, seqs = int(rng.integers(1, 400)), int(rng.choice([1, 3, 16])), int(rng.integers(0, 20))
+    width = int(rng.integers(1, 40))
+    table, lengths, refs = sequences(rng, seqs, pages, slots, width, fill=rng.uniform(0.05, 1.0)) if seqs else ([], [], [0] * pages)
+    if seed % 3 == 0:       # pages that no table names are held by something else; others are counted below 0
+        for p in rng.integers(0, pages, 5):
+            refs[p] += 1
+        refs = [-2 if r == 0 and rng.random() < 0.1 else r for r in refs]
+    check_compact(np.asarray(table).reshape(seqs, width), lengths, refs, slots, in_place=bool(seed % 2), seed=seed, pools=int(rng.integers(0, 3)),
+                  page=(1, slots, 5))
+
+
+@pytest.mark.parametrize("pages", [4095, 4096, 4097, 8192, 30000])
+@pytest.mark.parametrize("fill", [0.1, 0.5, 0.95])
+def test_compact_over_tiles_of_pages(pages, fill):
+    rng = np.random.default_rng(pages)
+    refs = (rng.random(pages) < fill).astype(int).tolist()
+    check_compact([[p] for p in np.nonzero(refs)[0][:50]], [1] * 50, refs, 1, pools=1, page=(3, 7), in_place=fill == 0.5)
+
+
+def test_compact_none_and_all():
+    check_compact([[-1]], [0], [0] * 50, 4)
+    check_compact([list(range(50))], [200], [1] * 50, 4)
+    check_compact([list(range(25, 50))], [100], [0] * 25 + [3] * 25, 4)
+    check_compact([[0]], [1], [1], 4)
+    check_compact([[0]], [0], [0], 4)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_compact_bad_rows(in_place):
+    check_compact([[5, 1], [9, 3], [-1, 5], [5, 5], [0, 3]], [8, 8, 8, 9, -1], [0, 1, 0, 1, 0, 2, 0, 0], 4, in_place=in_place)
+
+
+# ---------------------------------------------------------------- copy
+def check_copy(source, target, pages, pools=2, page=(2, 16, 8), dtype="bfloat16", seed=0, gap=0):
+    torch = torch_cuda()
+    banner(f"copy n={len(source)} pages={pages} pools={pools} page={page} {dtype}")
+    p = [pool_of(pages, page, dtype, seed + i, gap) for i in range(pools)]
+    before = [raw(x) for x in p]
+    st = ts.ts_pages_copy(gpu(source), gpu(target), p)
+    torch.cuda.synchronize()
+    moves, status = paged.copy_pairs(source, target, pages)
+    assert host(st).tolist() == status
+    for x, b in zip(p, before):
+        same(raw(x).ravel(), moved(b, x, moves).ravel(), "pool")
+
+
+@pytest.mark.parametrize("page,dtype,gap", [((3,), "uint8", 0), ((2, 16, 8), "bfloat16", 4), ((7, 33), "float16", 0), ((64, 16, 128), "float32", 0),
+                                            ((16385,), "uint8", 1)])
+def test_copy_sizes(page, dtype, gap):
+    rng = np.random.default_rng(len(page))
+    order = rng.permutation(60)
+    check_copy(order[:20].tolist(), order[20:40].tolist(), 60, page=page, dtype=dtype, gap=gap, pools=3)
+
+
+def test_copy_of_bad_and_repeated_pairs():
+    check_copy([0, 1, 2, 3, 4, -1, 9, 8, 1 << 30], [5, 6, 6, 9, 5, 7, 3, 10, 7], 10)
+    check_copy([0, 5], [5, 0], 8)                       # a swap is refused
+    check_copy([3, 3, 3], [4, 5, 6], 8)                 # one source, several targets
+    check_copy([3], [3], 8)
+    check_copy([], [], 8)
+    rng = np.random.default_rng(0)
+    check_copy(rng.integers(0, 40, 1000).tolist(), rng.integers(40, 90, 1000).tolist(), 90, page=(4, 4))
+
+
+def test_copy_of_more_pools_than_a_launch_takes():
+    check_copy([0, 1, 2], [5, 6, 4], 8, pools=130, page=(2, 9))
+
+
+# ---------------------------------------------------------------- refusals, graphs, streams
+def test_refusals_of_the_binding():
+    torch = torch_cuda()
+    pool = torch.zeros(8, 2, 4, 6, device="cuda")
+    i = torch.zeros(2, dtype=torch.int32, device="cuda")
+    table, refs = torch.zeros(2, 3, dtype=torch.int32, device="cuda"), torch.zeros(8, dtype=torch.int32, device="cuda")
+    for bad in (lambda: ts.PagePools([pool.transpose(1, 2)]), lambda: ts.PagePools([pool, pool[:7]]), lambda: ts.PagePools([pool.cpu()]),
+                lambda: ts.PagePools([pool[:, :1].expand(8, 2, 4, 6)]), lambda: ts.ts_pages_fork(table, i, refs[:7], i, 4, pools=[pool]),
+                lambda: ts.ts_pages_fork(table.long(), i, refs, i, 4), lambda: ts.ts_pages_fork(table, i, refs.long(), i, 4),
+                lambda: ts.ts_pages_fork(table, i[:1], refs, i, 4), lambda: ts.ts_pages_fork(table, i, refs, i, 4, n_new=i[:1]),
+                lambda: ts.ts_pages_fork(table, i, refs, i, 0), lambda: ts.ts_pages_fork(table, i, refs, i, 4, width=-1),
+                lambda: ts.ts_pages_compact(table, i, refs, 4, pools=[pool[:, 0], pool[:5]]), lambda: ts.ts_pages_compact(table.t(), i, refs, 4),
+                lambda: ts.ts_pages_copy(i, i[:1], [pool]), lambda: ts.ts_pages_copy(i, i, []), lambda: ts.ts_pages_copy(i.long(), i, [pool]),
+                lambda: ts.ts_cache_append(pool[0], pool[0], i, pool, pool, table, i),
+                lambda: ts.ts_cache_append(torch.zeros(1, 2, 6, device="cuda"), torch.zeros(1, 2, 6, device="cuda"), i, pool, pool, table, i),
+                lambda: ts.ts_cache_append(torch.zeros(1, 2, 6, device="cuda"), torch.zeros(2, 2, 6, device="cuda"),
+                                           torch.zeros(3, dtype=torch.int32, device="cuda"), pool, pool, table, i)):
+        with pytest.raises(ts.TopSelectError):
+            bad()
+
+
+def test_captured_step():
+    """Grow, append, attend and compact in one graph, replayed on new inputs with eager work between, against eager calls."""
+    torch = torch_cuda()
+    banner("pages: a captured step")
+    rng = np.random.default_rng(5)
+    slots, width, pages = 4, 8, 60
+    table, lengths, refs = sequences(rng, 6, pages, slots, width, fill=0.5)
+    lengths = [min(n, width * slots - 3) for n in lengths]
+    refs = [0] * pages
+    for row, n in zip(table, lengths):
+        for p in row[: -(-n // slots)]:
+            refs[p] += 1
+    parents = [[0, 0, 1, 2, 5, -1], [5, 4, 3, 2, 1, 0], [1, 1, 1, 1, 1, 1]]
+    t, n, r = gpu(table), gpu(lengths), gpu(refs)
+    parent, new, offsets = gpu(parents[0]), gpu([2] * 6), gpu(np.arange(7) * 2)
+    k, v = (torch.randn(pages, 2, slots, 16, device="cuda") for _ in range(2))
+    k0, v0 = k.clone(), v.clone()
+    fresh = torch.randn(12, 2, 16, device="cuda")
+    q = torch.randn(6, 4, 16, device="cuda")
+
+    def step():
+        f = ts.ts_pages_fork(t, n, r, parent, slots, n_new=new, pools=[k, v])
+        st = ts.ts_cache_append(fresh, fresh, offsets, k, v, f.table, f.lengths)
+        a = ts.ts_cache_attend(q, k, v, f.table, f.lengths)
+        c = ts.ts_pages_compact(f.table, f.lengths, f.refs, slots, pools=[k, v])
+        b = ts.ts_cache_attend(q, k, v, c.table, f.lengths)
+        return [*f, st, a.out, a.lse, a.status, *c, b.out, b.lse, b.status]
+    step()
+    torch.cuda.synchronize()
+    k.copy_(k0), v.copy_(v0)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for p in parents:
+        parent.copy_(gpu(p))
+        fresh.mul_(1.5)
+        k.copy_(k0), v.copy_(v0)
+        want = [x.clone() for x in step()]
+        wk, wv = k.clone(), v.clone()
+        assert torch.equal(want[5], want[-3])            # attention is the same wherever the pages are
+        k.copy_(k0), v.copy_(v0)
+        for x in got:
+            x.fill_(77)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want)) and torch.equal(k, wk) and torch.equal(v, wv)
+
+
+def test_decode_with_shared_prompt_and_eviction():
+    """A prompt is forked into samples that go on by themselves and end; at each step the attention of every sample is what it
+    would be over its own dense cache. Then the weights of a dense cache go to its eviction."""
+    torch = torch_cuda()
+    banner("pages: decode loop")
+    torch.manual_seed(0)
+    heads, dim, slots, width, pages, kids = 2, 16, 4, 12, 64, 5
+    k, v = (torch.full((pages, heads, slots, dim), float("nan"), device="cuda") for _ in range(2))
+    pools = ts.PagePools([k, v])
+    table = torch.full((1, width), -1, dtype=torch.int32, device="cuda")
+    refs, n = torch.zeros(pages, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    dense = [[torch.empty(0, heads, dim, device="cuda")] * 2]
+    parent, grow = [0], 10
+    for step in range(16):
+        f = ts.ts_pages_fork(table, n, refs, gpu(parent), slots, n_new=gpu([grow] * len(parent)), pools=pools, in_place=True)
+        table, n, refs = f.table, f.lengths, f.refs
+        fresh = torch.randn(2, len(parent) * grow, heads, dim, device="cuda")
+        st = ts.ts_cache_append(fresh[0], fresh[1], gpu(np.arange(len(parent) + 1) * grow), k, v, table, n)
+        dense = [[torch.cat([old, fresh[i, c * grow:(c + 1) * grow]]) for i, old in enumerate(dense[p])] for c, p in enumerate(parent)]
+        if step % 5 == 4:
+            c = ts.ts_pages_compact(table, n, refs, slots, pools=pools, in_place=True)
+            assert not host(c.status).any() and int(c.count) == int((refs > 0).sum())
+        q = torch.randn(len(parent), 2 * heads, dim, device="cuda")
+        a = ts.ts_cache_attend(q, k, v, table, n)
+        assert not host(f.status).any() and not host(st).any() and not host(a.status).any()
+        for c, (dk, dv) in enumerate(dense):
+            s = torch.einsum("hgd,nhd->hgn", q[c].view(heads, 2, dim).double(), dk.double()) / 4
+            w = torch.softmax(s, 2)
+            want = torch.einsum("hgn,nhd->hgd", w, dv.double()).reshape(2 * heads, dim)
+            # 40 positions of 16 dims: (2 * 17 * 14 + 2^3 * 10 + 300) u is less than 1e-4, and |v| < 6
+            assert float((a.out[c].double() - want).abs().max()) < 6e-4
+        grow = 1
+        parent = [0] * kids if step == 0 else list(range(len(parent)))
+        if step == 8:
+            parent = [2, 0, 0, 4]
+    # a dense cache is one page a sequence; its weights decide what stays
+    b, budget = 3, 20
+    kd, vd = (torch.randn(b, heads, budget + 4, dim, device="cuda") for _ in range(2))
+    rows = b * heads
+    score, position = torch.zeros(rows, budget + 4, device="cuda"), torch.arange(budget + 4, dtype=torch.int32, device="cuda").repeat(rows, 1)
+    ids, full = torch.arange(b, dtype=torch.int32, device="cuda").view(b, 1), torch.full((b,), budget + 4, dtype=torch.int32, device="cuda")
+    q = torch.randn(b, 2 * heads, dim, device="cuda")
+    a = ts.ts_cache_attend(q, kd, vd, ids, full, weights_slots=budget + 4)
+    e = ts.ts_cache_evict(score, position, full.repeat_interleave(heads), torch.full((rows,), budget, dtype=torch.int32, device="cuda"), budget,
+                          weights=a.weights.view(rows, 2, budget + 4), k_cache=kd, v_cache=vd, in_place=True)
+    assert not host(e.status).any() and not host(a.status).any()
+    total = a.weights.view(rows, 2, -1).double().sum(1).float()
+    kept = torch.sort(torch.topk(total, budget, dim=1).indices, 1).values
+    assert torch.equal(torch.sort(position[:, :budget].long(), 1).values, kept)
+    after = ts.ts_cache_attend(q, kd, vd, ids, e.lengths[::heads].contiguous())
+    w = a.weights.double().view(rows, 2, -1).gather(2, position[:, :budget].long()[:, None].expand(-1, 2, -1))
+    want = (w / w.sum(2, keepdim=True)) @ vd.double().view(rows, -1, dim)[:, :budget]
+    assert float((after.out.double().view(rows, 2, dim) - want).abs().max()) < 6e-4

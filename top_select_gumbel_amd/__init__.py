@@ -29,6 +29,10 @@ TS_ROW_BAD_P = 3
 TS_ROW_BAD_T = 4
 TS_ROW_BAD_MINP = 5
 TS_ROW_BAD_TOKEN = 6
+TS_ROW_BAD_PAGE = 7
+TS_ROW_BAD_LENGTH = 8
+TS_ROW_BAD_PARENT = 9
+TS_ROW_NO_PAGE = 10
 TS_ORDER_INDEX = 0
 TS_ORDER_VALUE = 1
 TS_OP_TOPK_SELECT = 0
@@ -46,7 +50,9 @@ TS_KNOB_NUCLEUS_PASSES = 4
 EXPORTED = (
     "ts_workspace_bytes", "ts_workspace_init", "ts_topk_select", "ts_topk_select_rows", "ts_topp_mask",
     "ts_sample_rows", "ts_sample_rows_noalloc", "ts_sample_rows_logp", "ts_topp_mask_minp", "ts_sample_rows_minp", "ts_sample_rows_rejection",
-    "ts_token_logp", "ts_token_logp_backward", "ts_cache_evict", "ts_gumbel_noise", "ts_noise_transform", "ts_read_ceiling", "ts_debug_set", "ts_status_string", "ts_last_error",
+    "ts_token_logp", "ts_token_logp_backward", "ts_cache_evict", "ts_cache_attend", "ts_cache_attend_workspace",
+    "ts_cache_append", "ts_pages_fork", "ts_pages_fork_workspace", "ts_pages_compact", "ts_pages_compact_workspace", "ts_pages_copy",
+    "ts_gumbel_noise", "ts_noise_transform", "ts_read_ceiling", "ts_debug_set", "ts_status_string", "ts_last_error",
 )
 
 _lib = None
@@ -100,6 +106,23 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         lib.ts_cache_evict.argtypes = [vp, i64, i64, i64, vp, i64, vp, vp, i32, vp, c.c_int, i64, i64, i64, i32, i32, vp, i64,
                                        vp, i64, vp, vp, vp, vp, vp, i64, vp, sz, vp]
         lib.ts_cache_evict.restype = c.c_int
+        lib.ts_cache_attend.argtypes = [vp, c.c_int, i64, i32, i32, i32, i64, i64, vp, vp, i64, i32, vp, i64, i64, vp, c.c_float, i32,
+                                        vp, i64, i64, vp, vp, c.c_int, i64, i64, i64, vp, vp, sz, vp]
+        lib.ts_cache_attend.restype = c.c_int
+        lib.ts_cache_attend_workspace.argtypes = [i64, i32, i32, i32, i64, i64]
+        lib.ts_cache_attend_workspace.restype = sz
+        lib.ts_cache_append.argtypes = [vp, vp, i64, i64, i32, i64, i64, i64, i64, i64, vp, vp, vp, i64, i32, vp, i64, i64, vp, vp, vp]
+        lib.ts_cache_append.restype = c.c_int
+        lib.ts_pages_fork.argtypes = [vp, i64, i64, i64, vp, vp, i64, i32, vp, vp, i64, vp, i64, i64, vp, vp, vp, i32, vp, vp, sz, vp]
+        lib.ts_pages_fork.restype = c.c_int
+        lib.ts_pages_fork_workspace.argtypes = [i64, i64, i64]
+        lib.ts_pages_fork_workspace.restype = sz
+        lib.ts_pages_compact.argtypes = [vp, i64, i64, i64, vp, vp, i64, i32, vp, i64, vp, vp, vp, vp, i32, vp, vp, sz, vp]
+        lib.ts_pages_compact.restype = c.c_int
+        lib.ts_pages_compact_workspace.argtypes = [i64]
+        lib.ts_pages_compact_workspace.restype = sz
+        lib.ts_pages_copy.argtypes = [vp, vp, i64, i64, vp, i32, vp, vp]
+        lib.ts_pages_copy.restype = c.c_int
         lib.ts_gumbel_noise.argtypes = [c.c_uint64, i32, vp, i64, vp, vp, vp, vp]
         lib.ts_noise_transform.restype = c.c_int
         lib.ts_noise_transform.argtypes = [vp, i64, vp, vp, vp]
@@ -574,6 +597,265 @@ def ts_cache_evict(score, position, lengths, keep, keep_max: int, weights=None, 
           out_lengths.data_ptr(), source.data_ptr(), status.data_ptr(), ctypes.byref(kc) if kc else None,
           ctypes.byref(vc) if vc else None, k_heads if kc else v_heads, ws.data_ptr(), nb)
     return CacheEvict(source, out_lengths, out_score, out_position, status)
+
+
+class _Paged(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p)] + [(n, ctypes.c_int64) for n in ("page_stride", "head_stride", "slot_stride")]
+
+
+def _paged(t, dtype, device, name: str):
+    """The ts_paged of a [pages, heads, slots, dim] tensor whose last dimension is contiguous."""
+    if t.dtype is not dtype or t.dim() != 4 or t.device != device:
+        raise TopSelectError(f"{name} must be a [pages, kv_heads, slots, dim] tensor of {dtype} on {device}")
+    p, h, s, d = t.stride()
+    if t.shape[3] > 1 and d != 1:
+        raise TopSelectError(f"{name} must have a contiguous last dimension")
+    size = t.element_size()
+    return _Paged(t.data_ptr(), p * size, h * size, s * size)
+
+
+def _page_table(table, device, name: str = "table"):
+    """(rows, width, row stride) of an int32 table of page numbers."""
+    if table.dtype is not _torch.int32 or table.dim() != 2 or table.device != device:
+        raise TopSelectError(f"{name} must be an int32 [sequences, width] tensor on {device}")
+    (rows, width), (row, col) = table.shape, table.stride()
+    if rows and width > 1 and col != 1:
+        raise TopSelectError(f"{name} must have unit column stride")
+    return rows, width, row if rows > 1 else width
+
+
+class CacheAttend(NamedTuple):
+    """Outputs of ts_cache_attend; None for what was not asked for."""
+    out: object         # [batch, q_heads, dim] of the queries' type
+    lse: object         # fp32 [batch, q_heads]
+    weights: object     # [batch, q_heads, weights_slots]
+    status: object      # int32 [batch]
+
+
+def ts_cache_attend(q, k_pages, v_pages, table, lengths, scale: Optional[float] = None, window: int = 0, want_lse: bool = True,
+                    weights_slots: int = 0, weights_dtype=None, out=None) -> CacheAttend:
+    """Attention of one new token of each sequence over its cached positions.
+
+    q [batch, q_heads, dim] (fp32, bf16 or fp16); k_pages, v_pages [pages, kv_heads, slots, dim] of its type, kv_heads a divisor of
+    q_heads; table int32 [batch, width]: position j lies in page table[b, j // slots], slot j % slots; lengths int32 [batch].
+    scale: 1 / sqrt(dim) unless given. window: only the last `window` positions (0: all). weights_slots: the first so many
+    positions' attention weights are returned too, in weights_dtype (the queries' type unless given); viewed as [batch * kv_heads,
+    group, weights_slots] they are ts_cache_evict's `weights`. out: a tensor for the output, apart from q."""
+    torch = _t()
+    lib = load_library()
+    device, dtype = q.device, q.dtype
+    code = _DTYPES.get(dtype)
+    if code is None or not q.is_cuda or q.dim() != 3:
+        raise TopSelectError("q must be a float32, bfloat16 or float16 [batch, q_heads, dim] CUDA/HIP tensor")
+    (b, hq, dim), (qb, qh, qd) = q.shape, q.stride()
+    if dim > 1 and qd != 1:
+        raise TopSelectError("q must have a contiguous last dimension")
+    kp, vp = _paged(k_pages, dtype, device, "k_pages"), _paged(v_pages, dtype, device, "v_pages")
+    pages, hk, slots, kdim = k_pages.shape
+    if v_pages.shape != k_pages.shape or kdim != dim:
+        raise TopSelectError("k_pages and v_pages must have one shape, with q's dim")
+    rows, width, table_stride = _page_table(table, device)
+    if rows != b:
+        raise TopSelectError(f"table must have {b} rows")
+    plen = _param(lengths, torch.int32, b, device, "lengths")
+    if plen is None:
+        raise TopSelectError("lengths is required")
+    if out is None:
+        out = torch.empty((b, hq, dim), dtype=dtype, device=device)
+        ob, oh = hq * dim, dim
+    else:
+        if out.dtype is not dtype or out.shape != q.shape or out.device != device or (dim > 1 and out.stride(2) != 1):
+            raise TopSelectError("out must have q's shape, type and device and a contiguous last dimension")
+        ob, oh, _ = out.stride()
+    (lse, status), (plse, pstatus) = _outputs(device, b * hq if want_lse else None, b)
+    weights, pw, wcode, wb, wh = None, None, 0, 0, 0
+    if weights_slots:
+        weights_dtype = dtype if weights_dtype is None else weights_dtype
+        wcode = _DTYPES.get(weights_dtype)
+        if wcode is None:
+            raise TopSelectError("weights_dtype must be float32, bfloat16 or float16")
+        if weights_slots < 0:
+            raise TopSelectError("weights_slots must not be negative")
+        weights = torch.empty((b, hq, weights_slots), dtype=weights_dtype, device=device)
+        pw, wb, wh = weights.data_ptr(), hq * weights_slots, weights_slots
+    # a workspace of the call's own, as in ts_token_logp
+    nb = lib.ts_cache_attend_workspace(b, hq, hk, dim, width * slots, weights_slots)
+    ws = torch.empty(nb, dtype=torch.uint8, device=device) if nb else None
+    _call(device, lib.ts_cache_attend, q.data_ptr(), code, b, hq, hk, dim, qb, qh, ctypes.byref(kp), ctypes.byref(vp), pages, slots,
+          table.data_ptr(), width, table_stride, plen, dim ** -0.5 if scale is None else scale, window, out.data_ptr(), ob, oh, plse,
+          pw, wcode, weights_slots, wb, wh, pstatus, _ptr(ws), nb)
+    return CacheAttend(out, lse if lse is None else lse.view(b, hq), weights, status.view(torch.int32))
+
+
+def ts_cache_append(k_new, v_new, offsets, k_pages, v_pages, table, lengths):
+    """Write the keys and values of each sequence's newest tokens into their pages: returns status int32 [batch].
+
+    k_new, v_new [tokens, kv_heads, dim] of the pages' type (any); offsets int32 [batch + 1]: tokens offsets[b] .. offsets[b + 1]
+    are the last positions of sequence b, whose length counts them already. k_pages, v_pages, table as in ts_cache_attend."""
+    torch = _t()
+    lib = load_library()
+    device, dtype = k_pages.device, k_pages.dtype
+    if not k_pages.is_cuda:
+        raise TopSelectError("k_pages must be a CUDA/HIP tensor")
+    kp, vp = _paged(k_pages, dtype, device, "k_pages"), _paged(v_pages, dtype, device, "v_pages")
+    pages, hk, slots, dim = k_pages.shape
+    if v_pages.shape != k_pages.shape:
+        raise TopSelectError("k_pages and v_pages must have one shape")
+    size, strides = k_pages.element_size(), []
+    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
+        if t.dtype is not dtype or t.dim() != 3 or t.device != device or t.shape[1] != hk or t.shape[2] != dim:
+            raise TopSelectError(f"{name} must be a [tokens, {hk}, {dim}] tensor of {dtype} on {device}")
+        if dim > 1 and t.stride(2) != 1:
+            raise TopSelectError(f"{name} must have a contiguous last dimension")
+        strides += [t.stride(0) * size, t.stride(1) * size]
+    if v_new.shape[0] != k_new.shape[0]:
+        raise TopSelectError("k_new and v_new must have as many tokens")
+    b, width, table_stride = _page_table(table, device)
+    plen = _param(lengths, torch.int32, b, device, "lengths")
+    poff = _param(offsets, torch.int32, b + 1, device, "offsets")
+    if plen is None or poff is None:
+        raise TopSelectError("offsets and lengths are required")
+    status = torch.empty(b, dtype=torch.int32, device=device)
+    _call(device, lib.ts_cache_append, k_new.data_ptr(), v_new.data_ptr(), k_new.shape[0], b, hk, dim * size, *strides, poff,
+          ctypes.byref(kp), ctypes.byref(vp), pages, slots, table.data_ptr(), width, table_stride, plen, status.data_ptr())
+    return status
+
+
+class _Pool(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("page_bytes", ctypes.c_int64)]
+
+
+class PagePools:
+    """Tensors whose pages are moved together (keys and values of every layer): [pages, ...] each, every page dense. Keep one
+    beside a cache: the calls that copy pages take it, or the tensors themselves, whose addresses they then collect each time."""
+
+    def __init__(self, tensors):
+        _t()
+        self.tensors = tuple(tensors)
+        self.array = (_Pool * max(1, len(self.tensors)))()
+        self.pages = self.tensors[0].shape[0] if self.tensors else None
+        self.device = self.tensors[0].device if self.tensors else None
+        for i, t in enumerate(self.tensors):
+            if not t.is_cuda or t.device != self.device or t.dim() < 2 or t.shape[0] != self.pages:
+                raise TopSelectError(f"pools must be [{self.pages}, ...] CUDA/HIP tensors on one device")
+            if not t[:1].is_contiguous() or t[:1].numel() == 0 and self.pages:
+                raise TopSelectError(f"pool {i}: every page must be dense and not empty")
+            size = t.element_size()
+            page_bytes = t[:1].numel() * size if self.pages else size
+            self.array[i] = _Pool(t.data_ptr(), t.stride(0) * size if self.pages > 1 else page_bytes, page_bytes)
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def _page_pools(pools, pages: int, device) -> PagePools:
+    if not isinstance(pools, PagePools):
+        pools = PagePools(pools)
+    if len(pools) and (pools.pages != pages or pools.device != device):
+        raise TopSelectError(f"pools must hold {pages} pages on {device}")
+    return pools
+
+
+def _page_refs(refs, device):
+    if refs.dtype is not _torch.int32 or refs.dim() != 1 or refs.device != device or not refs.is_contiguous() or not refs.is_cuda:
+        raise TopSelectError("refs must be a contiguous int32 [pages] CUDA/HIP tensor")
+    return refs.numel()
+
+
+class PagesFork(NamedTuple):
+    """Outputs of ts_pages_fork."""
+    table: object       # int32 [children, width]
+    lengths: object     # int32 [children]
+    refs: object        # int32 [pages] (in place: the given tensor)
+    status: object      # int32 [children]
+
+
+def ts_pages_fork(table, lengths, refs, parent, page_slots: int, n_new=None, pools=(), width: Optional[int] = None,
+                  in_place: bool = False) -> PagesFork:
+    """The next step's sequences: child i continues sequence parent[i] (int32, -1: none), grown by n_new[i] positions.
+
+    Sequences without a child are freed; of one with several, whole pages are shared and a part-filled last page is copied, in every
+    tensor of `pools` (a PagePools or tensors), for each child but the first. refs int32 [pages]: table entries that name each page,
+    free where not above 0. width: of the new table (the old one's unless given). in_place: refs is updated; else a new
+    tensor is returned."""
+    torch = _t()
+    lib = load_library()
+    device, i = refs.device, torch.int32
+    pages = _page_refs(refs, device)
+    seqs, w, stride = _page_table(table, device)
+    plen = _param(lengths, i, seqs, device, "lengths")
+    n = parent.numel()
+    pparent, pnew = _param(parent, i, n, device, "parent"), _param(n_new, i, n, device, "n_new")
+    if plen is None:
+        raise TopSelectError("lengths is required")
+    pools = _page_pools(pools, pages, device)
+    width = w if width is None else width
+    if width < 0:
+        raise TopSelectError("width must not be negative")
+    out_table = torch.empty((n, width), dtype=i, device=device)
+    out_lengths, status = torch.empty((2, n), dtype=i, device=device).unbind(0)
+    out_refs = refs if in_place else torch.empty_like(refs)
+    nb = lib.ts_pages_fork_workspace(seqs, n, pages)
+    ws = torch.empty(nb, dtype=torch.uint8, device=device)
+    _call(device, lib.ts_pages_fork, table.data_ptr(), seqs, w, stride, plen, refs.data_ptr(), pages, page_slots, pparent, pnew, n,
+          out_table.data_ptr(), width, width, out_lengths.data_ptr(), out_refs.data_ptr(), pools.array, len(pools), status.data_ptr(),
+          ws.data_ptr(), nb)
+    return PagesFork(out_table, out_lengths, out_refs, status)
+
+
+class PagesCompact(NamedTuple):
+    """Outputs of ts_pages_compact."""
+    table: object       # int32 [sequences, width] (in place: the given tensor)
+    refs: object        # int32 [pages] (in place: the given tensor)
+    map: object         # int32 [pages]: each page's new number, -1 for free ones
+    count: object       # int32 [1]: pages in use
+    status: object      # int32 [sequences]
+
+
+def ts_pages_compact(table, lengths, refs, page_slots: int, pools=(), in_place: bool = False) -> PagesCompact:
+    """Move the pages in use (refs above 0) to the lowest numbers, in every tensor of `pools`, and renumber the tables.
+
+    in_place: table and refs are updated; else new tensors are returned. The pools are changed in place."""
+    torch = _t()
+    lib = load_library()
+    device, i = refs.device, torch.int32
+    pages = _page_refs(refs, device)
+    seqs, w, stride = _page_table(table, device)
+    plen = _param(lengths, i, seqs, device, "lengths")
+    if plen is None:
+        raise TopSelectError("lengths is required")
+    pools = _page_pools(pools, pages, device)
+    out_map = torch.empty(pages, dtype=i, device=device)
+    count = torch.empty(1, dtype=i, device=device)
+    status = torch.empty(seqs, dtype=i, device=device)
+    out_table, out_stride, out_refs = (table, stride, refs) if in_place else (torch.empty((seqs, w), dtype=i, device=device), w,
+                                                                              torch.empty_like(refs))
+    nb = lib.ts_pages_compact_workspace(pages)
+    ws = torch.empty(nb, dtype=torch.uint8, device=device)
+    _call(device, lib.ts_pages_compact, table.data_ptr(), seqs, w, stride, plen, refs.data_ptr(), pages, page_slots,
+          out_table.data_ptr(), out_stride, out_refs.data_ptr(), out_map.data_ptr(), count.data_ptr(), pools.array, len(pools),
+          status.data_ptr(), ws.data_ptr(), nb)
+    return PagesCompact(out_table, out_refs, out_map, count, status)
+
+
+def ts_pages_copy(source, target, pools):
+    """Copy page source[i] to page target[i] (int32 [n]) in every tensor of `pools`: returns status int32 [n], TS_ROW_BAD_PAGE for
+    pairs that are not copied (a page out of range, or a source that is another pair's target)."""
+    torch = _t()
+    lib = load_library()
+    if not isinstance(pools, PagePools):
+        pools = PagePools(pools)
+    device, n = source.device, source.numel()
+    if not source.is_cuda:
+        raise TopSelectError("source must be a CUDA/HIP tensor")
+    if not len(pools) or pools.device != device:
+        raise TopSelectError(f"pools must be tensors on {device}")
+    ps, pt = _param(source, torch.int32, n, device, "source"), _param(target, torch.int32, n, device, "target")
+    if pt is None:
+        raise TopSelectError("target is required")
+    status = torch.empty(n, dtype=torch.int32, device=device)
+    _call(device, lib.ts_pages_copy, ps, pt, n, pools.pages, pools.array, len(pools), status.data_ptr())
+    return status
 
 
 def ts_gumbel_noise(seed: int, row: int, tokens):

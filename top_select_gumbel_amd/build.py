@@ -13,7 +13,7 @@ import tempfile
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRCS = [os.path.join(PKG, "csrc", f) for f in ("topselect.hip", "rejection.hip", "read_ceiling.hip", "logprobs.hip",
-                                               "evict.hip")]
+                                               "evict.hip", "attend.hip", "pages.hip")]
 INC = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libtopselect.so")
 

@@ -3804,6 +3804,10 @@ const char* ts_status_string(int status) {
     case TS_ROW_BAD_T: return "row temperature negative or non-finite";
     case TS_ROW_BAD_MINP: return "row min_p outside [0, 1]";
     case TS_ROW_BAD_TOKEN: return "row token outside [0, vocab)";
+    case TS_ROW_BAD_PAGE: return "row names a page outside the cache";
+    case TS_ROW_BAD_LENGTH: return "row length outside what its table holds";
+    case TS_ROW_BAD_PARENT: return "row parent is no sequence";
+    case TS_ROW_NO_PAGE: return "too few free pages for the row";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,71 @@
+// ts_pages.hpp -- what the kernels of paged caches share: division by the page size and the host's checks of layouts.
+#pragma once
+#include <algorithm>
+#include <initializer_list>
+#include <utility>
+#include <vector>
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "topselect.h"
+#include "ts_host.hpp"
+
+namespace tsp {
+
+constexpr int64_t kMaxLen = 0x7FFFFF00;      // positions of a sequence: tiles past the last one stay in 31 bits
+constexpr int64_t kMaxPages = 0x7FFFFFFF;
+
+// j / d for j < 2^31 by a product: with 2^(l-1) < d <= 2^l and mul = ceil(2^(31+l) / d) < 2^32 the product exceeds the
+// quotient's by less than j 2^l / 2^(31+l) < 1 of the next multiple.
+struct Divisor {
+  uint32_t mul;
+  int32_t shift;
+  Divisor() = default;
+  explicit Divisor(int32_t d) {
+    int l = 0;
+    while (((int64_t)1 << l) < d) ++l;
+    mul = (uint32_t)((((uint64_t)1 << (31 + l)) + (uint64_t)d - 1) / (uint64_t)d);
+    shift = 31 + l;
+  }
+  __host__ __device__ uint32_t of(uint32_t j) const { return (uint32_t)(((uint64_t)j * mul) >> shift); }
+};
+
+typedef std::initializer_list<std::pair<int64_t, int64_t>> Strides;   // (stride, count)
+
+// Whether every element of `inner` consecutive ones at these strides (none negative) lies within 2^62 bytes.
+inline bool reaches(int64_t inner, Strides strides, int64_t size) {
+  __int128 end = inner;
+  for (auto [stride, n] : strides) {
+    if (stride < 0 && n > 1) return false;
+    if (n > 1) end += (__int128)stride * (n - 1);
+  }
+  return end * size <= (__int128)1 << 62;
+}
+// ... and whether no two of them share memory: along the ascending strides each clears what lies below it.
+inline bool apart(int64_t inner, Strides strides, int64_t size) {
+  if (!reaches(inner, strides, size)) return false;
+  std::vector<std::pair<int64_t, int64_t>> by(strides);
+  std::sort(by.begin(), by.end());
+  int64_t end = inner;
+  for (auto [stride, n] : by) {
+    if (n <= 1) continue;
+    if (stride < end) return false;
+    end += stride * (n - 1);
+  }
+  return true;
+}
+
+inline int check_table(int64_t pages, int64_t page_slots, int64_t table_width, int64_t table_stride) {
+  if (pages < 0 || pages > kMaxPages) return tsh::fail(TS_ERR_INVALID_ARG, "pages = %lld outside [0, 2^31)", (long long)pages);
+  if (page_slots < 1 || page_slots > 1 << 30)
+    return tsh::fail(TS_ERR_INVALID_ARG, "page_slots = %lld outside [1, 2^30]", (long long)page_slots);
+  if (table_width < 0 || table_width > kMaxLen)
+    return tsh::fail(TS_ERR_INVALID_ARG, "table_width = %lld is negative or too large", (long long)table_width);
+  if (table_stride < table_width || table_stride > (int64_t)1 << 40)
+    return tsh::fail(TS_ERR_INVALID_ARG, "table_stride %lld < table_width %lld, or too large", (long long)table_stride,
+                     (long long)table_width);
+  return TS_OK;
+}
+
+}  // namespace tsp
