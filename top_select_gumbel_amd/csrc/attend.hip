@@ -47,6 +47,11 @@ constexpr int kAT = 256;       // threads
 constexpr int kAW = kAT / 64;  // waves; each takes every kAW-th tile of a segment
 constexpr int kCols = 16;      // query heads a row
 constexpr int kMaxDim = 256;
+#ifdef EXP_NT
+#define LOADK tsl::load16_once
+#else
+#define LOADK tsl::load16
+#endif
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
@@ -92,6 +97,7 @@ struct AParams {
   float* part;                    // [workgroups, 2, part_floats]
   int32_t whole;                  // a workgroup a row, no parts
   int32_t min_share;
+  int32_t tiny;                   // a row shorter than 16 bytes
 };
 
 __device__ __forceinline__ int rows_of(const AParams& P) { return P.kv_heads * P.head_tiles; }
@@ -111,32 +117,31 @@ __device__ __forceinline__ int32_t tiles_of(const Span& s) {
 }
 
 // ------------------------------------------------------------------ loads
-// CE elements of 16 / CE .. bytes from dim `d0` of the row at p, zeros past `dim`.
-template <int DT, int BYTES, bool FULL>
-__device__ __forceinline__ void load_piece(uint32_t* to, const char* p, int d0, int dim) {
-  constexpr int size = DT == TS_DTYPE_F32 ? 4 : 2;
-  constexpr int n = BYTES / size;
-  const char* at = p + d0 * size;
-  if (FULL || d0 + n <= dim) {
-    if constexpr (BYTES == 16) {
-      const u32x4 x = tsl::load16(at);
+// BYTES of a row's dims. The loads take no branch for a dim below the padded one: a piece that would reach past the row's end is
+// moved back to end with it (Piece below says where it starts), so every address is in the row. A row shorter than a piece
+// (`tiny`) is loaded by elements.
+template <int BYTES>
+__device__ __forceinline__ void load_piece(uint32_t* to, const char* at) {
+  if constexpr (BYTES == 16) {
+    const u32x4 x = LOADK(at);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) to[i] = x[i];
-    } else {
-      const u32x2 x = *reinterpret_cast<const u32x2_any*>(at);
-      to[0] = x[0];
-      to[1] = x[1];
-    }
-    return;
+    for (int i = 0; i < 4; ++i) to[i] = x[i];
+  } else {
+    const u32x2 x = *reinterpret_cast<const u32x2_any*>(at);
+    to[0] = x[0];
+    to[1] = x[1];
   }
+}
+template <int SIZE, int BYTES>
+__device__ __forceinline__ void load_tiny(uint32_t* to, const char* row, int byte, int row_bytes) {
 #pragma unroll
-  for (int i = 0; i < BYTES / 4; ++i) {
-    to[i] = 0;
-    if constexpr (size == 4) {
-      if (d0 + i < dim) to[i] = reinterpret_cast<const uint32_t*>(at)[i];
+  for (int i = 0; i < BYTES / SIZE; ++i) {
+    const int at = byte + i * SIZE;
+    if (SIZE == 4) {
+      to[i] = at < row_bytes ? *reinterpret_cast<const uint32_t*>(row + at) : 0;
     } else {
-      if (d0 + 2 * i < dim) to[i] = reinterpret_cast<const uint16_t*>(at)[2 * i];
-      if (d0 + 2 * i + 1 < dim) to[i] |= (uint32_t) reinterpret_cast<const uint16_t*>(at)[2 * i + 1] << 16;
+      const uint32_t x = at < row_bytes ? *reinterpret_cast<const uint16_t*>(row + at) : 0;
+      to[i / 2] = (i & 1) ? to[i / 2] | x << 16 : x;
     }
   }
 }
@@ -225,28 +230,51 @@ struct Wave {
   f32x4 o[S::kAcc];
   float m, l;
 
+  // The bytes of piece c of a key that are its own: all but those of the last block of 64, of which this lane's may lie past the
+  // row's end (none is its own) or reach past it (moved back: its first bytes are another's).
+  __device__ __forceinline__ void own(const AParams& P, int c, uint32_t* x) const {
+    if constexpr (!FULL) {
+      const int end = P.dim * S::kSize, byte = c * 64 + (lane() >> 4) * 16;
+      if (c * 64 + 64 <= end) return;                 // the same for all lanes
+      const int skip = P.tiny ? 0 : min(16, max(0, byte + 16 - end));
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const int s = min(4, max(0, skip - 4 * w));   // bytes of this word that are not
+        x[w] &= s == 4 ? 0u : 0xFFFFFFFFu << (8 * s);
+      }
+    }
+  }
+  __device__ __forceinline__ void load_row(const AParams& P, uint32_t (*to)[4], const char* row) const {
+    const int g = lane() >> 4, end = P.dim * S::kSize;
+    if (!FULL && P.tiny) {
+#pragma unroll
+      for (int c = 0; c < S::kKC; ++c) load_tiny<S::kSize, 16>(to[c], row, c * 64 + g * 16, end);
+      return;
+    }
+#pragma unroll
+    for (int c = 0; c < S::kKC; ++c) load_piece<16>(to[c], row + (FULL ? c * 64 + g * 16 : min(c * 64 + g * 16, end - 16)));
+  }
   __device__ __forceinline__ void load_q(const AParams& P, int b, int head0, int heads) {
-    const int g = lane() >> 4, i = lane() & 15;
-    const char* row = P.q + b * P.q_b + (int64_t)(head0 + min(i, heads - 1)) * P.q_h;
+    const int i = lane() & 15;
+    load_row(P, q, P.q + b * P.q_b + (int64_t)(head0 + min(i, heads - 1)) * P.q_h);
 #pragma unroll
     for (int c = 0; c < S::kKC; ++c) {
-      load_piece<DT, 16, FULL>(q[c], row, (c * 64 + g * 16) / S::kSize, P.dim);
+      own(P, c, q[c]);
       if (i >= heads) q[c][0] = q[c][1] = q[c][2] = q[c][3] = 0;
     }
   }
   __device__ __forceinline__ void load_k(const AParams& P, const char* kh, const Place<S::kHalves, UNI>& at, int first, int lo, int n) {
-    const int g = lane() >> 4, i = lane() & 15;
+    const int i = lane() & 15;
 #pragma unroll
     for (int h = 0; h < S::kHalves; ++h) {
       int32_t slot = at.slot[h];
       if constexpr (UNI) slot += max(min(first + 16 * h + i, n - 1), lo) - at.base[h];
-      const char* row = kh + at.page[h] * P.k_page + (int64_t)slot * P.k_slot;
-#pragma unroll
-      for (int c = 0; c < S::kKC; ++c) load_piece<DT, 16, FULL>(k[h][c], row, (c * 64 + g * 16) / S::kSize, P.dim);
+      load_row(P, k[h], kh + at.page[h] * P.k_page + (int64_t)slot * P.k_slot);
     }
   }
   __device__ __forceinline__ void load_v(const AParams& P, const char* vh, const Place<S::kHalves, UNI>& at, int first, int lo, int n) {
-    const int g = lane() >> 4, i = lane() & 15;
+    const int g = lane() >> 4, i = lane() & 15, end = P.dim * S::kSize;
+    constexpr int bytes = S::kCW * S::kSize;
 #pragma unroll
     for (int x = 0; x < S::kVR; ++x) {
       const int h = x >> 2, in = g * 4 + (x & 3);
@@ -260,17 +288,21 @@ struct Wave {
       }
       const char* row = vh + page * P.v_page + (int64_t)slot * P.v_slot;
 #pragma unroll
-      for (int p = 0; p < S::kNP; ++p)
-        load_piece<DT, S::kCW * S::kSize, FULL>(v[x][p], row, p * 16 * S::kCW + i * S::kCW, P.dim);
+      for (int p = 0; p < S::kNP; ++p) {
+        const int byte = (p * 16 + i) * bytes;
+        if (!FULL && P.tiny) load_tiny<S::kSize, bytes>(v[x][p], row, byte, end);
+        else load_piece<bytes>(v[x][p], row + (FULL ? byte : min(byte, end - bytes)));   // what lies past the dims is not stored
+      }
     }
   }
   // Scores of the loaded keys: s[h][r] is position first + 16 h + 4 g + r under head i.
-  __device__ __forceinline__ void scores(f32x4* s) const {
+  __device__ __forceinline__ void scores(const AParams& P, f32x4* s) {
 #pragma unroll
     for (int h = 0; h < S::kHalves; ++h) {
       s[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int c = 0; c < S::kKC; ++c) {
+        own(P, c, k[h][c]);
         if constexpr (S::kF32) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -348,15 +380,16 @@ struct Wave {
   }
 };
 
-// Results of a head's dims (g * 4 + r) * CW .. + CW of pass p, rounded once.
+// CW results of a head, the dims from d0 on, rounded once. (The values' piece there was moved back to end with the row.)
 template <int DT, int CW>
-__device__ __forceinline__ void store_dims(char* row, int d0, int dim, const float* x) {
+__device__ __forceinline__ void store_dims(char* row, int d0, int dim, bool tiny, const float* x) {
+  const int at = tiny ? d0 : min(d0, dim - CW);
 #pragma unroll
   for (int n = 0; n < CW; ++n) {
-    if (d0 + n >= dim) return;
-    if constexpr (DT == TS_DTYPE_F32) reinterpret_cast<float*>(row)[d0 + n] = x[n];
-    else if constexpr (DT == TS_DTYPE_BF16) reinterpret_cast<__bf16*>(row)[d0 + n] = (__bf16)x[n];
-    else reinterpret_cast<_Float16*>(row)[d0 + n] = (_Float16)x[n];
+    if (at + n < d0 || at + n >= dim) continue;
+    if constexpr (DT == TS_DTYPE_F32) reinterpret_cast<float*>(row)[at + n] = x[n];
+    else if constexpr (DT == TS_DTYPE_BF16) reinterpret_cast<__bf16*>(row)[at + n] = (__bf16)x[n];
+    else reinterpret_cast<_Float16*>(row)[at + n] = (_Float16)x[n];
   }
 }
 
@@ -473,7 +506,7 @@ __global__ __launch_bounds__(kAT, DP > 128 ? 1 : 2) void ts_attend_kernel(const 
         const int first = t * S::kTok, next = t + kAW;
         f32x4 s[S::kHalves];
         if (next < t_end) at.find(P, table, next * S::kTok, lo, n, bad);
-        W.scores(s);
+        W.scores(P, s);
         if (next < t_end) W.load_k(P, kh, at, next * S::kTok, lo, n);   // into the registers that the products have read
         if (first < lo || first + S::kTok > n) W.mask(s, first, lo, n);
         if (P.score && i < R.heads) {
@@ -533,7 +566,7 @@ __global__ __launch_bounds__(kAT, DP > 128 ? 1 : 2) void ts_attend_kernel(const 
         for (int c = 0; c < S::kCW; ++c) sum[c] = status == TS_ROW_OK && l == 0.0f ? 0.0f : sum[c] * inv;
         if (i < R.heads)
           store_dims<DT, S::kCW>(P.out + b * P.out_b + (int64_t)(R.head0 + i) * P.out_h,
-                                 (x >> 2) * 16 * S::kCW + (g * 4 + (x & 3)) * S::kCW, P.dim, sum);
+                                 (x >> 2) * 16 * S::kCW + (g * 4 + (x & 3)) * S::kCW, P.dim, P.tiny, sum);
       } else {
 #pragma unroll
         for (int c = 0; c < S::kCW; ++c) part[(x * S::kCW + c) * 64 + lane()] = sum[c];
@@ -622,7 +655,7 @@ __global__ __launch_bounds__(kAT) void ts_attend_join_kernel(const AParams P) {
   for (int c = 0; c < S::kCW; ++c) sum[c] = status != TS_ROW_OK ? NAN : l == 0.0f ? 0.0f : sum[c] * (1.0f / l);
   if (i < R.heads)
     store_dims<DT, S::kCW>(P.out + b * P.out_b + (int64_t)(R.head0 + i) * P.out_h,
-                           (x >> 2) * 16 * S::kCW + (g * 4 + (x & 3)) * S::kCW, P.dim, sum);
+                           (x >> 2) * 16 * S::kCW + (g * 4 + (x & 3)) * S::kCW, P.dim, P.tiny, sum);
   if (x == 0) {
     store_norm(P, R, m, l, S::kBias, status);
     if (P.status && lane() == 0) P.status[b] = status;
@@ -845,6 +878,7 @@ extern "C" int ts_cache_attend(const void* q, int dtype, int64_t batch, int32_t 
   P.part = reinterpret_cast<float*>(ws + pl.off_part);
   P.whole = pl.whole ? 1 : 0;
   P.min_share = kMinShare;
+  P.tiny = dim * size < 16;
   const hipStream_t s = (hipStream_t)stream;
   hipError_t e = dtype == TS_DTYPE_F32    ? launch_dim<TS_DTYPE_F32>(P, pl.rows, s)
                  : dtype == TS_DTYPE_BF16 ? launch_dim<TS_DTYPE_BF16>(P, pl.rows, s)
