@@ -47,6 +47,7 @@ constexpr int kAT = 256;       // threads
 constexpr int kAW = kAT / 64;  // waves; each takes every kAW-th tile of a segment
 constexpr int kCols = 16;      // query heads a row
 constexpr int kMaxDim = 256;
+enum { kFull, kPart, kTiny };  // a head's dims: the padded ones, fewer, fewer than 16 bytes
 #ifdef EXP_NT
 #define LOADK tsl::load16_once
 #else
@@ -96,8 +97,8 @@ struct AParams {
   int64_t* start;                 // [batch + 1]: tiles of the sequences before; then the share's size
   float* part;                    // [workgroups, 2, part_floats]
   int32_t whole;                  // a workgroup a row, no parts
-  int32_t min_share;
   int32_t tiny;                   // a row shorter than 16 bytes
+  int32_t end_block;              // the block of 64 bytes in which a row ends, -1: with its 16 bytes
 };
 
 __device__ __forceinline__ int rows_of(const AParams& P) { return P.kv_heads * P.head_tiles; }
@@ -221,45 +222,59 @@ struct Place {
 };
 
 // ------------------------------------------------------------------ a wave's running state
-template <int DT, int DP, bool FULL, bool UNI>
+__device__ const uint32_t zeros[4] = {0, 0, 0, 0};
+
+template <int DT, int DP, int MODE, bool UNI>
 struct Wave {
   using S = Shape<DT, DP>;
+  static constexpr bool FULL = MODE == kFull;
   uint32_t q[S::kKC][4];
   uint32_t k[S::kHalves][S::kKC][4];
   uint32_t v[S::kVR][S::kNP][S::kCW * S::kSize / 4];
   f32x4 o[S::kAcc];
+  uint32_t keep[4];
   float m, l;
 
-  // The bytes of piece c of a key that are its own: all but those of the last block of 64, of which this lane's may lie past the
-  // row's end (none is its own) or reach past it (moved back: its first bytes are another's).
-  __device__ __forceinline__ void own(const AParams& P, int c, uint32_t* x) const {
-    if constexpr (!FULL) {
-      const int end = P.dim * S::kSize, byte = c * 64 + (lane() >> 4) * 16;
-      if (c * 64 + 64 <= end) return;                 // the same for all lanes
-      const int skip = P.tiny ? 0 : min(16, max(0, byte + 16 - end));
+  // A piece that would reach past the row's end is moved back to end with it, and its first bytes, another piece's, are cleared
+  // before use: they lie in the one block of 64 bytes in which the row ends. Pieces past the end come from zeros.
+  __device__ __forceinline__ void prepare(const AParams& P) {
+    if constexpr (MODE == kPart) {
+      const int end = P.dim * S::kSize, over = end / 64 * 64 + (lane() >> 4) * 16 + 16 - end;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const int s = min(4, max(0, skip - 4 * w));   // bytes of this word that are not
-        x[w] &= s == 4 ? 0u : 0xFFFFFFFFu << (8 * s);
+        const int skip = over >= 16 ? 0 : min(4, max(0, over - 4 * w));
+        keep[w] = skip == 4 ? 0u : 0xFFFFFFFFu << (8 * skip);
       }
+    }
+  }
+  __device__ __forceinline__ void clear(const AParams& P, int c, uint32_t* x) const {
+    if constexpr (MODE == kPart) {
+      if (c != P.end_block) return;   // the same for all lanes
+#pragma unroll
+      for (int w = 0; w < 4; ++w) x[w] &= keep[w];
     }
   }
   __device__ __forceinline__ void load_row(const AParams& P, uint32_t (*to)[4], const char* row) const {
     const int g = lane() >> 4, end = P.dim * S::kSize;
-    if (!FULL && P.tiny) {
+    if constexpr (MODE == kTiny) {
 #pragma unroll
       for (int c = 0; c < S::kKC; ++c) load_tiny<S::kSize, 16>(to[c], row, c * 64 + g * 16, end);
       return;
     }
 #pragma unroll
-    for (int c = 0; c < S::kKC; ++c) load_piece<16>(to[c], row + (FULL ? c * 64 + g * 16 : min(c * 64 + g * 16, end - 16)));
+    for (int c = 0; c < S::kKC; ++c) {
+      const int byte = c * 64 + g * 16;
+      const char* at = row + byte;
+      if constexpr (!FULL) at = byte < end ? row + min(byte, end - 16) : reinterpret_cast<const char*>(zeros);
+      load_piece<16>(to[c], at);
+    }
   }
   __device__ __forceinline__ void load_q(const AParams& P, int b, int head0, int heads) {
     const int i = lane() & 15;
     load_row(P, q, P.q + b * P.q_b + (int64_t)(head0 + min(i, heads - 1)) * P.q_h);
 #pragma unroll
     for (int c = 0; c < S::kKC; ++c) {
-      own(P, c, q[c]);
+      clear(P, c, q[c]);
       if (i >= heads) q[c][0] = q[c][1] = q[c][2] = q[c][3] = 0;
     }
   }
@@ -290,7 +305,7 @@ struct Wave {
 #pragma unroll
       for (int p = 0; p < S::kNP; ++p) {
         const int byte = (p * 16 + i) * bytes;
-        if (!FULL && P.tiny) load_tiny<S::kSize, bytes>(v[x][p], row, byte, end);
+        if constexpr (MODE == kTiny) load_tiny<S::kSize, bytes>(v[x][p], row, byte, end);
         else load_piece<bytes>(v[x][p], row + (FULL ? byte : min(byte, end - bytes)));   // what lies past the dims is not stored
       }
     }
@@ -302,7 +317,7 @@ struct Wave {
       s[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int c = 0; c < S::kKC; ++c) {
-        own(P, c, k[h][c]);
+        clear(P, c, k[h][c]);
         if constexpr (S::kF32) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -416,118 +431,175 @@ __device__ __forceinline__ void store_norm(const AParams& P, const RowOut& R, fl
 }
 
 // ------------------------------------------------------------------ the pass over the cache
-template <int DT, int DP, bool FULL, bool UNI>
-__global__ __launch_bounds__(kAT, DP > 128 ? 1 : 2) void ts_attend_kernel(const AParams P) {
-  using S = Shape<DT, DP>;
-  __shared__ float sm_o[kAW][S::kAcc * 4][64];
-  __shared__ float sm_m[kAW][kCols], sm_l[kAW][kCols];
-  __shared__ uint64_t red64[kAW];
-  __shared__ int64_t found[2];
-  __shared__ int any_bad;
-  const int wv = __builtin_amdgcn_readfirstlane(wave()), g = lane() >> 4, i = lane() & 15;
-  const int rows = rows_of(P);
-  int b = 0, r = 0;
-  int32_t tile = 0;
-  int64_t left = 0;              // tiles of this workgroup's share that are still to do
-  if (P.whole) {
-    b = blockIdx.x / (unsigned)rows;
-    r = blockIdx.x - b * rows;
-    left = 1;
-  } else {
-    // Tiles of all sequences before; thread t adds up a stretch of them.
-    const int own = (P.batch + kAT - 1) / kAT, first = min(P.batch, (int)threadIdx.x * own), last = min(P.batch, first + own);
-    uint64_t sum = 0;
-    for (int x = first; x < last; ++x) sum += (uint64_t)tiles_of<S::kTok>(span_of(P, x)) * rows;
-    const uint64_t incl = wave_incl_scan64(sum);
-    if (lane() == 63) red64[wv] = incl;
-    if (threadIdx.x == 0) found[0] = -1;
-    bar();
-    uint64_t before = incl - sum, total = 0;
-#pragma unroll
-    for (int w = 0; w < kAW; ++w) {
-      before += w < wv ? red64[w] : 0;
-      total += red64[w];
-    }
-    int64_t share = ((int64_t)total + gridDim.x - 1) / gridDim.x;
-    share = max(share, (int64_t)P.min_share);
-    share = (share + kAW - 1) / kAW * kAW;
-    const int64_t pos = blockIdx.x * share;
-    int64_t at = (int64_t)before;
+// A stretch of a row's tiles that one workgroup goes through.
+struct Segment {
+  int32_t index, b, r;           // r: the sequence's row
+  int32_t lo, n, tiles;          // of the sequence
+  int32_t tile, todo;            // the first of the row's tiles, and how many
+  int64_t left;                  // tiles of the workgroup's share from here on
+};
+template <int TOK>
+__device__ __forceinline__ void segment_at(const AParams& P, Segment& s, int b) {
+  const Span span = span_of(P, b);
+  s.b = b;
+  s.lo = span.lo;
+  s.n = span.n;
+  s.tiles = tiles_of<TOK>(span);
+  s.todo = P.whole ? s.tiles : (int32_t)min((int64_t)(s.tiles - s.tile), s.left);
+}
+template <int TOK>
+__device__ __forceinline__ bool next_segment(const AParams& P, Segment& s) {
+  s.left -= s.todo;
+  if (P.whole || s.left <= 0) return false;   // the row is then finished: the share goes on past it
+  ++s.index;
+  s.tile = 0;
+  if (++s.r < rows_of(P)) {
+    s.todo = (int32_t)min((int64_t)s.tiles, s.left);
+    return true;
+  }
+  s.r = 0;
+  do {
+    segment_at<TOK>(P, s, s.b + 1);
+  } while (s.tiles == 0);
+  return true;
+}
+// The share's first segment: every wave adds up the tiles of all sequences by itself (lane x takes a stretch of them), so that no
+// barrier stands before the first loads.
+template <int TOK>
+__device__ __forceinline__ bool first_segment(const AParams& P, Segment& s) {
+  const int rows = rows_of(P), own = (P.batch + 63) / 64, first = min(P.batch, lane() * own), last = min(P.batch, first + own);
+  uint64_t sum = 0;
+  for (int x = first; x < last; ++x) sum += (uint64_t)tiles_of<TOK>(span_of(P, x)) * rows;
+  const uint64_t incl = wave_incl_scan64(sum), total = readlane64(incl, 63);
+  int64_t share = ((int64_t)total + gridDim.x - 1) / gridDim.x;
+  share = (max(share, (int64_t)1) + kAW - 1) / kAW * kAW;
+  const int64_t pos = blockIdx.x * share;
+  if (blockIdx.x == 0 && threadIdx.x < 64) {
+    int64_t at = (int64_t)(incl - sum);
     for (int x = first; x < last; ++x) {
-      const int64_t n = (int64_t)tiles_of<S::kTok>(span_of(P, x)) * rows;
-      if (blockIdx.x == 0) P.start[x] = at;
-      if (pos >= at && pos < at + n) {
-        found[0] = x;
-        found[1] = pos - at;
-      }
-      at += n;
+      P.start[x] = at;
+      at += (int64_t)tiles_of<TOK>(span_of(P, x)) * rows;
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (lane() == 0) {
       P.start[P.batch] = (int64_t)total;
       P.start[P.batch + 1] = share;
     }
-    bar();
-    if (found[0] < 0) return;
-    b = (int)found[0];
-    const int64_t in = found[1];
-    left = min(share, (int64_t)total - pos);
-    const int32_t tiles = tiles_of<S::kTok>(span_of(P, b));
-    r = (int)(in / tiles);
-    tile = (int32_t)(in - (int64_t)r * tiles);
   }
-  Wave<DT, DP, FULL, UNI> W;
-  while (left > 0) {
-    const Span span = span_of(P, b);
-    const int32_t tiles = tiles_of<S::kTok>(span);
-    if (!P.whole && tiles == 0) {
-      ++b;
-      continue;
+  if (pos >= (int64_t)total) return false;
+  const uint64_t past = __builtin_amdgcn_ballot_w64((int64_t)incl > pos);   // not 0: the last lane's is the total
+  const int l = __builtin_ctzll(past);
+  int64_t in = pos - (int64_t)readlane64(incl - sum, l);
+  int b = l * own;
+  int32_t tiles;
+  for (;; ++b) {
+    tiles = tiles_of<TOK>(span_of(P, b));
+    if (in < (int64_t)tiles * rows) break;
+    in -= (int64_t)tiles * rows;
+  }
+  s.index = 0;
+  s.left = min(share, (int64_t)total - pos);
+  s.r = (int)(in / tiles);
+  s.tile = (int32_t)(in - (int64_t)s.r * tiles);
+  segment_at<TOK>(P, s, b);
+  return true;
+}
+
+template <int DT, int DP, int MODE, bool UNI>
+__global__ __launch_bounds__(kAT, DP > 128 ? 1 : 2) void ts_attend_kernel(const AParams P) {
+  using S = Shape<DT, DP>;
+  constexpr int TOK = S::kTok;
+  __shared__ float sm_o[kAW][S::kAcc * 4][64];
+  __shared__ float sm_m[kAW][kCols], sm_l[kAW][kCols];
+  __shared__ int any_bad[2];
+  const int wv = __builtin_amdgcn_readfirstlane(wave()), g = lane() >> 4, i = lane() & 15;
+  Segment cur;
+  if (P.whole) {
+    const int rows = rows_of(P), b = blockIdx.x / (unsigned)rows;
+    cur.index = 0;
+    cur.r = blockIdx.x - b * rows;
+    cur.tile = 0;
+    cur.left = 1;
+    segment_at<TOK>(P, cur, b);
+  } else if (!first_segment<TOK>(P, cur)) {
+    return;
+  }
+  Wave<DT, DP, MODE, UNI> W;
+  W.prepare(P);
+  Place<S::kHalves, UNI> at;
+  // What this wave has loaded, or is about to: tile t of segment `ahead`, which may lie past the one that is worked on.
+  Segment ahead = cur;
+  int t = wv;                    // counted from the segment's first tile
+  bool bad = false;
+  auto settle = [&](Segment& s, int& tile) {
+    while (tile >= s.todo) {
+      if (!next_segment<TOK>(P, s)) return false;
+      tile = wv;
     }
-    const int32_t todo = P.whole ? tiles : (int32_t)min((int64_t)(tiles - tile), left);
-    const RowOut R = row_out(P, b, r);
-    const int hk = r / P.head_tiles;
-    const char *kh = P.k + hk * P.k_head, *vh = P.v + hk * P.v_head;
-    const int32_t* table = P.table + (int64_t)b * P.table_stride;
-    const int lo = span.lo, n = span.n;
-    const int t_end = lo / S::kTok + tile + todo;
-    bool bad = false;
+    return true;
+  };
+  auto position = [&](const Segment& s, int tile) { return (s.lo / TOK + s.tile + tile) * TOK; };
+  auto find = [&](const Segment& s, int tile) {
+    at.find(P, P.table + (int64_t)s.b * P.table_stride, position(s, tile), s.lo, s.n, bad);
+  };
+  auto load_q = [&](const Segment& s) {
+    const RowOut R = row_out(P, s.b, s.r);
+    W.load_q(P, s.b, R.head0, R.heads);
+  };
+  auto load_k = [&](const Segment& s, int tile) {
+    W.load_k(P, P.k + (s.r / P.head_tiles) * P.k_head, at, position(s, tile), s.lo, s.n);
+  };
+  auto load_v = [&](const Segment& s, int tile) {
+    W.load_v(P, P.v + (s.r / P.head_tiles) * P.v_head, at, position(s, tile), s.lo, s.n);
+  };
+  if (threadIdx.x < 2) any_bad[threadIdx.x] = 0;
+  bool have = settle(ahead, t), spoils = false;   // spoils: a page of the segments up to `ahead` was bad, and of which
+  if (have) {
+    find(ahead, t);
+    load_q(ahead);
+    load_k(ahead, t);
+    load_v(ahead, t);
+  }
+  for (;;) {
+    const RowOut R = row_out(P, cur.b, cur.r);
+    const int lo = cur.lo, n = cur.n;
     W.m = -INFINITY;
     W.l = 0.0f;
 #pragma unroll
     for (int a = 0; a < S::kAcc; ++a) W.o[a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    int t = lo / S::kTok + tile + wv;
-    if (t < t_end) {
-      Place<S::kHalves, UNI> at;
-      at.find(P, table, t * S::kTok, lo, n, bad);
-      W.load_q(P, b, R.head0, R.heads);
-      W.load_k(P, kh, at, t * S::kTok, lo, n);
-      W.load_v(P, vh, at, t * S::kTok, lo, n);
-      for (;;) {
-        const int first = t * S::kTok, next = t + kAW;
-        f32x4 s[S::kHalves];
-        if (next < t_end) at.find(P, table, next * S::kTok, lo, n, bad);
-        W.scores(P, s);
-        if (next < t_end) W.load_k(P, kh, at, next * S::kTok, lo, n);   // into the registers that the products have read
-        if (first < lo || first + S::kTok > n) W.mask(s, first, lo, n);
-        if (P.score && i < R.heads) {
-          float* to = P.score + ((int64_t)b * P.q_heads + R.head0 + i) * P.score_stride + first + g * 4;
-#pragma unroll
-          for (int h = 0; h < S::kHalves; ++h) *reinterpret_cast<f32x4*>(to + 16 * h) = s[h];
-        }
-        W.weigh(s, P.c);
-        W.accumulate(s);
-        if (next >= t_end) break;
-        W.load_v(P, vh, at, next * S::kTok, lo, n);
-        t = next;
+    spoils = false;
+    while (have && ahead.index == cur.index) {
+      const int first = position(cur, t);
+      spoils = spoils || bad;
+      bad = false;
+      Segment next = ahead;
+      int u = t + kAW;
+      have = settle(next, u);
+      f32x4 s[S::kHalves];
+      if (have) find(next, u);
+      W.scores(P, s);
+      if (have) {   // into the registers that the products have read
+        if (next.index != ahead.index) load_q(next);
+        load_k(next, u);
       }
+      if (first < lo || first + TOK > n) W.mask(s, first, lo, n);
+      if (P.score && i < R.heads) {
+        float* to = P.score + ((int64_t)cur.b * P.q_heads + R.head0 + i) * P.score_stride + first + g * 4;
+#pragma unroll
+        for (int h = 0; h < S::kHalves; ++h) *reinterpret_cast<f32x4*>(to + 16 * h) = s[h];
+      }
+      W.weigh(s, P.c);
+      W.accumulate(s);
+      if (have) load_v(next, u);
+      ahead = next;
+      t = u;
     }
     // join the waves
-    W.l = column_sum(W.l);
-    if (threadIdx.x == 0) any_bad = 0;
+    const float l_wave = column_sum(W.l);
     if (lane() < kCols) {
       sm_m[wv][i] = W.m;
-      sm_l[wv][i] = W.l;
+      sm_l[wv][i] = l_wave;
     }
+    if (__builtin_amdgcn_ballot_w64(spoils)) any_bad[cur.index & 1] = 1;
 #pragma unroll
     for (int p = 0; p < S::kNP; ++p)
 #pragma unroll
@@ -535,7 +607,6 @@ __global__ __launch_bounds__(kAT, DP > 128 ? 1 : 2) void ts_attend_kernel(const 
 #pragma unroll
         for (int c = 0; c < S::kCW; ++c) sm_o[wv][(p * 4 + x) * S::kCW + c][lane()] = W.o[p * S::kCW + c][x];
     bar();
-    if (bad) any_bad = 1;
     float m = -INFINITY, l = 0.0f, f[kAW];
 #pragma unroll
     for (int w = 0; w < kAW; ++w) m = fmaxf(m, sm_m[w][i]);
@@ -545,11 +616,11 @@ __global__ __launch_bounds__(kAT, DP > 128 ? 1 : 2) void ts_attend_kernel(const 
       f[w] = mw == m ? 1.0f : exp2_fast((mw - m) * P.c);   // also where both are -inf: that wave's sums are 0 or NaN
       l += f[w] * lw;
     }
-    bar();
-    const bool spoilt = any_bad != 0;
-    const bool complete = P.whole || (tile == 0 && todo == tiles);
-    const int status = span.status != TS_ROW_OK ? span.status : spoilt ? TS_ROW_BAD_PAGE : TS_ROW_OK;
-    float* part = P.part + ((int64_t)blockIdx.x * 2 + (tile == 0 ? 1 : 0)) * kPartFloats<DT, DP>;
+    const bool spoilt = any_bad[cur.index & 1] != 0;
+    const bool complete = cur.todo == cur.tiles;
+    int status = spoilt ? TS_ROW_BAD_PAGE : TS_ROW_OK;
+    if (cur.tiles == 0) status = span_of(P, cur.b).status;
+    float* part = P.part + ((int64_t)blockIdx.x * 2 + (cur.tile == 0 ? 1 : 0)) * kPartFloats<DT, DP>;
     const float inv = status != TS_ROW_OK ? NAN : l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
     for (int x0 = 0; x0 < S::kNP * 4; x0 += kAW) {
@@ -565,7 +636,7 @@ __global__ __launch_bounds__(kAT, DP > 128 ? 1 : 2) void ts_attend_kernel(const 
 #pragma unroll
         for (int c = 0; c < S::kCW; ++c) sum[c] = status == TS_ROW_OK && l == 0.0f ? 0.0f : sum[c] * inv;
         if (i < R.heads)
-          store_dims<DT, S::kCW>(P.out + b * P.out_b + (int64_t)(R.head0 + i) * P.out_h,
+          store_dims<DT, S::kCW>(P.out + cur.b * P.out_b + (int64_t)(R.head0 + i) * P.out_h,
                                  (x >> 2) * 16 * S::kCW + (g * 4 + (x & 3)) * S::kCW, P.dim, P.tiny, sum);
       } else {
 #pragma unroll
@@ -575,7 +646,7 @@ __global__ __launch_bounds__(kAT, DP > 128 ? 1 : 2) void ts_attend_kernel(const 
     if (wv == 0) {
       if (complete) {
         store_norm(P, R, m, l, S::kBias, status);
-        if (P.status && lane() == 0) P.status[b] = status;   // every row of a sequence finds the same
+        if (P.status && lane() == 0) P.status[cur.b] = status;   // every row of a sequence finds the same
       } else {
         float* tail = part + S::kAcc * 4 * 64;
         if (lane() < kCols) {
@@ -585,72 +656,74 @@ __global__ __launch_bounds__(kAT, DP > 128 ? 1 : 2) void ts_attend_kernel(const 
         if (lane() == 0) tail[2 * kCols] = spoilt ? 1.0f : 0.0f;
       }
     }
-    left -= P.whole ? 1 : todo;
-    tile += todo;
-    if (tile == tiles) {
-      tile = 0;
-      if (++r == rows) {
-        r = 0;
-        ++b;
-      }
-    }
+    const int index = cur.index;
+    if (!next_segment<TOK>(P, cur)) return;
     bar();
+    if (threadIdx.x == 0) any_bad[index & 1] = 0;   // its next use is two segments on, past the next barrier
   }
 }
 
 // ------------------------------------------------------------------ rows that several workgroups share
-// A workgroup a row and a quarter of its results; its waves take the parts in turn.
-template <int DT, int DP>
-__global__ __launch_bounds__(kAT) void ts_attend_join_kernel(const AParams P) {
+// A workgroup a row and one of its 4 passes of results; its waves take the parts in turn, each with a running maximum.
+template <int DT, int DP, int NW>
+__global__ __launch_bounds__(NW * 64) void ts_attend_join_kernel(const AParams P) {
   using S = Shape<DT, DP>;
-  __shared__ float sm_o[kAW][S::kCW][64];
-  __shared__ float sm_l[kAW][64];
+  __shared__ float sm_o[NW][S::kCW][64];
+  __shared__ float sm_m[NW][64], sm_l[NW][64];
+  __shared__ int any_bad;
   const int wv = __builtin_amdgcn_readfirstlane(wave()), g = lane() >> 4, i = lane() & 15;
   const int rows = rows_of(P), groups = S::kNP * 4;
   const int x = blockIdx.x % groups, row = blockIdx.x / groups, b = row / rows, r = row - b * rows;
+  const int64_t share = P.start[P.batch + 1], before = P.start[b];
   const Span span = span_of(P, b);
   const int32_t tiles = tiles_of<S::kTok>(span);
   const RowOut R = row_out(P, b, r);
-  const int64_t share = P.start[P.batch + 1], from = P.start[b] + (int64_t)r * tiles;
+  const int64_t from = before + (int64_t)r * tiles;
   const int64_t w0 = from / share, w1 = tiles ? (from + tiles - 1) / share : w0;
   if (tiles && w0 == w1) return;   // finished by its workgroup
   constexpr int64_t size = kPartFloats<DT, DP>;
-  // the first part is its workgroup's second one unless the row starts with the share
-  auto part_of = [&](int64_t w) { return P.part + (w * 2 + (w == w0 ? 1 : 0)) * size; };
   const int count = tiles ? (int)(w1 - w0 + 1) : 0;
-  float m = -INFINITY;
+  // the first part is its workgroup's second one, as the row starts inside the share or with it
+  const float* first = P.part + (w0 * 2 + 1) * size;
+  if (threadIdx.x == 0) any_bad = 0;
   bool bad = false;
-  for (int p = g; p < count; p += 4) {   // a column's four lanes take a part each
-    const float* tail = part_of(w0 + p) + S::kAcc * 4 * 64;
-    m = fmaxf(m, tail[i]);
-    bad = bad || tail[2 * kCols] != 0.0f;
-  }
-  m = column_max(m);
-  bad = __builtin_amdgcn_ballot_w64(bad) != 0;
-  float l = 0.0f, sum[S::kCW];
+  float m = -INFINITY, l = 0.0f, sum[S::kCW];
 #pragma unroll
   for (int c = 0; c < S::kCW; ++c) sum[c] = 0.0f;
 #pragma unroll 4
-  for (int p = wv; p < count; p += kAW) {
-    const float* part = part_of(w0 + p);
-    const float mp = part[S::kAcc * 4 * 64 + i];
-    const float f = mp == m ? 1.0f : exp2_fast((mp - m) * P.c);
-    l += f * part[S::kAcc * 4 * 64 + kCols + i];
+  for (int p = wv; p < count; p += NW) {
+    const float* part = p == 0 ? first : first + (2 * p - 1) * size;   // workgroup w0 + p, its first one
+    const float* tail = part + S::kAcc * 4 * 64;
+    const float mp = tail[i], lp = tail[kCols + i];
+    bad = bad || tail[2 * kCols] != 0.0f;
+    const float grown = fmaxf(m, mp);
+    const float f = m == grown ? 1.0f : exp2_fast((m - grown) * P.c), fp = mp == grown ? 1.0f : exp2_fast((mp - grown) * P.c);
+    m = grown;
+    l = l * f + lp * fp;
 #pragma unroll
-    for (int c = 0; c < S::kCW; ++c) sum[c] += f * part[(x * S::kCW + c) * 64 + lane()];
+    for (int c = 0; c < S::kCW; ++c) sum[c] = sum[c] * f + part[(x * S::kCW + c) * 64 + lane()] * fp;
   }
+  bar();
+  if (__builtin_amdgcn_ballot_w64(bad)) any_bad = 1;
+  sm_m[wv][lane()] = m;
   sm_l[wv][lane()] = l;
 #pragma unroll
   for (int c = 0; c < S::kCW; ++c) sm_o[wv][c][lane()] = sum[c];
   bar();
   if (wv != 0) return;
+#pragma unroll 4
+  for (int w = 1; w < NW; ++w) m = fmaxf(m, sm_m[w][lane()]);
+  l = 0.0f;
 #pragma unroll
-  for (int w = 1; w < kAW; ++w) {
-    l += sm_l[w][lane()];
+  for (int c = 0; c < S::kCW; ++c) sum[c] = 0.0f;
+#pragma unroll 4
+  for (int w = 0; w < NW; ++w) {
+    const float mw = sm_m[w][lane()], f = mw == m ? 1.0f : exp2_fast((mw - m) * P.c);
+    l += f * sm_l[w][lane()];
 #pragma unroll
-    for (int c = 0; c < S::kCW; ++c) sum[c] += sm_o[w][c][lane()];
+    for (int c = 0; c < S::kCW; ++c) sum[c] += f * sm_o[w][c][lane()];
   }
-  const int status = span.status != TS_ROW_OK ? span.status : bad ? TS_ROW_BAD_PAGE : TS_ROW_OK;
+  const int status = span.status != TS_ROW_OK ? span.status : any_bad ? TS_ROW_BAD_PAGE : TS_ROW_OK;
 #pragma unroll
   for (int c = 0; c < S::kCW; ++c) sum[c] = status != TS_ROW_OK ? NAN : l == 0.0f ? 0.0f : sum[c] * (1.0f / l);
   if (i < R.heads)
@@ -692,8 +765,11 @@ __global__ __launch_bounds__(kWT) void ts_attend_weights_kernel(const AParams P,
 }
 
 // ------------------------------------------------------------------ host side
-constexpr int kMinShare = 16;      // tiles: less is not worth a part
-constexpr int kGroupsMax = 512;   // workgroups of the pass: two a compute unit
+constexpr unsigned kWideJoin = 512;   // workgroups of the join that have 16 waves: few rows have many parts each
+#ifndef KG
+#define KG 512
+#endif
+constexpr int kGroupsMax = KG;   // workgroups of the pass: two a compute unit
 
 int dtype_size(int dtype) {
   return dtype == TS_DTYPE_F32 ? 4 : (dtype == TS_DTYPE_BF16 || dtype == TS_DTYPE_F16) ? 2 : 0;
@@ -737,10 +813,10 @@ bool attend_plan(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t dim, 
   return true;
 }
 
-template <int DT, int DP, bool FULL, bool UNI>
+template <int DT, int DP, int MODE, bool UNI>
 void launch_attend(const AParams& P, int64_t rows, hipStream_t s) {
   const unsigned grid = P.whole ? (unsigned)rows : (unsigned)kGroupsMax;
-  hipLaunchKernelGGL((ts_attend_kernel<DT, DP, FULL, UNI>), dim3(grid), dim3(kAT), 0, s, P);
+  hipLaunchKernelGGL((ts_attend_kernel<DT, DP, MODE, UNI>), dim3(grid), dim3(kAT), 0, s, P);
 }
 
 template <int DT, int DP>
@@ -748,14 +824,19 @@ hipError_t launch_type(AParams& P, int64_t rows, hipStream_t s) {
   static_assert(kPartFloats<DT, DP> == DP * 16 + 2 * kCols + 64, "a part's size");
   const bool uni = P.page_slots % 16 == 0;
   if (P.dim == DP) {
-    if (uni) launch_attend<DT, DP, true, true>(P, rows, s);
-    else launch_attend<DT, DP, true, false>(P, rows, s);
-  } else {
-    launch_attend<DT, DP, false, false>(P, rows, s);
+    if (uni) launch_attend<DT, DP, kFull, true>(P, rows, s);
+    else launch_attend<DT, DP, kFull, false>(P, rows, s);
+  } else if (!P.tiny) {
+    if (uni) launch_attend<DT, DP, kPart, true>(P, rows, s);
+    else launch_attend<DT, DP, kPart, false>(P, rows, s);
+  } else if constexpr (DP == 64) {
+    launch_attend<DT, DP, kTiny, false>(P, rows, s);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || P.whole) return e;
-  hipLaunchKernelGGL((ts_attend_join_kernel<DT, DP>), dim3((unsigned)(rows * Shape<DT, DP>::kNP * 4)), dim3(kAT), 0, s, P);
+  const dim3 grid((unsigned)(rows * Shape<DT, DP>::kNP * 4));
+  if (grid.x <= kWideJoin) hipLaunchKernelGGL((ts_attend_join_kernel<DT, DP, 16>), grid, dim3(1024), 0, s, P);
+  else hipLaunchKernelGGL((ts_attend_join_kernel<DT, DP, 4>), grid, dim3(256), 0, s, P);
   return hipGetLastError();
 }
 template <int DT>
@@ -877,8 +958,8 @@ extern "C" int ts_cache_attend(const void* q, int dtype, int64_t batch, int32_t 
   P.start = reinterpret_cast<int64_t*>(ws + pl.off_start);
   P.part = reinterpret_cast<float*>(ws + pl.off_part);
   P.whole = pl.whole ? 1 : 0;
-  P.min_share = kMinShare;
   P.tiny = dim * size < 16;
+  P.end_block = dim * size % 16 ? dim * size / 64 : -1;
   const hipStream_t s = (hipStream_t)stream;
   hipError_t e = dtype == TS_DTYPE_F32    ? launch_dim<TS_DTYPE_F32>(P, pl.rows, s)
                  : dtype == TS_DTYPE_BF16 ? launch_dim<TS_DTYPE_BF16>(P, pl.rows, s)
