@@ -21,10 +21,10 @@
 // cancel. fp16's P carries a factor of 2^15, so that weights down to 2^-39 of the largest stay above fp16's smallest number.
 // m, sums and outputs are fp32.
 //
-// The work is the list of all rows' tiles (a row: 16 query heads of a sequence), cut into equal shares, one for each
-// workgroup that the chip holds at once: ragged batches and few long rows fill it alike. A row that lies in one share is
-// finished there; the parts of others are joined by a second kernel (a row has at most two workgroups' parts that are not
-// whole shares).
+// The work is the list of all rows' tiles (a row: 16 query heads of a sequence), cut into equal stretches, one for each wave that
+// the chip holds at once: ragged batches and few long rows fill it alike, and waves wait for each other once, at the
+// end. A row that lies in one stretch is finished by its wave, one that lies in a workgroup's stretches by the workgroup;
+// the workgroups' parts of others (at most two a workgroup) are joined by a second kernel.
 #include <algorithm>
 #include <type_traits>
 #include <utility>
@@ -269,6 +269,12 @@ struct Wave {
       load_piece<16>(to[c], at);
     }
   }
+  __device__ __forceinline__ void clear_state() {
+    m = -INFINITY;
+    l = 0.0f;
+#pragma unroll
+    for (int a = 0; a < S::kAcc; ++a) o[a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
   __device__ __forceinline__ void load_q(const AParams& P, int b, int head0, int heads) {
     const int i = lane() & 15;
     load_row(P, q, P.q + b * P.q_b + (int64_t)(head0 + min(i, heads - 1)) * P.q_h);
@@ -431,50 +437,45 @@ __device__ __forceinline__ void store_norm(const AParams& P, const RowOut& R, fl
 }
 
 // ------------------------------------------------------------------ the pass over the cache
-// A stretch of a row's tiles that one workgroup goes through.
-struct Segment {
-  int32_t index, b, r;           // r: the sequence's row
+// A tile of a row, and how many are left of a wave's stretch, this one included.
+struct Cursor {
+  int32_t b, r;                  // sequence and its row
   int32_t lo, n, tiles;          // of the sequence
-  int32_t tile, todo;            // the first of the row's tiles, and how many
-  int64_t left;                  // tiles of the workgroup's share from here on
+  int32_t tile;                  // of the row
+  int64_t left;
 };
 template <int TOK>
-__device__ __forceinline__ void segment_at(const AParams& P, Segment& s, int b) {
+__device__ __forceinline__ void enter(const AParams& P, Cursor& c, int b) {
   const Span span = span_of(P, b);
-  s.b = b;
-  s.lo = span.lo;
-  s.n = span.n;
-  s.tiles = tiles_of<TOK>(span);
-  s.todo = P.whole ? s.tiles : (int32_t)min((int64_t)(s.tiles - s.tile), s.left);
+  c.b = b;
+  c.lo = span.lo;
+  c.n = span.n;
+  c.tiles = tiles_of<TOK>(span);
 }
 template <int TOK>
-__device__ __forceinline__ bool next_segment(const AParams& P, Segment& s) {
-  s.left -= s.todo;
-  if (P.whole || s.left <= 0) return false;   // the row is then finished: the share goes on past it
-  ++s.index;
-  s.tile = 0;
-  if (++s.r < rows_of(P)) {
-    s.todo = (int32_t)min((int64_t)s.tiles, s.left);
-    return true;
-  }
-  s.r = 0;
+__device__ __forceinline__ bool advance(const AParams& P, Cursor& c) {
+  if (--c.left <= 0) return false;
+  if (++c.tile < c.tiles) return true;
+  c.tile = 0;
+  if (++c.r < rows_of(P)) return true;
+  c.r = 0;
   do {
-    segment_at<TOK>(P, s, s.b + 1);
-  } while (s.tiles == 0);
+    enter<TOK>(P, c, c.b + 1);
+  } while (c.tiles == 0);   // there are tiles left, so a sequence with some follows
   return true;
 }
-// The share's first segment: every wave adds up the tiles of all sequences by itself (lane x takes a stretch of them), so that no
-// barrier stands before the first loads.
+// The wave's stretch of the list of all tiles. Every wave adds up the tiles of all sequences by itself (lane x takes some
+// sequences in a row), so that no barrier stands before the first loads.
 template <int TOK>
-__device__ __forceinline__ bool first_segment(const AParams& P, Segment& s) {
+__device__ __forceinline__ bool begin(const AParams& P, int wv, Cursor& c) {
   const int rows = rows_of(P), own = (P.batch + 63) / 64, first = min(P.batch, lane() * own), last = min(P.batch, first + own);
   uint64_t sum = 0;
   for (int x = first; x < last; ++x) sum += (uint64_t)tiles_of<TOK>(span_of(P, x)) * rows;
   const uint64_t incl = wave_incl_scan64(sum), total = readlane64(incl, 63);
-  int64_t share = ((int64_t)total + gridDim.x - 1) / gridDim.x;
-  share = (max(share, (int64_t)1) + kAW - 1) / kAW * kAW;
-  const int64_t pos = blockIdx.x * share;
-  if (blockIdx.x == 0 && threadIdx.x < 64) {
+  const int64_t groups = gridDim.x * (int64_t)kAW;
+  const int64_t stretch = max(((int64_t)total + groups - 1) / groups, (int64_t)1);
+  const int64_t pos = (blockIdx.x * (int64_t)kAW + wv) * stretch;
+  if (blockIdx.x == 0 && wv == 0) {
     int64_t at = (int64_t)(incl - sum);
     for (int x = first; x < last; ++x) {
       P.start[x] = at;
@@ -482,7 +483,7 @@ __device__ __forceinline__ bool first_segment(const AParams& P, Segment& s) {
     }
     if (lane() == 0) {
       P.start[P.batch] = (int64_t)total;
-      P.start[P.batch + 1] = share;
+      P.start[P.batch + 1] = stretch * kAW;
     }
   }
   if (pos >= (int64_t)total) return false;
@@ -490,163 +491,202 @@ __device__ __forceinline__ bool first_segment(const AParams& P, Segment& s) {
   const int l = __builtin_ctzll(past);
   int64_t in = pos - (int64_t)readlane64(incl - sum, l);
   int b = l * own;
-  int32_t tiles;
   for (;; ++b) {
-    tiles = tiles_of<TOK>(span_of(P, b));
-    if (in < (int64_t)tiles * rows) break;
-    in -= (int64_t)tiles * rows;
+    const int64_t n = (int64_t)tiles_of<TOK>(span_of(P, b)) * rows;
+    if (in < n) break;
+    in -= n;
   }
-  s.index = 0;
-  s.left = min(share, (int64_t)total - pos);
-  s.r = (int)(in / tiles);
-  s.tile = (int32_t)(in - (int64_t)s.r * tiles);
-  segment_at<TOK>(P, s, b);
+  enter<TOK>(P, c, b);
+  c.left = min(stretch, (int64_t)total - pos);
+  c.r = (int)(in / c.tiles);
+  c.tile = (int32_t)(in - (int64_t)c.r * c.tiles);
   return true;
 }
+
+// What a wave leaves for its workgroup of a row that it has a part of.
+struct Part {
+  int32_t b, r;                  // b < 0: none
+  int32_t begins, ends, bad;
+};
 
 template <int DT, int DP, int MODE, bool UNI>
 __global__ __launch_bounds__(kAT, DP > 128 ? 1 : 2) void ts_attend_kernel(const AParams P) {
   using S = Shape<DT, DP>;
   constexpr int TOK = S::kTok;
-  __shared__ float sm_o[kAW][S::kAcc * 4][64];
-  __shared__ float sm_m[kAW][kCols], sm_l[kAW][kCols];
-  __shared__ int any_bad[2];
+  // A wave has at most two rows in part: the one that its stretch starts in and the one that it ends in.
+  __shared__ float sm_o[kAW * 2][S::kAcc * 4][64];
+  __shared__ float sm_m[kAW * 2][kCols], sm_l[kAW * 2][kCols];
+  __shared__ Part sm_part[kAW * 2];
   const int wv = __builtin_amdgcn_readfirstlane(wave()), g = lane() >> 4, i = lane() & 15;
-  Segment cur;
+  Cursor c;
+  bool have;
   if (P.whole) {
     const int rows = rows_of(P), b = blockIdx.x / (unsigned)rows;
-    cur.index = 0;
-    cur.r = blockIdx.x - b * rows;
-    cur.tile = 0;
-    cur.left = 1;
-    segment_at<TOK>(P, cur, b);
-  } else if (!first_segment<TOK>(P, cur)) {
-    return;
+    enter<TOK>(P, c, b);
+    c.r = blockIdx.x - b * rows;
+    const int own = (c.tiles + kAW - 1) / kAW;
+    c.tile = wv * own;
+    c.left = min(own, c.tiles - c.tile);
+    have = c.left > 0;
+    if (c.tiles == 0) {   // no positions, or none that the table could hold
+      const int status = span_of(P, b).status;
+      const RowOut R = row_out(P, b, c.r);
+      float x[S::kCW];
+#pragma unroll
+      for (int e = 0; e < S::kCW; ++e) x[e] = status == TS_ROW_OK ? 0.0f : NAN;
+      for (int y = wv; y < S::kNP * 4; y += kAW)
+        if (i < R.heads)
+          store_dims<DT, S::kCW>(P.out + b * P.out_b + (int64_t)(R.head0 + i) * P.out_h,
+                                 (y >> 2) * 16 * S::kCW + (g * 4 + (y & 3)) * S::kCW, P.dim, P.tiny, x);
+      if (wv == 0) {
+        store_norm(P, R, -INFINITY, 0.0f, S::kBias, status);
+        if (P.status && lane() == 0) P.status[b] = status;
+      }
+      return;
+    }
+  } else {
+    have = begin<TOK>(P, wv, c);
   }
+  if (lane() < 2) sm_part[wv * 2 + lane()].b = -1;
   Wave<DT, DP, MODE, UNI> W;
   W.prepare(P);
   Place<S::kHalves, UNI> at;
-  // What this wave has loaded, or is about to: tile t of segment `ahead`, which may lie past the one that is worked on.
-  Segment ahead = cur;
-  int t = wv;                    // counted from the segment's first tile
-  bool bad = false;
-  auto settle = [&](Segment& s, int& tile) {
-    while (tile >= s.todo) {
-      if (!next_segment<TOK>(P, s)) return false;
-      tile = wv;
-    }
-    return true;
+  auto position = [&](const Cursor& c) { return (c.lo / TOK + c.tile) * TOK; };
+  auto find = [&](const Cursor& c, bool& bad) {
+    at.find(P, P.table + (int64_t)c.b * P.table_stride, position(c), c.lo, c.n, bad);
   };
-  auto position = [&](const Segment& s, int tile) { return (s.lo / TOK + s.tile + tile) * TOK; };
-  auto find = [&](const Segment& s, int tile) {
-    at.find(P, P.table + (int64_t)s.b * P.table_stride, position(s, tile), s.lo, s.n, bad);
+  auto load_q = [&](const Cursor& c) {
+    const RowOut R = row_out(P, c.b, c.r);
+    W.load_q(P, c.b, R.head0, R.heads);
   };
-  auto load_q = [&](const Segment& s) {
-    const RowOut R = row_out(P, s.b, s.r);
-    W.load_q(P, s.b, R.head0, R.heads);
-  };
-  auto load_k = [&](const Segment& s, int tile) {
-    W.load_k(P, P.k + (s.r / P.head_tiles) * P.k_head, at, position(s, tile), s.lo, s.n);
-  };
-  auto load_v = [&](const Segment& s, int tile) {
-    W.load_v(P, P.v + (s.r / P.head_tiles) * P.v_head, at, position(s, tile), s.lo, s.n);
-  };
-  if (threadIdx.x < 2) any_bad[threadIdx.x] = 0;
-  bool have = settle(ahead, t), spoils = false;   // spoils: a page of the segments up to `ahead` was bad, and of which
+  auto load_k = [&](const Cursor& c) { W.load_k(P, P.k + (c.r / P.head_tiles) * P.k_head, at, position(c), c.lo, c.n); };
+  auto load_v = [&](const Cursor& c) { W.load_v(P, P.v + (c.r / P.head_tiles) * P.v_head, at, position(c), c.lo, c.n); };
+  bool bad = false;              // a page of the row so far was outside the cache
+  int32_t begins = 1;            // the row's first tile was this wave's
   if (have) {
-    find(ahead, t);
-    load_q(ahead);
-    load_k(ahead, t);
-    load_v(ahead, t);
+    find(c, bad);
+    load_q(c);
+    load_k(c);
+    load_v(c);
+    begins = c.tile == 0;
+    W.clear_state();
   }
-  for (;;) {
-    const RowOut R = row_out(P, cur.b, cur.r);
-    const int lo = cur.lo, n = cur.n;
-    W.m = -INFINITY;
-    W.l = 0.0f;
-#pragma unroll
-    for (int a = 0; a < S::kAcc; ++a) W.o[a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    spoils = false;
-    while (have && ahead.index == cur.index) {
-      const int first = position(cur, t);
-      spoils = spoils || bad;
-      bad = false;
-      Segment next = ahead;
-      int u = t + kAW;
-      have = settle(next, u);
-      f32x4 s[S::kHalves];
-      if (have) find(next, u);
-      W.scores(P, s);
-      if (have) {   // into the registers that the products have read
-        if (next.index != ahead.index) load_q(next);
-        load_k(next, u);
-      }
-      if (first < lo || first + TOK > n) W.mask(s, first, lo, n);
-      if (P.score && i < R.heads) {
-        float* to = P.score + ((int64_t)cur.b * P.q_heads + R.head0 + i) * P.score_stride + first + g * 4;
+  while (have) {
+    const int first = position(c);
+    Cursor next = c;
+    have = advance<TOK>(P, next);
+    const bool ends = c.tile + 1 == c.tiles, other = ends || !have;   // the row, or this wave's part of it, ends here
+    bool next_bad = false;
+    f32x4 s[S::kHalves];
+    if (have) find(next, next_bad);
+    W.scores(P, s);
+    if (have) {   // into the registers that the products have read
+      if (ends) load_q(next);
+      load_k(next);
+    }
+    if (first < c.lo || first + TOK > c.n) W.mask(s, first, c.lo, c.n);
+    if (P.score) {
+      const RowOut R = row_out(P, c.b, c.r);
+      float* to = P.score + ((int64_t)c.b * P.q_heads + R.head0 + i) * P.score_stride + first + g * 4;
+      if (i < R.heads) {
 #pragma unroll
         for (int h = 0; h < S::kHalves; ++h) *reinterpret_cast<f32x4*>(to + 16 * h) = s[h];
       }
-      W.weigh(s, P.c);
-      W.accumulate(s);
-      if (have) load_v(next, u);
-      ahead = next;
-      t = u;
     }
-    // join the waves
-    const float l_wave = column_sum(W.l);
-    if (lane() < kCols) {
-      sm_m[wv][i] = W.m;
-      sm_l[wv][i] = l_wave;
+    W.weigh(s, P.c);
+    W.accumulate(s);
+    if (have) load_v(next);
+    if (other) {
+      const float l = column_sum(W.l);
+      const bool spoilt = __builtin_amdgcn_ballot_w64(bad) != 0;
+      if (begins && ends) {      // the row is this wave's alone
+        const RowOut R = row_out(P, c.b, c.r);
+        const float inv = spoilt ? NAN : l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+        for (int x = 0; x < S::kNP * 4; ++x) {
+          float y[S::kCW];
+#pragma unroll
+          for (int e = 0; e < S::kCW; ++e) y[e] = !spoilt && l == 0.0f ? 0.0f : W.o[(x >> 2) * S::kCW + e][x & 3] * inv;
+          if (i < R.heads)
+            store_dims<DT, S::kCW>(P.out + c.b * P.out_b + (int64_t)(R.head0 + i) * P.out_h,
+                                   (x >> 2) * 16 * S::kCW + (g * 4 + (x & 3)) * S::kCW, P.dim, P.tiny, y);
+        }
+        store_norm(P, R, W.m, l, S::kBias, spoilt ? TS_ROW_BAD_PAGE : TS_ROW_OK);
+        if (P.status && lane() == 0) P.status[c.b] = spoilt ? TS_ROW_BAD_PAGE : TS_ROW_OK;   // every row of a sequence finds the same
+      } else {
+        const int slot = wv * 2 + begins;
+        if (lane() < kCols) {
+          sm_m[slot][i] = W.m;
+          sm_l[slot][i] = l;
+        }
+        if (lane() == 0) sm_part[slot] = Part{c.b, c.r, begins, ends, spoilt};
+#pragma unroll
+        for (int x = 0; x < S::kNP * 4; ++x)
+#pragma unroll
+          for (int e = 0; e < S::kCW; ++e) sm_o[slot][x * S::kCW + e][lane()] = W.o[(x >> 2) * S::kCW + e][x & 3];
+      }
+      W.clear_state();
+      begins = 1;
+      bad = false;
     }
-    if (__builtin_amdgcn_ballot_w64(spoils)) any_bad[cur.index & 1] = 1;
+    bad = bad || next_bad;
+    c = next;
+  }
+  bar();
+  // Parts of one row follow each other.
+  for (int k = 0; k < kAW * 2;) {
+    const Part head = sm_part[k];
+    if (head.b < 0) {
+      ++k;
+      continue;
+    }
+    int end = k + 1, ends = head.ends, spoilt = head.bad;
+    float m = sm_m[k][i];
+    for (int j = k + 1; j < kAW * 2; ++j) {
+      const Part p = sm_part[j];
+      if (p.b < 0) continue;
+      if (p.b != head.b || p.r != head.r) break;
+      m = fmaxf(m, sm_m[j][i]);
+      ends = p.ends;
+      spoilt |= p.bad;
+      end = j + 1;
+    }
+    const bool complete = head.begins && ends;
+    float l = 0.0f, sum[S::kNP][S::kCW];
 #pragma unroll
     for (int p = 0; p < S::kNP; ++p)
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
+      for (int e = 0; e < S::kCW; ++e) sum[p][e] = 0.0f;
+    for (int j = k; j < end; ++j) {
+      if (sm_part[j].b < 0) continue;
+      const float mj = sm_m[j][i], f = mj == m ? 1.0f : exp2_fast((mj - m) * P.c);   // also where both are -inf: no sum there but 0 or NaN
+      l += f * sm_l[j][i];
 #pragma unroll
-        for (int c = 0; c < S::kCW; ++c) sm_o[wv][(p * 4 + x) * S::kCW + c][lane()] = W.o[p * S::kCW + c][x];
-    bar();
-    float m = -INFINITY, l = 0.0f, f[kAW];
+      for (int p = 0; p < S::kNP; ++p)
 #pragma unroll
-    for (int w = 0; w < kAW; ++w) m = fmaxf(m, sm_m[w][i]);
-#pragma unroll
-    for (int w = 0; w < kAW; ++w) {
-      const float mw = sm_m[w][i], lw = sm_l[w][i];
-      f[w] = mw == m ? 1.0f : exp2_fast((mw - m) * P.c);   // also where both are -inf: that wave's sums are 0 or NaN
-      l += f[w] * lw;
+        for (int e = 0; e < S::kCW; ++e) sum[p][e] += f * sm_o[j][(p * 4 + wv) * S::kCW + e][lane()];
     }
-    const bool spoilt = any_bad[cur.index & 1] != 0;
-    const bool complete = cur.todo == cur.tiles;
-    int status = spoilt ? TS_ROW_BAD_PAGE : TS_ROW_OK;
-    if (cur.tiles == 0) status = span_of(P, cur.b).status;
-    float* part = P.part + ((int64_t)blockIdx.x * 2 + (cur.tile == 0 ? 1 : 0)) * kPartFloats<DT, DP>;
-    const float inv = status != TS_ROW_OK ? NAN : l == 0.0f ? 0.0f : 1.0f / l;
+    const int status = spoilt ? TS_ROW_BAD_PAGE : TS_ROW_OK;
+    const RowOut R = row_out(P, head.b, head.r);
+    float* part = P.part + ((int64_t)blockIdx.x * 2 + head.begins) * kPartFloats<DT, DP>;
+    const float inv = spoilt ? NAN : l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
-    for (int x0 = 0; x0 < S::kNP * 4; x0 += kAW) {
-      const int x = x0 + wv;   // pass x / 4, row x % 4 of the results
-      float sum[S::kCW];
-#pragma unroll
-      for (int c = 0; c < S::kCW; ++c) {
-        sum[c] = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kAW; ++w) sum[c] += f[w] * sm_o[w][x * S::kCW + c][lane()];
-      }
+    for (int p = 0; p < S::kNP; ++p) {   // wave x: row x of the results
       if (complete) {
 #pragma unroll
-        for (int c = 0; c < S::kCW; ++c) sum[c] = status == TS_ROW_OK && l == 0.0f ? 0.0f : sum[c] * inv;
+        for (int e = 0; e < S::kCW; ++e) sum[p][e] = !spoilt && l == 0.0f ? 0.0f : sum[p][e] * inv;
         if (i < R.heads)
-          store_dims<DT, S::kCW>(P.out + cur.b * P.out_b + (int64_t)(R.head0 + i) * P.out_h,
-                                 (x >> 2) * 16 * S::kCW + (g * 4 + (x & 3)) * S::kCW, P.dim, P.tiny, sum);
+          store_dims<DT, S::kCW>(P.out + head.b * P.out_b + (int64_t)(R.head0 + i) * P.out_h, p * 16 * S::kCW + (g * 4 + wv) * S::kCW,
+                                 P.dim, P.tiny, sum[p]);
       } else {
 #pragma unroll
-        for (int c = 0; c < S::kCW; ++c) part[(x * S::kCW + c) * 64 + lane()] = sum[c];
+        for (int e = 0; e < S::kCW; ++e) part[((p * 4 + wv) * S::kCW + e) * 64 + lane()] = sum[p][e];
       }
     }
     if (wv == 0) {
       if (complete) {
         store_norm(P, R, m, l, S::kBias, status);
-        if (P.status && lane() == 0) P.status[cur.b] = status;   // every row of a sequence finds the same
+        if (P.status && lane() == 0) P.status[head.b] = status;
       } else {
         float* tail = part + S::kAcc * 4 * 64;
         if (lane() < kCols) {
@@ -656,10 +696,7 @@ __global__ __launch_bounds__(kAT, DP > 128 ? 1 : 2) void ts_attend_kernel(const 
         if (lane() == 0) tail[2 * kCols] = spoilt ? 1.0f : 0.0f;
       }
     }
-    const int index = cur.index;
-    if (!next_segment<TOK>(P, cur)) return;
-    bar();
-    if (threadIdx.x == 0) any_bad[index & 1] = 0;   // its next use is two segments on, past the next barrier
+    k = end;
   }
 }
 
@@ -766,10 +803,8 @@ __global__ __launch_bounds__(kWT) void ts_attend_weights_kernel(const AParams P,
 
 // ------------------------------------------------------------------ host side
 constexpr unsigned kWideJoin = 512;   // workgroups of the join that have 16 waves: few rows have many parts each
-#ifndef KG
-#define KG 512
-#endif
-constexpr int kGroupsMax = KG;   // workgroups of the pass: two a compute unit
+// Workgroups of the pass: as many as the chip holds at once, by their registers and LDS.
+constexpr int groups_of(int dp) { return dp == 64 ? 1024 : dp == 128 ? 512 : 256; }
 
 int dtype_size(int dtype) {
   return dtype == TS_DTYPE_F32 ? 4 : (dtype == TS_DTYPE_BF16 || dtype == TS_DTYPE_F16) ? 2 : 0;
@@ -807,7 +842,7 @@ bool attend_plan(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t dim, 
   if (!pl.whole) {
     pl.off_start = take((size_t)(batch + 2) * 8);
     const int dp = padded_dim((int)dim);
-    pl.off_part = take((size_t)kGroupsMax * 2 * (dp * 16 + 2 * kCols + 64) * 4);
+    pl.off_part = take((size_t)groups_of(dp) * 2 * (dp * 16 + 2 * kCols + 64) * 4);
   }
   pl.total = at;
   return true;
@@ -815,7 +850,7 @@ bool attend_plan(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t dim, 
 
 template <int DT, int DP, int MODE, bool UNI>
 void launch_attend(const AParams& P, int64_t rows, hipStream_t s) {
-  const unsigned grid = P.whole ? (unsigned)rows : (unsigned)kGroupsMax;
+  const unsigned grid = P.whole ? (unsigned)rows : (unsigned)groups_of(DP);
   hipLaunchKernelGGL((ts_attend_kernel<DT, DP, MODE, UNI>), dim3(grid), dim3(kAT), 0, s, P);
 }
 
