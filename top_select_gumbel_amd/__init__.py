@@ -604,22 +604,24 @@ class _Paged(ctypes.Structure):
 
 
 def _paged(t, dtype, device, name: str):
-    """The ts_paged of a [pages, heads, slots, dim] tensor whose last dimension is contiguous."""
-    if t.dtype is not dtype or t.dim() != 4 or t.device != device:
+    """(the ts_paged of a [pages, heads, slots, dim] tensor whose last dimension is contiguous, its shape)."""
+    shape = t.shape
+    if t.dtype is not dtype or len(shape) != 4 or t.device != device:
         raise TopSelectError(f"{name} must be a [pages, kv_heads, slots, dim] tensor of {dtype} on {device}")
     p, h, s, d = t.stride()
-    if t.shape[3] > 1 and d != 1:
+    if d != 1 and shape[3] > 1:
         raise TopSelectError(f"{name} must have a contiguous last dimension")
-    size = t.element_size()
-    return _Paged(t.data_ptr(), p * size, h * size, s * size)
+    size = dtype.itemsize
+    return _Paged(t.data_ptr(), p * size, h * size, s * size), shape
 
 
 def _page_table(table, device, name: str = "table"):
     """(rows, width, row stride) of an int32 table of page numbers."""
-    if table.dtype is not _torch.int32 or table.dim() != 2 or table.device != device:
+    shape = table.shape
+    if table.dtype is not _torch.int32 or len(shape) != 2 or table.device != device:
         raise TopSelectError(f"{name} must be an int32 [sequences, width] tensor on {device}")
-    (rows, width), (row, col) = table.shape, table.stride()
-    if rows and width > 1 and col != 1:
+    (rows, width), (row, col) = shape, table.stride()
+    if col != 1 and rows and width > 1:
         raise TopSelectError(f"{name} must have unit column stride")
     return rows, width, row if rows > 1 else width
 
@@ -641,18 +643,18 @@ def ts_cache_attend(q, k_pages, v_pages, table, lengths, scale: Optional[float] 
     scale: 1 / sqrt(dim) unless given. window: only the last `window` positions (0: all). weights_slots: the first so many
     positions' attention weights are returned too, in weights_dtype (the queries' type unless given); viewed as [batch * kv_heads,
     group, weights_slots] they are ts_cache_evict's `weights`. out: a tensor for the output, apart from q."""
-    torch = _t()
-    lib = load_library()
-    device, dtype = q.device, q.dtype
+    torch = _torch or _t()
+    lib = _lib or load_library()
+    device, dtype, shape = q.device, q.dtype, q.shape
     code = _DTYPES.get(dtype)
-    if code is None or not q.is_cuda or q.dim() != 3:
+    if code is None or not q.is_cuda or len(shape) != 3:
         raise TopSelectError("q must be a float32, bfloat16 or float16 [batch, q_heads, dim] CUDA/HIP tensor")
-    (b, hq, dim), (qb, qh, qd) = q.shape, q.stride()
-    if dim > 1 and qd != 1:
+    (b, hq, dim), (qb, qh, qd) = shape, q.stride()
+    if qd != 1 and dim > 1:
         raise TopSelectError("q must have a contiguous last dimension")
-    kp, vp = _paged(k_pages, dtype, device, "k_pages"), _paged(v_pages, dtype, device, "v_pages")
-    pages, hk, slots, kdim = k_pages.shape
-    if v_pages.shape != k_pages.shape or kdim != dim:
+    kp, (pages, hk, slots, kdim) = _paged(k_pages, dtype, device, "k_pages")
+    vp, vshape = _paged(v_pages, dtype, device, "v_pages")
+    if vshape != (pages, hk, slots, kdim) or kdim != dim:
         raise TopSelectError("k_pages and v_pages must have one shape, with q's dim")
     rows, width, table_stride = _page_table(table, device)
     if rows != b:
@@ -660,14 +662,16 @@ def ts_cache_attend(q, k_pages, v_pages, table, lengths, scale: Optional[float] 
     plen = _param(lengths, torch.int32, b, device, "lengths")
     if plen is None:
         raise TopSelectError("lengths is required")
+    empty = torch.empty
     if out is None:
-        out = torch.empty((b, hq, dim), dtype=dtype, device=device)
+        out = empty((b, hq, dim), dtype=dtype, device=device)
         ob, oh = hq * dim, dim
     else:
-        if out.dtype is not dtype or out.shape != q.shape or out.device != device or (dim > 1 and out.stride(2) != 1):
+        if out.dtype is not dtype or out.shape != shape or out.device != device or (dim > 1 and out.stride(2) != 1):
             raise TopSelectError("out must have q's shape, type and device and a contiguous last dimension")
         ob, oh, _ = out.stride()
-    (lse, status), (plse, pstatus) = _outputs(device, b * hq if want_lse else None, b)
+    status = torch.empty_like(lengths)
+    lse = empty((b, hq), dtype=torch.float32, device=device) if want_lse else None
     weights, pw, wcode, wb, wh = None, None, 0, 0, 0
     if weights_slots:
         weights_dtype = dtype if weights_dtype is None else weights_dtype
@@ -676,15 +680,15 @@ def ts_cache_attend(q, k_pages, v_pages, table, lengths, scale: Optional[float] 
             raise TopSelectError("weights_dtype must be float32, bfloat16 or float16")
         if weights_slots < 0:
             raise TopSelectError("weights_slots must not be negative")
-        weights = torch.empty((b, hq, weights_slots), dtype=weights_dtype, device=device)
+        weights = empty((b, hq, weights_slots), dtype=weights_dtype, device=device)
         pw, wb, wh = weights.data_ptr(), hq * weights_slots, weights_slots
     # a workspace of the call's own, as in ts_token_logp
     nb = lib.ts_cache_attend_workspace(b, hq, hk, dim, width * slots, weights_slots)
-    ws = torch.empty(nb, dtype=torch.uint8, device=device) if nb else None
+    ws = empty(nb, dtype=torch.uint8, device=device) if nb else None
     _call(device, lib.ts_cache_attend, q.data_ptr(), code, b, hq, hk, dim, qb, qh, ctypes.byref(kp), ctypes.byref(vp), pages, slots,
-          table.data_ptr(), width, table_stride, plen, dim ** -0.5 if scale is None else scale, window, out.data_ptr(), ob, oh, plse,
-          pw, wcode, weights_slots, wb, wh, pstatus, _ptr(ws), nb)
-    return CacheAttend(out, lse if lse is None else lse.view(b, hq), weights, status.view(torch.int32))
+          table.data_ptr(), width, table_stride, plen, dim ** -0.5 if scale is None else scale, window, out.data_ptr(), ob, oh,
+          lse.data_ptr() if want_lse else None, pw, wcode, weights_slots, wb, wh, status.data_ptr(), ws.data_ptr() if nb else None, nb)
+    return CacheAttend(out, lse, weights, status)
 
 
 def ts_cache_append(k_new, v_new, offsets, k_pages, v_pages, table, lengths):
@@ -692,31 +696,30 @@ def ts_cache_append(k_new, v_new, offsets, k_pages, v_pages, table, lengths):
 
     k_new, v_new [tokens, kv_heads, dim] of the pages' type (any); offsets int32 [batch + 1]: tokens offsets[b] .. offsets[b + 1]
     are the last positions of sequence b, whose length counts them already. k_pages, v_pages, table as in ts_cache_attend."""
-    torch = _t()
-    lib = load_library()
+    torch = _torch or _t()
+    lib = _lib or load_library()
     device, dtype = k_pages.device, k_pages.dtype
     if not k_pages.is_cuda:
         raise TopSelectError("k_pages must be a CUDA/HIP tensor")
-    kp, vp = _paged(k_pages, dtype, device, "k_pages"), _paged(v_pages, dtype, device, "v_pages")
-    pages, hk, slots, dim = k_pages.shape
-    if v_pages.shape != k_pages.shape:
+    kp, (pages, hk, slots, dim) = _paged(k_pages, dtype, device, "k_pages")
+    vp, vshape = _paged(v_pages, dtype, device, "v_pages")
+    if vshape != (pages, hk, slots, dim):
         raise TopSelectError("k_pages and v_pages must have one shape")
-    size, strides = k_pages.element_size(), []
+    size, strides, tokens = dtype.itemsize, [], k_new.shape[0]
     for t, name in ((k_new, "k_new"), (v_new, "v_new")):
-        if t.dtype is not dtype or t.dim() != 3 or t.device != device or t.shape[1] != hk or t.shape[2] != dim:
-            raise TopSelectError(f"{name} must be a [tokens, {hk}, {dim}] tensor of {dtype} on {device}")
-        if dim > 1 and t.stride(2) != 1:
+        if t.dtype is not dtype or t.shape != (tokens, hk, dim) or t.device != device:
+            raise TopSelectError(f"{name} must be a [{tokens}, {hk}, {dim}] tensor of {dtype} on {device}")
+        st, sh, sd = t.stride()
+        if sd != 1 and dim > 1:
             raise TopSelectError(f"{name} must have a contiguous last dimension")
-        strides += [t.stride(0) * size, t.stride(1) * size]
-    if v_new.shape[0] != k_new.shape[0]:
-        raise TopSelectError("k_new and v_new must have as many tokens")
+        strides += [st * size, sh * size]
     b, width, table_stride = _page_table(table, device)
     plen = _param(lengths, torch.int32, b, device, "lengths")
     poff = _param(offsets, torch.int32, b + 1, device, "offsets")
     if plen is None or poff is None:
         raise TopSelectError("offsets and lengths are required")
-    status = torch.empty(b, dtype=torch.int32, device=device)
-    _call(device, lib.ts_cache_append, k_new.data_ptr(), v_new.data_ptr(), k_new.shape[0], b, hk, dim * size, *strides, poff,
+    status = torch.empty_like(lengths)
+    _call(device, lib.ts_cache_append, k_new.data_ptr(), v_new.data_ptr(), tokens, b, hk, dim * size, *strides, poff,
           ctypes.byref(kp), ctypes.byref(vp), pages, slots, table.data_ptr(), width, table_stride, plen, status.data_ptr())
     return status
 
