@@ -214,7 +214,7 @@ struct ForkArgs {
   int32_t *out_table, *out_lengths, *out_refs, *status;
   int64_t table_stride, out_stride;
   int32_t seqs, children, table_width, out_width, pages, page_slots, max_len, out_max, tiles;
-  Divisor by_page;
+  Divisor by_page, by_width, by_out;   // the widths' for the one workgroup
   SeqInfo* seq;                 // [seqs]
   ChildInfo* child;             // [children]
   uint32_t* start;              // [children + 1]: fresh pages of the children before
@@ -398,13 +398,174 @@ __global__ __launch_bounds__(kPT) void ts_pages_back_kernel(const ForkArgs F) {
   }
 }
 
+// All of it by one workgroup, where that one goes through the counts and tables in less time than five launches take.
+constexpr int kOT = 1024, kOW = kOT / 64;    // its threads
+constexpr int kOneSeqs = kOT;                // most sequences, and children: one a thread
+// Most pages and table entries together. (Fork, pages + entries of both tables: 8000 + 6000 18 us against 32 with five launches,
+// 30000 + 32000 24 against 32, 60000 + 64000 36 against 32. Compaction: 8192 + 4500 201 against 208, most of it copies, 30000 +
+// 16000 34 against 25.)
+constexpr int64_t kOneFork = 1 << 16, kOneCompact = 1 << 14;
+static_assert(kOneFork <= 64 * kOT && kOneCompact <= 64 * kOT, "a count a thread for each chunk of 64 pages");
+
+// Sum over the workgroup of the values of the threads before this one, and of all.
+__device__ __forceinline__ uint32_t one_scan(uint32_t v, uint32_t* red, uint32_t& all) {
+  const uint32_t incl = wave_incl_scan(v);
+  if (lane() == 63) red[wave()] = incl;
+  bar();
+  uint32_t before = incl - v;
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < kOW; ++w) {
+    before += w < wave() ? red[w] : 0;
+    all += red[w];
+  }
+  bar();
+  return before;
+}
+// masks[c]: for which of the counts 64 c .. + 64 `test` holds; before[c]: for how many before those. Returns how many in all.
+template <class F>
+__device__ __forceinline__ uint32_t count_chunks(const int32_t* refs, int pages, uint64_t* masks, uint32_t* before, uint32_t* red, F test) {
+  const int chunks = (pages + 63) / 64;
+  for (int c0 = wave(); c0 < chunks; c0 += 8 * kOW) {
+    int32_t r[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) r[u] = refs[min((c0 + u * kOW) * 64 + lane(), pages - 1)];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int c = c0 + u * kOW;
+      const uint64_t m = __builtin_amdgcn_ballot_w64(c * 64 + lane() < pages && test(r[u]));
+      if (c < chunks && lane() == 0) masks[c] = m;
+    }
+  }
+  bar();
+  uint32_t all;
+  const int t = threadIdx.x;
+  before[t] = one_scan(t < chunks ? (uint32_t)__popcll(masks[t]) : 0u, red, all);
+  bar();
+  return all;
+}
+
+__global__ __launch_bounds__(kOT) void ts_pages_fork_one_kernel(const ForkArgs F) {
+  __shared__ int32_t children[kOneSeqs], length[kOneSeqs], parents[kOneSeqs];
+  __shared__ uint32_t first[kOneSeqs], bad[kOneSeqs], start[kOneSeqs + 1];
+  __shared__ ChildInfo info[kOneSeqs];
+  __shared__ uint64_t masks[kOT];
+  __shared__ uint32_t before_chunk[kOT], red[kOW];
+  const int t = threadIdx.x;
+  if (F.out_refs != F.refs) {
+#pragma unroll 8
+    for (int p = t; p < F.pages; p += kOT) F.out_refs[p] = F.refs[p];
+  }
+  children[t] = 0;
+  first[t] = 0xFFFFFFFFu;
+  bad[t] = 0;
+  length[t] = t < F.seqs ? F.lengths[t] : 0;
+  const int parent = t < F.children ? F.parent[t] : -1, grow = t < F.children && F.n_new ? F.n_new[t] : 0;
+  parents[t] = parent;
+  bar();
+  if (length[t] < 0 || length[t] > F.max_len) bad[t] = TS_ROW_BAD_LENGTH;
+  if (parent >= 0 && parent < F.seqs) {
+    atomicAdd(&children[parent], 1);
+    atomicMin(&first[parent], (uint32_t)t);
+  }
+  bar();
+#pragma unroll 8
+  for (int i = t; i < F.seqs * F.table_width; i += kOT) {
+    const int s = (int)F.by_width.of((uint32_t)i), x = i - s * F.table_width;
+    const int page = F.table[s * F.table_stride + x];
+    if (bad[s] != TS_ROW_BAD_LENGTH && x < pages_of(F.by_page, length[s]) && (uint32_t)page >= (uint32_t)F.pages) bad[s] = TS_ROW_BAD_PAGE;
+  }
+  bar_all();
+  ChildInfo C{0, 0, 0, 0, TS_ROW_OK};
+  if (t < F.children) {
+    if (parent < -1 || parent >= F.seqs) {
+      C.status = TS_ROW_BAD_PARENT;
+    } else if (parent >= 0) {
+      const int n = length[parent];
+      if (bad[parent]) C.status = (int32_t)bad[parent];
+      else if (n > F.out_max) C.status = TS_ROW_BAD_LENGTH;
+      else {
+        C.old = n;
+        C.copies = first[parent] != (uint32_t)t && (int)F.by_page.of(n) != pages_of(F.by_page, n);
+      }
+    }
+    C.grown = C.old;
+    if (C.status == TS_ROW_OK) {
+      if (grow < 0 || grow > F.out_max - C.old) C.status = TS_ROW_BAD_LENGTH;
+      else C.grown = C.old + grow;
+    }
+    C.need = (uint32_t)(C.copies + pages_of(F.by_page, C.grown) - pages_of(F.by_page, C.old));
+    info[t] = C;
+  }
+  uint32_t wanted, all;
+  const uint32_t mine = one_scan(C.need, red, wanted);
+  start[t] = mine;
+  if (t == 0) start[F.children] = wanted;   // of the threads past the children, too
+#pragma unroll 8
+  for (int i = t; i < F.seqs * F.table_width; i += kOT) {
+    const int s = (int)F.by_width.of((uint32_t)i), x = i - s * F.table_width, n = length[s];
+    const int heirs = n > F.out_max ? 0 : children[s], whole = bad[s] ? 0 : (int)F.by_page.of(n);
+    if (heirs == 1 || bad[s]) continue;
+    if (x < whole) atomicAdd(&F.out_refs[F.table[s * F.table_stride + x]], heirs - 1);
+    else if (heirs == 0 && x < pages_of(F.by_page, n)) atomicAdd(&F.out_refs[F.table[s * F.table_stride + x]], -1);
+  }
+#pragma unroll 8
+  for (int i = t; i < F.children * F.out_width; i += kOT) {
+    const int c = (int)F.by_out.of((uint32_t)i), x = i - c * F.out_width;
+    F.out_table[c * F.out_stride + x] = x < pages_of(F.by_page, info[c].old) ? F.table[parents[c] * F.table_stride + x] : -1;
+  }
+  bar_all();
+  // the free pages, in order: as many as are wanted
+  all = count_chunks(F.out_refs, F.pages, masks, before_chunk, red, [](int32_t r) { return r <= 0; });
+  for (int c = wave(); c < (F.pages + 63) / 64; c += kOW) {
+    if (before_chunk[c] >= wanted) break;
+    const uint32_t rank = before_chunk[c] + mbcnt(masks[c]);
+    const int page = c * 64 + lane();
+    if (!(masks[c] >> lane() & 1) || rank >= wanted) continue;
+    int lo = 0, hi = F.children;   // start[lo] <= rank < start[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (start[mid] <= rank) lo = mid;
+      else hi = mid;
+    }
+    const ChildInfo& I = info[lo];
+    if (start[lo] + I.need > all) continue;
+    const int k = (int)(rank - start[lo]) - I.copies, at = k < 0 ? (int)F.by_page.of(I.old) : pages_of(F.by_page, I.old) + k;
+    if (k < 0) {
+      F.source[lo] = F.table[parents[lo] * F.table_stride + at];
+      F.target[lo] = page;
+    }
+    F.out_table[lo * F.out_stride + at] = page;
+    F.out_refs[page] = 1;
+  }
+  bool empty = false;
+  if (t < F.children) {
+    const bool fits = mine + C.need <= all;
+    empty = !fits && C.copies;
+    F.out_lengths[t] = fits ? C.grown : empty ? 0 : C.old;
+    if (F.status) F.status[t] = C.status != TS_ROW_OK ? C.status : fits ? TS_ROW_OK : TS_ROW_NO_PAGE;
+    if (!(fits && C.copies)) F.source[t] = -1;
+    bad[t] = empty;
+  }
+  if (!__syncthreads_or(empty)) return;
+  for (int c = wave(); c < F.children; c += kOW) {   // what an emptied child would have shared is given back
+    if (!bad[c]) continue;
+    const int whole = (int)F.by_page.of(info[c].old);
+    int32_t* row = F.out_table + c * F.out_stride;
+    for (int x = lane(); x <= whole; x += 64) {
+      if (x < whole) atomicAdd(&F.out_refs[F.table[parents[c] * F.table_stride + x]], -1);
+      row[x] = -1;
+    }
+  }
+}
+
 // ------------------------------------------------------------------ compact
 struct CompactArgs {
   const int32_t *table, *lengths, *refs;
   int32_t *out_table, *out_refs, *map, *count, *status;
   int64_t table_stride, out_stride;
   int32_t seqs, table_width, pages, page_slots, max_len, tiles;
-  Divisor by_page;
+  Divisor by_page, by_width;
   uint32_t* tile_live;              // [tiles]
   int32_t *source, *target;         // [pages / 2]: what moves where
   int32_t* moves;                   // how many; pages in use
@@ -516,6 +677,70 @@ __global__ __launch_bounds__(kPT) void ts_pages_renumber_kernel(const CompactArg
     C.out_refs[src] = 0;
     __hip_atomic_store(&C.map[src], dst, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
+}
+
+// All but the copies by one workgroup, as for the fork.
+__global__ __launch_bounds__(kOT) void ts_pages_compact_one_kernel(const CompactArgs C) {
+  __shared__ uint64_t masks[kOT];
+  __shared__ uint32_t before_chunk[kOT], red[kOW];
+  __shared__ int32_t length[kOneSeqs], bad[kOneSeqs];
+  const int t = threadIdx.x, chunks = (C.pages + 63) / 64;
+  const uint32_t all = count_chunks(C.refs, C.pages, masks, before_chunk, red, [](int32_t r) { return r > 0; });
+  // pages in use below the count
+  const int cut = (int)(all / 64);
+  const uint32_t below = cut < chunks ? before_chunk[cut] + (uint32_t)__popcll(masks[cut] & (((uint64_t)1 << (all % 64)) - 1)) : all;
+  const bool in_place = C.out_refs == C.refs;
+#pragma unroll 4
+  for (int c = wave(); c < chunks; c += kOW) {
+    const int p = c * 64 + lane();
+    if (p >= C.pages) continue;
+    const bool is = masks[c] >> lane() & 1;
+    const uint32_t rank = before_chunk[c] + mbcnt(masks[c]);   // pages in use before this one
+    const int32_t r = in_place ? 0 : C.refs[p];
+    if (p < (int)all) {
+      C.map[p] = is ? p : -1;
+      if (!is) C.target[p - rank] = p;
+      else if (!in_place) C.out_refs[p] = r;
+    } else if (is) {
+      C.source[rank - below] = p;
+    } else {
+      C.map[p] = -1;
+      C.out_refs[p] = 0;
+    }
+  }
+  const int moves = (int)(all - below);
+  if (t == 0) {
+    C.moves[0] = moves;
+    if (C.count) *C.count = (int)all;
+  }
+  bar_all();
+#pragma unroll 4
+  for (int i = t; i < moves; i += kOT) {
+    const int src = C.source[i], dst = C.target[i];
+    C.map[src] = dst;
+    C.out_refs[dst] = C.refs[src];
+    C.out_refs[src] = 0;
+  }
+  bar_all();
+  length[t] = t < C.seqs ? C.lengths[t] : 0;
+  bad[t] = 0;
+  bar();
+#pragma unroll 4
+  for (int i = t; i < C.seqs * C.table_width; i += kOT) {
+    const int s = (int)C.by_width.of((uint32_t)i), x = i - s * C.table_width, n = length[s];
+    const bool sound = n >= 0 && n <= C.max_len;
+    const int page = C.table[s * C.table_stride + x];
+    int to = sound ? -1 : page;
+    if (sound && x < pages_of(C.by_page, n)) {
+      const int m = (uint32_t)page < (uint32_t)C.pages ? C.map[page] : -1;
+      if (m < 0) bad[s] = 1;
+      to = m < 0 ? page : m;
+    }
+    C.out_table[s * C.out_stride + x] = to;
+  }
+  bar();
+  if (t < C.seqs && C.status)
+    C.status[t] = length[t] < 0 || length[t] > C.max_len ? TS_ROW_BAD_LENGTH : bad[t] ? TS_ROW_BAD_PAGE : TS_ROW_OK;
 }
 
 // ------------------------------------------------------------------ host side
@@ -743,6 +968,8 @@ int ts_pages_fork(const int32_t* table, int64_t seqs, int64_t table_width, int64
   F.out_max = (int32_t)std::min<int64_t>(out_width * page_slots, tsp::kMaxLen);
   F.tiles = (int32_t)pl.tiles;
   F.by_page = Divisor(page_slots);
+  F.by_width = Divisor((int32_t)std::min<int64_t>(std::max<int64_t>(table_width, 1), kOneFork));
+  F.by_out = Divisor((int32_t)std::min<int64_t>(std::max<int64_t>(out_width, 1), kOneFork));
   F.seq = reinterpret_cast<SeqInfo*>(ws);
   F.child = reinterpret_cast<ChildInfo*>(ws + pl.off_child);
   F.start = reinterpret_cast<uint32_t*>(ws + pl.off_start);
@@ -750,6 +977,13 @@ int ts_pages_fork(const int32_t* table, int64_t seqs, int64_t table_width, int64
   F.source = reinterpret_cast<int32_t*>(ws + pl.off_source);
   F.target = reinterpret_cast<int32_t*>(ws + pl.off_target);
   const hipStream_t s = (hipStream_t)stream;
+  if (children > 0 && seqs <= kOneSeqs && children <= kOneSeqs && pages + seqs * table_width + children * out_width <= kOneFork) {
+    hipLaunchKernelGGL(ts_pages_fork_one_kernel, dim3(1), dim3(kOT), 0, s, F);
+    rc = launched("fork");
+    if (rc != TS_OK) return rc;
+    const hipError_t e = move_pages(pools, n_pools, F.source, F.target, nullptr, (int32_t)children, s);
+    return e == hipSuccess ? TS_OK : fail(TS_ERR_LAUNCH, "fork copy launch failed: %s", hipGetErrorString(e));
+  }
   const int64_t plan_grid = std::max<int64_t>({seqs, std::min<int64_t>(1024, pl.tiles), 1});
   hipLaunchKernelGGL(ts_pages_plan_kernel, dim3((unsigned)plan_grid), dim3(kPT), 0, s, F);
   rc = launched("fork plan");
@@ -815,11 +1049,19 @@ int ts_pages_compact(const int32_t* table, int64_t seqs, int64_t table_width, in
   C.max_len = (int32_t)std::min<int64_t>(table_width * page_slots, tsp::kMaxLen);
   C.tiles = (int32_t)pl.tiles;
   C.by_page = Divisor(page_slots);
+  C.by_width = Divisor((int32_t)std::min<int64_t>(std::max<int64_t>(table_width, 1), kOneFork));
   C.tile_live = reinterpret_cast<uint32_t*>(ws);
   C.source = reinterpret_cast<int32_t*>(ws + pl.off_source);
   C.target = reinterpret_cast<int32_t*>(ws + pl.off_target);
   C.moves = reinterpret_cast<int32_t*>(ws + pl.off_moves);
   const hipStream_t s = (hipStream_t)stream;
+  if (seqs <= kOneSeqs && pages + seqs * table_width <= kOneCompact) {
+    hipLaunchKernelGGL(ts_pages_compact_one_kernel, dim3(1), dim3(kOT), 0, s, C);
+    rc = launched("compact");
+    if (rc != TS_OK) return rc;
+    const hipError_t e = move_pages(pools, n_pools, C.source, C.target, C.moves, (int32_t)(pages / 2), s);
+    return e == hipSuccess ? TS_OK : fail(TS_ERR_LAUNCH, "compact copy launch failed: %s", hipGetErrorString(e));
+  }
   hipLaunchKernelGGL(ts_pages_live_kernel, dim3((unsigned)pl.tiles), dim3(kPT), 0, s, C);
   rc = launched("compact count");
   if (rc != TS_OK) return rc;
