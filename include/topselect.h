@@ -405,7 +405,7 @@ typedef struct ts_paged {   /* one layer's keys or values: slot s of page p unde
  * anything. NaN and infinities in attended keys and values act as in the formula (a non-finite value may give NaN where
  * the formula has an infinity). Sequences with a non-OK status get NaN. Scores, sums and outputs are fp32, rounded once; p_j below 2^-126 counts as 0; results
  * depend on the batch in their last bits only (the sums' order), and are the same bits for the same call.
- * Workspace: ts_cache_attend_workspace(..., max_len = table_width * page_slots, ...); it may be 0.
+ * Workspace: ts_cache_attend_workspace(..., max_len = table_width * page_slots, ...); it may be 0 (and the workspace NULL).
  */
 size_t ts_cache_attend_workspace(int64_t batch, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t max_len, int64_t weights_slots);
 int ts_cache_attend(const void* q, int dtype, int64_t batch, int32_t q_heads, int32_t kv_heads, int32_t dim,

@@ -24,7 +24,7 @@ def attend(lib, **kw):
     pages = ts._Paged(1 << 20, 4096, 1024, 64)
     return call(lib.ts_cache_attend, dict(
         q=FAKE, dtype=1, batch=3, q_heads=8, kv_heads=4, dim=32, q_b=256, q_h=32, k=pages, v=pages, pages=10, slots=16, table=FAKE,
-        width=20, stride=20, lengths=FAKE, scale=0.1, window=0, out=1 << 22, o_b=256, o_h=32, lse=None, weights=None, w_dtype=0,
+        width=200, stride=200, lengths=FAKE, scale=0.1, window=0, out=1 << 22, o_b=256, o_h=32, lse=None, weights=None, w_dtype=0,
         w_slots=0, w_b=0, w_h=0, status=None, ws=FAKE, ws_bytes=BIG), **kw)
 
 
@@ -33,7 +33,7 @@ def attend(lib, **kw):
     (dict(q_heads=0), "heads"), (dict(q_heads=-4), "heads"), (dict(q_heads=1 << 17), "q_heads"), (dict(dim=0), "dim"), (dict(dim=257), "dim"),
     (dict(scale=0.0), "scale"), (dict(scale=-1.0), "scale"), (dict(scale=float("nan")), "scale"), (dict(scale=float("inf")), "scale"),
     (dict(window=-1), "window"), (dict(pages=-1), "pages"), (dict(pages=1 << 31), "pages"), (dict(slots=0), "page_slots"),
-    (dict(width=-1), "table_width"), (dict(stride=19), "table_stride"), (dict(q=None), "NULL"), (dict(table=None), "NULL"),
+    (dict(width=-1), "table_width"), (dict(stride=199), "table_stride"), (dict(q=None), "NULL"), (dict(table=None), "NULL"),
     (dict(lengths=None), "NULL"), (dict(out=None), "NULL"), (dict(pages=0), "pages"), (dict(q=FAKE + 1), "aligned"),
     (dict(out=FAKE + 1), "aligned"), (dict(q_b=-1), "q:"), (dict(q_b=1 << 61), "q:"), (dict(o_h=31), "overlap"), (dict(o_b=255), "overlap"),
     (dict(o_b=-256), "overlap"), (dict(k=ts._Paged(None, 64, 64, 64)), "NULL"), (dict(k=None), "NULL"), (dict(v=None), "NULL"),
@@ -51,12 +51,14 @@ def test_attend_refusals(lib, kw, word):
 
 def test_attend_workspace(lib):
     assert attend(lib, batch=0, q=None, table=None, lengths=None, out=None, ws=None, ws_bytes=0) == ts.TS_OK
-    need = lib.ts_cache_attend_workspace(3, 8, 4, 32, 20 * 16, 0)
+    need = lib.ts_cache_attend_workspace(3, 8, 4, 32, 200 * 16, 0)
     assert need > 0 and need % 256 == 0
     assert attend(lib, ws=None) == ts.TS_ERR_WORKSPACE
     assert attend(lib, ws=FAKE + 16) == ts.TS_ERR_WORKSPACE
     assert attend(lib, ws_bytes=need - 1) == ts.TS_ERR_WORKSPACE and "needs" in ts.ts_last_error()
-    assert lib.ts_cache_attend_workspace(3, 8, 4, 32, 320, 100) > need
+    assert lib.ts_cache_attend_workspace(3, 8, 4, 32, 200 * 16, 200 * 16) > need
+    assert lib.ts_cache_attend_workspace(3, 8, 4, 32, 100, 0) == 0      # short sequences need none
+    assert attend(lib, width=6, stride=6, ws=None, ws_bytes=0, pages=0) == ts.TS_ERR_INVALID_ARG and "pages" in ts.ts_last_error()
     for bad in [(-1, 8, 4, 32, 9, 0), (1, 8, 3, 32, 9, 0), (1, 8, 0, 32, 9, 0), (1, 8, 4, 0, 9, 0), (1, 8, 4, 300, 9, 0), (1, 8, 4, 32, -1, 0),
                 (1, 8, 4, 32, 9, -1), (1 << 62, 8, 4, 32, 9, 0)]:
         assert lib.ts_cache_attend_workspace(*bad) == 0

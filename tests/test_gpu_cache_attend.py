@@ -387,3 +387,28 @@ def test_refusals_of_the_binding():
     refused(out=torch.empty(1, 6, 64, dtype=a["q"].dtype, device="cuda").expand(3, 6, 64))
     refused(q=torch.empty(3, 5, 64, dtype=a["q"].dtype, device="cuda"))
     assert not host(ts.ts_cache_attend(**a).status).any()
+
+
+@pytest.mark.parametrize("n", [511, 512, 513, 1000, 1024, 1025])
+def test_rows_of_one_workgroup_and_of_several(n):
+    rng = np.random.default_rng(n)
+    check(lengths=np.r_[n, rng.integers(0, n + 1, 3)], wtype="float32", hk=1, hq=5)
+    check(lengths=np.r_[n, rng.integers(0, n + 1, 130)], hk=2, hq=2, dim=16, dtype="float16")      # rows enough for the chip
+    check(lengths=[5 * n, n], window=n, hk=1, hq=2, dtype="float32")
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_batches(seed):
+    rng = np.random.default_rng(1000 + seed)
+    hk, group = int(rng.choice([1, 2, 3])), int(rng.choice([1, 2, 5, 16, 20]))
+    lengths = np.exp(rng.uniform(0, np.log(3000), int(rng.integers(1, 12)))).astype(int)
+    lengths[rng.random(len(lengths)) < 0.1] = 0
+    check(lengths=lengths, hk=hk, hq=hk * group, dim=int(rng.choice([5, 16, 64, 100, 128, 250])), slots=int(rng.choice([1, 7, 16, 48, 500])),
+          dtype=TYPES[seed % 3], window=int(rng.choice([0, 0, 40, 700])), wtype=[None, "float32", "bfloat16", "float16"][seed % 4],
+          seed=seed, slots_first=bool(seed & 1))
+
+
+def test_many_tiny_sequences_beside_long_ones():
+    """Rows of one tile each fall to a few waves; one row spans many workgroups."""
+    lengths = np.r_[np.arange(1, 60), 30000, np.ones(40, int), 12000]
+    check(lengths=lengths, hk=1, hq=3, dim=64, slots=16, dtype="bfloat16", wtype="float32")

@@ -447,3 +447,47 @@ def test_decode_with_shared_prompt_and_eviction():
     w = a.weights.double().view(rows, 2, -1).gather(2, position[:, :budget].long()[:, None].expand(-1, 2, -1))
     want = (w / w.sum(2, keepdim=True)) @ vd.double().view(rows, -1, dim)[:, :budget]
     assert float((after.out.double().view(rows, 2, dim) - want).abs().max()) < 6e-4
+
+
+# ---------------------------------------------------------------- caches past one workgroup
+@pytest.mark.parametrize("pages,seqs,width,in_place", [(70_000, 40, 30, False), (66_000, 3, 20_000, True), (5000, 1100, 8, False), (9000, 30, 5000, True)])
+def test_fork_by_several_launches(pages, seqs, width, in_place):
+    rng = np.random.default_rng(pages)
+    table, lengths, refs = sequences(rng, seqs, pages, 2, width, fill=0.6)
+    n = seqs + 7
+    check_fork(table, lengths, refs, rng.integers(-1, seqs, n), rng.integers(0, 5, n), 2, pools=1, page=(4, 2), in_place=in_place)
+    parent = np.where(np.arange(n) < seqs, np.arange(n), -1)
+    parent[0], parent[1] = -3, seqs
+    new = rng.integers(0, max(4, 4 * pages // n), n)                        # more than there are
+    new[2] = -1
+    check_fork(table, lengths, refs, parent, new, 2, pools=1, page=(4, 2), in_place=in_place)
+
+
+def test_fork_by_several_launches_with_too_few_pages_for_copies():
+    rng = np.random.default_rng(3)
+    table, lengths, refs = sequences(rng, 50, 1200, 4, 30, share=0.0, fill=1.0)
+    parent = np.sort(rng.integers(0, 50, 1500))
+    r = check_fork(table, lengths, refs, parent, np.zeros(1500, int), 4, pools=1, page=(4, 2))
+    st = host(r.status)
+    assert (st == ts.TS_ROW_NO_PAGE).any() and (st == 0).any()
+    table[3][0], table[7][1], lengths[9] = -1, 1 << 30, 1 << 20
+    lengths[3], lengths[7] = 8, 8
+    check_fork(table, lengths, refs, parent, np.ones(1500, int), 4, pools=1, page=(4, 2))
+
+
+@pytest.mark.parametrize("pages,seqs,width,in_place", [(20_000, 50, 100, False), (70_000, 20, 300, True), (300, 1100, 20, False), (40_000, 4, 6000, True)])
+def test_compact_by_several_launches(pages, seqs, width, in_place):
+    rng = np.random.default_rng(pages)
+    table, lengths, refs = sequences(rng, seqs, pages, 2, width, fill=0.5)
+    table[1][0], lengths[2] = -1, -1
+    check_compact(table, lengths, refs, 2, pools=1, page=(3, 7), in_place=in_place)
+
+
+@pytest.mark.parametrize("pages", [1, 63, 64, 65, 127, 128, 1000, 4096, 16384])
+@pytest.mark.parametrize("fill", [0.02, 0.5, 0.97])
+def test_compact_at_chunks_of_64_pages(pages, fill):
+    rng = np.random.default_rng(pages)
+    refs = (rng.random(pages) < fill).astype(int)
+    for shift in (0, 64, pages // 2):
+        check_compact([[0]], [0], np.roll(refs, shift).tolist(), 1, pools=1, page=(5,), dtype="uint8")
+    check_compact([[0]], [0], np.sort(refs).tolist(), 1, pools=1, page=(5,), dtype="uint8")

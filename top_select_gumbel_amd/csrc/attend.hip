@@ -932,8 +932,11 @@ struct APlan {
   size_t off_norm = 0, off_start = 0, off_part = 0, total = 0;
   bool whole = false;
 };
-// Rows of so few positions are left to one workgroup each: what would be joined is less than the join.
-constexpr int64_t kWholeSlots = 256;
+// Rows of few positions are left to one workgroup each, which saves the join's launch; of more where there are rows enough to fill
+// the chip that way, but not so many that equal shares do, whatever their lengths. (us a call, a workgroup a row against
+// shares; sequences of 8 rows: 64 x 250 14.4 against 20.6, 8 x 500 14.4 against 18, 256 x 500 93 against 96, 8 x 1000 22
+// against 18, 64 x 1000 46 against 51, 64 of up to 1000 36 against 38, 256 of up to 1000 108 against 105.)
+constexpr int64_t kWholeSlots = 512, kWholeMore = 1024, kWholeRows = 256, kWholeMost = 1024;
 
 bool attend_plan(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t dim, int64_t max_len, int64_t w_slots, APlan& pl) {
   if (batch < 0 || batch > (1 << 24) || kv_heads < 1 || q_heads < kv_heads || q_heads > (1 << 16) || q_heads % kv_heads || dim < 1 ||
@@ -942,7 +945,7 @@ bool attend_plan(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t dim, 
   const int64_t tiles = (q_heads / kv_heads + kCols - 1) / kCols;
   pl.rows = batch * kv_heads * tiles;
   if (pl.rows * 64 > (int64_t)0xFFFFFFFF / 1024) return false;   // a launch has fewer than 2^32 threads
-  pl.whole = max_len <= kWholeSlots;
+  pl.whole = max_len <= kWholeSlots || (max_len <= kWholeMore && pl.rows >= kWholeRows && pl.rows <= kWholeMost);
   pl.score_stride = w_slots ? (w_slots + 31) / 32 * 32 : 0;
   if (w_slots && batch * q_heads * ((w_slots + 1023) / 1024) > (int64_t)0xFFFFFFFF / 1024 - pl.rows * 64) return false;
   size_t at = 0;
@@ -1012,7 +1015,8 @@ hipError_t launch_dim(AParams& P, int64_t rows, hipStream_t s) {
 extern "C" size_t ts_cache_attend_workspace(int64_t batch, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t max_len,
                                             int64_t weights_slots) {
   APlan pl;
-  return attend_plan(batch, q_heads, kv_heads, dim, max_len, weights_slots, pl) ? pl.total : 0;
+  if (weights_slots > 0) max_len = std::min(max_len, weights_slots);
+  return attend_plan(batch, q_heads, kv_heads, dim, std::min(max_len, tsp::kMaxLen), weights_slots, pl) ? pl.total : 0;
 }
 
 extern "C" int ts_cache_attend(const void* q, int dtype, int64_t batch, int32_t q_heads, int32_t kv_heads, int32_t dim,
@@ -1061,7 +1065,7 @@ extern "C" int ts_cache_attend(const void* q, int dtype, int64_t batch, int32_t 
   APlan pl;
   const int64_t max_len = std::min<int64_t>(std::min<int64_t>(table_width * page_slots, tsp::kMaxLen),
                                             out_weights ? weights_slots : tsp::kMaxLen);
-  if (!attend_plan(batch, q_heads, kv_heads, dim, max_len, weights_slots, pl))
+  if (!attend_plan(batch, q_heads, kv_heads, dim, window > 0 ? std::min<int64_t>(max_len, window) : max_len, weights_slots, pl))
     return fail(TS_ERR_INVALID_ARG, "batch x heads x slots too large");
   if (pl.total) {
     if (!workspace) return fail(TS_ERR_WORKSPACE, "workspace is NULL");
