@@ -407,7 +407,8 @@ typedef struct ts_paged {   /* one layer's keys or values: slot s of page p unde
  * depend on the batch in their last bits only (the sums' order), and are the same bits for the same call.
  * Workspace: ts_cache_attend_workspace(..., max_len = table_width * page_slots, ...); it may be 0 (and the workspace NULL).
  */
-size_t ts_cache_attend_workspace(int64_t batch, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t max_len, int64_t weights_slots);
+size_t ts_cache_attend_workspace(int dtype, int64_t batch, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t max_len,
+                                 int64_t weights_slots);
 int ts_cache_attend(const void* q, int dtype, int64_t batch, int32_t q_heads, int32_t kv_heads, int32_t dim,
                     int64_t q_batch_stride, int64_t q_head_stride, const ts_paged* k_pages, const ts_paged* v_pages, int64_t pages,
                     int32_t page_slots, const int32_t* table, int64_t table_width, int64_t table_stride, const int32_t* lengths,

@@ -51,17 +51,18 @@ def test_attend_refusals(lib, kw, word):
 
 def test_attend_workspace(lib):
     assert attend(lib, batch=0, q=None, table=None, lengths=None, out=None, ws=None, ws_bytes=0) == ts.TS_OK
-    need = lib.ts_cache_attend_workspace(3, 8, 4, 32, 200 * 16, 0)
+    need = lib.ts_cache_attend_workspace(1, 3, 8, 4, 32, 200 * 16, 0)
     assert need > 0 and need % 256 == 0
     assert attend(lib, ws=None) == ts.TS_ERR_WORKSPACE
     assert attend(lib, ws=FAKE + 16) == ts.TS_ERR_WORKSPACE
     assert attend(lib, ws_bytes=need - 1) == ts.TS_ERR_WORKSPACE and "needs" in ts.ts_last_error()
-    assert lib.ts_cache_attend_workspace(3, 8, 4, 32, 200 * 16, 200 * 16) > need
-    assert lib.ts_cache_attend_workspace(3, 8, 4, 32, 100, 0) == 0      # short sequences need none
+    assert lib.ts_cache_attend_workspace(1, 3, 8, 4, 32, 200 * 16, 200 * 16) > need
+    assert lib.ts_cache_attend_workspace(1, 3, 8, 4, 32, 100, 0) == 0      # short sequences need none
     assert attend(lib, width=6, stride=6, ws=None, ws_bytes=0, pages=0) == ts.TS_ERR_INVALID_ARG and "pages" in ts.ts_last_error()
     for bad in [(-1, 8, 4, 32, 9, 0), (1, 8, 3, 32, 9, 0), (1, 8, 0, 32, 9, 0), (1, 8, 4, 0, 9, 0), (1, 8, 4, 300, 9, 0), (1, 8, 4, 32, -1, 0),
                 (1, 8, 4, 32, 9, -1), (1 << 62, 8, 4, 32, 9, 0)]:
-        assert lib.ts_cache_attend_workspace(*bad) == 0
+        assert lib.ts_cache_attend_workspace(1, *bad) == 0
+    assert lib.ts_cache_attend_workspace(3, 3, 8, 4, 32, 3200, 0) == 0
 
 
 def append(lib, **kw):

@@ -109,7 +109,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         lib.ts_cache_attend.argtypes = [vp, c.c_int, i64, i32, i32, i32, i64, i64, vp, vp, i64, i32, vp, i64, i64, vp, c.c_float, i32,
                                         vp, i64, i64, vp, vp, c.c_int, i64, i64, i64, vp, vp, sz, vp]
         lib.ts_cache_attend.restype = c.c_int
-        lib.ts_cache_attend_workspace.argtypes = [i64, i32, i32, i32, i64, i64]
+        lib.ts_cache_attend_workspace.argtypes = [c.c_int, i64, i32, i32, i32, i64, i64]
         lib.ts_cache_attend_workspace.restype = sz
         lib.ts_cache_append.argtypes = [vp, vp, i64, i64, i32, i64, i64, i64, i64, i64, vp, vp, vp, i64, i32, vp, i64, i64, vp, vp, vp]
         lib.ts_cache_append.restype = c.c_int
@@ -683,7 +683,7 @@ def ts_cache_attend(q, k_pages, v_pages, table, lengths, scale: Optional[float] 
         weights = empty((b, hq, weights_slots), dtype=weights_dtype, device=device)
         pw, wb, wh = weights.data_ptr(), hq * weights_slots, weights_slots
     # a workspace of the call's own, as in ts_token_logp
-    nb = lib.ts_cache_attend_workspace(b, hq, hk, dim, width * slots, weights_slots)
+    nb = lib.ts_cache_attend_workspace(code, b, hq, hk, dim, width * slots, weights_slots)
     ws = empty(nb, dtype=torch.uint8, device=device) if nb else None
     _call(device, lib.ts_cache_attend, q.data_ptr(), code, b, hq, hk, dim, qb, qh, ctypes.byref(kp), ctypes.byref(vp), pages, slots,
           table.data_ptr(), width, table_stride, plen, dim ** -0.5 if scale is None else scale, window, out.data_ptr(), ob, oh,

@@ -536,7 +536,7 @@ __device__ __forceinline__ bool begin(const AParams& P, int wv, Cursor& c) {
   const int l = __builtin_ctzll(past);
   int64_t in = pos - (int64_t)readlane64(incl - sum, l);
   int b = l * own;
-  for (;; ++b) {
+  for (; own > 1; ++b) {
     const int64_t n = places_of<TOK>(P, span_of(P, b));
     if (in < n) break;
     in -= n;
@@ -917,7 +917,10 @@ __global__ __launch_bounds__(NW * 64) void ts_attend_join_kernel(const AParams P
 }
 
 // ------------------------------------------------------------------ host side
-constexpr int64_t kFineJoin = 1024, kWideJoin = 512;
+// How the join's work is cut: by rows' results of 8 a lane, unless rows are so few that single ones fill the chip better (at most
+// kFineJoin workgroups); rows of very many parts each have 16 waves. (us a call: 64 rows of 33 tiles 20.7, by single results 23.9;
+// 16 rows of 4096 tiles 174.7 with 4 waves, 177.6 with 16; 8 rows of 63 tiles 14.0 and 15.1; one row of 4096 tiles 34.7 with 16.)
+constexpr int64_t kFineJoin = 512, kWideJoin = 2;
 constexpr double kCacheBytes = 256e6;   // the last-level cache
 // Workgroups of the pass: as many as the chip holds at once, by their registers and LDS.
 constexpr int groups_of(int dp) { return dp <= 128 ? 512 : 256; }
@@ -925,6 +928,7 @@ constexpr int groups_of(int dp) { return dp <= 128 ? 512 : 256; }
 int dtype_size(int dtype) {
   return dtype == TS_DTYPE_F32 ? 4 : (dtype == TS_DTYPE_BF16 || dtype == TS_DTYPE_F16) ? 2 : 0;
 }
+int tile_of(int dtype) { return dtype == TS_DTYPE_F32 ? Shape<TS_DTYPE_F32, 64>::kTok : Shape<TS_DTYPE_BF16, 64>::kTok; }
 int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
 struct APlan {
@@ -932,20 +936,20 @@ struct APlan {
   size_t off_norm = 0, off_start = 0, off_part = 0, total = 0;
   bool whole = false;
 };
-// Rows of few positions are left to one workgroup each, which saves the join's launch; of more where there are rows enough to fill
+// Rows of few tiles are left to one workgroup each, which saves the join's launch; of more where there are rows enough to fill
 // the chip that way, but not so many that equal shares do, whatever their lengths. (us a call, a workgroup a row against
-// shares; sequences of 8 rows: 64 x 250 14.4 against 20.6, 8 x 500 14.4 against 18, 256 x 500 93 against 96, 8 x 1000 22
-// against 18, 64 x 1000 46 against 51, 64 of up to 1000 36 against 38, 256 of up to 1000 108 against 105.)
-constexpr int64_t kWholeSlots = 512, kWholeMore = 1024, kWholeRows = 256, kWholeMost = 1024;
+// shares, tiles of 32; sequences of 8 rows: 64 x 250 positions 14.4 against 20.6, 8 x 500 14.4 against 18, 256 x 500 93 against 96,
+// 8 x 1000 22 against 18, 64 x 1000 46 against 51, 64 of up to 1000 36 against 38, 256 of up to 1000 108 against 105.)
+constexpr int64_t kWholeTiles = 16, kWholeMore = 32, kWholeRows = 256, kWholeMost = 1024;
 
-bool attend_plan(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t dim, int64_t max_len, int64_t w_slots, APlan& pl) {
+bool attend_plan(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t dim, int64_t max_len, int64_t w_slots, int tile, APlan& pl) {
   if (batch < 0 || batch > (1 << 24) || kv_heads < 1 || q_heads < kv_heads || q_heads > (1 << 16) || q_heads % kv_heads || dim < 1 ||
       dim > kMaxDim || max_len < 0 || max_len > 0x7FFFFF00 || w_slots < 0 || w_slots > 0x7FFFFF00)
     return false;
   const int64_t tiles = (q_heads / kv_heads + kCols - 1) / kCols;
   pl.rows = batch * kv_heads * tiles;
   if (pl.rows * 64 > (int64_t)0xFFFFFFFF / 1024) return false;   // a launch has fewer than 2^32 threads
-  pl.whole = max_len <= kWholeSlots || (max_len <= kWholeMore && pl.rows >= kWholeRows && pl.rows <= kWholeMost);
+  pl.whole = max_len <= kWholeTiles * tile || (max_len <= kWholeMore * tile && pl.rows >= kWholeRows && pl.rows <= kWholeMost);
   pl.score_stride = w_slots ? (w_slots + 31) / 32 * 32 : 0;
   if (w_slots && batch * q_heads * ((w_slots + 1023) / 1024) > (int64_t)0xFFFFFFFF / 1024 - pl.rows * 64) return false;
   size_t at = 0;
@@ -996,8 +1000,8 @@ hipError_t launch_type(AParams& P, int64_t rows, hipStream_t s) {
     if (P.weights) blocks += (int64_t)P.batch * P.q_heads * ((P.w_slots + threads * 4 - 1) / (threads * 4));
     hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(threads), 0, s, P);
   };
-  if (coarse > kWideJoin || P.whole) join(ts_attend_join_kernel<DT, DP, 4, S::kCW>, coarse, 256);
-  else if (coarse * S::kCW > kFineJoin) join(ts_attend_join_kernel<DT, DP, 16, S::kCW>, coarse, 1024);
+  if (P.whole || coarse * S::kCW > kFineJoin) join(ts_attend_join_kernel<DT, DP, 4, S::kCW>, coarse, 256);
+  else if (rows > kWideJoin) join(ts_attend_join_kernel<DT, DP, 4, 1>, coarse * S::kCW, 256);
   else join(ts_attend_join_kernel<DT, DP, 16, 1>, coarse * S::kCW, 1024);
   return hipGetLastError();
 }
@@ -1012,11 +1016,12 @@ hipError_t launch_dim(AParams& P, int64_t rows, hipStream_t s) {
 
 }  // namespace
 
-extern "C" size_t ts_cache_attend_workspace(int64_t batch, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t max_len,
+extern "C" size_t ts_cache_attend_workspace(int dtype, int64_t batch, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t max_len,
                                             int64_t weights_slots) {
   APlan pl;
+  if (!dtype_size(dtype)) return 0;
   if (weights_slots > 0) max_len = std::min(max_len, weights_slots);
-  return attend_plan(batch, q_heads, kv_heads, dim, std::min(max_len, tsp::kMaxLen), weights_slots, pl) ? pl.total : 0;
+  return attend_plan(batch, q_heads, kv_heads, dim, std::min(max_len, tsp::kMaxLen), weights_slots, tile_of(dtype), pl) ? pl.total : 0;
 }
 
 extern "C" int ts_cache_attend(const void* q, int dtype, int64_t batch, int32_t q_heads, int32_t kv_heads, int32_t dim,
@@ -1065,7 +1070,8 @@ extern "C" int ts_cache_attend(const void* q, int dtype, int64_t batch, int32_t 
   APlan pl;
   const int64_t max_len = std::min<int64_t>(std::min<int64_t>(table_width * page_slots, tsp::kMaxLen),
                                             out_weights ? weights_slots : tsp::kMaxLen);
-  if (!attend_plan(batch, q_heads, kv_heads, dim, window > 0 ? std::min<int64_t>(max_len, window) : max_len, weights_slots, pl))
+  if (!attend_plan(batch, q_heads, kv_heads, dim, window > 0 ? std::min<int64_t>(max_len, window) : max_len, weights_slots,
+                   tile_of(dtype), pl))
     return fail(TS_ERR_INVALID_ARG, "batch x heads x slots too large");
   if (pl.total) {
     if (!workspace) return fail(TS_ERR_WORKSPACE, "workspace is NULL");
