@@ -408,6 +408,22 @@ def test_random_batches(seed):
           seed=seed, slots_first=bool(seed & 1))
 
 
+@pytest.mark.parametrize("n", [40, 600])
+def test_more_rows_than_65535(n):
+    """9000 times the same sequence of 8 heads: every one has the first one's bits, or the next ones' of another share."""
+    torch = torch_cuda()
+    a = plain_call(3, batch=1, n=n)
+    k, v = (a[x][:, :1].expand(-1, 8, -1, -1).contiguous() for x in ("k_pages", "v_pages"))
+    q = a["q"][:, :1].expand(9000, 8, 64).contiguous()
+    lengths = torch.full((9000,), n - 1, dtype=torch.int32, device="cuda")
+    r = ts.ts_cache_attend(q, k, v, a["table"].expand(9000, -1).contiguous(), lengths)
+    want = paged.attend_row(host(q[:1].double())[0], host(k.double()), host(v.double()), a["table"][0].tolist(), n - 1, 0.125, 0, 0)
+    compare(want, host(r.out[0].double()), host(r.lse[0].double()), None, 0.125, "bfloat16", None, 1, "first")
+    # shares end at other positions of the row, which changes the sums' order: within a half step of each other, and a few u
+    assert float((r.out.double() - r.out[0, 0].double()).abs().max()) <= 2.0 ** -7 * float(r.out[0, 0].double().abs().max())
+    assert float((r.lse.double() - r.lse[0, 0].double()).abs().max()) < 1e-5 and not bool(r.status.any())
+
+
 def test_many_tiny_sequences_beside_long_ones():
     """Rows of one tile each fall to a few waves; one row spans many workgroups."""
     lengths = np.r_[np.arange(1, 60), 30000, np.ones(40, int), 12000]

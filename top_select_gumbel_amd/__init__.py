@@ -626,6 +626,13 @@ def _page_table(table, device, name: str = "table"):
     return rows, width, row if rows > 1 else width
 
 
+def _page_lengths(lengths, rows: int, device):
+    """Pointer of the int32 [rows] lengths."""
+    if lengths is None or lengths.dim() != 1:
+        raise TopSelectError(f"lengths must be an int32 [{rows}] tensor on {device}")
+    return _param(lengths, _torch.int32, rows, device, "lengths")
+
+
 class CacheAttend(NamedTuple):
     """Outputs of ts_cache_attend; None for what was not asked for."""
     out: object         # [batch, q_heads, dim] of the queries' type
@@ -659,9 +666,7 @@ def ts_cache_attend(q, k_pages, v_pages, table, lengths, scale: Optional[float] 
     rows, width, table_stride = _page_table(table, device)
     if rows != b:
         raise TopSelectError(f"table must have {b} rows")
-    plen = _param(lengths, torch.int32, b, device, "lengths")
-    if plen is None:
-        raise TopSelectError("lengths is required")
+    plen = _page_lengths(lengths, b, device)
     empty = torch.empty
     if out is None:
         out = empty((b, hq, dim), dtype=dtype, device=device)
@@ -714,10 +719,9 @@ def ts_cache_append(k_new, v_new, offsets, k_pages, v_pages, table, lengths):
             raise TopSelectError(f"{name} must have a contiguous last dimension")
         strides += [st * size, sh * size]
     b, width, table_stride = _page_table(table, device)
-    plen = _param(lengths, torch.int32, b, device, "lengths")
-    poff = _param(offsets, torch.int32, b + 1, device, "offsets")
-    if plen is None or poff is None:
-        raise TopSelectError("offsets and lengths are required")
+    plen, poff = _page_lengths(lengths, b, device), _param(offsets, torch.int32, b + 1, device, "offsets")
+    if poff is None:
+        raise TopSelectError("offsets is required")
     status = torch.empty_like(lengths)
     _call(device, lib.ts_cache_append, k_new.data_ptr(), v_new.data_ptr(), tokens, b, hk, dim * size, *strides, poff,
           ctypes.byref(kp), ctypes.byref(vp), pages, slots, table.data_ptr(), width, table_stride, plen, status.data_ptr())
@@ -730,7 +734,8 @@ class _Pool(ctypes.Structure):
 
 class PagePools:
     """Tensors whose pages are moved together (keys and values of every layer): [pages, ...] each, every page dense. Keep one
-    beside a cache: the calls that copy pages take it, or the tensors themselves, whose addresses they then collect each time."""
+    beside a cache: the calls that copy pages take it, or the tensors themselves, whose addresses they then collect each time.
+    It holds the tensors, and their addresses as they were when it was made."""
 
     def __init__(self, tensors):
         _t()
@@ -781,22 +786,22 @@ def ts_pages_fork(table, lengths, refs, parent, page_slots: int, n_new=None, poo
     tensor of `pools` (a PagePools or tensors), for each child but the first. refs int32 [pages]: table entries that name each page,
     free where not above 0. width: of the new table (the old one's unless given). in_place: refs is updated; else a new
     tensor is returned."""
-    torch = _t()
-    lib = load_library()
+    torch = _torch or _t()
+    lib = _lib or load_library()
     device, i = refs.device, torch.int32
     pages = _page_refs(refs, device)
     seqs, w, stride = _page_table(table, device)
-    plen = _param(lengths, i, seqs, device, "lengths")
-    n = parent.numel()
+    plen = _page_lengths(lengths, seqs, device)
+    if parent is None or parent.dim() != 1:
+        raise TopSelectError("parent must be an int32 [children] tensor")
+    n = parent.shape[0]
     pparent, pnew = _param(parent, i, n, device, "parent"), _param(n_new, i, n, device, "n_new")
-    if plen is None:
-        raise TopSelectError("lengths is required")
     pools = _page_pools(pools, pages, device)
     width = w if width is None else width
     if width < 0:
         raise TopSelectError("width must not be negative")
     out_table = torch.empty((n, width), dtype=i, device=device)
-    out_lengths, status = torch.empty((2, n), dtype=i, device=device).unbind(0)
+    out_lengths, status = torch.empty_like(parent), torch.empty_like(parent)
     out_refs = refs if in_place else torch.empty_like(refs)
     nb = lib.ts_pages_fork_workspace(seqs, n, pages)
     ws = torch.empty(nb, dtype=torch.uint8, device=device)
@@ -819,18 +824,15 @@ def ts_pages_compact(table, lengths, refs, page_slots: int, pools=(), in_place: 
     """Move the pages in use (refs above 0) to the lowest numbers, in every tensor of `pools`, and renumber the tables.
 
     in_place: table and refs are updated; else new tensors are returned. The pools are changed in place."""
-    torch = _t()
-    lib = load_library()
+    torch = _torch or _t()
+    lib = _lib or load_library()
     device, i = refs.device, torch.int32
     pages = _page_refs(refs, device)
     seqs, w, stride = _page_table(table, device)
-    plen = _param(lengths, i, seqs, device, "lengths")
-    if plen is None:
-        raise TopSelectError("lengths is required")
+    plen = _page_lengths(lengths, seqs, device)
     pools = _page_pools(pools, pages, device)
-    out_map = torch.empty(pages, dtype=i, device=device)
+    out_map, status = torch.empty_like(refs), torch.empty_like(lengths)
     count = torch.empty(1, dtype=i, device=device)
-    status = torch.empty(seqs, dtype=i, device=device)
     out_table, out_stride, out_refs = (table, stride, refs) if in_place else (torch.empty((seqs, w), dtype=i, device=device), w,
                                                                               torch.empty_like(refs))
     nb = lib.ts_pages_compact_workspace(pages)
@@ -844,19 +846,20 @@ def ts_pages_compact(table, lengths, refs, page_slots: int, pools=(), in_place: 
 def ts_pages_copy(source, target, pools):
     """Copy page source[i] to page target[i] (int32 [n]) in every tensor of `pools`: returns status int32 [n], TS_ROW_BAD_PAGE for
     pairs that are not copied (a page out of range, or a source that is another pair's target)."""
-    torch = _t()
-    lib = load_library()
+    torch = _torch or _t()
+    lib = _lib or load_library()
     if not isinstance(pools, PagePools):
         pools = PagePools(pools)
-    device, n = source.device, source.numel()
-    if not source.is_cuda:
-        raise TopSelectError("source must be a CUDA/HIP tensor")
+    device = source.device
+    if not source.is_cuda or source.dim() != 1:
+        raise TopSelectError("source must be an int32 [n] CUDA/HIP tensor")
+    n = source.shape[0]
     if not len(pools) or pools.device != device:
         raise TopSelectError(f"pools must be tensors on {device}")
     ps, pt = _param(source, torch.int32, n, device, "source"), _param(target, torch.int32, n, device, "target")
     if pt is None:
         raise TopSelectError("target is required")
-    status = torch.empty(n, dtype=torch.int32, device=device)
+    status = torch.empty_like(source)
     _call(device, lib.ts_pages_copy, ps, pt, n, pools.pages, pools.array, len(pools), status.data_ptr())
     return status
 

@@ -808,12 +808,11 @@ __global__ __launch_bounds__(NW * 64) void ts_attend_join_kernel(const AParams P
     const Span span = span_of(P, b);
     const int32_t tiles = tiles_of<S::kTok>(span);
     float2 norm;
-    Parts<DT, DP> parts(P, b, hk * P.head_tiles + in / kCols, P.whole ? 0 : tiles);
-    if (span.status != TS_ROW_OK) {
-      norm = float2{0.0f, NAN};
+    if (P.whole) {
+      norm = P.norm[row];
     } else if (tiles == 0) {
-      norm = float2{-INFINITY, 0.0f};
-    } else if (parts.count <= 1) {
+      norm = float2{-INFINITY, span.status != TS_ROW_OK ? NAN : 0.0f};
+    } else if (const Parts<DT, DP> parts(P, b, hk * P.head_tiles + in / kCols, tiles); parts.count == 1) {
       norm = P.norm[row];
     } else {
       const int col = in % kCols;
@@ -948,10 +947,10 @@ bool attend_plan(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t dim, 
     return false;
   const int64_t tiles = (q_heads / kv_heads + kCols - 1) / kCols;
   pl.rows = batch * kv_heads * tiles;
-  if (pl.rows * 64 > (int64_t)0xFFFFFFFF / 1024) return false;   // a launch has fewer than 2^32 threads
+  if (pl.rows * 16 > (int64_t)0xFFFFFFFF / 512) return false;   // a launch has fewer than 2^32 threads, a join's 16 x 256 a row at most
   pl.whole = max_len <= kWholeTiles * tile || (max_len <= kWholeMore * tile && pl.rows >= kWholeRows && pl.rows <= kWholeMost);
   pl.score_stride = w_slots ? (w_slots + 31) / 32 * 32 : 0;
-  if (w_slots && batch * q_heads * ((w_slots + 1023) / 1024) > (int64_t)0xFFFFFFFF / 1024 - pl.rows * 64) return false;
+  if (w_slots && batch * q_heads * ((w_slots + 1023) / 1024) > (int64_t)0xFFFFFFFF / 512) return false;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
