@@ -97,13 +97,13 @@ __device__ __forceinline__ void copy_page(const MoveArgs& M, int from, int to, i
   }
 }
 
+// Workgroup `block` of those that copy a list's pages.
 template <class U>
-__global__ __launch_bounds__(kPT) void ts_pages_move_kernel(const MoveArgs M) {
-  const int pair = blockIdx.x / (unsigned)M.parts, part = blockIdx.x - pair * M.parts;
+__device__ __forceinline__ void move_pages(const MoveArgs& M, unsigned block) {
+  const int pair = block / (unsigned)M.parts, part = block - pair * M.parts;
   if (M.count && pair >= *M.count) return;
   const int from = M.source[pair];
-  if (from < 0) return;
-  copy_page<U>(M, from, M.target[pair], part);
+  if (from >= 0) copy_page<U>(M, from, M.target[pair], part);
 }
 
 // ------------------------------------------------------------------ copy
@@ -213,14 +213,20 @@ struct ChildInfo {
   uint32_t need;                // fresh pages: a copy's, then the growth's
   int32_t copies, status;
 };
+// What a child's row ends up with.
+struct EndInfo {
+  int32_t inherited, filled;    // pages of its parent's row as they are; pages in all, the fresh ones between
+  int32_t back;                 // whole pages of its parent that it would have shared, had it found a page for its copy
+};
 struct ForkArgs {
   const int32_t *table, *lengths, *refs, *parent, *n_new;
   int32_t *out_table, *out_lengths, *out_refs, *status;
   int64_t table_stride, out_stride;
   int32_t seqs, children, table_width, out_width, pages, page_slots, max_len, out_max, tiles;
-  Divisor by_page, by_width, by_out;   // the widths' for the one workgroup
+  Divisor by_page, by_width;    // by_width: for the one workgroup
   SeqInfo* seq;                 // [seqs]
   ChildInfo* child;             // [children]
+  EndInfo* end;                 // [children]
   uint32_t* start;              // [children + 1]: fresh pages of the children before
   uint32_t* tile_free;          // [tiles]
   int32_t *source, *target;     // [children]: pages to copy
@@ -262,7 +268,7 @@ __global__ __launch_bounds__(kPT) void ts_pages_plan_kernel(const ForkArgs F) {
   }
 }
 
-// A workgroup a sequence: its pages' counts go by what became of it. A workgroup a child: its inherited pages, and what it needs.
+// A workgroup a sequence: its pages' counts go by what became of it. A thread a child: what it inherits and needs.
 __global__ __launch_bounds__(kPT) void ts_pages_share_kernel(const ForkArgs F) {
   if ((int)blockIdx.x < F.seqs) {
     const int s = blockIdx.x;
@@ -274,10 +280,10 @@ __global__ __launch_bounds__(kPT) void ts_pages_share_kernel(const ForkArgs F) {
     if (held > whole && I.children == 0 && threadIdx.x == 0) atomicAdd(&F.out_refs[F.table[s * F.table_stride + whole]], -1);
     return;
   }
-  const int c = blockIdx.x - F.seqs;
+  const int c = ((int)blockIdx.x - F.seqs) * kPT + threadIdx.x;
+  if (c >= F.children) return;
   const int p = F.parent[c], grow = F.n_new ? F.n_new[c] : 0;
   ChildInfo C{0, 0, 0, 0, TS_ROW_OK};
-  int of = -1;
   if (p < -1 || p >= F.seqs) {
     C.status = TS_ROW_BAD_PARENT;
   } else if (p >= 0) {
@@ -285,7 +291,6 @@ __global__ __launch_bounds__(kPT) void ts_pages_share_kernel(const ForkArgs F) {
     if (I.status != TS_ROW_OK) C.status = I.status;
     else if (I.length > F.out_max) C.status = TS_ROW_BAD_LENGTH;
     else {
-      of = p;
       C.old = I.length;
       C.copies = I.first != c && (int)F.by_page.of(I.length) != pages_of(F.by_page, I.length);
     }
@@ -295,11 +300,19 @@ __global__ __launch_bounds__(kPT) void ts_pages_share_kernel(const ForkArgs F) {
     if (grow < 0 || grow > F.out_max - C.old) C.status = TS_ROW_BAD_LENGTH;
     else C.grown = C.old + grow;
   }
-  const int before = pages_of(F.by_page, C.old);
-  C.need = (uint32_t)(C.copies + pages_of(F.by_page, C.grown) - before);
-  int32_t* row = F.out_table + c * F.out_stride;
-  for (int x = threadIdx.x; x < F.out_width; x += kPT) row[x] = x < before ? F.table[of * F.table_stride + x] : -1;
-  if (threadIdx.x == 0) F.child[c] = C;
+  C.need = (uint32_t)(C.copies + pages_of(F.by_page, C.grown) - pages_of(F.by_page, C.old));
+  F.child[c] = C;
+}
+
+// A child's outputs, once it is known whether its fresh pages are there.
+__device__ __forceinline__ void end_child(const ForkArgs& F, int c, const ChildInfo& C, bool fits) {
+  const bool empty = !fits && C.copies;
+  const int length = fits ? C.grown : empty ? 0 : C.old;
+  F.out_lengths[c] = length;
+  if (F.status) F.status[c] = C.status != TS_ROW_OK ? C.status : fits ? TS_ROW_OK : TS_ROW_NO_PAGE;
+  if (!(fits && C.copies)) F.source[c] = -1;   // else the copy's pages are filled in with the page that it gets
+  F.end[c] = EndInfo{empty ? 0 : pages_of(F.by_page, C.old) - C.copies, pages_of(F.by_page, length),
+                     empty ? (int)F.by_page.of(C.old) : 0};
 }
 
 // A workgroup a tile of pages: its free ones. The last workgroup: the children's needs, summed.
@@ -346,15 +359,8 @@ __global__ __launch_bounds__(kPT) void ts_pages_assign_kernel(const ForkArgs F) 
   if (!tile_block) {
     const int c = ((int)blockIdx.x - F.tiles) * kPT + threadIdx.x;
     if (c >= F.children) return;
-    ChildInfo C = F.child[c];
-    const bool fits = F.start[c] + C.need <= all;
-    const bool empty = !fits && C.copies;
-    F.out_lengths[c] = fits ? C.grown : empty ? 0 : C.old;
-    if (F.status) F.status[c] = C.status != TS_ROW_OK ? C.status : fits ? TS_ROW_OK : TS_ROW_NO_PAGE;
-    if (!(fits && C.copies)) {   // else the copy's pages are filled in with the page that it gets
-      F.source[c] = -1;
-      F.target[c] = empty ? -2 : -1;   // -2: what it would have shared is given back
-    }
+    const ChildInfo C = F.child[c];
+    end_child(F, c, C, F.start[c] + C.need <= all);
     return;
   }
   const uint32_t wanted = F.start[F.children];
@@ -390,19 +396,25 @@ __global__ __launch_bounds__(kPT) void ts_pages_assign_kernel(const ForkArgs F) 
   }
 }
 
-// A workgroup a child that found no page for its copy: its row is emptied, its whole pages' counts go down.
-__global__ __launch_bounds__(kPT) void ts_pages_back_kernel(const ForkArgs F) {
-  const int c = blockIdx.x;
-  if (F.target[c] != -2) return;
-  const int whole = (int)F.by_page.of(F.child[c].old);
-  int32_t* row = F.out_table + c * F.out_stride;
-  for (int x = threadIdx.x; x <= whole; x += kPT) {
-    if (x < whole) atomicAdd(&F.out_refs[row[x]], -1);
-    row[x] = -1;
+// A workgroup a child: its row, but for the fresh pages, and what it gives back. Then the copies of pages.
+template <class U>
+__global__ __launch_bounds__(kPT) void ts_pages_hand_over_kernel(const ForkArgs F, const MoveArgs M, int rows) {
+  if ((int)blockIdx.x >= rows) {
+    move_pages<U>(M, blockIdx.x - rows);
+    return;
   }
+  const int c = blockIdx.x;
+  const EndInfo E = F.end[c];
+  const int of = F.parent[c];
+  int32_t* row = F.out_table + c * F.out_stride;
+  for (int x = threadIdx.x; x < F.out_width; x += kPT) {
+    if (x < E.inherited) row[x] = F.table[of * F.table_stride + x];
+    else if (x >= E.filled) row[x] = -1;
+  }
+  for (int x = threadIdx.x; x < E.back; x += kPT) atomicAdd(&F.out_refs[F.table[of * F.table_stride + x]], -1);
 }
 
-// All of it by one workgroup, where that one goes through the counts and tables in less time than five launches take.
+// All but that last step by one workgroup, where it goes through the counts and tables in less time than four launches take.
 constexpr int kOT = 1024, kOW = kOT / 64;    // its threads
 constexpr int kOneSeqs = kOT;                // most sequences, and children: one a thread
 // Most pages and table entries together. (Fork, pages + entries of both tables: 8000 + 6000 18 us against 32 with five launches,
@@ -513,11 +525,6 @@ __global__ __launch_bounds__(kOT) void ts_pages_fork_one_kernel(const ForkArgs F
     if (x < whole) atomicAdd(&F.out_refs[F.table[s * F.table_stride + x]], heirs - 1);
     else if (heirs == 0 && x < pages_of(F.by_page, n)) atomicAdd(&F.out_refs[F.table[s * F.table_stride + x]], -1);
   }
-#pragma unroll 8
-  for (int i = t; i < F.children * F.out_width; i += kOT) {
-    const int c = (int)F.by_out.of((uint32_t)i), x = i - c * F.out_width;
-    F.out_table[c * F.out_stride + x] = x < pages_of(F.by_page, info[c].old) ? F.table[parents[c] * F.table_stride + x] : -1;
-  }
   bar_all();
   // the free pages, in order: as many as are wanted
   all = count_chunks(F.out_refs, F.pages, masks, before_chunk, red, [](int32_t r) { return r <= 0; });
@@ -542,25 +549,7 @@ __global__ __launch_bounds__(kOT) void ts_pages_fork_one_kernel(const ForkArgs F
     F.out_table[lo * F.out_stride + at] = page;
     F.out_refs[page] = 1;
   }
-  bool empty = false;
-  if (t < F.children) {
-    const bool fits = mine + C.need <= all;
-    empty = !fits && C.copies;
-    F.out_lengths[t] = fits ? C.grown : empty ? 0 : C.old;
-    if (F.status) F.status[t] = C.status != TS_ROW_OK ? C.status : fits ? TS_ROW_OK : TS_ROW_NO_PAGE;
-    if (!(fits && C.copies)) F.source[t] = -1;
-    bad[t] = empty;
-  }
-  if (!__syncthreads_or(empty)) return;
-  for (int c = wave(); c < F.children; c += kOW) {   // what an emptied child would have shared is given back
-    if (!bad[c]) continue;
-    const int whole = (int)F.by_page.of(info[c].old);
-    int32_t* row = F.out_table + c * F.out_stride;
-    for (int x = lane(); x <= whole; x += 64) {
-      if (x < whole) atomicAdd(&F.out_refs[F.table[parents[c] * F.table_stride + x]], -1);
-      row[x] = -1;
-    }
-  }
+  if (t < F.children) end_child(F, t, C, mine + C.need <= all);
 }
 
 // ------------------------------------------------------------------ compact
@@ -569,7 +558,7 @@ struct CompactArgs {
   int32_t *out_table, *out_refs, *map, *count, *status;
   int64_t table_stride, out_stride;
   int32_t seqs, table_width, pages, page_slots, max_len, tiles;
-  Divisor by_page, by_width;
+  Divisor by_page;
   uint32_t* tile_live;              // [tiles]
   int32_t *source, *target;         // [pages / 2]: what moves where
   int32_t* moves;                   // how many; pages in use
@@ -636,9 +625,14 @@ __global__ __launch_bounds__(kPT) void ts_pages_list_kernel(const CompactArgs C)
   }
 }
 
-// A workgroup a sequence: its row renumbered. Then tiles of pages: the counts and the map of what moves.
-__global__ __launch_bounds__(kPT) void ts_pages_renumber_kernel(const CompactArgs C) {
+// A workgroup a sequence: its row renumbered. Then tiles of pages: the counts and the map of what moves. Then the copies.
+template <class U>
+__global__ __launch_bounds__(kPT) void ts_pages_settle_kernel(const CompactArgs C, const MoveArgs M, int groups) {
   __shared__ uint32_t red[kPW];
+  if ((int)blockIdx.x >= C.seqs + groups) {
+    move_pages<U>(M, blockIdx.x - C.seqs - groups);
+    return;
+  }
   if ((int)blockIdx.x < C.seqs) {
     const int s = blockIdx.x, n = C.lengths[s];
     const bool sound = n >= 0 && n <= C.max_len;
@@ -665,9 +659,9 @@ __global__ __launch_bounds__(kPT) void ts_pages_renumber_kernel(const CompactArg
     return;
   }
   const int moves = *C.moves;
-  const int64_t groups = gridDim.x - C.seqs, from = ((int64_t)blockIdx.x - C.seqs) * kPT + threadIdx.x;
+  const int64_t from = ((int64_t)blockIdx.x - C.seqs) * kPT + threadIdx.x, step = (int64_t)groups * kPT;
   const int all = C.moves[1];
-  for (int64_t p = from; p < C.pages; p += groups * kPT) {
+  for (int64_t p = from; p < C.pages; p += step) {
     const int m = __hip_atomic_load(&C.map[p], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if (m == p) {
       if (C.out_refs != C.refs) C.out_refs[p] = C.refs[p];
@@ -675,7 +669,7 @@ __global__ __launch_bounds__(kPT) void ts_pages_renumber_kernel(const CompactArg
       C.out_refs[p] = 0;
     }
   }
-  for (int64_t i = from; i < moves; i += groups * kPT) {
+  for (int64_t i = from; i < moves; i += step) {
     const int src = C.source[i], dst = C.target[i];
     C.out_refs[dst] = C.refs[src];
     C.out_refs[src] = 0;
@@ -683,68 +677,34 @@ __global__ __launch_bounds__(kPT) void ts_pages_renumber_kernel(const CompactArg
   }
 }
 
-// All but the copies by one workgroup, as for the fork.
+// The count and the list by one workgroup, as for the fork.
 __global__ __launch_bounds__(kOT) void ts_pages_compact_one_kernel(const CompactArgs C) {
   __shared__ uint64_t masks[kOT];
   __shared__ uint32_t before_chunk[kOT], red[kOW];
-  __shared__ int32_t length[kOneSeqs], bad[kOneSeqs];
-  const int t = threadIdx.x, chunks = (C.pages + 63) / 64;
+  const int chunks = (C.pages + 63) / 64;
   const uint32_t all = count_chunks(C.refs, C.pages, masks, before_chunk, red, [](int32_t r) { return r > 0; });
   // pages in use below the count
   const int cut = (int)(all / 64);
   const uint32_t below = cut < chunks ? before_chunk[cut] + (uint32_t)__popcll(masks[cut] & (((uint64_t)1 << (all % 64)) - 1)) : all;
-  const bool in_place = C.out_refs == C.refs;
 #pragma unroll 4
   for (int c = wave(); c < chunks; c += kOW) {
     const int p = c * 64 + lane();
     if (p >= C.pages) continue;
     const bool is = masks[c] >> lane() & 1;
     const uint32_t rank = before_chunk[c] + mbcnt(masks[c]);   // pages in use before this one
-    const int32_t r = in_place ? 0 : C.refs[p];
     if (p < (int)all) {
-      C.map[p] = is ? p : -1;
       if (!is) C.target[p - rank] = p;
-      else if (!in_place) C.out_refs[p] = r;
-    } else if (is) {
-      C.source[rank - below] = p;
+      C.map[p] = is ? p : -1;
     } else {
-      C.map[p] = -1;
-      C.out_refs[p] = 0;
+      if (is) C.source[rank - below] = p;
+      C.map[p] = is ? -2 - (int)(rank - below) : -1;
     }
   }
-  const int moves = (int)(all - below);
-  if (t == 0) {
-    C.moves[0] = moves;
+  if (threadIdx.x == 0) {
+    C.moves[0] = (int)(all - below);
+    C.moves[1] = (int)all;
     if (C.count) *C.count = (int)all;
   }
-  bar_all();
-#pragma unroll 4
-  for (int i = t; i < moves; i += kOT) {
-    const int src = C.source[i], dst = C.target[i];
-    C.map[src] = dst;
-    C.out_refs[dst] = C.refs[src];
-    C.out_refs[src] = 0;
-  }
-  bar_all();
-  length[t] = t < C.seqs ? C.lengths[t] : 0;
-  bad[t] = 0;
-  bar();
-#pragma unroll 4
-  for (int i = t; i < C.seqs * C.table_width; i += kOT) {
-    const int s = (int)C.by_width.of((uint32_t)i), x = i - s * C.table_width, n = length[s];
-    const bool sound = n >= 0 && n <= C.max_len;
-    const int page = C.table[s * C.table_stride + x];
-    int to = sound ? -1 : page;
-    if (sound && x < pages_of(C.by_page, n)) {
-      const int m = (uint32_t)page < (uint32_t)C.pages ? C.map[page] : -1;
-      if (m < 0) bad[s] = 1;
-      to = m < 0 ? page : m;
-    }
-    C.out_table[s * C.out_stride + x] = to;
-  }
-  bar();
-  if (t < C.seqs && C.status)
-    C.status[t] = length[t] < 0 || length[t] > C.max_len ? TS_ROW_BAD_LENGTH : bad[t] ? TS_ROW_BAD_PAGE : TS_ROW_OK;
 }
 
 // ------------------------------------------------------------------ host side
@@ -763,14 +723,14 @@ int check_pools(const ts_pool* pools, int32_t n, int64_t pages) {
   return TS_OK;
 }
 
-// f(args, U): a launch for up to kPoolsMax pools of one page size, with the copies' unit: 16 bytes at any address where a
-// page has so many, else single bytes.
+// f(args, U, workgroups): a launch for up to kPoolsMax pools of one page size, with the copies' unit: 16 bytes at any address where
+// a page has so many, else single bytes. One launch at least, where there are no pools.
 template <class F>
 hipError_t each_pools(const ts_pool* pools, int32_t n, MoveArgs M, F f) {
   std::vector<bool> done((size_t)n, false);
-  for (int32_t i = 0; i < n; ++i) {
-    if (done[i]) continue;
-    M.page_bytes = pools[i].page_bytes;
+  for (int32_t i = 0; i < std::max(n, 1); ++i) {
+    if (i < n && done[i]) continue;
+    M.page_bytes = n ? pools[i].page_bytes : 1;
     M.pools = 0;
     for (int32_t j = i; j < n && M.pools < kPoolsMax; ++j)
       if (!done[j] && pools[j].page_bytes == M.page_bytes) {
@@ -781,28 +741,25 @@ hipError_t each_pools(const ts_pool* pools, int32_t n, MoveArgs M, F f) {
     const int64_t chunks = (M.page_bytes + span - 1) / span * M.pools;
     const int64_t pairs = std::max<int64_t>(M.most, 1);
     M.parts = (int32_t)std::max<int64_t>(1, std::min<int64_t>({chunks, (kMoveGroups + pairs - 1) / pairs, 0x7FFFFFFF}));
-    if (unit == 16) f(M, u32x4{});
-    else f(M, uint8_t{});
+    const int64_t groups = M.pools ? (int64_t)M.most * M.parts : 0;
+    if (unit == 16) f(M, u32x4{}, groups);
+    else f(M, uint8_t{}, groups);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
-hipError_t move_pages(const ts_pool* pools, int32_t n, const int32_t* source, const int32_t* target, const int32_t* count,
-                      int32_t most, hipStream_t s) {
-  if (most == 0) return hipSuccess;
+MoveArgs moves_of(const int32_t* source, const int32_t* target, const int32_t* count, int64_t most) {
   MoveArgs M{};
   M.source = source;
   M.target = target;
   M.count = count;
-  M.most = most;
-  return each_pools(pools, n, M, [&](const MoveArgs& m, auto u) {
-    hipLaunchKernelGGL(ts_pages_move_kernel<decltype(u)>, dim3((unsigned)((int64_t)m.most * m.parts)), dim3(kPT), 0, s, m);
-  });
+  M.most = (int32_t)most;
+  return M;
 }
 
 struct ForkPlan {
-  size_t off_child = 0, off_start = 0, off_free = 0, off_source = 0, off_target = 0, total = 0;
+  size_t off_child = 0, off_end = 0, off_start = 0, off_free = 0, off_source = 0, off_target = 0, total = 0;
   int64_t tiles = 0;
 };
 constexpr int64_t kMaxSeqs = 1 << 22;   // rows of a table, so that a launch of a workgroup each has fewer than 2^32 threads
@@ -817,6 +774,7 @@ bool fork_plan(int64_t seqs, int64_t children, int64_t pages, ForkPlan& pl) {
   };
   take((size_t)seqs * sizeof(SeqInfo));
   pl.off_child = take((size_t)children * sizeof(ChildInfo));
+  pl.off_end = take((size_t)children * sizeof(EndInfo));
   pl.off_start = take((size_t)(children + 1) * 4);
   pl.off_free = take((size_t)pl.tiles * 4);
   pl.off_source = take((size_t)children * 4);
@@ -977,38 +935,37 @@ int ts_pages_fork(const int32_t* table, int64_t seqs, int64_t table_width, int64
   F.tiles = (int32_t)pl.tiles;
   F.by_page = Divisor(page_slots);
   F.by_width = Divisor((int32_t)std::min<int64_t>(std::max<int64_t>(table_width, 1), kOneFork));
-  F.by_out = Divisor((int32_t)std::min<int64_t>(std::max<int64_t>(out_width, 1), kOneFork));
   F.seq = reinterpret_cast<SeqInfo*>(ws);
   F.child = reinterpret_cast<ChildInfo*>(ws + pl.off_child);
+  F.end = reinterpret_cast<EndInfo*>(ws + pl.off_end);
   F.start = reinterpret_cast<uint32_t*>(ws + pl.off_start);
   F.tile_free = reinterpret_cast<uint32_t*>(ws + pl.off_free);
   F.source = reinterpret_cast<int32_t*>(ws + pl.off_source);
   F.target = reinterpret_cast<int32_t*>(ws + pl.off_target);
   const hipStream_t s = (hipStream_t)stream;
-  if (children > 0 && seqs <= kOneSeqs && children <= kOneSeqs && pages + seqs * table_width + children * out_width <= kOneFork) {
+  if (children > 0 && seqs <= kOneSeqs && children <= kOneSeqs && pages + seqs * table_width <= kOneFork) {
     hipLaunchKernelGGL(ts_pages_fork_one_kernel, dim3(1), dim3(kOT), 0, s, F);
     rc = launched("fork");
+  } else {
+    const int64_t plan_grid = std::max<int64_t>({seqs, std::min<int64_t>(1024, pl.tiles), 1}), child_blocks = (children + kPT - 1) / kPT;
+    hipLaunchKernelGGL(ts_pages_plan_kernel, dim3((unsigned)plan_grid), dim3(kPT), 0, s, F);
+    rc = launched("fork plan");
+    if (rc != TS_OK || seqs + children == 0) return rc;
+    hipLaunchKernelGGL(ts_pages_share_kernel, dim3((unsigned)(seqs + child_blocks)), dim3(kPT), 0, s, F);
+    rc = launched("fork share");
+    if (rc != TS_OK || children == 0) return rc;
+    hipLaunchKernelGGL(ts_pages_count_kernel, dim3((unsigned)(pl.tiles + 1)), dim3(kPT), 0, s, F);
+    rc = launched("fork count");
     if (rc != TS_OK) return rc;
-    const hipError_t e = move_pages(pools, n_pools, F.source, F.target, nullptr, (int32_t)children, s);
-    return e == hipSuccess ? TS_OK : fail(TS_ERR_LAUNCH, "fork copy launch failed: %s", hipGetErrorString(e));
+    hipLaunchKernelGGL(ts_pages_assign_kernel, dim3((unsigned)(pl.tiles + child_blocks)), dim3(kPT), 0, s, F);
+    rc = launched("fork assign");
   }
-  const int64_t plan_grid = std::max<int64_t>({seqs, std::min<int64_t>(1024, pl.tiles), 1});
-  hipLaunchKernelGGL(ts_pages_plan_kernel, dim3((unsigned)plan_grid), dim3(kPT), 0, s, F);
-  rc = launched("fork plan");
-  if (rc != TS_OK || seqs + children == 0) return rc;
-  hipLaunchKernelGGL(ts_pages_share_kernel, dim3((unsigned)(seqs + children)), dim3(kPT), 0, s, F);
-  rc = launched("fork share");
-  if (rc != TS_OK || children == 0) return rc;
-  hipLaunchKernelGGL(ts_pages_count_kernel, dim3((unsigned)(pl.tiles + 1)), dim3(kPT), 0, s, F);
-  rc = launched("fork count");
   if (rc != TS_OK) return rc;
-  hipLaunchKernelGGL(ts_pages_assign_kernel, dim3((unsigned)(pl.tiles + (children + kPT - 1) / kPT)), dim3(kPT), 0, s, F);
-  rc = launched("fork assign");
-  if (rc != TS_OK) return rc;
-  hipLaunchKernelGGL(ts_pages_back_kernel, dim3((unsigned)children), dim3(kPT), 0, s, F);
-  rc = launched("fork back");
-  if (rc != TS_OK) return rc;
-  const hipError_t e = move_pages(pools, n_pools, F.source, F.target, nullptr, (int32_t)children, s);
+  int rows = (int)children;   // by the first launch
+  const hipError_t e = each_pools(pools, n_pools, moves_of(F.source, F.target, nullptr, children), [&](const MoveArgs& m, auto u, int64_t n) {
+    hipLaunchKernelGGL(ts_pages_hand_over_kernel<decltype(u)>, dim3((unsigned)(rows + n)), dim3(kPT), 0, s, F, m, rows);
+    rows = 0;
+  });
   return e == hipSuccess ? TS_OK : fail(TS_ERR_LAUNCH, "fork copy launch failed: %s", hipGetErrorString(e));
 }
 
@@ -1057,30 +1014,32 @@ int ts_pages_compact(const int32_t* table, int64_t seqs, int64_t table_width, in
   C.max_len = (int32_t)std::min<int64_t>(table_width * page_slots, tsp::kMaxLen);
   C.tiles = (int32_t)pl.tiles;
   C.by_page = Divisor(page_slots);
-  C.by_width = Divisor((int32_t)std::min<int64_t>(std::max<int64_t>(table_width, 1), kOneFork));
   C.tile_live = reinterpret_cast<uint32_t*>(ws);
   C.source = reinterpret_cast<int32_t*>(ws + pl.off_source);
   C.target = reinterpret_cast<int32_t*>(ws + pl.off_target);
   C.moves = reinterpret_cast<int32_t*>(ws + pl.off_moves);
   const hipStream_t s = (hipStream_t)stream;
-  if (seqs <= kOneSeqs && pages + seqs * table_width <= kOneCompact) {
+  if (pages <= kOneCompact) {
     hipLaunchKernelGGL(ts_pages_compact_one_kernel, dim3(1), dim3(kOT), 0, s, C);
     rc = launched("compact");
+  } else {
+    hipLaunchKernelGGL(ts_pages_live_kernel, dim3((unsigned)pl.tiles), dim3(kPT), 0, s, C);
+    rc = launched("compact count");
     if (rc != TS_OK) return rc;
-    const hipError_t e = move_pages(pools, n_pools, C.source, C.target, C.moves, (int32_t)(pages / 2), s);
-    return e == hipSuccess ? TS_OK : fail(TS_ERR_LAUNCH, "compact copy launch failed: %s", hipGetErrorString(e));
+    hipLaunchKernelGGL(ts_pages_list_kernel, dim3((unsigned)pl.tiles), dim3(kPT), 0, s, C);
+    rc = launched("compact list");
   }
-  hipLaunchKernelGGL(ts_pages_live_kernel, dim3((unsigned)pl.tiles), dim3(kPT), 0, s, C);
-  rc = launched("compact count");
   if (rc != TS_OK) return rc;
-  hipLaunchKernelGGL(ts_pages_list_kernel, dim3((unsigned)pl.tiles), dim3(kPT), 0, s, C);
-  rc = launched("compact list");
-  if (rc != TS_OK) return rc;
-  const int64_t groups = std::min<int64_t>(1024, pl.tiles * 4);
-  hipLaunchKernelGGL(ts_pages_renumber_kernel, dim3((unsigned)(seqs + groups)), dim3(kPT), 0, s, C);
-  rc = launched("compact renumber");
-  if (rc != TS_OK) return rc;
-  const hipError_t e = move_pages(pools, n_pools, C.source, C.target, C.moves, (int32_t)(pages / 2), s);
+  const int groups = (int)std::min<int64_t>(1024, pl.tiles * 4);
+  bool first = true;
+  const hipError_t e = each_pools(pools, n_pools, moves_of(C.source, C.target, C.moves, pages / 2), [&](const MoveArgs& m, auto u, int64_t n) {
+    CompactArgs c = C;
+    if (!first) c.seqs = 0;
+    const int g = first ? groups : 0;
+    first = false;
+    if (c.seqs + g + n > 0)
+      hipLaunchKernelGGL(ts_pages_settle_kernel<decltype(u)>, dim3((unsigned)(c.seqs + g + n)), dim3(kPT), 0, s, c, m, g);
+  });
   return e == hipSuccess ? TS_OK : fail(TS_ERR_LAUNCH, "compact copy launch failed: %s", hipGetErrorString(e));
 }
 
@@ -1095,17 +1054,8 @@ int ts_pages_copy(const int32_t* source, const int32_t* target, int64_t n, int64
   int dev;
   rc = check_device(&dev);
   if (rc != TS_OK) return rc;
-  MoveArgs M{};
-  M.source = source;
-  M.target = target;
-  M.most = (int32_t)n;
   const hipStream_t s = (hipStream_t)stream;
-  if (n_pools == 0) {   // the verdicts alone
-    M.parts = 1;
-    hipLaunchKernelGGL(ts_pages_copy_kernel<uint8_t>, dim3((unsigned)n), dim3(kPT), 0, s, M, (int)pages, pair_status);
-    return launched("page copy");
-  }
-  const hipError_t e = each_pools(pools, n_pools, M, [&](const MoveArgs& m, auto u) {
+  const hipError_t e = each_pools(pools, n_pools, moves_of(source, target, nullptr, n), [&](const MoveArgs& m, auto u, int64_t) {
     hipLaunchKernelGGL(ts_pages_copy_kernel<decltype(u)>, dim3((unsigned)(n * m.parts)), dim3(kPT), 0, s, m, (int)pages, pair_status);
   });
   return e == hipSuccess ? TS_OK : fail(TS_ERR_LAUNCH, "page copy launch failed: %s", hipGetErrorString(e));
