@@ -450,7 +450,8 @@ typedef struct ts_pool {   /* an array of pages: page p is the page_bytes bytes 
  *               before it fit): it keeps its parent's positions and does not grow, and is left empty if it needed a copy.
  *               TS_ROW_BAD_LENGTH: n_new negative or past out_width: the same, or the parent's length bad or past out_width: empty.
  *               TS_ROW_BAD_PAGE, TS_ROW_BAD_PARENT: the parent's row, or parent[i], is bad: empty.
- * The pages of a sequence whose own row is bad keep their counts. Workspace: ts_pages_fork_workspace.
+ * The pages of a sequence whose own row is bad keep their counts. At most 65536 sequences and children. Arrays must not overlap
+ * apart from the cases named. Workspace: ts_pages_fork_workspace.
  */
 size_t ts_pages_fork_workspace(int64_t seqs, int64_t children, int64_t pages);
 int ts_pages_fork(const int32_t* table, int64_t seqs, int64_t table_width, int64_t table_stride, const int32_t* lengths,
@@ -476,7 +477,7 @@ int ts_pages_compact(const int32_t* table, int64_t seqs, int64_t table_width, in
                      int32_t* row_status, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
- * ts_pages_copy -- page source[i] of every pool to page target[i], for n pairs (device arrays).
+ * ts_pages_copy -- page source[i] of every pool to page target[i], for n pairs (device arrays), at most 65536.
  *   pair_status [n] int32 or NULL: TS_ROW_BAD_PAGE for a pair that is not copied because a page of it does not exist or its source is
  *               another pair's target. Of several pairs with one target the last is copied.
  * Needs no workspace.

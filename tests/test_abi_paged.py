@@ -97,9 +97,9 @@ def fork(lib, **kw):
 
 
 @pytest.mark.parametrize("kw,word", [
-    (dict(seqs=-1), "seqs"), (dict(seqs=(1 << 22) + 1), "seqs"), (dict(children=-1), "children"), (dict(pages=-1), "pages"),
-    (dict(slots=0), "page_slots"), (dict(stride=7), "table_stride"), (dict(out_stride=8), "table_stride"), (dict(out_width=-1), "table_width"),
-    (dict(children=1 << 20, out_width=1 << 20, out_stride=1 << 20), "too large"), (dict(table=None), "NULL"), (dict(lengths=None), "NULL"),
+    (dict(seqs=-1), "seqs"), (dict(seqs=(1 << 16) + 1), "seqs"), (dict(children=-1), "children"), (dict(pages=-1), "pages"),
+    (dict(children=(1 << 16) + 1), "children"), (dict(slots=0), "page_slots"), (dict(stride=7), "table_stride"), (dict(out_stride=8), "table_stride"), (dict(out_width=-1), "table_width"),
+    (dict(children=1 << 16, out_width=1 << 20, out_stride=1 << 20), "too large"), (dict(table=None), "NULL"), (dict(lengths=None), "NULL"),
     (dict(parent=None), "NULL"), (dict(out_table=None), "NULL"), (dict(out_lengths=None), "NULL"), (dict(refs=None), "NULL"),
     (dict(out_refs=None), "NULL"), (dict(out_table=FAKE), "may not be"), (dict(n=-1), "n_pools"), (dict(pools=None), "NULL"),
     (dict(pools=pools(ts._Pool(None, 64, 64))), "NULL"), (dict(pools=pools(ts._Pool(FAKE, 63, 64))), "page_stride"),
@@ -142,7 +142,7 @@ def test_compact_workspace(lib):
 
 
 @pytest.mark.parametrize("kw,word", [
-    (dict(n=-1), "n ="), (dict(n=(1 << 22) + 1), "n ="), (dict(pages=-1), "pages"), (dict(source=None), "NULL"), (dict(target=None), "NULL"),
+    (dict(n=-1), "n ="), (dict(n=(1 << 16) + 1), "n ="), (dict(pages=-1), "pages"), (dict(source=None), "NULL"), (dict(target=None), "NULL"),
     (dict(np=-1), "n_pools"), (dict(pools=None), "NULL"), (dict(pools=pools(ts._Pool(FAKE, 63, 64))), "page_stride"),
 ])
 def test_copy_refusals(lib, kw, word):

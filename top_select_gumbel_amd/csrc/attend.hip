@@ -44,7 +44,7 @@ using tsp::Divisor;
 namespace {
 
 constexpr int kAT = 256;       // threads
-constexpr int kAW = kAT / 64;  // waves; each takes every kAW-th tile of a segment
+constexpr int kAW = kAT / 64;  // waves
 constexpr int kCols = 16;      // query heads a row
 constexpr int kMaxDim = 256;
 enum { kFull, kPart, kTiny };  // a head's dims: the padded ones, fewer, fewer than 16 bytes
@@ -54,8 +54,6 @@ typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 // Layout of a type and of a head's dims padded to DP.
 template <int DT, int DP>
@@ -67,7 +65,7 @@ struct Shape {
   static constexpr int kKC = DP * kSize / 64;                // 16-byte pieces of a key a lane
   static constexpr int kCW = kF32 ? 4 : (DP >= 128 ? 8 : 4); // consecutive dims of a value a lane
   static constexpr int kNP = DP / (16 * kCW);                // times
-  static constexpr int kVR = kTok / 4;                       // positions whose values a lane loads
+  static constexpr int kVR = kTok / 4;                       // positions whose values a lane holds
   static constexpr int kAcc = kNP * kCW;                     // result vectors
   static constexpr float kBias = DT == TS_DTYPE_F16 ? 15.0f : 0.0f;
 };
@@ -122,9 +120,9 @@ __device__ __forceinline__ int32_t tiles_of(const Span& s) {
 }
 
 // ------------------------------------------------------------------ loads
-// BYTES of a row's dims. The loads take no branch for a dim below the padded one: a piece that would reach past the row's end is
-// moved back to end with it (Piece below says where it starts), so every address is in the row. A row shorter than a piece
-// (`tiny`) is loaded by elements.
+// BYTES of a row. The loads take no branch for a dim below the padded one: a piece that would reach past the row's end is moved back
+// to end with it, so every address is in the row. (With a branch a piece, heads of 80 fp32 dims took 24 us where these take 9.)
+// A row shorter than a piece (kTiny) is loaded by elements. ONCE: past the caches.
 template <int BYTES, bool ONCE>
 __device__ __forceinline__ void load_piece(uint32_t* to, const char* at) {
   if constexpr (BYTES == 16) {
@@ -163,37 +161,26 @@ __device__ __forceinline__ float column_sum(float x) {
   return x + __shfl_xor(x, 32);
 }
 
-// WORDS: 32-bit words of a lane's part of the operands: 4 for products over 32 indexes, 2 for those over 16 (4 a lane).
-template <int DT, int WORDS>
+template <int DT>
 __device__ __forceinline__ f32x4 mma(const uint32_t* a, const uint32_t* b, f32x4 c) {
-  if constexpr (DT == TS_DTYPE_BF16 && WORDS == 4) {
+  if constexpr (DT == TS_DTYPE_BF16) {
     bf16x8 x, y;
     __builtin_memcpy(&x, a, 16);
     __builtin_memcpy(&y, b, 16);
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, c, 0, 0, 0);
-  } else if constexpr (DT == TS_DTYPE_BF16) {
-    s16x4 x, y;
-    __builtin_memcpy(&x, a, 8);
-    __builtin_memcpy(&y, b, 8);
-    return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(x, y, c, 0, 0, 0);
-  } else if constexpr (WORDS == 4) {
+  } else {
     f16x8 x, y;
     __builtin_memcpy(&x, a, 16);
     __builtin_memcpy(&y, b, 16);
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(x, y, c, 0, 0, 0);
-  } else {
-    f16x4 x, y;
-    __builtin_memcpy(&x, a, 8);
-    __builtin_memcpy(&y, b, 8);
-    return __builtin_amdgcn_mfma_f32_16x16x16f16(x, y, c, 0, 0, 0);
   }
 }
 
-// Two fp32 values rounded to 16 bits, and what the rounding left over, rounded too.
+// Two fp32 values in 16 bits, and what that left over, rounded to 16 bits too.
 template <int DT>
 __device__ __forceinline__ void split(float a, float b, uint32_t& hi, uint32_t& lo) {
   if constexpr (DT == TS_DTYPE_BF16) {
-    // hi is cut off, not rounded: the rest is then never negative, and 2^-16 of the value at the rounding of lo
+    // hi is cut off (one operation less than rounded): the rest is below 2^-7 of the value, and lo loses 2^-9 of that
     const uint32_t ua = __float_as_uint(a) & 0xFFFF0000u, ub = __float_as_uint(b) & 0xFFFF0000u;
     hi = (ua >> 16) | ub;
     const __bf16 la = (__bf16)(a - __uint_as_float(ua)), lb = (__bf16)(b - __uint_as_float(ub));
@@ -344,7 +331,7 @@ struct Wave {
           for (int j = 0; j < 4; ++j)
             s[h] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(k[h][c][j]), __uint_as_float(q[c][j]), s[h], 0, 0, 0);
         } else {
-          s[h] = mma<DT, 4>(k[h][c], q[c], s[h]);
+          s[h] = mma<DT>(k[h][c], q[c], s[h]);
         }
       }
     }
@@ -398,20 +385,19 @@ struct Wave {
             o[p * S::kCW + n] =
                 __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(v[r][p][n]), s[0][r], o[p * S::kCW + n], 0, 0, 0);
     } else {
-      constexpr int words = S::kVR / 2;
-      uint32_t hi[words], lo[words];
+      uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int x = 0; x < words; ++x) split<DT>(s[x >> 1][2 * (x & 1)], s[x >> 1][2 * (x & 1) + 1], hi[x], lo[x]);
+      for (int x = 0; x < 4; ++x) split<DT>(s[x >> 1][2 * (x & 1)], s[x >> 1][2 * (x & 1) + 1], hi[x], lo[x]);
 #pragma unroll
       for (int p = 0; p < S::kNP; ++p)
 #pragma unroll
         for (int n = 0; n < S::kCW; ++n) {
-          uint32_t a[words];   // dim n of the lane's positions
+          uint32_t a[4];   // dim n of the lane's eight positions
 #pragma unroll
-          for (int x = 0; x < words; ++x)
+          for (int x = 0; x < 4; ++x)
             a[x] = __builtin_amdgcn_perm(v[2 * x + 1][p][n >> 1], v[2 * x][p][n >> 1], (n & 1) ? 0x07060302u : 0x05040100u);
-          o[p * S::kCW + n] = mma<DT, words>(a, hi, o[p * S::kCW + n]);
-          o[p * S::kCW + n] = mma<DT, words>(a, lo, o[p * S::kCW + n]);
+          o[p * S::kCW + n] = mma<DT>(a, hi, o[p * S::kCW + n]);
+          o[p * S::kCW + n] = mma<DT>(a, lo, o[p * S::kCW + n]);
         }
     }
   }
@@ -501,9 +487,10 @@ __device__ __forceinline__ bool advance(const AParams& P, Cursor& c) {
   c.tile = 0;
   if (++c.r < rows_of(P)) return true;
   c.r = 0;
-  do {
+  do {                           // there are tiles left, so a sequence with some follows
+    if (c.b + 1 >= P.batch) return false;
     enter<TOK>(P, c, c.b + 1);
-  } while (c.tiles == 0);   // there are tiles left, so a sequence with some follows
+  } while (c.tiles == 0);
   return true;
 }
 // The wave's stretch of the list. Every wave adds up the places of all sequences by itself (lane x takes some
@@ -536,7 +523,7 @@ __device__ __forceinline__ bool begin(const AParams& P, int wv, Cursor& c) {
   const int l = __builtin_ctzll(past);
   int64_t in = pos - (int64_t)readlane64(incl - sum, l);
   int b = l * own;
-  for (; own > 1; ++b) {
+  for (; own > 1 && b + 1 < P.batch; ++b) {
     const int64_t n = places_of<TOK>(P, span_of(P, b));
     if (in < n) break;
     in -= n;

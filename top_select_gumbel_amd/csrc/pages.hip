@@ -417,10 +417,10 @@ __global__ __launch_bounds__(kPT) void ts_pages_hand_over_kernel(const ForkArgs 
 // All but that last step by one workgroup, where it goes through the counts and tables in less time than four launches take.
 constexpr int kOT = 1024, kOW = kOT / 64;    // its threads
 constexpr int kOneSeqs = kOT;                // most sequences, and children: one a thread
-// Most pages and table entries together. (Fork, pages + entries of both tables: 8000 + 6000 18 us against 32 with five launches,
-// 30000 + 32000 24 against 32, 60000 + 64000 36 against 32. Compaction: 8192 + 4500 201 against 208, most of it copies, 30000 +
-// 16000 34 against 25.)
-constexpr int64_t kOneFork = 1 << 16, kOneCompact = 1 << 14;
+// Most pages and entries of the old table together, and most pages of a compaction. (us a call, one workgroup against all of them;
+// fork, pages + entries: 8000 + 3000 18.6 and 26.0, 30000 + 16000 21.4 and 25.9, 40000 + 20000 25.3 and 26.1, 50000 + 24000
+// 28.9 and 26.2; compaction, pages: 8000 18.4 and 21.0, 30000 20.5 and 21.4, 40000 25.3 and 24.2.)
+constexpr int64_t kOneFork = 1 << 16, kOneCompact = 1 << 15;
 static_assert(kOneFork <= 64 * kOT && kOneCompact <= 64 * kOT, "a count a thread for each chunk of 64 pages");
 
 // Sum over the workgroup of the values of the threads before this one, and of all.
@@ -763,8 +763,10 @@ struct ForkPlan {
   int64_t tiles = 0;
 };
 constexpr int64_t kMaxSeqs = 1 << 22;   // rows of a table, so that a launch of a workgroup each has fewer than 2^32 threads
+// Each sequence looks through all children for its own, each pair of a copy through all targets: of so many at most (0.3 ms).
+constexpr int64_t kMaxFork = 1 << 16, kMaxPairs = 1 << 16;
 bool fork_plan(int64_t seqs, int64_t children, int64_t pages, ForkPlan& pl) {
-  if (seqs < 0 || seqs > kMaxSeqs || children < 0 || children > kMaxSeqs || pages < 0 || pages > tsp::kMaxPages) return false;
+  if (seqs < 0 || seqs > kMaxFork || children < 0 || children > kMaxFork || pages < 0 || pages > tsp::kMaxPages) return false;
   pl.tiles = (pages + kPTile - 1) / kPTile;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -899,7 +901,7 @@ int ts_pages_fork(const int32_t* table, int64_t seqs, int64_t table_width, int64
   if (rc != TS_OK) return rc;
   ForkPlan pl;
   if (!fork_plan(seqs, children, pages, pl))
-    return fail(TS_ERR_INVALID_ARG, "seqs = %lld or children = %lld outside [0, 2^22]", (long long)seqs, (long long)children);
+    return fail(TS_ERR_INVALID_ARG, "seqs = %lld or children = %lld outside [0, 65536]", (long long)seqs, (long long)children);
   if (children > 0 && out_width > 0x7FFFFFFF / children - 1) return fail(TS_ERR_INVALID_ARG, "children x out_width too large");
   if (seqs == 0 && children == 0 && pages == 0) return TS_OK;
   if (seqs > 0 && ((!table && table_width > 0) || !lengths)) return fail(TS_ERR_INVALID_ARG, "table and lengths are required (NULL given)");
@@ -1045,7 +1047,7 @@ int ts_pages_compact(const int32_t* table, int64_t seqs, int64_t table_width, in
 
 int ts_pages_copy(const int32_t* source, const int32_t* target, int64_t n, int64_t pages, const ts_pool* pools, int32_t n_pools,
                   int32_t* pair_status, void* stream) {
-  if (n < 0 || n > kMaxSeqs) return fail(TS_ERR_INVALID_ARG, "n = %lld outside [0, 2^22]", (long long)n);
+  if (n < 0 || n > kMaxPairs) return fail(TS_ERR_INVALID_ARG, "n = %lld outside [0, 65536]", (long long)n);
   if (pages < 0 || pages > tsp::kMaxPages) return fail(TS_ERR_INVALID_ARG, "pages = %lld outside [0, 2^31)", (long long)pages);
   int rc = check_pools(pools, n_pools, pages);
   if (rc != TS_OK) return rc;
