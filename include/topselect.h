@@ -440,12 +440,13 @@ typedef struct ts_pool {   /* an array of pages: page p is the page_bytes bytes 
  * ts_pages_fork -- the next step's sequences: child i continues sequence parent[i] (-1: none), grown by n_new[i] positions.
  * A sequence that no child continues is freed; one that several continue is forked: its whole pages are shared, its part-filled last
  * page stays with its first child and is copied for each other. refs[p] counts the table entries that name page p (and
- * whatever else holds it); pages whose count is not above 0 are free. Fresh pages are the lowest that are free once all
+ * whatever else holds it: such a page is not changed as long as it is full, a part-filled one goes on with the first child); pages
+ * whose count is not above 0 are free. Fresh pages are the lowest that are free once all
  * children have taken over what they share, child after child, a child's copy first. Pages that the growth reaches are not cleared.
  *   parent, n_new   [children] int32; n_new may be NULL (0).
  *   out_table   [children, out_width] at out_stride, -1 past a child's pages; apart from `table`.
  *   out_lengths [children];  out_refs [pages], may be refs.
- *   pools       the n_pools arrays (host memory: keys and values of every layer) in which pages are copied.
+ *   pools       the n_pools arrays (at most 4096; host memory: keys and values of every layer) in which pages are copied.
  *   row_status  [children] or NULL. TS_ROW_NO_PAGE: not enough free pages for the child (each takes its turn whether or not those
  *               before it fit): it keeps its parent's positions and does not grow, and is left empty if it needed a copy.
  *               TS_ROW_BAD_LENGTH: n_new negative or past out_width: the same, or the parent's length bad or past out_width: empty.
@@ -468,7 +469,7 @@ int ts_pages_fork(const int32_t* table, int64_t seqs, int64_t table_width, int64
  *   pools       as for ts_pages_fork.
  *   row_status  [seqs] or NULL. TS_ROW_BAD_LENGTH: the row's table stays as it is; TS_ROW_BAD_PAGE: it names pages that do not exist
  *               or are free; those entries stay.
- * Workspace: ts_pages_compact_workspace.
+ * At most 2^24 pages. Workspace: ts_pages_compact_workspace.
  */
 size_t ts_pages_compact_workspace(int64_t pages);
 int ts_pages_compact(const int32_t* table, int64_t seqs, int64_t table_width, int64_t table_stride, const int32_t* lengths,

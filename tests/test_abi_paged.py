@@ -126,6 +126,7 @@ def compact(lib, **kw):
 
 @pytest.mark.parametrize("kw,word", [
     (dict(seqs=-1), "seqs"), (dict(pages=-1), "pages"), (dict(pages=0), "pages"), (dict(slots=0), "page_slots"), (dict(stride=7), "table_stride"),
+    (dict(pages=(1 << 24) + 1), "pages"), (dict(n=4097), "n_pools"),
     (dict(out_stride=7), "out_stride"), (dict(out_stride=9), "input's place"), (dict(table=None), "NULL"), (dict(out_table=None), "NULL"),
     (dict(lengths=None), "NULL"), (dict(refs=None), "NULL"), (dict(out_refs=None), "NULL"), (dict(out_map=None), "NULL"),
     (dict(pools=None), "NULL"), (dict(n=-1), "n_pools"), (dict(pools=pools(ts._Pool(FAKE, 63, 64))), "page_stride"),

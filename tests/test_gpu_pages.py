@@ -491,3 +491,24 @@ def test_compact_at_chunks_of_64_pages(pages, fill):
     for shift in (0, 64, pages // 2):
         check_compact([[0]], [0], np.roll(refs, shift).tolist(), 1, pools=1, page=(5,), dtype="uint8")
     check_compact([[0]], [0], np.sort(refs).tolist(), 1, pools=1, page=(5,), dtype="uint8")
+
+
+def test_pools_of_several_page_sizes():
+    """Sizes in no order, more of one than a launch takes: every pool is copied once."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(2)
+    sizes = rng.permutation([5] * 70 + [16] * 3 + [300] * 65 + [1, 17, 4096, 40000])
+    p = [pool_of(9, (int(n),), "uint8", 50 + i) for i, n in enumerate(sizes)]
+    before = [raw(x) for x in p]
+    st = ts.ts_pages_copy(gpu([1, 8, 3]), gpu([0, 4, 4]), p)
+    torch.cuda.synchronize()
+    assert not host(st).any()
+    for x, b in zip(p, before):
+        same(raw(x).ravel(), moved(b, x, [(1, 0), (3, 4)]).ravel(), "pool")
+    before = [raw(x) for x in p]
+    refs = [0, 1, 0, 0, 1, 0, 0, 1, 1]
+    r = ts.ts_pages_compact(gpu([[1, 4], [7, 8]]), gpu([2, 2]), gpu(refs), 1, pools=p)
+    torch.cuda.synchronize()
+    assert host(r.table).tolist() == [[1, 0], [2, 3]] and host(r.refs).tolist() == [1, 1, 1, 1, 0, 0, 0, 0, 0]
+    for x, b in zip(p, before):
+        same(raw(x).ravel(), moved(b, x, [(4, 0), (7, 2), (8, 3)]).ravel(), "pool")

@@ -25,6 +25,10 @@
 // the chip holds at once: ragged batches and few long rows fill it alike, and waves wait for each other once, at the
 // end. A row that lies in one stretch is finished by its wave, one that lies in a workgroup's stretches by the workgroup;
 // the workgroups' parts of others (at most two a workgroup) are joined by a second kernel.
+//
+// Measured, 32 query heads on 8 of 128 dims in bf16: 64 sequences of up to 4096 positions, 583 MB, 98 us for the pass (6.0 TB/s; a
+// plain read 6.8) and 6 for the join; one of n positions 8.8 us at 500, 17.5 at 16000, 87 at 128000 (524 MB). The first 7 us are a
+// chain of misses (lengths, page numbers, keys); from there on the memory bounds it.
 #include <algorithm>
 #include <type_traits>
 #include <utility>

@@ -5,11 +5,11 @@
 // page p; a page is free when it is not above 0. No other state: what is free is found by counting, tiles of pages first, so that
 // the i-th free page is the same whatever the launch. Everything stays on the device; nothing waits for the host.
 //
-// All of it is bound by memory: a page's copy by the rate of a large copy, the bookkeeping by the latency of its few
-// dependent launches.
+// All of it is bound by memory: a page's copy by the rate of a large copy (1024 pages of 8 x 32 KB 107 us, 5.0 TB/s read and written;
+// 51119 tokens of 4 KB appended 83 us, 5.0 TB/s), the bookkeeping by what one compute unit reads or by the latency of a few
+// dependent launches (64 sequences and 20000 pages 16.6 + 3.9 us).
 #include <algorithm>
 #include <type_traits>
-#include <vector>
 
 #include "topselect.h"
 #include "ts_device.hpp"
@@ -709,7 +709,7 @@ __global__ __launch_bounds__(kOT) void ts_pages_compact_one_kernel(const Compact
 
 // ------------------------------------------------------------------ host side
 int check_pools(const ts_pool* pools, int32_t n, int64_t pages) {
-  if (n < 0 || n > 1 << 20) return fail(TS_ERR_INVALID_ARG, "n_pools = %d outside [0, 2^20]", (int)n);
+  if (n < 0 || n > 4096) return fail(TS_ERR_INVALID_ARG, "n_pools = %d outside [0, 4096]", (int)n);
   if (n > 0 && !pools) return fail(TS_ERR_INVALID_ARG, "pools is NULL");
   for (int32_t i = 0; i < n; ++i) {
     const ts_pool& p = pools[i];
@@ -723,20 +723,31 @@ int check_pools(const ts_pool* pools, int32_t n, int64_t pages) {
   return TS_OK;
 }
 
+// The first pool with pool i's page size.
+int32_t first_of(const ts_pool* pools, int32_t i) {
+  int32_t j = 0;
+  while (pools && pools[j].page_bytes != pools[i].page_bytes) ++j;
+  return j;
+}
 // f(args, U, workgroups): a launch for up to kPoolsMax pools of one page size, with the copies' unit: 16 bytes at any address where
 // a page has so many, else single bytes. One launch at least, where there are no pools.
 template <class F>
 hipError_t each_pools(const ts_pool* pools, int32_t n, MoveArgs M, F f) {
-  std::vector<bool> done((size_t)n, false);
-  for (int32_t i = 0; i < std::max(n, 1); ++i) {
-    if (i < n && done[i]) continue;
+  int32_t next = 0;
+  for (int32_t i = 0; i < std::max(n, 1); i = next) {
+    // from pool i on, those of its page size; after the last of them, the next size's first
     M.page_bytes = n ? pools[i].page_bytes : 1;
     M.pools = 0;
-    for (int32_t j = i; j < n && M.pools < kPoolsMax; ++j)
-      if (!done[j] && pools[j].page_bytes == M.page_bytes) {
-        M.pool[M.pools++] = Pool{static_cast<char*>(pools[j].data), pools[j].page_stride};
-        done[j] = true;
-      }
+    int32_t j = i;
+    for (; j < n && M.pools < kPoolsMax; ++j)
+      if (pools[j].page_bytes == M.page_bytes) M.pool[M.pools++] = Pool{static_cast<char*>(pools[j].data), pools[j].page_stride};
+    while (j < n && pools[j].page_bytes != M.page_bytes) ++j;
+    if (j < n) {
+      next = j;
+    } else {
+      const int32_t head = first_of(pools, i);
+      for (next = head + 1; next < n && first_of(pools, next) != next; ++next) {}
+    }
     const int64_t unit = M.page_bytes >= 16 ? 16 : 1, span = (int64_t)kPT * kCopyU * unit;
     const int64_t chunks = (M.page_bytes + span - 1) / span * M.pools;
     const int64_t pairs = std::max<int64_t>(M.most, 1);
@@ -789,7 +800,7 @@ struct CompactPlan {
   int64_t tiles = 0;
 };
 bool compact_plan(int64_t pages, CompactPlan& pl) {
-  if (pages < 0 || pages > tsp::kMaxPages) return false;
+  if (pages < 0 || pages > 1 << 24) return false;   // a launch has a workgroup for each page that may move
   pl.tiles = (pages + kPTile - 1) / kPTile;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -984,8 +995,8 @@ int ts_pages_compact(const int32_t* table, int64_t seqs, int64_t table_width, in
   if (rc == TS_OK) rc = check_pools(pools, n_pools, pages);
   if (rc != TS_OK) return rc;
   CompactPlan pl;
-  if (!compact_plan(pages, pl) || seqs < 0 || seqs > kMaxSeqs)
-    return fail(TS_ERR_INVALID_ARG, "seqs = %lld outside [0, 2^22]", (long long)seqs);
+  if (!compact_plan(pages, pl)) return fail(TS_ERR_INVALID_ARG, "pages = %lld outside [1, 2^24]", (long long)pages);
+  if (seqs < 0 || seqs > kMaxSeqs) return fail(TS_ERR_INVALID_ARG, "seqs = %lld outside [0, 2^22]", (long long)seqs);
   if (out_stride < table_width) return fail(TS_ERR_INVALID_ARG, "out_stride %lld < table_width %lld", (long long)out_stride, (long long)table_width);
   if (seqs > 0 && (((!table || !out_table) && table_width > 0) || !lengths))
     return fail(TS_ERR_INVALID_ARG, "table, out_table and lengths are required (NULL given)");

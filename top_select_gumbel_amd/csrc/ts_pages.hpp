@@ -3,7 +3,6 @@
 #include <algorithm>
 #include <initializer_list>
 #include <utility>
-#include <vector>
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -45,13 +44,25 @@ inline bool reaches(int64_t inner, Strides strides, int64_t size) {
 // ... and whether no two of them share memory: along the ascending strides each clears what lies below it.
 inline bool apart(int64_t inner, Strides strides, int64_t size) {
   if (!reaches(inner, strides, size)) return false;
-  std::vector<std::pair<int64_t, int64_t>> by(strides);
-  std::sort(by.begin(), by.end());
-  int64_t end = inner;
-  for (auto [stride, n] : by) {
-    if (n <= 1) continue;
-    if (stride < end) return false;
-    end += stride * (n - 1);
+  int64_t end = inner, last = 0;
+  int given = 0;   // the strides up to `last`, in the order that they are given, have been taken
+  for (size_t taken = 0; taken < strides.size(); ++taken) {
+    // the smallest of those that are left
+    const std::pair<int64_t, int64_t>* next = nullptr;
+    int at = 0, of = 0;
+    for (const auto& s : strides) {
+      const bool done = taken > 0 && (s.first < last || (s.first == last && at < given));
+      if (!done && (!next || s.first < next->first)) {
+        next = &s;
+        of = at;
+      }
+      ++at;
+    }
+    last = next->first;
+    given = of + 1;
+    if (next->second <= 1) continue;
+    if (next->first < end) return false;
+    end += next->first * (next->second - 1);
   }
   return true;
 }
