@@ -669,7 +669,7 @@ def ts_cache_attend(q, k_pages, v_pages, table, lengths, scale: Optional[float] 
     plen = _page_lengths(lengths, b, device)
     empty = torch.empty
     if out is None:
-        out = empty((b, hq, dim), dtype=dtype, device=device)
+        out = torch.empty_like(q) if q.is_contiguous() else empty(shape, dtype=dtype, device=device)
         ob, oh = hq * dim, dim
     else:
         if out.dtype is not dtype or out.shape != shape or out.device != device or (dim > 1 and out.stride(2) != 1):

@@ -113,11 +113,11 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 struct Span {
   int32_t lo, n, status;
 };
-__device__ __forceinline__ Span span_of(const AParams& P, int b) {
-  const int32_t n = P.lengths[b];
+__device__ __forceinline__ Span span_from(const AParams& P, int32_t n) {
   if (n < 0 || n > P.max_len) return Span{0, 0, TS_ROW_BAD_LENGTH};
   return Span{P.window > 0 ? max(0, n - P.window) : 0, n, TS_ROW_OK};
 }
+__device__ __forceinline__ Span span_of(const AParams& P, int b) { return span_from(P, P.lengths[b]); }
 template <int TOK>
 __device__ __forceinline__ int32_t tiles_of(const Span& s) {
   return (s.n + TOK - 1) / TOK - s.lo / TOK;
@@ -476,8 +476,8 @@ struct Cursor {
   int64_t left;
 };
 template <int TOK>
-__device__ __forceinline__ void enter(const AParams& P, Cursor& c, int b) {
-  const Span span = span_of(P, b);
+__device__ __forceinline__ void enter(const AParams& P, Cursor& c, int b, int32_t n) {
+  const Span span = span_from(P, n);
   c.b = b;
   c.lo = span.lo;
   c.n = span.n;
@@ -493,7 +493,7 @@ __device__ __forceinline__ bool advance(const AParams& P, Cursor& c) {
   c.r = 0;
   do {                           // there are tiles left, so a sequence with some follows
     if (c.b + 1 >= P.batch) return false;
-    enter<TOK>(P, c, c.b + 1);
+    enter<TOK>(P, c, c.b + 1, P.lengths[c.b + 1]);
   } while (c.tiles == 0);
   return true;
 }
@@ -503,7 +503,11 @@ template <int TOK>
 __device__ __forceinline__ bool begin(const AParams& P, int wv, Cursor& c) {
   const int own = (P.batch + 63) / 64, first = min(P.batch, lane() * own), last = min(P.batch, first + own);
   uint64_t sum = 0;
-  for (int x = first; x < last; ++x) sum += (uint64_t)places_of<TOK>(P, span_of(P, x));
+  int32_t n = 0;                 // of the lane's last sequence
+  for (int x = first; x < last; ++x) {
+    n = P.lengths[x];
+    sum += (uint64_t)places_of<TOK>(P, span_from(P, n));
+  }
   const uint64_t incl = wave_incl_scan64(sum), total = readlane64(incl, 63);
   // Workgroup w of G has places w total / G .. (w + 1) total / G (rounded down), and its waves likewise: within one of each other.
   // Every wave has one, unless there are fewer than a workgroup's waves.
@@ -527,12 +531,16 @@ __device__ __forceinline__ bool begin(const AParams& P, int wv, Cursor& c) {
   const int l = __builtin_ctzll(past);
   int64_t in = pos - (int64_t)readlane64(incl - sum, l);
   int b = l * own;
-  for (; own > 1 && b + 1 < P.batch; ++b) {
-    const int64_t n = places_of<TOK>(P, span_of(P, b));
-    if (in < n) break;
-    in -= n;
+  n = __builtin_amdgcn_readlane(n, l);
+  if (own > 1) {
+    for (; b + 1 < P.batch; ++b) {
+      const int64_t places = places_of<TOK>(P, span_of(P, b));
+      if (in < places) break;
+      in -= places;
+    }
+    n = P.lengths[b];
   }
-  enter<TOK>(P, c, b);
+  enter<TOK>(P, c, b, n);
   c.r = (int)quotient(in, c.tiles + 1);
   c.tile = (int32_t)(in - (int64_t)c.r * (c.tiles + 1));
   if (c.tile < c.tiles) return true;
@@ -559,7 +567,7 @@ __global__ __launch_bounds__(kAT, DP > 128 ? 1 : 2) void ts_attend_kernel(const 
   bool have;
   if (P.whole) {
     const int rows = rows_of(P), b = blockIdx.x / (unsigned)rows;
-    enter<TOK>(P, c, b);
+    enter<TOK>(P, c, b, P.lengths[b]);
     c.r = blockIdx.x - b * rows;
     const int own = (c.tiles + kAW - 1) / kAW;
     c.tile = wv * own;
