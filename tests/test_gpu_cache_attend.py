@@ -362,6 +362,28 @@ def test_offsets_past_32_bits():
     assert equal(r, near) and not host(r.status).any()
 
 
+def test_views_of_queries_tables_and_outputs():
+    """Queries shared by all sequences (stride 0) or heads first in memory, a table whose rows lie apart, outputs heads first."""
+    torch = torch_cuda()
+    a = plain_call(9)
+    want = ts.ts_cache_attend(**a)
+    heads_first = a["q"].transpose(0, 1).contiguous().transpose(0, 1)
+    table = torch.full((3, 99), -5, dtype=torch.int32, device="cuda")[:, : a["table"].shape[1]].copy_(a["table"])
+    out = torch.empty(6, 3, 64, dtype=a["q"].dtype, device="cuda").transpose(0, 1)
+    r = ts.ts_cache_attend(**{**a, "q": heads_first, "table": table}, out=out)
+    assert r.out.data_ptr() == out.data_ptr() and equal(r, want)
+    one = a["q"][:1].expand(3, 6, 64)
+    assert equal(ts.ts_cache_attend(**{**a, "q": one}), ts.ts_cache_attend(**{**a, "q": one.contiguous()}))
+    # keys and values that share memory: read only
+    shared = ts.ts_cache_attend(**{**a, "v_pages": a["k_pages"]})
+    assert equal(shared, ts.ts_cache_attend(**{**a, "v_pages": a["k_pages"].clone()}))
+    # the same pages in two sequences' tables
+    both = a["table"][:1].expand(3, -1).contiguous()
+    n = torch.full((3,), int(a["lengths"][0]), dtype=torch.int32, device="cuda")
+    r = ts.ts_cache_attend(**{**a, "table": both, "lengths": n, "q": one})
+    assert float((r.out[1:].double() - r.out[0].double()).abs().max()) <= 2.0 ** -7 * float(r.out.double().abs().max())
+
+
 def test_refusals_of_the_binding():
     torch = torch_cuda()
     a = plain_call()

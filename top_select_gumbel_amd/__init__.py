@@ -649,7 +649,7 @@ def ts_cache_attend(q, k_pages, v_pages, table, lengths, scale: Optional[float] 
     q_heads; table int32 [batch, width]: position j lies in page table[b, j // slots], slot j % slots; lengths int32 [batch].
     scale: 1 / sqrt(dim) unless given. window: only the last `window` positions (0: all). weights_slots: the first so many
     positions' attention weights are returned too, in weights_dtype (the queries' type unless given); viewed as [batch * kv_heads,
-    group, weights_slots] they are ts_cache_evict's `weights`. out: a tensor for the output, apart from q."""
+    group, weights_slots] they are ts_cache_evict's `weights`. out: a tensor for the output, apart from q. For decoding: no gradient."""
     torch = _torch or _t()
     lib = _lib or load_library()
     device, dtype, shape = q.device, q.dtype, q.shape
