@@ -34,7 +34,7 @@ def attend(lib, **kw):
     (dict(scale=0.0), "scale"), (dict(scale=-1.0), "scale"), (dict(scale=float("nan")), "scale"), (dict(scale=float("inf")), "scale"),
     (dict(window=-1), "window"), (dict(pages=-1), "pages"), (dict(pages=1 << 31), "pages"), (dict(slots=0), "page_slots"),
     (dict(width=-1), "table_width"), (dict(stride=199), "table_stride"), (dict(q=None), "NULL"), (dict(table=None), "NULL"),
-    (dict(lengths=None), "NULL"), (dict(out=None), "NULL"), (dict(pages=0), "pages"), (dict(q=FAKE + 1), "aligned"),
+    (dict(lengths=None), "NULL"), (dict(out=None), "NULL"), (dict(out=FAKE), "may not be q"), (dict(pages=0), "pages"), (dict(q=FAKE + 1), "aligned"),
     (dict(out=FAKE + 1), "aligned"), (dict(q_b=-1), "q:"), (dict(q_b=1 << 61), "q:"), (dict(o_h=31), "overlap"), (dict(o_b=255), "overlap"),
     (dict(o_b=-256), "overlap"), (dict(k=ts._Paged(None, 64, 64, 64)), "NULL"), (dict(k=None), "NULL"), (dict(v=None), "NULL"),
     (dict(k=ts._Paged(FAKE + 1, 64, 64, 64)), "aligned"), (dict(v=ts._Paged(FAKE, 64, 64, 63)), "aligned"),

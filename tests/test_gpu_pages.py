@@ -512,3 +512,25 @@ def test_pools_of_several_page_sizes():
     assert host(r.table).tolist() == [[1, 0], [2, 3]] and host(r.refs).tolist() == [1, 1, 1, 1, 0, 0, 0, 0, 0]
     for x, b in zip(p, before):
         same(raw(x).ravel(), moved(b, x, [(4, 0), (7, 2), (8, 3)]).ravel(), "pool")
+
+
+def test_offsets_past_32_bits():
+    """Pages of 1 GB, the last of them 5 GB into the pool; slots 5 GB into a cache."""
+    torch = torch_cuda()
+    banner("pages: 6 GB")
+    pool = torch.zeros((6, 1 << 30), dtype=torch.uint8, device="cuda")
+    pool[5].view(torch.int32).copy_(torch.arange(1 << 28, dtype=torch.int32, device="cuda"))
+    st = ts.ts_pages_copy(gpu([5]), gpu([1]), [pool])
+    assert host(st).tolist() == [0] and torch.equal(pool[1], pool[5]) and not bool(pool[0].any()) and not bool(pool[2].any())
+    r = ts.ts_pages_compact(gpu([[5, 1]]), gpu([2]), gpu([0, 1, 0, 0, 0, 1]), 1, pools=[pool])
+    assert host(r.table).tolist() == [[0, 1]] and torch.equal(pool[0], pool[5])
+    pool.zero_()
+    k = pool.view(torch.bfloat16).view(6 << 14, 1, 256, 128)                   # pages of 64 KB
+    v = torch.zeros_like(k)
+    fresh = torch.randn((300, 1, 128), device="cuda").to(torch.bfloat16)
+    last = k.shape[0] - 1
+    st = ts.ts_cache_append(fresh, fresh, gpu([0, 300]), k, v, gpu([[7, last]]), gpu([400]))
+    assert host(st).tolist() == [0]
+    for x in (k, v):
+        assert torch.equal(torch.cat([x[7, 0, 100:], x[last, 0, :144]]), fresh[:, 0])
+        assert not bool(x[last, 0, 144:].any()) and not bool(x[7, 0, :100].any()) and not bool(x[last - 1].any()) and not bool(x[8].any())

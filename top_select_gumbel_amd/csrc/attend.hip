@@ -1049,6 +1049,7 @@ extern "C" int ts_cache_attend(const void* q, int dtype, int64_t batch, int32_t 
   }
   if (batch == 0) return TS_OK;
   if (!q || (!table && table_width > 0) || !lengths || !out) return fail(TS_ERR_INVALID_ARG, "q, table, lengths and out are required (NULL given)");
+  if (out == q) return fail(TS_ERR_INVALID_ARG, "out may not be q: other waves still read it");
   if (pages < 1) return fail(TS_ERR_INVALID_ARG, "pages = %lld < 1", (long long)pages);
   if ((uintptr_t)q % size || (uintptr_t)out % size || (out_weights && (uintptr_t)out_weights % w_size))
     return fail(TS_ERR_INVALID_ARG, "q, out or out_weights is not aligned to its type");
