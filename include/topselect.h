@@ -398,7 +398,7 @@ typedef struct ts_paged {   /* one layer's keys or values: slot s of page p unde
  *   scale       in [2^-64, 2^64].
  *   out         may not overlap q.   out_lse  [batch, q_heads] fp32 or NULL.
  *   out_weights [batch, q_heads, weights_slots] of `weights_dtype` at the given strides (elements) or NULL (weights_slots 0):
- *               0 outside [lo, n). With batch * kv_heads rows of q_heads / kv_heads weights it is what ts_cache_evict takes.
+ *               0 outside [lo, n), whatever the scores. With batch * kv_heads rows of q_heads / kv_heads weights it is what ts_cache_evict takes.
  *               A length above weights_slots gives TS_ROW_BAD_LENGTH.
  *   row_status  [batch] int32 or NULL.
  * A sequence of no positions, or whose scores are all -inf, gives out 0, lse -inf, weights 0. Slots outside [lo, n) may hold

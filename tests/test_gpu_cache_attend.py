@@ -450,3 +450,48 @@ def test_many_tiny_sequences_beside_long_ones():
     """Rows of one tile each fall to a few waves; one row spans many workgroups."""
     lengths = np.r_[np.arange(1, 60), 30000, np.ones(40, int), 12000]
     check(lengths=lengths, hk=1, hq=3, dim=64, slots=16, dtype="bfloat16", wtype="float32")
+
+
+def weights_of_a_spoilt_score(route, dtype, wtype, value, window):
+    """Sequence 0 attends a key that makes one head's score NaN or +inf; sequence 1's page number is bad; 2 is sound, 3 empty.
+    Of 0's spoilt heads every attended weight is NaN (so is the sum), every other slot 0: only rejected sequences have NaN there."""
+    torch = torch_cuda()
+    # one launch; several workgroups' stretches with rows that one of them finishes; a row that many of them share
+    n, room, batch = {"whole": (90, 128, 4), "finished": (90, 2000, 4000), "joined": (9000, 9100, 4)}[route]
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    t, slots, dim = getattr(torch, dtype), 16, 32
+    width, held = -(-room // slots), -(-n // slots)
+    k, v = (torch.randn((4 * held, 2, slots, dim), generator=gen, device="cuda").to(t) for _ in range(2))
+    table = torch.full((batch, width), -1, dtype=torch.int32, device="cuda")
+    table[:4, :held] = torch.arange(4 * held, dtype=torch.int32, device="cuda").view(4, held)
+    table[4:, :held] = table[2, :held]
+    q = torch.randn((batch, 6, dim), generator=gen, device="cuda").to(t)
+    q[:, 3:, 0] = 1.0
+    lengths = torch.full((batch,), n, dtype=torch.int32, device="cuda")
+    lengths[3] = 0
+    at = n - 20                                                   # inside every window
+    k[table[0, at // slots].long(), 1, at % slots, 0] = value     # of heads 3, 4 and 5
+    table[1, (n - 1) // slots] = 1 << 30
+    banner(f"attend: weights of a spoilt score {route} {dtype} {wtype} {value} window={window}")
+    r = ts.ts_cache_attend(q, k, v, table, lengths, window=window, weights_slots=n + 7, weights_dtype=getattr(torch, wtype))
+    status, w = host(r.status), host(r.weights[:4].double())
+    assert status[:4].tolist() == [0, ts.TS_ROW_BAD_PAGE, 0, 0] and not status[4:].any()
+    lo = max(0, n - window) if window else 0
+    attended = np.zeros(n + 7, bool)
+    attended[lo:n] = True
+    for h in range(6):
+        if h >= 3:
+            assert np.isnan(w[0, h, attended]).all() and np.isnan(host(r.out[0, h].double())).all() and np.isnan(float(r.lse[0, h]))
+        else:
+            assert (w[0, h, attended] > 0).any() and np.isfinite(w[0, h]).all()
+        for b in (0, 2):
+            assert (w[b, h, ~attended] == 0).all(), f"head {h} of sequence {b}: weights outside its positions"
+        assert np.isfinite(w[2, h]).all() and not w[3, h].any() and np.isnan(w[1, h]).all()
+
+
+@pytest.mark.parametrize("route", ["whole", "finished", "joined"])
+@pytest.mark.parametrize("dtype,wtype", [("bfloat16", "bfloat16"), ("float32", "float32"), ("float16", "float32")])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_weights_outside_the_positions_of_a_spoilt_score(route, dtype, wtype, value):
+    for window in (0, 37):
+        weights_of_a_spoilt_score(route, dtype, wtype, value, window)

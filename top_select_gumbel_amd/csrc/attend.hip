@@ -93,7 +93,7 @@ struct AParams {
   int32_t w_slots;
   float* score;                   // [batch * q_heads, score_stride]: s_j, where weights are asked for
   int64_t score_stride;
-  float2* norm;                   // [batch * q_heads]: the row's m and 1 / sum (with fp16's factor), for the weights
+  float2* norm;                   // [batch * q_heads]: the row's m (NaN: it is refused) and 1 / sum (with fp16's factor), for the weights
   int64_t* start;                 // [batch + 1]: places of the sequences before; then how many workgroups share them
   float* part;                    // [workgroups, 2, part_floats]
   int32_t whole;                  // a workgroup a row, no parts
@@ -457,7 +457,7 @@ __device__ __forceinline__ void store_norm(const AParams& P, const RowOut& R, fl
   if (i >= R.heads) return;
   const int64_t at = (int64_t)R.b * P.q_heads + R.head0 + i;
   if (P.lse) P.lse[at] = status != TS_ROW_OK ? NAN : sum == 0.0f ? -INFINITY : m * P.scale + logf(ldexpf(sum, -(int)bias));
-  if (P.norm) P.norm[at] = status != TS_ROW_OK ? float2{0.0f, NAN} : float2{m, sum == 0.0f ? 0.0f : 1.0f / sum};
+  if (P.norm) P.norm[at] = status != TS_ROW_OK ? float2{NAN, NAN} : float2{m, sum == 0.0f ? 0.0f : 1.0f / sum};
 }
 
 // ------------------------------------------------------------------ the pass over the cache
@@ -763,7 +763,8 @@ struct Parts {
   __device__ __forceinline__ const float* at(int p) const { return first + max(2 * p - 1, 0) * kSize; }
 };
 
-// exp(scale (s - m)) / sum of positions j0 .. + 4 of a query head, 0 outside [lo, n), from the stored scores.
+// exp(scale (s - m)) / sum of positions j0 .. + 4 of a query head, 0 outside [lo, n), from the stored scores; all NaN in a refused
+// row. An m of NaN is what tells that: a running maximum passes over NaN scores, while the sum of a sound row may well be NaN.
 __device__ __forceinline__ void store_weights(const AParams& P, int b, int head, const Span& span, float m, float inv, float bias, int j0) {
   if (j0 >= P.w_slots) return;
   f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -773,7 +774,7 @@ __device__ __forceinline__ void store_weights(const AParams& P, int b, int head,
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const int j = j0 + e;
-    float w = inv != inv ? NAN : 0.0f;
+    float w = m != m ? NAN : 0.0f;
     if (j >= span.lo && j < span.n) w = exp2_fast((x[e] - base) * P.c + bias) * inv;
     x[e] = w;
   }
@@ -810,7 +811,7 @@ __global__ __launch_bounds__(NW * 64) void ts_attend_join_kernel(const AParams P
     if (P.whole) {
       norm = P.norm[row];
     } else if (tiles == 0) {
-      norm = float2{-INFINITY, span.status != TS_ROW_OK ? NAN : 0.0f};
+      norm = float2{span.status != TS_ROW_OK ? NAN : -INFINITY, 0.0f};
     } else if (const Parts<DT, DP> parts(P, b, hk * P.head_tiles + in / kCols, tiles); parts.count == 1) {
       norm = P.norm[row];
     } else {
@@ -830,7 +831,7 @@ __global__ __launch_bounds__(NW * 64) void ts_attend_join_kernel(const AParams P
         l = l * (m == grown ? 1.0f : exp2_fast((m - grown) * P.c)) + lo * (mo == grown ? 1.0f : exp2_fast((mo - grown) * P.c));
         m = grown;
       }
-      norm = float2{m, __builtin_amdgcn_ballot_w64(bad) ? NAN : l == 0.0f ? 0.0f : 1.0f / l};
+      norm = __builtin_amdgcn_ballot_w64(bad) ? float2{NAN, NAN} : float2{m, l == 0.0f ? 0.0f : 1.0f / l};
     }
     store_weights(P, b, head, span, norm.x, norm.y, S::kBias, j0);
     return;
