@@ -480,7 +480,7 @@ int ts_pages_compact(const int32_t* table, int64_t seqs, int64_t table_width, in
 /*
  * ts_pages_copy -- page source[i] of every pool to page target[i], for n pairs (device arrays), at most 65536.
  *   pair_status [n] int32 or NULL: TS_ROW_BAD_PAGE for a pair that is not copied because a page of it does not exist or its source is
- *               another pair's target. Of several pairs with one target the last is copied.
+ *               another pair's target. Of several other pairs with one target the last is copied, whatever refused ones follow it.
  * Needs no workspace.
  */
 int ts_pages_copy(const int32_t* source, const int32_t* target, int64_t n, int64_t pages, const ts_pool* pools, int32_t n_pools,

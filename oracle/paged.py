@@ -213,11 +213,11 @@ def compact(table, lengths, refs, slots: int) -> CompactResult:
 
 
 def copy_pairs(source, target, pages: int) -> Tuple[List[Tuple[int, int]], List[int]]:
-    """The copies that are made, and every pair's status."""
-    targets, moves, status = list(map(int, target)), [], []
+    """The copies that are made, and every pair's status. Of the sound pairs with one target the last is copied."""
+    targets, last, status = list(map(int, target)), {}, []
     for i, (s, t) in enumerate(zip(map(int, source), targets)):
         bad = not (0 <= s < pages and 0 <= t < pages) or any(x == s for j, x in enumerate(targets) if j != i)
         status.append(STATUS_BAD_PAGE if bad else STATUS_OK)
-        if not bad and t not in targets[i + 1:]:
-            moves.append((s, t))
-    return moves, status
+        if not bad:
+            last[t] = i
+    return [(int(source[i]), targets[i]) for i in sorted(last.values())], status

@@ -534,3 +534,34 @@ def test_offsets_past_32_bits():
     for x in (k, v):
         assert torch.equal(torch.cat([x[7, 0, 100:], x[last, 0, :144]]), fresh[:, 0])
         assert not bool(x[last, 0, 144:].any()) and not bool(x[7, 0, :100].any()) and not bool(x[last - 1].any()) and not bool(x[8].any())
+
+
+# ---------------------------------------------------------------- refused pairs beside sound ones
+@pytest.mark.parametrize("pairs", [
+    [(1, 6), (-1, 6)], [(1, 6), (1 << 30, 6), (-5, 6)],                  # the later one names no page
+    [(1, 5), (5, 5)],                                                    # its source is the first one's target
+    [(1, 6), (2, 6), (-1, 6), (3, 6), (-1, 6), (6, 6)],                  # the last sound one of several, not the first
+    [(2, 6), (7, 6), (3, 7)],                                            # its source is another target's
+    [(-1, 6), (1, 6), (-1, 4), (6, 4), (2, 4)], [(-1, 6), (-1, 6)], [(6, 6), (6, 6), (9, 6)],
+    [(1, 1 << 30), (-1, 1 << 30), (2, -1), (3, -1)],
+])
+def test_copy_of_sound_and_refused_pairs_with_one_target(pairs):
+    source, target = zip(*pairs)
+    check_copy(list(source), list(target), 9)
+
+
+@pytest.mark.parametrize("n,pages,bad", [(300, 40, 0.5), (1000, 64, 0.9), (3000, 5000, 0.3), (2000, 9, 0.99)])
+def test_copy_of_many_pairs_some_refused(n, pages, bad):
+    rng = np.random.default_rng(n)
+    half = max(1, pages // 2)
+    source, target = rng.integers(0, half, n), rng.integers(half, pages, n)
+    wrong = rng.random(n) < bad
+    source[wrong] = rng.choice([-1, pages, half, pages - 1], int(wrong.sum()))
+    check_copy(source.tolist(), target.tolist(), pages, page=(4, 4), pools=1)
+
+
+def test_copy_of_a_target_whose_last_sound_pair_comes_early():
+    """Behind it stand more refused pairs than a workgroup has threads: out of range, or reading other pairs' targets."""
+    for filler in (-1, 7, 6):
+        check_copy([1, 2] + [filler] * 700 + [3], [6, 6] + [6] * 700 + [7], 9, page=(4, 4), pools=1)
+    check_copy([1] + [7] * 700 + [2] + [8] * 300 + [3, 4], [6] * 1002 + [7, 8], 9, page=(4, 4), pools=1)

@@ -105,3 +105,31 @@ def test_copy_pairs():
     moves, st = paged.copy_pairs([0, 5], [5, 0], 8)              # a swap: each would read what the other writes
     assert moves == [] and st == [7, 7]
     assert paged.append([3, 5], [0, 2, 3], [[1, 0], [7, 2]], 2, 4, 3) == ([(0, 1, 1), (1, 0, 0)], [0, 8])
+
+
+def test_copy_pairs_refused_beside_sound():
+    for pairs, want, status in (
+            ([(1, 6), (-1, 6)], [(1, 6)], [0, 7]),
+            ([(1, 5), (5, 5)], [(1, 5)], [0, 7]),
+            ([(1, 6), (2, 6), (-1, 6)], [(2, 6)], [0, 0, 7]),
+            ([(2, 6), (7, 6), (3, 7)], [(2, 6), (3, 7)], [0, 7, 0]),
+            ([(-1, 6), (-1, 6)], [], [7, 7])):
+        source, target = zip(*pairs)
+        assert paged.copy_pairs(source, target, 8) == (want, status)
+
+
+@pytest.mark.parametrize("seed", range(30))
+def test_copy_pairs_does_what_its_statuses_say(seed):
+    """Every target of a pair with status 0 holds the page of the last such pair afterwards, and no other page changes."""
+    rng = np.random.default_rng(seed)
+    pages, n = int(rng.integers(2, 12)), int(rng.integers(1, 20))
+    source, target = (rng.integers(-1, pages + 1, n).tolist() for _ in range(2))
+    moves, status = paged.copy_pairs(source, target, pages)
+    want = list(range(pages))
+    for s, t, st in zip(source, target, status):
+        if st == 0:
+            want[t] = s
+    got = list(range(pages))
+    for s, t in moves:
+        got[t] = s                                            # sources are never targets, so any order will do
+    assert got == want and len({t for _, t in moves}) == len(moves)

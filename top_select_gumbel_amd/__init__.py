@@ -845,7 +845,8 @@ def ts_pages_compact(table, lengths, refs, page_slots: int, pools=(), in_place: 
 
 def ts_pages_copy(source, target, pools):
     """Copy page source[i] to page target[i] (int32 [n]) in every tensor of `pools`: returns status int32 [n], TS_ROW_BAD_PAGE for
-    pairs that are not copied (a page out of range, or a source that is another pair's target)."""
+    pairs that are refused (a page out of range, or a source that is another pair's target); of the others with one target the last
+    is copied."""
     torch = _torch or _t()
     lib = _lib or load_library()
     if not isinstance(pools, PagePools):
