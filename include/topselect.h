@@ -448,7 +448,8 @@ typedef struct ts_pool {   /* an array of pages: page p is the page_bytes bytes 
  *   out_lengths [children];  out_refs [pages], may be refs.
  *   pools       the n_pools arrays (at most 4096; host memory: keys and values of every layer) in which pages are copied.
  *   row_status  [children] or NULL. TS_ROW_NO_PAGE: not enough free pages for the child (each takes its turn whether or not those
- *               before it fit): it keeps its parent's positions and does not grow, and is left empty if it needed a copy.
+ *               before it fit; one that needs no page is never refused): it keeps its parent's positions and does not grow, and
+ *               is left empty if it needed a copy.
  *               TS_ROW_BAD_LENGTH: n_new negative or past out_width: the same, or the parent's length bad or past out_width: empty.
  *               TS_ROW_BAD_PAGE, TS_ROW_BAD_PARENT: the parent's row, or parent[i], is bad: empty.
  * The pages of a sequence whose own row is bad keep their counts. At most 65536 sequences and children. Arrays must not overlap

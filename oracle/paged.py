@@ -143,7 +143,8 @@ def fork(table, lengths, refs: Sequence[int], parent, n_new, slots: int, width: 
                 total = n + grow
         need = int(copied) + -(-total // slots) - -(-n // slots)
         row = list(held[p]) if p >= 0 else []
-        if taken + need <= len(free):
+        found = need == 0 or taken + need <= len(free)      # who needs no page misses none, whoever came before
+        if found:
             fresh = free[taken: taken + need]
             if copied:
                 out.copies.append((row[-1], fresh[0]))
@@ -156,7 +157,7 @@ def fork(table, lengths, refs: Sequence[int], parent, n_new, slots: int, width: 
             if copied:
                 give_back += row[:-1]
                 row, total = [], 0
-        for page in free[taken: taken + need] if taken + need <= len(free) else []:
+        for page in free[taken: taken + need] if found else []:
             refs[page] = 1
         taken += need
         out.table.append(row + [-1] * (width - len(row)))

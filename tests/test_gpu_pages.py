@@ -565,3 +565,49 @@ def test_copy_of_a_target_whose_last_sound_pair_comes_early():
     for filler in (-1, 7, 6):
         check_copy([1, 2] + [filler] * 700 + [3], [6, 6] + [6] * 700 + [7], 9, page=(4, 4), pools=1)
     check_copy([1] + [7] * 700 + [2] + [8] * 300 + [3, 4], [6] * 1002 + [7, 8], 9, page=(4, 4), pools=1)
+
+
+# ---------------------------------------------------------------- children that need no page
+def test_fork_of_children_without_needs_after_the_pages_ran_out():
+    """A token into a part-filled page, nothing new, or no parent at all: no page is needed, so none can be missing."""
+    table, refs = [[0, 1, -1], [2, -1, -1], [3, -1, -1]], [1, 1, 1, 1, 0]
+    for in_place in (False, True):
+        r = check_fork(table, [6, 4, 3], refs, [0, 1, 2, 0, -1, 2, 1], [0, 9, 1, 0, 0, 0, 0], 4, width=5, in_place=in_place)
+        assert host(r.status).tolist() == [0, ts.TS_ROW_NO_PAGE, 0, ts.TS_ROW_NO_PAGE, 0, ts.TS_ROW_NO_PAGE, 0]
+        assert host(r.lengths).tolist() == [6, 4, 4, 0, 0, 0, 4]
+    # no free page at all
+    r = check_fork([[0, 1], [2, 3]], [7, 6], [1, 1, 1, 1], [0, 1, -1, -1], [2, 1, 0, 1], 4, width=3)
+    assert host(r.status).tolist() == [ts.TS_ROW_NO_PAGE, 0, 0, ts.TS_ROW_NO_PAGE] and host(r.lengths).tolist() == [7, 7, 0, 0]
+    # a bad n_new or parent is told as such, also there
+    r = check_fork([[0, 1], [2, 3]], [7, 6], [1, 1, 1, 1], [0, 1, 7], [2, -1, 0], 4, width=3)
+    assert host(r.status).tolist() == [ts.TS_ROW_NO_PAGE, ts.TS_ROW_BAD_LENGTH, ts.TS_ROW_BAD_PARENT]
+
+
+def test_fork_of_children_without_needs_by_several_launches():
+    """The same for more children than one workgroup takes: a decode step of a pool that is one page short."""
+    slots, seqs = 16, 1100
+    lengths = np.full(seqs, 20)
+    lengths[[3, 500]] = 32                                   # these start a page, the others go on in theirs
+    table = np.arange(2 * seqs).reshape(seqs, 2)
+    refs = [1] * (2 * seqs) + [0]
+    r = check_fork(np.pad(table, ((0, 0), (0, 1)), constant_values=-1), lengths.tolist(), refs, list(range(seqs)) + [-1],
+                   [1] * seqs + [0], slots, pools=1, page=(4, 2))
+    st = host(r.status)
+    assert st[500] == ts.TS_ROW_NO_PAGE and not np.delete(st, 500).any()
+    assert (np.delete(host(r.lengths), [3, 500, seqs]) == 21).all()
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_fork_random_with_few_free_pages(seed):
+    """Forks over a pool that is used up, by one workgroup and by several launches."""
+    rng = np.random.default_rng(700 + seed)
+    seqs = int(rng.integers(2, 30)) if seed % 3 else 1050
+    slots, width = int(rng.choice([3, 16])), 6
+    table, lengths, refs = sequences(rng, seqs, seqs * 4, slots, width, share=0.2, fill=0.9)
+    free = [p for p, r in enumerate(refs) if r == 0]
+    for p in free[int(rng.integers(0, 4)):]:
+        refs[p] = 1                                          # held by something else
+    n = seqs + int(rng.integers(0, 10))
+    parent = np.where(rng.random(n) < 0.9, np.arange(n) % seqs, -1)
+    check_fork(table, lengths, refs, parent, rng.integers(0, 2, n), slots, width=width + seed % 2, pools=1, page=(4, 2),
+               in_place=bool(seed & 1), seed=seed)

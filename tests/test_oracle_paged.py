@@ -133,3 +133,12 @@ def test_copy_pairs_does_what_its_statuses_say(seed):
     for s, t in moves:
         got[t] = s                                            # sources are never targets, so any order will do
     assert got == want and len({t for _, t in moves}) == len(moves)
+
+
+def test_fork_children_without_needs():
+    """Children that need no page are not refused for want of pages, whoever came before them."""
+    r = paged.fork([[0, 1, -1], [2, -1, -1], [3, -1, -1]], [6, 4, 3], [1, 1, 1, 1, 0], [0, 1, 2, 0, -1, 2, 1], [0, 9, 1, 0, 0, 0, 0], 4, 5)
+    assert r.status == [0, 10, 0, 10, 0, 10, 0] and r.lengths == [6, 4, 4, 0, 0, 0, 4]
+    assert r.refs == counts(r.table, 5) and r.copies == []
+    r = paged.fork([[0, 1]], [7], [1, 1], [0, -1, 5, 0], [1, 0, 0, -1], 4, 2)
+    assert r.status == [0, 0, paged.STATUS_BAD_PARENT, paged.STATUS_BAD_LENGTH] and r.lengths == [8, 0, 0, 0]

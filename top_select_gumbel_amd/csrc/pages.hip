@@ -349,13 +349,17 @@ __global__ __launch_bounds__(kPT) void ts_pages_share_kernel(const ForkArgs F) {
   F.child[c] = C;
 }
 
+// Whether a child's fresh pages are among the free ones, given the needs of those before it. One that needs none always fits,
+// also behind a child that asked for too many.
+__device__ __forceinline__ bool fits(const ChildInfo& C, uint32_t before, uint32_t free) { return C.need == 0 || before + C.need <= free; }
+
 // A child's outputs, once it is known whether its fresh pages are there.
-__device__ __forceinline__ void end_child(const ForkArgs& F, int c, const ChildInfo& C, bool fits) {
-  const bool empty = !fits && C.copies;
-  const int length = fits ? C.grown : empty ? 0 : C.old;
+__device__ __forceinline__ void end_child(const ForkArgs& F, int c, const ChildInfo& C, bool found) {
+  const bool empty = !found && C.copies;
+  const int length = found ? C.grown : empty ? 0 : C.old;
   F.out_lengths[c] = length;
-  if (F.status) F.status[c] = C.status != TS_ROW_OK ? C.status : fits ? TS_ROW_OK : TS_ROW_NO_PAGE;
-  if (!(fits && C.copies)) F.source[c] = -1;   // else the copy's pages are filled in with the page that it gets
+  if (F.status) F.status[c] = C.status != TS_ROW_OK ? C.status : found ? TS_ROW_OK : TS_ROW_NO_PAGE;
+  if (!(found && C.copies)) F.source[c] = -1;   // else the copy's pages are filled in with the page that it gets
   F.end[c] = EndInfo{empty ? 0 : pages_of(F.by_page, C.old) - C.copies, pages_of(F.by_page, length),
                      empty ? (int)F.by_page.of(C.old) : 0};
 }
@@ -405,7 +409,7 @@ __global__ __launch_bounds__(kPT) void ts_pages_assign_kernel(const ForkArgs F) 
     const int c = ((int)blockIdx.x - F.tiles) * kPT + threadIdx.x;
     if (c >= F.children) return;
     const ChildInfo C = F.child[c];
-    end_child(F, c, C, F.start[c] + C.need <= all);
+    end_child(F, c, C, fits(C, F.start[c], all));
     return;
   }
   const uint32_t wanted = F.start[F.children];
@@ -594,7 +598,7 @@ __global__ __launch_bounds__(kOT) void ts_pages_fork_one_kernel(const ForkArgs F
     F.out_table[lo * F.out_stride + at] = page;
     F.out_refs[page] = 1;
   }
-  if (t < F.children) end_child(F, t, C, mine + C.need <= all);
+  if (t < F.children) end_child(F, t, C, fits(C, mine, all));
 }
 
 // ------------------------------------------------------------------ compact
