@@ -399,7 +399,7 @@ typedef struct ts_paged {   /* one layer's keys or values: slot s of page p unde
  *   out         may not overlap q.   out_lse  [batch, q_heads] fp32 or NULL.
  *   out_weights [batch, q_heads, weights_slots] of `weights_dtype` at the given strides (elements) or NULL (weights_slots 0):
  *               0 outside [lo, n), whatever the scores. With batch * kv_heads rows of q_heads / kv_heads weights it is what ts_cache_evict takes.
- *               A length above weights_slots gives TS_ROW_BAD_LENGTH.
+ *               A length above weights_slots (at most 2^31 - 4096) gives TS_ROW_BAD_LENGTH.
  *   row_status  [batch] int32 or NULL.
  * A sequence of no positions, or whose scores are all -inf, gives out 0, lse -inf, weights 0. Slots outside [lo, n) may hold
  * anything. NaN and infinities in attended keys and values act as in the formula (a non-finite value may give NaN where

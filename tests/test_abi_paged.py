@@ -188,3 +188,15 @@ def test_divisor_of_the_kernels():
         for j in [0, 1, d - 1, d, d + 1, 2 * d - 1, (1 << 31) - 1, (1 << 31) // d * d - 1, (1 << 31) // d * d] + [rng.randrange(1 << 31) for _ in range(20)]:
             if 0 <= j < 1 << 31:
                 assert (j * mul) >> (31 + bits) == j // d
+
+
+def test_attend_weights_slots_limit(lib):
+    """Sums of weights_slots and a workgroup's positions (4096 at most) stay below 2^31 up to the limit."""
+    most = 0x7FFFF000
+    assert most + 4096 - 1 < 1 << 31 and -(-most // 4096) * 4096 < 1 << 31
+    call = dict(batch=1, weights=1 << 30, w_dtype=1, w_b=1 << 40, w_h=1 << 32, ws=None)
+    for slots in (most + 1, most + 4095, 0x7FFFFF00, 0x7FFFFF01, (1 << 32) + 8):
+        assert attend(lib, w_slots=slots, **call) == ts.TS_ERR_INVALID_ARG and "large" in ts.ts_last_error()
+        assert lib.ts_cache_attend_workspace(1, 1, 8, 4, 32, 3200, slots) == 0
+    assert attend(lib, w_slots=most, **call) == ts.TS_ERR_WORKSPACE
+    assert lib.ts_cache_attend_workspace(1, 1, 8, 4, 32, 3200, most) > 8 * most * 4

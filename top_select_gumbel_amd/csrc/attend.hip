@@ -941,9 +941,12 @@ struct APlan {
 // 8 x 1000 22 against 18, 64 x 1000 46 against 51, 64 of up to 1000 36 against 38, 256 of up to 1000 108 against 105.)
 constexpr int64_t kWholeTiles = 16, kWholeMore = 32, kWholeRows = 256, kWholeMost = 1024;
 
+// Weights of a head: a workgroup's positions (16 waves' 4096 at most) past the last one stay in 31 bits.
+constexpr int64_t kMaxWeights = 0x7FFFF000;
+
 bool attend_plan(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t dim, int64_t max_len, int64_t w_slots, int tile, APlan& pl) {
   if (batch < 0 || batch > (1 << 24) || kv_heads < 1 || q_heads < kv_heads || q_heads > (1 << 16) || q_heads % kv_heads || dim < 1 ||
-      dim > kMaxDim || max_len < 0 || max_len > 0x7FFFFF00 || w_slots < 0 || w_slots > 0x7FFFFF00)
+      dim > kMaxDim || max_len < 0 || max_len > tsp::kMaxLen || w_slots < 0 || w_slots > kMaxWeights)
     return false;
   const int64_t tiles = (q_heads / kv_heads + kCols - 1) / kCols;
   pl.rows = batch * kv_heads * tiles;
