@@ -194,9 +194,9 @@ def test_attend_weights_slots_limit(lib):
     """Sums of weights_slots and a workgroup's positions (4096 at most) stay below 2^31 up to the limit."""
     most = 0x7FFFF000
     assert most + 4096 - 1 < 1 << 31 and -(-most // 4096) * 4096 < 1 << 31
-    call = dict(batch=1, weights=1 << 30, w_dtype=1, w_b=1 << 40, w_h=1 << 32, ws=None)
+    call = dict(batch=1, q_heads=2, kv_heads=2, weights=1 << 30, w_dtype=1, w_b=1 << 40, w_h=1 << 32, ws=None)
     for slots in (most + 1, most + 4095, 0x7FFFFF00, 0x7FFFFF01, (1 << 32) + 8):
         assert attend(lib, w_slots=slots, **call) == ts.TS_ERR_INVALID_ARG and "large" in ts.ts_last_error()
-        assert lib.ts_cache_attend_workspace(1, 1, 8, 4, 32, 3200, slots) == 0
+        assert lib.ts_cache_attend_workspace(1, 1, 2, 2, 32, 3200, slots) == 0
     assert attend(lib, w_slots=most, **call) == ts.TS_ERR_WORKSPACE
-    assert lib.ts_cache_attend_workspace(1, 1, 8, 4, 32, 3200, most) > 8 * most * 4
+    assert lib.ts_cache_attend_workspace(1, 1, 2, 2, 32, 3200, most) > 2 * most * 4
