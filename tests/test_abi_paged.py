@@ -200,3 +200,58 @@ def test_attend_weights_slots_limit(lib):
         assert lib.ts_cache_attend_workspace(1, 1, 2, 2, 32, 3200, slots) == 0
     assert attend(lib, w_slots=most, **call) == ts.TS_ERR_WORKSPACE
     assert lib.ts_cache_attend_workspace(1, 1, 2, 2, 32, 3200, most) > 2 * most * 4
+
+
+@pytest.mark.parametrize("kw,meets", [
+    # q [3, 8, 32] in 16 bits from FAKE on, rows of 64 bytes; the strides are in elements
+    (dict(out=FAKE + 2), True), (dict(out=FAKE + 1536 - 2), True), (dict(out=FAKE + 1536), False), (dict(out=FAKE - 1534), True),
+    (dict(out=FAKE - 1536), False),
+    # halves of one buffer [3, 2, 8, 32], and of [3, 8, 64]: side by side, or shifted by an element
+    (dict(q_b=512, o_b=512, out=FAKE + 512), False), (dict(q_b=512, o_b=512, out=FAKE + 510), True),
+    (dict(q_b=512, o_b=512, out=FAKE + 514), True), (dict(q_b=512, o_b=512, out=FAKE - 512), False), (dict(q_b=512, o_b=512, out=FAKE - 1024), True),
+    (dict(q_b=512, q_h=64, o_b=512, o_h=64, out=FAKE + 64), False), (dict(q_b=512, q_h=64, o_b=512, o_h=64, out=FAKE + 62), True),
+    (dict(q_b=512, q_h=64, o_b=512, o_h=64, out=FAKE - 64), False), (dict(q_b=512, q_h=64, o_b=512, o_h=64, out=FAKE + 66), True),
+    # other strides: the output's heads first, between the queries' rows or onto one of them
+    (dict(q_b=512, q_h=64, o_b=64, o_h=192, out=FAKE + 64), False), (dict(q_b=512, q_h=64, o_b=64, o_h=192, out=FAKE + 128), True),
+    (dict(q_b=512, q_h=64, o_b=96, o_h=320, out=FAKE + 2752), True),
+    # one sequence: its stride counts for nothing; queries shared by all
+    (dict(batch=1, q_b=0, o_b=1, out=FAKE + 512), False), (dict(batch=1, q_b=1 << 30, o_b=1, out=FAKE + 510), True),
+    (dict(q_b=0, out=FAKE + 512), False), (dict(q_b=0, out=FAKE + 510), True), (dict(q_b=0, q_h=0, out=FAKE + 64), False),
+    (dict(q_b=0, q_h=0, out=FAKE + 62), True),
+])
+def test_attend_output_beside_the_queries(lib, kw, meets):
+    """An output that shares memory with the queries is refused, one between them is not (the next check's error comes)."""
+    a = dict(batch=3, q_b=256, q_h=32, o_b=256, o_h=32)
+    a.update({k: v for k, v in kw.items() if k != "out"})
+
+    def rows(at, b, h):
+        return {at + 2 * (i * (b if a["batch"] > 1 else 0) + j * h) + 2 * d for i in range(a["batch"]) for j in range(8) for d in range(32)}
+    assert bool(rows(FAKE, a["q_b"], a["q_h"]) & rows(kw["out"], a["o_b"], a["o_h"])) == meets     # the case is what it says
+    got = attend(lib, ws=None, **kw)
+    if meets:
+        assert got == ts.TS_ERR_INVALID_ARG and "overlaps" in ts.ts_last_error()
+    else:
+        assert got == ts.TS_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_attend_output_beside_the_queries_at_random(lib, seed):
+    import random
+    rng = random.Random(seed)
+    for _ in range(40):
+        batch, hq, dim = rng.randint(1, 4), rng.randint(1, 5), rng.randint(1, 9)
+
+        def strides(apart):
+            inner, outer = rng.sample([(hq, "h"), (batch, "b")], 2)
+            s = {inner[1]: dim + rng.choice([0, 0, 1, 7])}
+            s[outer[1]] = s[inner[1]] * (inner[0] - 1) + dim + rng.choice([0, 0, 2, 9, 40])
+            return s if apart or rng.random() < 0.7 else {"b": rng.randint(0, 30), "h": rng.randint(0, 30)}
+        q, o, shift = strides(False), strides(True), rng.randint(-60, 60)
+        at = FAKE + 2 * shift
+
+        def rows(at, s):
+            return {at + 2 * (i * s["b"] + j * s["h"] + d) for i in range(batch) for j in range(hq) for d in range(dim)}
+        meets = bool(rows(FAKE, q) & rows(at, o))
+        # 2000 slots a row: sequences that need a workspace, which is missing
+        got = attend(lib, batch=batch, q_heads=hq, kv_heads=1, dim=dim, q_b=q["b"], q_h=q["h"], o_b=o["b"], o_h=o["h"], out=at, ws=None)
+        assert got == (ts.TS_ERR_INVALID_ARG if meets else ts.TS_ERR_WORKSPACE), (seed, batch, hq, dim, q, o, shift, ts.ts_last_error())

@@ -1076,6 +1076,9 @@ extern "C" int ts_cache_attend(const void* q, int dtype, int64_t batch, int32_t 
   if (!attend_plan(batch, q_heads, kv_heads, dim, window > 0 ? std::min<int64_t>(max_len, window) : max_len, weights_slots,
                    tile_of(dtype), pl))
     return fail(TS_ERR_INVALID_ARG, "batch x heads x slots too large");
+  if (tsp::meet({(uintptr_t)q, (int64_t)dim * size, {q_batch_stride * size, q_head_stride * size}, {batch, q_heads}},
+                {(uintptr_t)out, (int64_t)dim * size, {out_batch_stride * size, out_head_stride * size}, {batch, q_heads}}))
+    return fail(TS_ERR_INVALID_ARG, "out overlaps q, which other waves still read");
   if (pl.total) {
     if (!workspace) return fail(TS_ERR_WORKSPACE, "workspace is NULL");
     if (((uintptr_t)workspace & 255u) != 0) return fail(TS_ERR_WORKSPACE, "workspace is not 256-byte aligned");
