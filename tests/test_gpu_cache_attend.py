@@ -495,3 +495,11 @@ def weights_of_a_spoilt_score(route, dtype, wtype, value, window):
 def test_weights_outside_the_positions_of_a_spoilt_score(route, dtype, wtype, value):
     for window in (0, 37):
         weights_of_a_spoilt_score(route, dtype, wtype, value, window)
+
+
+@pytest.mark.parametrize("window", [(1 << 31) - 1, 1 << 31, (1 << 32) + 5, 1 << 62])
+def test_windows_past_any_length(window):
+    a = plain_call(4)
+    assert equal(ts.ts_cache_attend(**a, window=window), ts.ts_cache_attend(**a))
+    with pytest.raises(ts.TopSelectError):
+        ts.ts_cache_attend(**a, window=-window)

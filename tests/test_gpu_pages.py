@@ -611,3 +611,16 @@ def test_fork_random_with_few_free_pages(seed):
     parent = np.where(rng.random(n) < 0.9, np.arange(n) % seqs, -1)
     check_fork(table, lengths, refs, parent, rng.integers(0, 2, n), slots, width=width + seed % 2, pools=1, page=(4, 2),
                in_place=bool(seed & 1), seed=seed)
+
+
+# ---------------------------------------------------------------- arguments
+@pytest.mark.parametrize("slots", [(1 << 32) + 4, -(1 << 32) + 4, 1 << 31, (1 << 30) + 1, 0, -4])
+def test_page_sizes_that_are_none(slots):
+    torch = torch_cuda()
+    table, refs = gpu([[0, 1], [2, 3]]), gpu([1, 1, 1, 1, 0])
+    for call in (lambda: ts.ts_pages_fork(table, gpu([8, 5]), refs, gpu([0, 1]), slots, in_place=True),
+                 lambda: ts.ts_pages_compact(table, gpu([8, 5]), refs, slots, in_place=True)):
+        with pytest.raises(ts.TopSelectError):
+            call()
+    torch.cuda.synchronize()
+    assert host(refs).tolist() == [1, 1, 1, 1, 0] and host(table).tolist() == [[0, 1], [2, 3]]

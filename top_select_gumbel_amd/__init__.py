@@ -667,6 +667,9 @@ def ts_cache_attend(q, k_pages, v_pages, table, lengths, scale: Optional[float] 
     if rows != b:
         raise TopSelectError(f"table must have {b} rows")
     plen = _page_lengths(lengths, b, device)
+    if window < 0:
+        raise TopSelectError("window must not be negative")
+    window = min(window, 0x7FFFFFFF)      # longer than any sequence; ctypes would take a larger one's low 32 bits
     empty = torch.empty
     if out is None:
         out = torch.empty_like(q) if q.is_contiguous() else empty(shape, dtype=dtype, device=device)
@@ -764,6 +767,12 @@ def _page_pools(pools, pages: int, device) -> PagePools:
     return pools
 
 
+def _page_slots(page_slots: int) -> int:
+    if not 1 <= page_slots <= 1 << 30:    # the library's limit; ctypes would take a larger one's low 32 bits
+        raise TopSelectError(f"page_slots = {page_slots} outside [1, 2^30]")
+    return page_slots
+
+
 def _page_refs(refs, device):
     if refs.dtype is not _torch.int32 or refs.dim() != 1 or refs.device != device or not refs.is_contiguous() or not refs.is_cuda:
         raise TopSelectError("refs must be a contiguous int32 [pages] CUDA/HIP tensor")
@@ -805,7 +814,7 @@ def ts_pages_fork(table, lengths, refs, parent, page_slots: int, n_new=None, poo
     out_refs = refs if in_place else torch.empty_like(refs)
     nb = lib.ts_pages_fork_workspace(seqs, n, pages)
     ws = torch.empty(nb, dtype=torch.uint8, device=device)
-    _call(device, lib.ts_pages_fork, table.data_ptr(), seqs, w, stride, plen, refs.data_ptr(), pages, page_slots, pparent, pnew, n,
+    _call(device, lib.ts_pages_fork, table.data_ptr(), seqs, w, stride, plen, refs.data_ptr(), pages, _page_slots(page_slots), pparent, pnew, n,
           out_table.data_ptr(), width, width, out_lengths.data_ptr(), out_refs.data_ptr(), pools.array, len(pools), status.data_ptr(),
           ws.data_ptr(), nb)
     return PagesFork(out_table, out_lengths, out_refs, status)
@@ -837,7 +846,7 @@ def ts_pages_compact(table, lengths, refs, page_slots: int, pools=(), in_place: 
                                                                               torch.empty_like(refs))
     nb = lib.ts_pages_compact_workspace(pages)
     ws = torch.empty(nb, dtype=torch.uint8, device=device)
-    _call(device, lib.ts_pages_compact, table.data_ptr(), seqs, w, stride, plen, refs.data_ptr(), pages, page_slots,
+    _call(device, lib.ts_pages_compact, table.data_ptr(), seqs, w, stride, plen, refs.data_ptr(), pages, _page_slots(page_slots),
           out_table.data_ptr(), out_stride, out_refs.data_ptr(), out_map.data_ptr(), count.data_ptr(), pools.array, len(pools),
           status.data_ptr(), ws.data_ptr(), nb)
     return PagesCompact(out_table, out_refs, out_map, count, status)
