@@ -255,3 +255,10 @@ def test_attend_output_beside_the_queries_at_random(lib, seed):
         # 2000 slots a row: sequences that need a workspace, which is missing
         got = attend(lib, batch=batch, q_heads=hq, kv_heads=1, dim=dim, q_b=q["b"], q_h=q["h"], o_b=o["b"], o_h=o["h"], out=at, ws=None)
         assert got == (ts.TS_ERR_INVALID_ARG if meets else ts.TS_ERR_WORKSPACE), (seed, batch, hq, dim, q, o, shift, ts.ts_last_error())
+
+
+def test_append_without_table_columns(lib):
+    """A table of width 0 may be NULL, as for the other calls: nothing is read of it (the slots that share memory come next)."""
+    bad = ts._Paged(FAKE, 4096, 1024, 63)
+    assert append(lib, table=None, width=0, stride=0, k=bad) == ts.TS_ERR_INVALID_ARG and "share" in ts.ts_last_error()
+    assert append(lib, table=None, width=1, stride=1, k=bad) == ts.TS_ERR_INVALID_ARG and "NULL" in ts.ts_last_error()

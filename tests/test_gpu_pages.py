@@ -624,3 +624,13 @@ def test_page_sizes_that_are_none(slots):
             call()
     torch.cuda.synchronize()
     assert host(refs).tolist() == [1, 1, 1, 1, 0] and host(table).tolist() == [[0, 1], [2, 3]]
+
+
+def test_append_to_tables_without_columns():
+    """Sequences that hold nothing: their tables may have no column, and no new token is the only one that fits."""
+    torch = torch_cuda()
+    k, v = (torch.zeros(4, 2, 4, 8, device="cuda") for _ in range(2))
+    table, fresh = torch.empty((3, 0), dtype=torch.int32, device="cuda"), torch.ones(2, 2, 8, device="cuda")
+    assert host(ts.ts_cache_append(fresh[:0], fresh[:0], gpu([0, 0, 0, 0]), k, v, table, gpu([0, 0, 0]))).tolist() == [0, 0, 0]
+    st = ts.ts_cache_append(fresh, fresh, gpu([0, 1, 1, 2]), k, v, table, gpu([0, 1, 1]))
+    assert host(st).tolist() == [ts.TS_ROW_BAD_LENGTH] * 3 and not bool(k.any()) and not bool(v.any())

@@ -891,7 +891,7 @@ int ts_cache_append(const void* k_new, const void* v_new, int64_t tokens, int64_
   int rc = tsp::check_table(pages, page_slots, table_width, table_stride);
   if (rc != TS_OK) return rc;
   if (batch == 0) return TS_OK;
-  if (!offsets || !table || !lengths) return fail(TS_ERR_INVALID_ARG, "offsets, table and lengths are required (NULL given)");
+  if (!offsets || (!table && table_width > 0) || !lengths) return fail(TS_ERR_INVALID_ARG, "offsets, table and lengths are required (NULL given)");
   if (tokens > 0 && (!k_new || !v_new)) return fail(TS_ERR_INVALID_ARG, "k_new or v_new is NULL");
   if (!tsp::reaches(slot_bytes, {{k_token_stride, tokens}, {k_head_stride, kv_heads}}, 1) ||
       !tsp::reaches(slot_bytes, {{v_token_stride, tokens}, {v_head_stride, kv_heads}}, 1))
