@@ -403,7 +403,8 @@ typedef struct ts_paged {   /* one layer's keys or values: slot s of page p unde
  *   row_status  [batch] int32 or NULL.
  * A sequence of no positions, or whose scores are all -inf, gives out 0, lse -inf, weights 0. Slots outside [lo, n) may hold
  * anything. NaN and infinities in attended keys and values act as in the formula (a non-finite value may give NaN where
- * the formula has an infinity). Sequences with a non-OK status get NaN. Scores, sums and outputs are fp32, rounded once; p_j below 2^-126 counts as 0; results
+ * the formula has an infinity). Sequences with a non-OK status get NaN. Scores, sums and outputs are fp32, rounded once (a sum
+ * p_j |v_j| past fp32's largest number is infinite, also where out is not); p_j below 2^-126 counts as 0; results
  * depend on the batch in their last bits only (the sums' order), and are the same bits for the same call.
  * Workspace: ts_cache_attend_workspace(..., max_len = table_width * page_slots, ...); it may be 0 (and the workspace NULL).
  */

@@ -7,7 +7,7 @@
 //
 // All of it is bound by memory: a page's copy by the rate of a large copy (1024 pages of 8 x 32 KB 107 us, 5.0 TB/s read and written;
 // 51119 tokens of 4 KB appended 83 us, 5.0 TB/s), the bookkeeping by what one compute unit reads or by the latency of a few
-// dependent launches (64 sequences and 20000 pages 16.6 + 3.9 us).
+// dependent launches (64 sequences and 20000 pages 17.2 + 4.0 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -823,7 +823,8 @@ struct ForkPlan {
   int64_t tiles = 0;
 };
 constexpr int64_t kMaxSeqs = 1 << 22;   // rows of a table, so that a launch of a workgroup each has fewer than 2^32 threads
-// Each sequence looks through all children for its own, each pair of a copy through all targets: of so many at most (0.3 ms).
+// Each sequence looks through all children for its own, each pair of a copy through all targets: of so many at most (a fork of 65536
+// sequences 1.3 ms, of 8192 59 us; 65536 pairs 1.5 ms).
 constexpr int64_t kMaxFork = 1 << 16, kMaxPairs = 1 << 16;
 bool fork_plan(int64_t seqs, int64_t children, int64_t pages, ForkPlan& pl) {
   if (seqs < 0 || seqs > kMaxFork || children < 0 || children > kMaxFork || pages < 0 || pages > tsp::kMaxPages) return false;
