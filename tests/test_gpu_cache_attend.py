@@ -503,3 +503,20 @@ def test_windows_past_any_length(window):
     assert equal(ts.ts_cache_attend(**a, window=window), ts.ts_cache_attend(**a))
     with pytest.raises(ts.TopSelectError):
         ts.ts_cache_attend(**a, window=-window)
+
+
+def test_output_between_the_queries_of_one_buffer():
+    """[batch, 2, heads, dim]: queries and outputs by turns are accepted and leave each other alone; shifted into them they are refused."""
+    torch = torch_cuda()
+    a = plain_call(8)
+    want = ts.ts_cache_attend(**a)
+    buf = torch.zeros(3, 2, 6, 64, dtype=a["q"].dtype, device="cuda")
+    buf[:, 0] = a["q"]
+    r = ts.ts_cache_attend(**{**a, "q": buf[:, 0]}, out=buf[:, 1])
+    assert equal(r, want) and torch.equal(buf[:, 0], a["q"]) and torch.equal(buf[:, 1], want.out)
+    flat = torch.zeros(3 * 6 * 64 + 64, dtype=a["q"].dtype, device="cuda")
+    q, out = flat[:-64].view(3, 6, 64), flat[64:].view(3, 6, 64)
+    with pytest.raises(ts.TopSelectError, match="overlaps"):
+        ts.ts_cache_attend(**{**a, "q": q}, out=out)
+    with pytest.raises(ts.TopSelectError):
+        ts.ts_cache_attend(**{**a, "q": q}, out=q)

@@ -19,7 +19,7 @@
 // P is taken in two 16-bit parts, hi of P (bf16's cut off, fp16's rounded) and lo = P - hi rounded, and both are multiplied: what
 // is lost is 2^-16 of a weight (fp16: 2^-22) or less, where a single rounding would lose 2^-8 (2^-11), more than the output's
 // own rounding when many weights cancel. fp16's P carries a factor of 2^15, so that weights down to 2^-39 of the largest stay
-// above fp16's smallest number.
+// above fp16's smallest number; below 2^-18 of the largest, where lo has no normal numbers left, 2^-40 of the largest is lost.
 // m, sums and outputs are fp32.
 //
 // The work is the list of all rows' tiles (a row: 16 query heads of a sequence), cut into equal stretches, one for each wave that
@@ -28,8 +28,8 @@
 // the workgroups' parts of others (at most two a workgroup) are joined by a second kernel.
 //
 // Measured, 32 query heads on 8 of 128 dims in bf16: 64 sequences of up to 4096 positions, 583 MB, 98 us for the pass (6.0 TB/s; a
-// plain read 6.8) and 7 for the join; one of n positions 9.5 us at 2000, 17.9 at 16000, 88 at 128000 (524 MB); 13.6 at 500, which takes no join. The first 7 us are a
-// chain of misses (lengths, page numbers, keys); from there on the memory bounds it.
+// plain read 6.8) and 7 for the join; one of n positions 9.5 us at 2000, 17.9 at 16000, 88 at 128000 (524 MB), and 13.6 at 500,
+// which takes no join. The first 7 us are a chain of misses (lengths, page numbers, keys); from there on the memory bounds it.
 #include <algorithm>
 #include <type_traits>
 #include <utility>
@@ -185,7 +185,8 @@ __device__ __forceinline__ f32x4 mma(const uint32_t* a, const uint32_t* b, f32x4
 template <int DT>
 __device__ __forceinline__ void split(float a, float b, uint32_t& hi, uint32_t& lo) {
   if constexpr (DT == TS_DTYPE_BF16) {
-    // hi is cut off (one operation less than rounded): the rest is below 2^-7 of the value, and lo loses half a step of that, 2^-16 of the value at most
+    // hi is cut off (one operation less than rounded): the rest is below 2^-7 of the value, and lo loses half a step of that, 2^-16
+    // of the value at most
     const uint32_t ua = __float_as_uint(a) & 0xFFFF0000u, ub = __float_as_uint(b) & 0xFFFF0000u;
     hi = (ua >> 16) | ub;
     const __bf16 la = (__bf16)(a - __uint_as_float(ua)), lb = (__bf16)(b - __uint_as_float(ub));
